@@ -486,6 +486,115 @@ uint64_t moe_lora_wait_limit_ns(void);
 int moe_lora_set_deterministic(int32_t on);
 int32_t moe_lora_deterministic(void);
 
+/* element types of the operators below */
+#define MLR_DTYPE_BF16 0
+#define MLR_DTYPE_F32 1
+
+/*
+ * Tokens sorted by expert and back, with their gradients (the step that the
+ * fused layer runs inside; here for training and for other expert products).
+ *
+ * A pair p = t*topk + k is token t's k-th choice.  Pairs are sorted by
+ * topk_ids[p], stable in p; pairs whose id is not in [0, num_experts) are
+ * masked: they come after all others, hold zero rows and count for nothing.
+ * The id -1 masks a pair silently, any other one also sets MLR_STATUS_INDEX.
+ * With P = num_tokens * topk and pos(p) the place of pair p:
+ *
+ * moe_permute: rows[pos(p)] = x[p / topk].
+ *   x               [num_tokens, hidden] of type `dtype`; x and rows null: only the order
+ *   rows            out [P, hidden]
+ *   pair_pos        out [P]: pos(p), or ~pos(p) (negative) for a masked pair
+ *   expert_offsets  out [num_experts + 1]: first row of each expert, then the
+ *                   number of rows that belong to one
+ *   workspace       moe_permute_workspace_bytes(...), 256-byte aligned
+ * moe_unpermute: y[t] = sum_k topk_weights[t, k] * rows[pos(t, k)], in
+ *   increasing k, in fp32; topk_weights null: weights of 1, which is the
+ *   gradient of moe_permute (rows = the gradient of its rows).
+ * moe_unpermute_backward: d_rows[pos(t, k)] = topk_weights[t, k] * dy[t] (0 for
+ *   a masked pair), d_weights[t, k] = <dy[t], rows[pos(t, k)]> in fp32 (0 for a
+ *   masked pair).
+ *   rows [P, hidden], y and dy [num_tokens, hidden] of type `dtype`; weights float32 [P].
+ * A pair_pos beyond P sets MLR_STATUS_INDEX and is skipped.  Results are
+ * bit-identical between runs.
+ * Limits: topk <= 256 and num_experts <= 16384 (moe_permute), P < 2^31.
+ */
+size_t moe_permute_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts);
+int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_tokens, int32_t topk, int32_t hidden,
+                int32_t num_experts, int32_t dtype, void* rows, int32_t* pair_pos, int32_t* expert_offsets,
+                void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+int moe_unpermute(const void* rows, const int32_t* pair_pos, const float* topk_weights, int32_t num_tokens,
+                  int32_t topk, int32_t hidden, int32_t dtype, void* y, int32_t* d_status, void* stream);
+int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair_pos, const float* topk_weights,
+                           int32_t num_tokens, int32_t topk, int32_t hidden, int32_t dtype, void* d_rows,
+                           float* d_weights, int32_t* d_status, void* stream);
+
+/*
+ * Microscaled 4-bit floats: quantisation, its inverse, and the experts'
+ * products on the FP4 tensor cores.
+ *
+ * A value is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) times the
+ * scale of its block of consecutive columns:
+ *   MLR_FP4_MX  blocks of 32, scale 2^(b - 127) stored as the byte b (255: NaN);
+ *               b is the smallest with max|x| <= 6 * 2^(b - 127) (127 for a
+ *               block of zeros)
+ *   MLR_FP4_NV  blocks of 16, E4M3 scale times the matrix's float32 tensor
+ *               scale g (1 where none is given): the scale is the rounded
+ *               min(max|x| / (6 g), 448); g must be positive and finite
+ * Codes are rounded to nearest, ties to the even code.  A block that holds an
+ * infinity or a NaN gets a NaN scale and zero codes.
+ *
+ * Layout of a matrix [rows, cols]:
+ *   codes   two per byte, even column in the low half; a row takes
+ *           moe_fp4_pitch(cols) bytes (a multiple of 16), zero past cols
+ *   scales  per 128 rows moe_fp4_scale_atoms(cols, fmt) atoms of 512 bytes; an
+ *           atom holds 128 rows x 4 blocks, row r and block c at byte
+ *           16 (r % 32) + 4 (r / 32) + c.  Blocks past cols are zero; rows
+ *           past the last one are not written.
+ * A stack of matrices has ceil(rows / 128) such row blocks for each.  Rows
+ * sorted by expert have num_rows / 128 + num_experts (integer division) row
+ * blocks, expert e's rows beginning at row block expert_offsets[e] / 128 + e.
+ *
+ * moe_fp4_quantize: x [num_matrices, rows, cols]; tensor_scale null or
+ *   [num_matrices] (NVFP4 only).
+ * moe_fp4_quantize_permuted: tokens x [num_tokens, cols] quantised once and
+ *   written to their pairs' sorted rows (topk_ids, pair_pos and expert_offsets
+ *   as moe_permute leaves them); tensor_scale null or [1].  A masked pair's
+ *   row has zero codes.  Limit: topk <= 512.
+ * moe_fp4_quantize_swiglu: sorted rows [num_rows, 2 cols], gate then up, to
+ *   the codes of up * gate / (1 + exp(-gate)), all in fp32.  Rows past
+ *   expert_offsets[num_experts] have zero codes.
+ * moe_fp4_dequantize: (code * block scale) * tensor scale, rounded once to
+ *   `dtype`.  expert_offsets null: a stack of num_matrices; else sorted rows of
+ *   num_matrices experts (tensor_scale [1]), zeros past the last expert's.
+ * moe_fp4_expert_product: y[r, n] = g_a g_w[e] sum_c A[r, c] W[e, n, c] for
+ *   each sorted row r and its expert e, summed in fp32, bf16 out [num_rows,
+ *   outputs]; w a stack [num_experts, outputs, cols]; a_tensor_scale null or
+ *   [1], w_tensor_scale null or [num_experts] (NVFP4 only).  Rows past the
+ *   last expert's are zeros.  Offsets that are not 0 <= o[e] <= o[e + 1] <=
+ *   num_rows set MLR_STATUS_INDEX and y is not written.
+ * Codes and scales are 16-byte aligned.  Limits: cols <= 524288, num_experts <= 16384.
+ */
+#define MLR_FP4_MX 0
+#define MLR_FP4_NV 1
+int64_t moe_fp4_pitch(int32_t cols);
+int32_t moe_fp4_scale_atoms(int32_t cols, int32_t fmt);
+int moe_fp4_quantize(const void* x, int32_t num_matrices, int32_t rows, int32_t cols, int32_t dtype, int32_t fmt,
+                     const float* tensor_scale, uint8_t* codes, uint8_t* scales, void* stream);
+int moe_fp4_quantize_permuted(const void* x, const int32_t* topk_ids, const int32_t* pair_pos,
+                              const int32_t* expert_offsets, int32_t num_tokens, int32_t topk, int32_t cols,
+                              int32_t num_experts, int32_t dtype, int32_t fmt, const float* tensor_scale,
+                              uint8_t* codes, uint8_t* scales, int32_t* d_status, void* stream);
+int moe_fp4_quantize_swiglu(const void* gate_up, const int32_t* expert_offsets, int32_t num_rows, int32_t cols,
+                            int32_t num_experts, int32_t dtype, int32_t fmt, const float* tensor_scale,
+                            uint8_t* codes, uint8_t* scales, int32_t* d_status, void* stream);
+int moe_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const int32_t* expert_offsets,
+                       int32_t num_matrices, int32_t rows, int32_t cols, int32_t fmt, const float* tensor_scale,
+                       int32_t dtype, void* out, void* stream);
+int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_tensor_scale,
+                           const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale,
+                           const int32_t* expert_offsets, int32_t num_rows, int32_t num_experts, int32_t outputs,
+                           int32_t cols, int32_t fmt, mlr_bf16* y, int32_t* d_status, void* stream);
+
 int moe_lora_profile_stages(uint32_t mask);
 int moe_lora_profile_begin(int32_t max_calls);
 int moe_lora_profile_end(double* stage_ms, int32_t max_stages, int32_t* n_stages, int32_t* n_calls);

@@ -1,0 +1,562 @@
+// fp4_quantize.cu -- quantisation to microscaled 4-bit floats and back.
+//
+// Per row and block of consecutive columns (32 for MXFP4, 16 for NVFP4), with
+// m = max |x| over the block:
+//   MXFP4  scale 2^s, s the smallest integer in [-127, 126] with m <= 6 * 2^s
+//          (s = 0 for m = 0), stored as the byte s + 127
+//   NVFP4  E4M3 scale q = rn(min(m / (6 g), 448)) for the matrix's fp32 tensor
+//          scale g (1 if none), and r = 1 / (q g), each step rounded to fp32
+//          (r = 0 for q = 0, at most the largest float)
+// and the code of x is x * 2^-s or x * r rounded to the nearest E2M1 value
+// (0, 0.5, 1, 1.5, 2, 3, 4, 6; ties to the even code, saturating, sign kept).
+// A block that holds an infinity or a NaN gets a NaN scale and zero codes, so
+// that what is computed from it is NaN.  Layouts: mlr_fp4.cuh.
+//
+// One thread holds 16 consecutive columns of a row (MXFP4: two neighbours
+// exchange their maxima), so a row is read once and nothing is kept outside
+// registers; bound by HBM: reads x, writes half a byte per value plus one byte
+// per block.
+#include "mlr_fp4.cuh"
+#include "mlr_profile.cuh"
+
+namespace mlr {
+namespace {
+
+constexpr int kQThreads = 256;
+constexpr int kQDests = 512;  // (row, destination) pairs a block keeps in shared memory
+enum Source { kMatrix, kTokens, kSwiglu };
+
+// What a block's rows are and where their codes and scales go.
+struct QuantParams {
+  const void* x;
+  int64_t rows;        // source rows
+  int cols, ng, nga;   // columns; 16-column groups of the code pitch; of the atoms
+  int rpb;             // source rows per block
+  uint32_t ng_magic;   // ceil(2^32 / nga)
+  int64_t group_rows;  // kMatrix: rows per matrix
+  int64_t group_blocks;
+  const float* tensor_scale;  // kMatrix: one per matrix; else one; null: 1
+  const int32_t* ids;         // kTokens: [T, K]
+  const int32_t* pair_pos;
+  const int32_t* offsets;     // kTokens, kSwiglu: [E + 1]
+  int K, E;
+  int64_t P;  // sorted rows
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t pitch, block_bytes;  // bytes of a code row; of a 128-row block's atoms
+  int32_t* status;
+};
+
+// A destination of a quantised row: its code row (-1: none) and the byte of
+// its first scale (-1: a masked row, codes zero and no scales).
+struct Dest {
+  int64_t row, scale;
+};
+
+__device__ __forceinline__ Dest sorted_dest(const QuantParams& p, int64_t r, int e) {
+  const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
+  if (o0 < 0 || r < o0 || r >= o1 || r >= p.P) {
+    set_status(p.status, MLR_STATUS_INDEX);
+    return Dest{-1, -1};
+  }
+  const int j = (int)r - o0;
+  return Dest{r, (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j)};
+}
+
+// The expert of sorted row r: the last e with offsets[e] <= r; E if r is past
+// the last expert's rows.
+__device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets, int E, int64_t r) {
+  if (r >= __ldg(offsets + E)) return E;
+  int lo = 0, hi = E;  // offsets[lo] <= r < offsets[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(offsets + mid) <= r) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <int SRC>
+__device__ __forceinline__ Dest dest_of(const QuantParams& p, int64_t row, int k) {
+  if (SRC == kMatrix) {
+    const int64_t g = row / p.group_rows;
+    const int64_t r = row - g * p.group_rows;
+    return Dest{row, (g * p.group_blocks + r / 128) * p.block_bytes + fp4_scale_byte((int)(r & 127))};
+  }
+  if (SRC == kTokens) {
+    const int q = __ldg(p.pair_pos + row * p.K + k);
+    if (q < 0) return Dest{~q < p.P ? (int64_t)~q : -1, -1};
+    const int e = __ldg(p.ids + row * p.K + k);
+    if (e < 0 || e >= p.E) {
+      set_status(p.status, MLR_STATUS_INDEX);
+      return Dest{-1, -1};
+    }
+    return sorted_dest(p, q, e);
+  }
+  const int e = row_expert(p.offsets, p.E, row);
+  return e == p.E ? Dest{row, -1} : sorted_dest(p, row, e);
+}
+
+// 16 columns of a row as fp32, zeros past the end.  VEC: rows and base are
+// 16-byte aligned and the columns a multiple of 16 bytes.
+template <bool VEC>
+__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16]) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      if (8 * h < n) q = __ldg(reinterpret_cast<const uint4*>(p) + h);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
+        v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? __uint_as_float((uint32_t)__ldg(p + i) << 16) : 0.f;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load16(const float* p, int n, float (&v)[16]) {
+  if (VEC) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (4 * h < n) q = __ldg(reinterpret_cast<const float4*>(p) + h);
+      v[4 * h] = q.x;
+      v[4 * h + 1] = q.y;
+      v[4 * h + 2] = q.z;
+      v[4 * h + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? __ldg(p + i) : 0.f;
+  }
+}
+
+// u * SiLU(g) with the roundings of the separate operations (no contraction).
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.f, expf(-g))), u);
+}
+
+// Eight values times r as E2M1 codes, value i in bits [4i, 4i + 4).
+__device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float r) {
+  uint32_t o;
+  asm("{\n\t"
+      ".reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t"
+      "}"
+      : "=r"(o)
+      : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r), "f"(v[5] * r), "f"(v[6] * r),
+        "f"(v[7] * r));
+  return o;
+}
+
+// MXFP4: the scale byte of a block from the bits of its largest magnitude, and
+// the exact reciprocal of the scale.
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax, float* r) {
+  int s = 0;
+  if (amax != 0) {
+    // amax = 1.f x 2^(ef - 127): 2^(s + 2) x 1.5 covers it from f = 0.5 down
+    const int ef = (int)(amax >> 23);
+    s = ef - 127 - ((amax & 0x7fffffu) <= 0x400000u ? 2 : 1);
+    if (ef == 0 || s < -127) s = -127;
+  }
+  *r = __int_as_float((127 - s) << 23);
+  return (uint32_t)(s + 127);
+}
+// NVFP4: the same for an E4M3 scale under the tensor scale g.
+__device__ __forceinline__ uint32_t nv_scale(float amax, float g, float* r) {
+  // a block of zeros has scale 0 even under the scale 0 of a matrix of zeros
+  const float t = amax > 0.f ? fminf(__fdiv_rn(amax, __fmul_rn(6.f, g)), 448.f) : 0.f;
+  const uint32_t q = f32x2_to_e4m3x2(t, 0.f) & 0xffu;
+  float qf;
+  asm("{\n\t"
+      ".reg .b32 p;\n\t.reg .f16 a, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 p, %1;\n\t"
+      "mov.b32 {a, b}, p;\n\t"
+      "cvt.f32.f16 %0, a;\n\t"
+      "}"
+      : "=f"(qf)
+      : "h"((uint16_t)q));
+  const float d = __fmul_rn(qf, g);
+  *r = d > 0.f ? fminf(__fdiv_rn(1.f, d), 3.4028234663852886e38f) : 0.f;
+  return q;
+}
+
+template <typename E_, int FMT, int SRC, bool VEC>
+__global__ void __launch_bounds__(kQThreads)
+quantize_kernel(const QuantParams p) {
+  __shared__ Dest dest[kQDests];
+  pdl_wait();
+  pdl_trigger();
+  const int K = SRC == kTokens ? p.K : 1;
+  const int64_t r0 = (int64_t)blockIdx.x * p.rpb;
+  const int nr = (int)min((int64_t)p.rpb, p.rows - r0);
+  for (int i = threadIdx.x; i < nr * K; i += kQThreads) dest[i] = dest_of<SRC>(p, r0 + i / K, i % K);
+  __syncthreads();
+  const E_* x = static_cast<const E_*>(p.x);
+  const int total = nr * p.nga;
+  // whole warps stay in the loop: neighbours exchange maxima and scales
+  for (int i0 = 0; i0 < total; i0 += kQThreads) {
+    const int i = i0 + threadIdx.x;
+    const bool in = i < total;
+    const int lr = in ? (int)__umulhi((uint32_t)i, p.ng_magic) : 0;
+    const int g = in ? i - lr * p.nga : 0;
+    const int64_t row = r0 + lr;
+    const int c = 16 * g;
+    const int n = in ? min(16, p.cols - c) : 0;  // <= 0 past the last column
+    float v[16];
+    if (SRC == kSwiglu) {
+      float u[16];
+      load16<VEC>(x + row * 2 * p.cols + c, n, v);
+      load16<VEC>(x + row * 2 * p.cols + p.cols + c, n, u);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = swiglu(v[j], u[j]);
+    } else {
+      load16<VEC>(x + row * p.cols + c, n, v);
+    }
+    uint32_t amax = 0;  // as bits: a NaN counts above infinity
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+    if (FMT == MLR_FP4_MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    float r;
+    uint32_t s;
+    if (FMT == MLR_FP4_MX) {
+      s = mx_scale(amax, &r);
+    } else {
+      const float ts = p.tensor_scale == nullptr ? 1.f : __ldg(p.tensor_scale + (SRC == kMatrix ? row / p.group_rows : 0));
+      s = nv_scale(__uint_as_float(amax), ts, &r);
+    }
+    uint2 q = make_uint2(to_e2m1x8(v, r), to_e2m1x8(v + 8, r));
+    if (amax >= 0x7f800000u) {
+      s = FMT == MLR_FP4_MX ? 0xffu : 0x7fu;
+      q = make_uint2(0, 0);
+    }
+    if (n <= 0) s = 0;  // scale blocks past the last column
+    // four scales of the row's atom in one word
+    if (FMT == MLR_FP4_MX) {
+      s |= __shfl_down_sync(0xffffffffu, s, 2) << 8;
+      s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
+    } else {
+      s |= __shfl_down_sync(0xffffffffu, s, 1) << 8;
+      s |= __shfl_down_sync(0xffffffffu, s, 2) << 16;
+    }
+    if (!in) continue;
+    constexpr int kLanes = FMT == MLR_FP4_MX ? 8 : 4;  // 16-column groups per atom
+    for (int k = 0; k < K; ++k) {
+      const Dest d = dest[lr * K + k];
+      if (d.row < 0) continue;
+      if (g < p.ng)
+        *reinterpret_cast<uint2*>(p.codes + d.row * p.pitch + 8 * g) = d.scale < 0 ? make_uint2(0, 0) : q;
+      if (g % kLanes == 0 && d.scale >= 0)
+        *reinterpret_cast<uint32_t*>(p.scales + d.scale + (int64_t)(g / kLanes) * kAtomBytes) = s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- back again --
+struct DequantParams {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* tensor_scale;
+  const int32_t* offsets;  // null: matrices of group_rows rows
+  int64_t rows, group_rows, group_blocks;
+  int E, cols, ng, rpb;
+  uint32_t ng_magic;
+  int64_t pitch, block_bytes;
+  void* out;
+};
+
+// value = (code x block scale) x tensor scale, rounded once to the output type
+// (code x block scale is exact).  Rows past the last expert's are zeros.
+template <typename O, int FMT, bool VEC>
+__global__ void __launch_bounds__(kQThreads)
+dequantize_kernel(const DequantParams p) {
+  __shared__ Dest src[kQDests];  // .scale as in the quantisation, .row: the matrix
+  pdl_wait();
+  pdl_trigger();
+  const int64_t r0 = (int64_t)blockIdx.x * p.rpb;
+  const int nr = (int)min((int64_t)p.rpb, p.rows - r0);
+  for (int i = threadIdx.x; i < nr; i += kQThreads) {
+    const int64_t row = r0 + i;
+    Dest d{0, -1};
+    if (p.offsets == nullptr) {
+      const int64_t g = row / p.group_rows, r = row - g * p.group_rows;
+      d = Dest{g, (g * p.group_blocks + r / 128) * p.block_bytes + fp4_scale_byte((int)(r & 127))};
+    } else {
+      const int e = row_expert(p.offsets, p.E, row);
+      if (e < p.E) {
+        const int o0 = __ldg(p.offsets + e);
+        const int j = (int)row - o0;
+        if (o0 >= 0 && j >= 0)
+          d.scale = (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j);
+      }
+    }
+    src[i] = d;
+  }
+  __syncthreads();
+  O* out = static_cast<O*>(p.out);
+  const int total = nr * p.ng;
+  for (int i = threadIdx.x; i < total; i += kQThreads) {
+    const int lr = (int)__umulhi((uint32_t)i, p.ng_magic);
+    const int g = i - lr * p.ng;
+    const int64_t row = r0 + lr;
+    const int c = 16 * g, n = min(16, p.cols - c);
+    if (n <= 0) continue;
+    const Dest d = src[lr];
+    float s = 0.f, ts = 1.f;
+    uint2 q = make_uint2(0, 0);
+    if (d.scale >= 0) {
+      q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * p.pitch + 8 * g));
+      const int b = FMT == MLR_FP4_MX ? g / 2 : g;
+      const uint32_t sb = __ldg(p.scales + d.scale + (int64_t)(b / 4) * kAtomBytes + b % 4);
+      if (FMT == MLR_FP4_MX) {
+        s = __uint_as_float(sb == 0 ? 0x00400000u : sb == 255 ? 0x7fc00000u : sb << 23);
+      } else {
+        asm("{\n\t.reg .b32 p;\n\t.reg .f16 a, b;\n\t"
+            "cvt.rn.f16x2.e4m3x2 p, %1;\n\tmov.b32 {a, b}, p;\n\tcvt.f32.f16 %0, a;\n\t}"
+            : "=f"(s)
+            : "h"((uint16_t)sb));
+        if (p.tensor_scale != nullptr) ts = __ldg(p.tensor_scale + d.row);
+      }
+    }
+    float v[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t w = h ? q.y : q.x;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // E2M1 to fp32: sign, two exponent bits (bias 1), one fraction bit
+        const uint32_t m = (w >> (4 * j)) & 7u;
+        const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
+        const float z = __uint_as_float(__float_as_uint(a) | ((w >> (4 * j)) & 8u) << 28);
+        v[8 * h + j] = __fmul_rn(__fmul_rn(z, s), ts);
+      }
+    }
+    O* o = out + row * p.cols + c;
+    if constexpr (sizeof(O) == 4) {
+      if (VEC) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          if (4 * h < n) reinterpret_cast<float4*>(o)[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < n) o[j] = v[j];
+      }
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+      if (VEC) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (8 * h < n) reinterpret_cast<uint4*>(o)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j < n) o[j] = (O)(w[j / 2] >> (16 * (j % 2)));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side --
+// Source rows per block: about four passes of the block, fewer when that would
+// leave SMs without a block, and at most kQDests destinations.
+int rows_per_block(int64_t rows, int groups, int K) {
+  int64_t r = ceil_div(4 * kQThreads, groups);
+  const int64_t spread = ceil_div(rows, 4 * 152);
+  if (r > spread) r = spread;
+  if (r > kQDests / K) r = kQDests / K;
+  if (r > 65535 / groups) r = 65535 / groups;  // the row division by multiplication holds below 2^16
+  return r < 1 ? 1 : (int)r;
+}
+
+bool fmt_ok(int32_t fmt) { return fmt == MLR_FP4_MX || fmt == MLR_FP4_NV; }
+bool dtype_ok(int32_t d) { return d == MLR_DTYPE_BF16 || d == MLR_DTYPE_F32; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+constexpr int kMaxCols = 1 << 19;
+
+template <typename E_, int FMT, int SRC>
+int launch_quantize(const QuantParams& p, bool vec, cudaStream_t stream) {
+  const int64_t blocks = ceil_div(p.rows, p.rpb);
+  if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  const cudaError_t err =
+      vec ? launch_pdl(quantize_kernel<E_, FMT, SRC, true>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p)
+          : launch_pdl(quantize_kernel<E_, FMT, SRC, false>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p);
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MLR_ERR_CUDA;
+  }
+  note_launch();
+  return MLR_OK;
+}
+
+// Fills the layout fields and launches; p has its source and destination set.
+template <int SRC>
+int quantize(QuantParams& p, int32_t dtype, int32_t fmt, cudaStream_t stream) {
+  if (p.rows == 0) return MLR_OK;
+  const int es = dtype == MLR_DTYPE_BF16 ? 2 : 4;
+  if (p.x == nullptr || p.codes == nullptr || p.scales == nullptr ||
+      (reinterpret_cast<uintptr_t>(p.x) & (es - 1)) != 0 || !aligned16(p.codes) || !aligned16(p.scales))
+    return MLR_ERR_INVALID;
+  p.pitch = fp4_pitch(p.cols);
+  p.ng = (int)(p.pitch / 8);
+  const int atoms = fp4_atoms(p.cols, fmt);
+  p.nga = atoms * (fmt == MLR_FP4_MX ? 8 : 4);
+  p.block_bytes = (int64_t)atoms * kAtomBytes;
+  p.rpb = rows_per_block(p.rows, p.nga, SRC == kTokens ? p.K : 1);
+  p.ng_magic = (uint32_t)ceil_div(int64_t{1} << 32, p.nga);
+  const bool vec = (int64_t)p.cols * es % 16 == 0 && aligned16(p.x);
+  if (dtype == MLR_DTYPE_BF16)
+    return fmt == MLR_FP4_MX ? launch_quantize<uint16_t, MLR_FP4_MX, SRC>(p, vec, stream)
+                             : launch_quantize<uint16_t, MLR_FP4_NV, SRC>(p, vec, stream);
+  return fmt == MLR_FP4_MX ? launch_quantize<float, MLR_FP4_MX, SRC>(p, vec, stream)
+                           : launch_quantize<float, MLR_FP4_NV, SRC>(p, vec, stream);
+}
+
+int check_quantize(int64_t cols, int32_t dtype, int32_t fmt, const float* tensor_scale) {
+  if (cols < 1 || !dtype_ok(dtype) || !fmt_ok(fmt)) return MLR_ERR_INVALID;
+  if (fmt == MLR_FP4_MX && tensor_scale != nullptr) return MLR_ERR_INVALID;
+  return cols > kMaxCols ? MLR_ERR_UNSUPPORTED : MLR_OK;
+}
+
+template <typename O, int FMT>
+int launch_dequantize(const DequantParams& p, bool vec, cudaStream_t stream) {
+  const int64_t blocks = ceil_div(p.rows, p.rpb);
+  if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  const cudaError_t err =
+      vec ? launch_pdl(dequantize_kernel<O, FMT, true>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p)
+          : launch_pdl(dequantize_kernel<O, FMT, false>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p);
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MLR_ERR_CUDA;
+  }
+  note_launch();
+  return MLR_OK;
+}
+
+}  // namespace
+}  // namespace mlr
+
+extern "C" int64_t moe_fp4_pitch(int32_t cols) { return cols < 1 ? -1 : mlr::fp4_pitch(cols); }
+
+extern "C" int32_t moe_fp4_scale_atoms(int32_t cols, int32_t fmt) {
+  return cols < 1 || !mlr::fmt_ok(fmt) ? -1 : mlr::fp4_atoms(cols, fmt);
+}
+
+extern "C" int moe_fp4_quantize(const void* x, int32_t num_matrices, int32_t rows, int32_t cols, int32_t dtype,
+                                int32_t fmt, const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                void* stream) {
+  using namespace mlr;
+  const int code = check_quantize(cols, dtype, fmt, tensor_scale);
+  if (code != MLR_OK) return code;
+  if (num_matrices < 0 || rows < 0) return MLR_ERR_INVALID;
+  QuantParams p{};
+  p.x = x;
+  p.rows = (int64_t)num_matrices * rows;
+  p.cols = cols;
+  p.group_rows = rows;
+  p.group_blocks = ceil_div(rows, 128);
+  p.tensor_scale = tensor_scale;
+  p.codes = codes;
+  p.scales = scales;
+  return quantize<kMatrix>(p, dtype, fmt, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_fp4_quantize_permuted(const void* x, const int32_t* topk_ids, const int32_t* pair_pos,
+                                         const int32_t* expert_offsets, int32_t num_tokens, int32_t topk,
+                                         int32_t cols, int32_t num_experts, int32_t dtype, int32_t fmt,
+                                         const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                         int32_t* d_status, void* stream) {
+  using namespace mlr;
+  const int code = check_quantize(cols, dtype, fmt, tensor_scale);
+  if (code != MLR_OK) return code;
+  if (num_tokens < 0 || topk < 1 || num_experts < 1) return MLR_ERR_INVALID;
+  if (topk > kQDests || (int64_t)num_tokens * topk >= INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  if (num_tokens > 0 && (topk_ids == nullptr || pair_pos == nullptr || expert_offsets == nullptr))
+    return MLR_ERR_INVALID;
+  QuantParams p{};
+  p.x = x;
+  p.rows = num_tokens;
+  p.cols = cols;
+  p.tensor_scale = tensor_scale;
+  p.ids = topk_ids;
+  p.pair_pos = pair_pos;
+  p.offsets = expert_offsets;
+  p.K = topk;
+  p.E = num_experts;
+  p.P = (int64_t)num_tokens * topk;
+  p.codes = codes;
+  p.scales = scales;
+  p.status = d_status;
+  return quantize<kTokens>(p, dtype, fmt, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_fp4_quantize_swiglu(const void* gate_up, const int32_t* expert_offsets, int32_t num_rows,
+                                       int32_t cols, int32_t num_experts, int32_t dtype, int32_t fmt,
+                                       const float* tensor_scale, uint8_t* codes, uint8_t* scales,
+                                       int32_t* d_status, void* stream) {
+  using namespace mlr;
+  const int code = check_quantize(cols, dtype, fmt, tensor_scale);
+  if (code != MLR_OK) return code;
+  if (num_rows < 0 || num_experts < 1) return MLR_ERR_INVALID;
+  if (num_rows > 0 && expert_offsets == nullptr) return MLR_ERR_INVALID;
+  QuantParams p{};
+  p.x = gate_up;
+  p.rows = num_rows;
+  p.cols = cols;
+  p.tensor_scale = tensor_scale;
+  p.offsets = expert_offsets;
+  p.E = num_experts;
+  p.P = num_rows;
+  p.codes = codes;
+  p.scales = scales;
+  p.status = d_status;
+  return quantize<kSwiglu>(p, dtype, fmt, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int moe_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, const int32_t* expert_offsets,
+                                  int32_t num_matrices, int32_t rows, int32_t cols, int32_t fmt,
+                                  const float* tensor_scale, int32_t dtype, void* out, void* stream_) {
+  using namespace mlr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const int code = check_quantize(cols, dtype, fmt, tensor_scale);
+  if (code != MLR_OK) return code;
+  if (num_matrices < 0 || rows < 0) return MLR_ERR_INVALID;
+  DequantParams p{};
+  p.rows = expert_offsets != nullptr ? rows : (int64_t)num_matrices * rows;
+  if (p.rows == 0) return MLR_OK;
+  const int es = dtype == MLR_DTYPE_BF16 ? 2 : 4;
+  if (codes == nullptr || scales == nullptr || out == nullptr || !aligned16(codes) || !aligned16(scales) ||
+      (reinterpret_cast<uintptr_t>(out) & (es - 1)) != 0 || (expert_offsets != nullptr && num_matrices < 1))
+    return MLR_ERR_INVALID;
+  p.codes = codes;
+  p.scales = scales;
+  p.tensor_scale = tensor_scale;
+  p.offsets = expert_offsets;
+  p.group_rows = rows;
+  p.group_blocks = ceil_div(rows, 128);
+  p.E = num_matrices;
+  p.cols = cols;
+  p.pitch = fp4_pitch(cols);
+  p.ng = (int)(p.pitch / 8);
+  p.block_bytes = (int64_t)fp4_atoms(cols, fmt) * kAtomBytes;
+  p.rpb = rows_per_block(p.rows, p.ng, 1);
+  p.ng_magic = (uint32_t)ceil_div(int64_t{1} << 32, p.ng);
+  p.out = out;
+  const bool vec = (int64_t)cols * es % 16 == 0 && aligned16(out);
+  if (dtype == MLR_DTYPE_BF16)
+    return fmt == MLR_FP4_MX ? launch_dequantize<uint16_t, MLR_FP4_MX>(p, vec, stream)
+                             : launch_dequantize<uint16_t, MLR_FP4_NV>(p, vec, stream);
+  return fmt == MLR_FP4_MX ? launch_dequantize<float, MLR_FP4_MX>(p, vec, stream)
+                           : launch_dequantize<float, MLR_FP4_NV>(p, vec, stream);
+}
