@@ -572,7 +572,8 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *   [1], w_tensor_scale null or [num_experts] (NVFP4 only).  Rows past the
  *   last expert's are zeros.  Offsets that are not 0 <= o[e] <= o[e + 1] <=
  *   num_rows set MLR_STATUS_INDEX and y is not written.
- * Codes and scales are 16-byte aligned.  Limits: cols <= 524288, num_experts <= 16384.
+ * Codes and scales are 16-byte aligned.  Limits: cols <= 524288; the product:
+ *   num_experts <= 2048, num_experts * outputs < 2^31.
  */
 #define MLR_FP4_MX 0
 #define MLR_FP4_NV 1

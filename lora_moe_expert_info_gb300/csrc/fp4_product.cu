@@ -2,95 +2,344 @@
 //
 //   y[r, n] = g_a g_w[e] sum_c A[r, c] W[e, n, c],   e the expert of row r
 //
-// with A and W given as E2M1 codes and block scales (mlr_fp4.cuh), products
-// and sums in fp32, y rounded once to bf16.  Rows past the last expert's are
-// zeros.  One block per expert and 64 outputs walks the expert's rows, 64 at a
-// time, with both operands dequantised into shared memory.
+// with A and W given as E2M1 codes and block scales (mlr_fp4.cuh), on the
+// block-scaled FP4 tensor cores: the scales are applied inside the MMA, sums
+// are held in fp32 and y is rounded once to bf16.  Rows past the last expert's
+// are zeros.
+//
+// An item is 128 outputs (rows of W, the MMA's M) by one tile of up to NT rows
+// of one expert (the MMA's N), so that few rows waste little of the tensor
+// core and every weight is read once per tile.  One persistent CTA per SM
+// walks a static share of the items; roles are warps:
+//   warp 0      loads: per K step of 256 columns one TMA box of W, one of A
+//               (128-byte rows, 128-byte swizzle) and the steps' scale atoms
+//               into a ring of stages
+//   warp 1      scales from the stage to TMEM (tcgen05.cp), then one MMA per
+//               64 columns
+//   warps 4-7   accumulators from TMEM, scaled and rounded, to y
+#include <cudaTypedefs.h>
+
 #include "mlr_fp4.cuh"
 #include "mlr_profile.cuh"
 
 namespace mlr {
 namespace {
 
-constexpr int kPT = 64, kPC = 32, kPThreads = 256;
+constexpr int kProductThreads = 256;
+constexpr int kMaxProductExperts = 2048;
+constexpr int kKStep = 256;      // columns per ring stage: 128 bytes of codes per row
+constexpr uint64_t kGraceNs = 1000000;  // after an abort: time for issued copies to land
 
-struct ProductParams {
-  const uint8_t *a, *sa, *w, *sw;
-  const float *ga, *gw;
-  const int32_t* offsets;
-  int P, E, N, cols;
-  int64_t pitch, block_bytes, w_blocks;
-  uint16_t* y;
-  int32_t* status;
+template <int NT> struct ProductCfg;
+// few rows per expert: short row tiles leave room for a deeper ring
+template <> struct ProductCfg<64> { static constexpr int kStages = 7, kAccBufs = 2; };
+template <> struct ProductCfg<256> { static constexpr int kStages = 4, kAccBufs = 1; };
+
+template <int NT, int FMT> struct Shape {
+  static constexpr int kAtoms = kKStep / (4 * fp4_block(FMT));  // scale atoms per stage and 128 rows
+  static constexpr int kRowBlocks = (NT + 127) / 128;
+  static constexpr int kWBytes = 128 * 128, kABytes = NT * 128;
+  static constexpr int kSfBytes = kAtoms * kAtomBytes;
+  static constexpr int kStageBytes = kWBytes + kABytes + (1 + kRowBlocks) * kSfBytes;
+  static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
+  static constexpr int S = ProductCfg<NT>::kStages, kBufs = ProductCfg<NT>::kAccBufs;
+  // TMEM columns: accumulators, then per stage the scales of W and of A
+  static constexpr int kSfCols = kAtoms * 4 * (1 + kRowBlocks);
+  static constexpr int kSfCol0 = kBufs * NT;
+  static_assert(kSfCol0 + S * kSfCols <= 512, "TMEM columns");
 };
 
-template <int FMT>
-__device__ __forceinline__ float fp4_value(const uint8_t* row, const uint8_t* scale_row, int c) {
-  const uint32_t w = (row[c >> 1] >> (4 * (c & 1))) & 15u;
-  const uint32_t m = w & 7u;
-  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-  const int b = c / fp4_block(FMT);
-  const uint32_t sb = scale_row[(int64_t)(b / 4) * kAtomBytes + b % 4];
-  float s;
-  if (FMT == MLR_FP4_MX) s = __uint_as_float(sb == 0 ? 0x00400000u : sb == 255 ? 0x7fc00000u : sb << 23);
-  else {
-    const uint32_t e = sb >> 3, f = sb & 7u;
-    s = sb == 0x7f ? __uint_as_float(0x7fc00000u)
-                   : e == 0 ? (float)f * 0.001953125f : __uint_as_float((e + 120u) << 23 | f << 20);
-  }
-  return (w & 8u ? -a : a) * s;
+struct __align__(16) Ctl {
+  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint32_t tmem;
+  int abort;
+  int tiles[kMaxProductExperts + 1];  // row tiles of all earlier experts
+};
+
+template <int NT, int FMT>
+constexpr int smem_bytes() {
+  return Shape<NT, FMT>::S * Shape<NT, FMT>::kStride + (int)sizeof(Ctl) + 1024;
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(kPThreads)
-product_kernel(const ProductParams p) {
-  __shared__ float as[kPC][kPT + 1], ws[kPC][kPT + 1];
-  pdl_wait();
-  pdl_trigger();
-  const int e = blockIdx.y, n0 = blockIdx.x * kPT, tid = threadIdx.x;
-  const int tx = tid & 15, ty = tid >> 4;
-  int bad = 0;
-  for (int i = tid; i < p.E; i += kPThreads) bad |= p.offsets[i] < 0 || p.offsets[i] > p.offsets[i + 1];
-  bad |= p.offsets[p.E] > p.P;
+struct Maps {
+  CUtensorMap w;     // [E * N, pitch] in boxes of 128 rows
+  CUtensorMap a[5];  // [P, pitch] in boxes of 16 << i rows
+};
+
+struct Params {
+  const uint8_t *sa, *sw;
+  const float *ga, *gw;
+  const int32_t* offsets;
+  int P, E, N, nblk, ksteps, cols, atoms;
+  uint16_t* y;
+  int32_t* status;
+  uint64_t wait_ns;
+};
+
+struct Item {
+  int e, row0, rows;  // expert, first sorted row, rows of the tile
+  int sblk;           // 128-row scale block of row0
+  int n0;             // first output
+};
+
+template <int NT>
+__device__ __forceinline__ Item item_of(const Params& p, const Ctl& c, int item) {
+  const int t = item / p.nblk;
+  int lo = 0, hi = p.E;  // tiles[lo] <= t < tiles[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (c.tiles[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  Item it;
+  it.e = lo;
+  const int o0 = __ldg(p.offsets + lo), o1 = __ldg(p.offsets + lo + 1);
+  const int j0 = (t - c.tiles[lo]) * NT;
+  it.row0 = o0 + j0;
+  it.rows = min(NT, o1 - it.row0);
+  it.sblk = o0 / 128 + lo + j0 / 128;
+  it.n0 = (item - t * p.nblk) * 128;
+  return it;
+}
+__device__ __forceinline__ int mma_rows(int rows) { return (rows + 15) & ~15; }
+
+// Row tiles per expert, scanned over the experts; false (and the status bit)
+// if the offsets are not 0 <= o[e] <= o[e + 1] <= P.
+template <int NT>
+__device__ bool scan_tiles(const Params& p, Ctl& c) {
+  __shared__ int warp_tot[kProductThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.E + kProductThreads - 1) / kProductThreads;
+  const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
+  bool bad = tid == 0 && __ldg(p.offsets + p.E) > p.P;
+  int local = 0;
+  for (int e = e0; e < e1; ++e) {
+    const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
+    if (o0 < 0 || o1 < o0) bad = true;
+    else local += (int)(((int64_t)o1 - o0 + NT - 1) / NT);
+  }
+  int inc = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_tot[warp] = inc;
   if (__syncthreads_or(bad)) {
     if (tid == 0) set_status(p.status, MLR_STATUS_INDEX);
-    return;
+    return false;
   }
-  const int lo = p.offsets[e], hi = p.offsets[e + 1];
-  for (int r0 = lo; r0 < hi; r0 += kPT) {
-    float acc[4][4] = {};
-    for (int c0 = 0; c0 < p.cols; c0 += kPC) {
-      for (int i = tid; i < kPT * kPC; i += kPThreads) {
-        const int r = i / kPC, c = c0 + i % kPC;
-        float va = 0.f, vw = 0.f;
-        if (c < p.cols && r0 + r < hi) {
-          const int j = r0 + r - lo;
-          va = fp4_value<FMT>(p.a + (int64_t)(r0 + r) * p.pitch,
-                              p.sa + (int64_t)(lo / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j), c);
-        }
-        if (c < p.cols && n0 + r < p.N)
-          vw = fp4_value<FMT>(p.w + ((int64_t)e * p.N + n0 + r) * p.pitch,
-                              p.sw + (e * p.w_blocks + (n0 + r) / 128) * p.block_bytes + fp4_scale_byte(n0 + r), c);
-        as[i % kPC][r] = va;
-        ws[i % kPC][r] = vw;
-      }
-      __syncthreads();
-      for (int c = 0; c < kPC; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[c][ty + 16 * i], ws[c][tx + 16 * j], acc[i][j]);
-      __syncthreads();
+  int run = inc - local;
+  for (int w = 0; w < warp; ++w) run += warp_tot[w];
+  for (int e = e0; e < e1; ++e) {
+    c.tiles[e] = run;
+    run += (__ldg(p.offsets + e + 1) - __ldg(p.offsets + e) + NT - 1) / NT;
+  }
+  if (tid == kProductThreads - 1) c.tiles[p.E] = run;
+  __syncthreads();
+  return true;
+}
+
+template <int NT, int FMT>
+__global__ void __launch_bounds__(kProductThreads, 1)
+product_kernel(const __grid_constant__ Maps maps, const Params p) {
+  using Sh = Shape<NT, FMT>;
+  constexpr int S = Sh::S;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctl& c = *reinterpret_cast<Ctl*>(smem + S * Sh::kStride);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = &c.abort;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&c.full[s], 1);
+      mbar_init(&c.empty[s], 1);
     }
-    const float g = (p.ga ? *p.ga : 1.f) * (p.gw ? p.gw[e] : 1.f);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int r = r0 + ty + 16 * i, n = n0 + tx + 16 * j;
-        if (r < hi && n < p.N) p.y[(int64_t)r * p.N + n] = f32_to_bf16_bits(g * acc[i][j]);
-      }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&c.acc_full[b], 1);
+      mbar_init(&c.acc_empty[b], 128);
+    }
+    c.abort = 0;
+    fence_mbar_init();
   }
-  for (int r = p.offsets[p.E] + e; r < p.P; r += p.E)
-    if (tid < kPT && n0 + tid < p.N) p.y[(int64_t)r * p.N + n0 + tid] = 0;
+  if (warp == 1) {
+    tmem_alloc(&c.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = c.tmem;
+  const bool ok_offsets = scan_tiles<NT>(p, c);
+  const int n_items = ok_offsets ? c.tiles[p.E] * p.nblk : 0;
+
+  if (warp == 0 && lane == 0) {
+    // ================================ loads ================================
+    int g = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
+      const Item it = item_of<NT>(p, c, item);
+      int bi = 0;  // the shortest box that holds the tile
+      while ((16 << bi) < it.rows) ++bi;
+      const int rblocks = (it.rows + 127) / 128;
+      const int wrow = it.e * p.N + it.n0;
+      const uint8_t* sw = p.sw + ((int64_t)it.e * p.nblk + it.n0 / 128) * p.atoms * kAtomBytes;
+      const uint8_t* sa = p.sa + (int64_t)it.sblk * p.atoms * kAtomBytes;
+      for (int k = 0; k < p.ksteps; ++k, ++g) {
+        const int st = g % S;
+        if (!mbar_wait(&c.empty[st], ((g / S) & 1) ^ 1, abort, p.wait_ns)) { ok = false; break; }
+        uint8_t* sb = smem + st * Sh::kStride;
+        const uint32_t sf = smem_u32(sb) + Sh::kWBytes + Sh::kABytes;
+        const int a0 = k * Sh::kAtoms;
+        const uint32_t abytes = (uint32_t)min(Sh::kAtoms, p.atoms - a0) * kAtomBytes;
+        mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128 + (1 + rblocks) * abytes);
+        tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
+        tma_load_2d(sb + Sh::kWBytes, &maps.a[bi], &c.full[st], k * 128, it.row0);
+        bulk_load(sf, sw + (int64_t)a0 * kAtomBytes, abytes, &c.full[st]);
+        for (int b = 0; b < rblocks; ++b)
+          bulk_load(sf + (1 + b) * Sh::kSfBytes, sa + ((int64_t)b * p.atoms + a0) * kAtomBytes, abytes, &c.full[st]);
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ================================= MMA =================================
+    int g = 0, il = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
+      const Item it = item_of<NT>(p, c, item);
+      const int rblocks = (it.rows + 127) / 128;
+      const int N = mma_rows(it.rows);
+      const int b = il % Sh::kBufs;
+      if (!mbar_wait(&c.acc_empty[b], ((il / Sh::kBufs) & 1) ^ 1, abort, p.wait_ns)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + b * NT;
+      for (int k = 0; k < p.ksteps; ++k, ++g) {
+        const int st = g % S;
+        if (!mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t sb = smem_u32(smem + st * Sh::kStride);
+        const uint32_t sf = sb + Sh::kWBytes + Sh::kABytes;
+        // this stage's cells: per atom four columns of W, then four per row
+        // block of A (the MMA of an empty stage's predecessor has finished)
+        const uint32_t tw = tmem + Sh::kSfCol0 + st * Sh::kSfCols;
+        const uint32_t ta = tw + 4 * Sh::kAtoms;
+        const int na = min(Sh::kAtoms, p.atoms - k * Sh::kAtoms);
+        for (int i = 0; i < na; ++i) {
+          copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
+          for (int r = 0; r < rblocks; ++r)
+            copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
+        }
+        const int nm = min(4, (p.cols - k * kKStep + 63) / 64);
+        for (int m = 0; m < nm; ++m) {
+          const int i = FMT == MLR_FP4_MX ? m >> 1 : m;
+          mma_fp4<FMT>(acc, sdesc_sw128(sb + m * 32), sdesc_sw128(sb + Sh::kWBytes + m * 32),
+                       idesc_fp4<FMT>(128, N, FMT == MLR_FP4_MX ? 2 * (m & 1) : 0), tw + 4 * i,
+                       ta + 4 * Sh::kRowBlocks * i, (k > 0 || m > 0) ? 1u : 0u);
+        }
+        mma_commit(&c.empty[st]);
+      }
+      if (ok) mma_commit(&c.acc_full[b]);
+    }
+  } else if (warp >= 4) {
+    // =============================== epilogue ==============================
+    const int m = (warp & 3) * 32 + lane;  // output of the item; TMEM lane
+    if (ok_offsets)
+      for (int64_t i = (int64_t)__ldg(p.offsets + p.E) * p.N + (int64_t)blockIdx.x * 128 + m; i < (int64_t)p.P * p.N;
+           i += (int64_t)gridDim.x * 128)
+        p.y[i] = 0;
+    int il = 0;
+    for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++il) {
+      const Item it = item_of<NT>(p, c, item);
+      const int b = il % Sh::kBufs;
+      // one lane's verdict for the warp: the TMEM loads take all lanes
+      const bool w_ok = mbar_wait(&c.acc_full[b], (il / Sh::kBufs) & 1, abort, p.wait_ns);
+      if (!__all_sync(0xffffffffu, w_ok)) break;
+      tc_fence_after();
+      const float s = (p.ga ? __ldg(p.ga) : 1.f) * (p.gw ? __ldg(p.gw + it.e) : 1.f);
+      const uint32_t t = tmem + b * NT + ((uint32_t)(warp & 3) << 21);
+      const int n = it.n0 + m;
+      uint16_t* yp = p.y + (int64_t)it.row0 * p.N + n;
+      for (int c0 = 0; c0 < it.rows; c0 += 16) {
+        float v[16];
+        tmem_ld16(t + c0, v);
+        if (n < p.N)
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c0 + j < it.rows) yp[(int64_t)(c0 + j) * p.N] = f32_to_bf16_bits(s * v[j]);
+      }
+      tc_fence_before();
+      mbar_arrive(&c.acc_empty[b]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();  // every role has left: the abort flag is final
+  if (*abort) {
+    if (tid == 0) set_status(p.status, MLR_STATUS_TIMEOUT);
+    sleep_for_ns(kGraceNs);  // copies and MMAs already issued finish before the teardown
+    __syncthreads();
+  }
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side --
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Code rows of `pitch` bytes in boxes of 128 bytes x box_rows, 128-byte swizzle.
+// Bytes past the pitch and rows past the last read as zero codes.
+bool code_map(CUtensorMap* m, const void* base, uint64_t pitch, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {pitch, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int product_sms() {
+  static int n[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (n[dev] == 0) {
+    int v = 0;
+    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
+    n[dev] = v;
+  }
+  return n[dev];
+}
+
+template <int NT, int FMT>
+int launch_product(const Maps& maps, const Params& p, cudaStream_t stream) {
+  constexpr int smem = smem_bytes<NT, FMT>();
+  static_assert(smem <= 227 * 1024, "shared memory per CTA");
+  if (cudaFuncSetAttribute(product_kernel<NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return MLR_ERR_CUDA;
+  // at most one partial tile per expert beyond the full ones
+  const int64_t tiles = (p.P < p.E ? p.P : p.E) + (int64_t)p.P / NT;
+  const int64_t items = tiles * p.nblk;
+  if (items > INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  const int grid = (int)(items < product_sms() ? items : product_sms());
+  if (launch_pdl(product_kernel<NT, FMT>, dim3(grid), dim3(kProductThreads), smem, stream, maps, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MLR_ERR_CUDA;
+  }
+  note_launch();
+  return MLR_OK;
 }
 
 }  // namespace
@@ -106,20 +355,24 @@ extern "C" int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_s
   if (num_rows < 0 || num_experts < 1 || outputs < 1 || cols < 1 || (fmt != MLR_FP4_MX && fmt != MLR_FP4_NV))
     return MLR_ERR_INVALID;
   if (fmt == MLR_FP4_MX && (a_tensor_scale != nullptr || w_tensor_scale != nullptr)) return MLR_ERR_INVALID;
-  if (num_experts > 16384) return MLR_ERR_UNSUPPORTED;
+  if (num_experts > kMaxProductExperts || cols > (1 << 19) || (int64_t)num_experts * outputs > INT32_MAX)
+    return MLR_ERR_UNSUPPORTED;
   if (num_rows == 0) return MLR_OK;
   for (const void* q : {static_cast<const void*>(a_codes), static_cast<const void*>(a_scales),
                         static_cast<const void*>(w_codes), static_cast<const void*>(w_scales)})
     if (q == nullptr || (reinterpret_cast<uintptr_t>(q) & 15) != 0) return MLR_ERR_INVALID;
   if (expert_offsets == nullptr || y == nullptr) return MLR_ERR_INVALID;
-  ProductParams p{a_codes, a_scales, w_codes, w_scales, a_tensor_scale, w_tensor_scale, expert_offsets,
-                  num_rows, num_experts, outputs, cols, fp4_pitch(cols),
-                  (int64_t)fp4_atoms(cols, fmt) * kAtomBytes, ceil_div(outputs, 128), y, d_status};
-  const dim3 grid((unsigned)ceil_div(outputs, kPT), (unsigned)num_experts);
-  const cudaError_t err =
-      fmt == MLR_FP4_MX ? launch_pdl(product_kernel<MLR_FP4_MX>, grid, dim3(kPThreads), 0, stream, p)
-                        : launch_pdl(product_kernel<MLR_FP4_NV>, grid, dim3(kPThreads), 0, stream, p);
-  if (err != cudaSuccess) return MLR_ERR_CUDA;
-  note_launch();
-  return MLR_OK;
+  const uint64_t pitch = (uint64_t)fp4_pitch(cols);
+  Maps maps;
+  bool ok = code_map(&maps.w, w_codes, pitch, (uint64_t)num_experts * outputs, 128);
+  for (int i = 0; i < 5; ++i) ok = ok && code_map(&maps.a[i], a_codes, pitch, (uint64_t)num_rows, 16u << i);
+  if (!ok) return MLR_ERR_CUDA;
+  Params p{a_scales, w_scales, a_tensor_scale, w_tensor_scale, expert_offsets, num_rows, num_experts, outputs,
+           (int)ceil_div(outputs, 128), (int)ceil_div(cols, kKStep), cols, fp4_atoms(cols, fmt), y, d_status,
+           wait_limit_ns()};
+  // an average expert of at most 32 rows rarely needs a second 64-row tile
+  const bool small = num_rows <= 32 * (int64_t)num_experts || num_rows <= 64;
+  if (fmt == MLR_FP4_MX)
+    return small ? launch_product<64, MLR_FP4_MX>(maps, p, stream) : launch_product<256, MLR_FP4_MX>(maps, p, stream);
+  return small ? launch_product<64, MLR_FP4_NV>(maps, p, stream) : launch_product<256, MLR_FP4_NV>(maps, p, stream);
 }

@@ -23,4 +23,48 @@ __host__ __device__ constexpr int fp4_atoms(int64_t cols, int fmt) { return (int
 // Byte of scale block 0 of a row within its 128-row block's atoms.
 __device__ __forceinline__ int fp4_scale_byte(int r) { return 16 * (r & 31) + 4 * ((r >> 5) & 3); }
 
+// ---- block-scaled FP4 MMAs ----
+
+// Instruction descriptor of kind::mxf4 / kind::mxf4nvf4: E2M1 A and B, both
+// K-major (K = 64), fp32 D; UE8M0 scales (bit 23) for MXFP4, UE4M3 for NVFP4.
+// sf: byte of the scale cells where this MMA's scales begin (0 or 2).
+template <int FMT>
+__device__ __forceinline__ uint32_t idesc_fp4(uint32_t M, uint32_t N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | ((FMT == MLR_FP4_MX ? 1u : 0u) << 23) |
+         ((M >> 7) << 27) | (sf << 29);
+}
+// D[tmem] (+)= (A x scales) (B x scales)^T over 64 columns: two (MXFP4) or four
+// (NVFP4) scales per row, bytes of one TMEM cell; the cell of A's row m is at
+// lane m, column sfa + m / 32, that of B's row n at lane n % 32 of every lane
+// quarter, column sfb + n / 32.
+template <int FMT>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                        uint32_t accumulate) {
+  if (FMT == MLR_FP4_MX)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+// One scale atom (512 bytes: 32 rows of 16) from shared memory to four TMEM
+// columns, repeated in every lane quarter.  Ordered before later MMAs of the
+// same thread.
+__device__ __forceinline__ void copy_scale_atom(uint32_t taddr, uint32_t saddr) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc_noswz(saddr, 16, 128))
+               : "memory");
+}
+// Untiled bulk copy (16-byte aligned addresses, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 }  // namespace mlr
