@@ -203,44 +203,62 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
           bulk_load(sf + (1 + b) * Sh::kSfBytes, sa + ((int64_t)b * p.atoms + a0) * kAtomBytes, abytes, &c.full[st]);
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ================================= MMA =================================
+    // The whole warp walks the steps, so that every operand is uniform over it
+    // and stays in uniform registers; one elected lane issues.  (With a single
+    // lane in the loop each MMA took 240 cycles to issue whatever its N, each
+    // scale copy 95.)
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sb0 = smem_u32(smem);
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
-      const Item it = item_of<NT>(p, c, item);
-      const int rblocks = (it.rows + 127) / 128;
-      const int N = mma_rows(it.rows);
+      const int rows = __shfl_sync(0xffffffffu, item_of<NT>(p, c, item).rows, 0);
       const int b = il % Sh::kBufs;
-      if (!mbar_wait(&c.acc_empty[b], ((il / Sh::kBufs) & 1) ^ 1, abort, p.wait_ns)) break;
+      ok = __all_sync(0xffffffffu, mbar_wait(&c.acc_empty[b], ((il / Sh::kBufs) & 1) ^ 1, abort, p.wait_ns));
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tmem + b * NT;
+      const uint32_t acc = tm + b * NT;
+      const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(rows), 2);
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
-        if (!mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t sb = smem_u32(smem + st * Sh::kStride);
+        const uint32_t sb = sb0 + st * Sh::kStride;
         const uint32_t sf = sb + Sh::kWBytes + Sh::kABytes;
         // this stage's cells: per atom four columns of W, then four per row
-        // block of A (the MMA of an empty stage's predecessor has finished)
-        const uint32_t tw = tmem + Sh::kSfCol0 + st * Sh::kSfCols;
+        // block of A (the MMAs that read them last have finished: the stage
+        // was free)
+        const uint32_t tw = tm + Sh::kSfCol0 + st * Sh::kSfCols;
         const uint32_t ta = tw + 4 * Sh::kAtoms;
-        const int na = min(Sh::kAtoms, p.atoms - k * Sh::kAtoms);
-        for (int i = 0; i < na; ++i) {
-          copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
-          for (int r = 0; r < rblocks; ++r)
-            copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
+        const int na = p.atoms - k * Sh::kAtoms, nm = (p.cols - k * kKStep + 63) / 64;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < Sh::kAtoms; ++i) {
+            if (i < na) {
+              copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
+#pragma unroll
+              for (int r = 0; r < Sh::kRowBlocks; ++r)
+                if (r * 128 < rows)
+                  copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int i = FMT == MLR_FP4_MX ? m >> 1 : m;
+            if (m < nm)
+              mma_fp4<FMT>(acc, sdesc_sw128(sb + m * 32), sdesc_sw128(sb + Sh::kWBytes + m * 32),
+                           FMT == MLR_FP4_MX && (m & 1) ? id2 : id0, tw + 4 * i, ta + 4 * Sh::kRowBlocks * i,
+                           (k > 0 || m > 0) ? 1u : 0u);
+          }
+          mma_commit(&c.empty[st]);
         }
-        const int nm = min(4, (p.cols - k * kKStep + 63) / 64);
-        for (int m = 0; m < nm; ++m) {
-          const int i = FMT == MLR_FP4_MX ? m >> 1 : m;
-          mma_fp4<FMT>(acc, sdesc_sw128(sb + m * 32), sdesc_sw128(sb + Sh::kWBytes + m * 32),
-                       idesc_fp4<FMT>(128, N, FMT == MLR_FP4_MX ? 2 * (m & 1) : 0), tw + 4 * i,
-                       ta + 4 * Sh::kRowBlocks * i, (k > 0 || m > 0) ? 1u : 0u);
-        }
-        mma_commit(&c.empty[st]);
+        __syncwarp();
       }
-      if (ok) mma_commit(&c.acc_full[b]);
+      if (ok && elect_one()) mma_commit(&c.acc_full[b]);
+      __syncwarp();
     }
   } else if (warp >= 4) {
     // =============================== epilogue ==============================
