@@ -16,7 +16,7 @@
 //               into a ring of stages
 //   warp 1      scales from the stage to TMEM (tcgen05.cp), then one MMA per
 //               64 columns
-//   warps 4-7   accumulators from TMEM, scaled and rounded, to y
+//   warps 4-11  accumulators from TMEM, scaled and rounded, to y
 #include <cudaTypedefs.h>
 
 #include "mlr_fp4.cuh"
@@ -25,7 +25,8 @@
 namespace mlr {
 namespace {
 
-constexpr int kProductThreads = 256;
+constexpr int kProductThreads = 384;
+constexpr int kEpilogueThreads = 256;  // warps 4-11: two per TMEM lane quarter
 constexpr int kMaxProductExperts = 2048;
 constexpr int kKStep = 256;      // columns per ring stage: 128 bytes of codes per row
 constexpr uint64_t kGraceNs = 1000000;  // after an abort: time for issued copies to land
@@ -140,6 +141,50 @@ __device__ bool scan_tiles(const Params& p, Ctl& c) {
   return true;
 }
 
+// TMEM -> registers without waiting: this warp's 32 lanes, 32 columns.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Waits for every load of the warp; the registers pass through it, so that
+// they are not read before.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// 32 rows of y from c0 of the tile, this lane's output n.  Neighbouring lanes
+// trade values so that each stores two outputs of one row at once.
+__device__ __forceinline__ void store_chunk(const Params& p, uint16_t* yp, const uint32_t (&v)[32], float s, int n,
+                                            int c0, int rows, int lane) {
+  if ((p.N & 1) == 0) {
+    const int odd = lane & 1;
+    uint16_t* q = yp + (int64_t)(c0 + odd) * p.N - odd;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float a = s * __uint_as_float(v[j]), b = s * __uint_as_float(v[j + 1]);
+      const float o = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+      uint32_t w;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(odd ? b : o), "f"(odd ? o : a));
+      if (c0 + j + odd < rows && n < p.N) *reinterpret_cast<uint32_t*>(q) = w;
+      q += 2 * (int64_t)p.N;
+    }
+  } else if (n < p.N) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (c0 + j < rows) yp[(int64_t)(c0 + j) * p.N] = f32_to_bf16_bits(s * __uint_as_float(v[j]));
+  }
+}
+
 template <int NT, int FMT>
 __global__ void __launch_bounds__(kProductThreads, 1)
 product_kernel(const __grid_constant__ Maps maps, const Params p) {
@@ -158,7 +203,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
-      mbar_init(&c.acc_empty[b], 128);
+      mbar_init(&c.acc_empty[b], kEpilogueThreads);
     }
     c.abort = 0;
     fence_mbar_init();
@@ -262,33 +307,42 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     }
   } else if (warp >= 4) {
     // =============================== epilogue ==============================
+    // Two warps per lane quarter take alternate chunks of 32 accumulator
+    // columns (rows of y); the next chunk is read from TMEM while this one is
+    // stored.
     const int m = (warp & 3) * 32 + lane;  // output of the item; TMEM lane
+    const int half = (warp - 4) >> 2;
     if (ok_offsets)
-      for (int64_t i = (int64_t)__ldg(p.offsets + p.E) * p.N + (int64_t)blockIdx.x * 128 + m; i < (int64_t)p.P * p.N;
-           i += (int64_t)gridDim.x * 128)
+      for (int64_t i = (int64_t)__ldg(p.offsets + p.E) * p.N + (int64_t)blockIdx.x * kEpilogueThreads + tid - 128;
+           i < (int64_t)p.P * p.N; i += (int64_t)gridDim.x * kEpilogueThreads)
         p.y[i] = 0;
     int il = 0;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++il) {
       const Item it = item_of<NT>(p, c, item);
+      const float s = (p.ga ? __ldg(p.ga) : 1.f) * (p.gw ? __ldg(p.gw + it.e) : 1.f);
       const int b = il % Sh::kBufs;
-      // one lane's verdict for the warp: the TMEM loads take all lanes
+      // the warp leaves together: the TMEM loads take all its lanes
       const bool w_ok = mbar_wait(&c.acc_full[b], (il / Sh::kBufs) & 1, abort, p.wait_ns);
       if (!__all_sync(0xffffffffu, w_ok)) break;
       tc_fence_after();
-      const float s = (p.ga ? __ldg(p.ga) : 1.f) * (p.gw ? __ldg(p.gw + it.e) : 1.f);
       const uint32_t t = tmem + b * NT + ((uint32_t)(warp & 3) << 21);
       const int n = it.n0 + m;
       uint16_t* yp = p.y + (int64_t)it.row0 * p.N + n;
-      for (int c0 = 0; c0 < it.rows; c0 += 16) {
-        float v[16];
-        tmem_ld16(t + c0, v);
-        if (n < p.N)
+      uint32_t v[2][32];
+      int c0 = half * 32;
+      if (c0 < it.rows) tmem_ld32_async(t + c0, v[0]);
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c0 + j < it.rows) yp[(int64_t)(c0 + j) * p.N] = f32_to_bf16_bits(s * v[j]);
+      for (int u = 0; u < NT / 64; ++u, c0 += 64) {
+        if (c0 >= it.rows) break;
+        tmem_ld_wait(v[u & 1]);
+        if (u + 1 < NT / 64 && c0 + 64 < it.rows) tmem_ld32_async(t + c0 + 64, v[(u + 1) & 1]);
+        else {
+          tc_fence_before();
+          mbar_arrive(&c.acc_empty[b]);  // the last read of this thread
+        }
+        store_chunk(p, yp, v[u & 1], s, n, c0, it.rows, lane);
       }
-      tc_fence_before();
-      mbar_arrive(&c.acc_empty[b]);
+      if (half * 32 >= it.rows) mbar_arrive(&c.acc_empty[b]);
     }
   }
   __syncwarp();
