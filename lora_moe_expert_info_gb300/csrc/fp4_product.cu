@@ -102,6 +102,25 @@ __device__ __forceinline__ Item item_of(const Params& p, const Ctl& c, int item)
   it.n0 = (item - t * p.nblk) * 128;
   return it;
 }
+// The items of a CTA, 32 at a time: lane l looks up the l-th next one, so that
+// a role pays the search once for 32 items.  Whole warps call it, for i = 0, 1, ...
+template <int NT>
+struct ItemWalk {
+  Item mine;
+  __device__ __forceinline__ Item at(const Params& p, const Ctl& c, int i, int n_items, int lane) {
+    if ((i & 31) == 0) {
+      const int64_t item = blockIdx.x + (int64_t)(i + lane) * gridDim.x;
+      if (item < n_items) mine = item_of<NT>(p, c, (int)item);
+    }
+    Item it;
+    it.e = __shfl_sync(0xffffffffu, mine.e, i & 31);
+    it.row0 = __shfl_sync(0xffffffffu, mine.row0, i & 31);
+    it.rows = __shfl_sync(0xffffffffu, mine.rows, i & 31);
+    it.sblk = __shfl_sync(0xffffffffu, mine.sblk, i & 31);
+    it.n0 = __shfl_sync(0xffffffffu, mine.n0, i & 31);
+    return it;
+  }
+};
 __device__ __forceinline__ int mma_rows(int rows) { return (rows + 15) & ~15; }
 
 // Row tiles per expert, scanned over the experts; false (and the status bit)
@@ -221,31 +240,40 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
   const bool ok_offsets = scan_tiles<NT>(p, c);
   const int n_items = ok_offsets ? c.tiles[p.E] * p.nblk : 0;
 
-  if (warp == 0 && lane == 0) {
+  ItemWalk<NT> walk;
+  walk.mine = Item{};
+  if (warp == 0) {
     // ================================ loads ================================
-    int g = 0;
+    int g = 0, il = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x) {
-      const Item it = item_of<NT>(p, c, item);
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
+      const Item it = walk.at(p, c, il, n_items, lane);
       int bi = 0;  // the shortest box that holds the tile
       while ((16 << bi) < it.rows) ++bi;
+      const CUtensorMap* ma = &maps.a[bi];
       const int rblocks = (it.rows + 127) / 128;
       const int wrow = it.e * p.N + it.n0;
       const uint8_t* sw = p.sw + ((int64_t)it.e * p.nblk + it.n0 / 128) * p.atoms * kAtomBytes;
       const uint8_t* sa = p.sa + (int64_t)it.sblk * p.atoms * kAtomBytes;
+      const int64_t sa_block = (int64_t)p.atoms * kAtomBytes;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
-        if (!mbar_wait(&c.empty[st], ((g / S) & 1) ^ 1, abort, p.wait_ns)) { ok = false; break; }
+        ok = __all_sync(0xffffffffu, mbar_wait(&c.empty[st], ((g / S) & 1) ^ 1, abort, p.wait_ns));
+        if (!ok) break;
         uint8_t* sb = smem + st * Sh::kStride;
         const uint32_t sf = smem_u32(sb) + Sh::kWBytes + Sh::kABytes;
         const int a0 = k * Sh::kAtoms;
         const uint32_t abytes = (uint32_t)min(Sh::kAtoms, p.atoms - a0) * kAtomBytes;
-        mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128 + (1 + rblocks) * abytes);
-        tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
-        tma_load_2d(sb + Sh::kWBytes, &maps.a[bi], &c.full[st], k * 128, it.row0);
-        bulk_load(sf, sw + (int64_t)a0 * kAtomBytes, abytes, &c.full[st]);
-        for (int b = 0; b < rblocks; ++b)
-          bulk_load(sf + (1 + b) * Sh::kSfBytes, sa + ((int64_t)b * p.atoms + a0) * kAtomBytes, abytes, &c.full[st]);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128 + (1 + rblocks) * abytes);
+          tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
+          tma_load_2d(sb + Sh::kWBytes, ma, &c.full[st], k * 128, it.row0);
+          bulk_load(sf, sw + a0 * kAtomBytes, abytes, &c.full[st]);
+          bulk_load(sf + Sh::kSfBytes, sa + a0 * kAtomBytes, abytes, &c.full[st]);
+          if (Sh::kRowBlocks > 1 && rblocks > 1)
+            bulk_load(sf + 2 * Sh::kSfBytes, sa + sa_block + a0 * kAtomBytes, abytes, &c.full[st]);
+        }
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
@@ -259,7 +287,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
-      const int rows = __shfl_sync(0xffffffffu, item_of<NT>(p, c, item).rows, 0);
+      const int rows = walk.at(p, c, il, n_items, lane).rows;
       const int b = il % Sh::kBufs;
       ok = __all_sync(0xffffffffu, mbar_wait(&c.acc_empty[b], ((il / Sh::kBufs) & 1) ^ 1, abort, p.wait_ns));
       if (!ok) break;
@@ -318,7 +346,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         p.y[i] = 0;
     int il = 0;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++il) {
-      const Item it = item_of<NT>(p, c, item);
+      const Item it = walk.at(p, c, il, n_items, lane);
       const float s = (p.ga ? __ldg(p.ga) : 1.f) * (p.gw ? __ldg(p.gw + it.e) : 1.f);
       const int b = il % Sh::kBufs;
       // the warp leaves together: the TMEM loads take all its lanes
