@@ -33,8 +33,11 @@ constexpr uint64_t kGraceNs = 1000000;  // after an abort: time for issued copie
 
 template <int NT> struct ProductCfg;
 // few rows per expert: short row tiles leave room for a deeper ring
-template <> struct ProductCfg<64> { static constexpr int kStages = 7, kAccBufs = 2; };
-template <> struct ProductCfg<256> { static constexpr int kStages = 4, kAccBufs = 1; };
+template <> struct ProductCfg<64> { static constexpr int kStages = 7, kAcc1 = 64; };
+// two accumulators of 256 columns and the scales do not fit TMEM: the second
+// accumulator begins 128 columns in, and the epilogue drains the shared half
+// first, so that the next tile's MMAs wait for half a drain only
+template <> struct ProductCfg<256> { static constexpr int kStages = 4, kAcc1 = 128; };
 
 template <int NT, int FMT> struct Shape {
   static constexpr int kAtoms = kKStep / (4 * fp4_block(FMT));  // scale atoms per stage and 128 rows
@@ -43,15 +46,20 @@ template <int NT, int FMT> struct Shape {
   static constexpr int kSfBytes = kAtoms * kAtomBytes;
   static constexpr int kStageBytes = kWBytes + kABytes + (1 + kRowBlocks) * kSfBytes;
   static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
-  static constexpr int S = ProductCfg<NT>::kStages, kBufs = ProductCfg<NT>::kAccBufs;
-  // TMEM columns: accumulators, then per stage the scales of W and of A
+  static constexpr int S = ProductCfg<NT>::kStages;
+  static constexpr int kAcc1 = ProductCfg<NT>::kAcc1;  // TMEM column of the second accumulator
+  static constexpr int kShared = NT - kAcc1;           // columns that both accumulators use
+  // TMEM columns after the accumulators: slots for a step's scales of W and A
   static constexpr int kSfCols = kAtoms * 4 * (1 + kRowBlocks);
-  static constexpr int kSfCol0 = kBufs * NT;
-  static_assert(kSfCol0 + S * kSfCols <= 512, "TMEM columns");
+  static constexpr int kSfCol0 = kAcc1 + NT;
+  static constexpr int kSlots = (512 - kSfCol0) / kSfCols < S ? (512 - kSfCol0) / kSfCols : S;
+  static_assert(kSlots >= 2, "TMEM columns");
+  static_assert(kShared == 0 || (kShared == kAcc1 && kShared % 128 == 0), "halves of 128 columns");
 };
 
 struct __align__(16) Ctl {
   uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint64_t edge[2];  // the columns shared with the other accumulator have been read
   uint32_t tmem;
   int abort;
   int tiles[kMaxProductExperts + 1];  // row tiles of all earlier experts
@@ -223,6 +231,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
       mbar_init(&c.acc_empty[b], kEpilogueThreads);
+      mbar_init(&c.edge[b], kEpilogueThreads);
     }
     c.abort = 0;
     fence_mbar_init();
@@ -288,23 +297,30 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
       const int rows = walk.at(p, c, il, n_items, lane).rows;
-      const int b = il % Sh::kBufs;
-      ok = __all_sync(0xffffffffu, mbar_wait(&c.acc_empty[b], ((il / Sh::kBufs) & 1) ^ 1, abort, p.wait_ns));
+      const int b = il & 1;
+      ok = mbar_wait(&c.acc_empty[b], ((il >> 1) & 1) ^ 1, abort, p.wait_ns);
+      if (Sh::kShared > 0 && il > 0)
+        ok = mbar_wait(&c.edge[b ^ 1], ((il - 1) >> 1) & 1, abort, p.wait_ns) && ok;
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t acc = tm + b * NT;
+      const uint32_t acc = tm + b * Sh::kAcc1;
       const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(rows), 2);
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
-        ok = __all_sync(0xffffffffu, mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns));
+        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
+        // the MMAs that read this slot of scales have finished: with a slot
+        // per stage they had when the stage was free; with fewer slots wait
+        // for the step that used it last
+        if (Sh::kSlots < S && g >= Sh::kSlots)
+          ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sb = sb0 + st * Sh::kStride;
         const uint32_t sf = sb + Sh::kWBytes + Sh::kABytes;
-        // this stage's cells: per atom four columns of W, then four per row
-        // block of A (the MMAs that read them last have finished: the stage
-        // was free)
-        const uint32_t tw = tm + Sh::kSfCol0 + st * Sh::kSfCols;
+        // the slot's cells: per atom four columns of W, then four per row block of A
+        const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
         const uint32_t ta = tw + 4 * Sh::kAtoms;
         const int na = p.atoms - k * Sh::kAtoms, nm = (p.cols - k * kKStep + 63) / 64;
         if (elect_one()) {
@@ -336,8 +352,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
   } else if (warp >= 4) {
     // =============================== epilogue ==============================
     // Two warps per lane quarter take alternate chunks of 32 accumulator
-    // columns (rows of y); the next chunk is read from TMEM while this one is
-    // stored.
+    // columns (rows of y), first those that the next tile's accumulator shares.
     const int m = (warp & 3) * 32 + lane;  // output of the item; TMEM lane
     const int half = (warp - 4) >> 2;
     if (ok_offsets)
@@ -348,29 +363,30 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++il) {
       const Item it = walk.at(p, c, il, n_items, lane);
       const float s = (p.ga ? __ldg(p.ga) : 1.f) * (p.gw ? __ldg(p.gw + it.e) : 1.f);
-      const int b = il % Sh::kBufs;
+      const int b = il & 1;
       // the warp leaves together: the TMEM loads take all its lanes
-      const bool w_ok = mbar_wait(&c.acc_full[b], (il / Sh::kBufs) & 1, abort, p.wait_ns);
+      const bool w_ok = mbar_wait(&c.acc_full[b], (il >> 1) & 1, abort, p.wait_ns);
       if (!__all_sync(0xffffffffu, w_ok)) break;
       tc_fence_after();
-      const uint32_t t = tmem + b * NT + ((uint32_t)(warp & 3) << 21);
+      const uint32_t t = tmem + b * Sh::kAcc1 + ((uint32_t)(warp & 3) << 21);
       const int n = it.n0 + m;
       uint16_t* yp = p.y + (int64_t)it.row0 * p.N + n;
-      uint32_t v[2][32];
-      int c0 = half * 32;
-      if (c0 < it.rows) tmem_ld32_async(t + c0, v[0]);
+      constexpr int kParts = NT > 128 ? 2 : 1;  // parts of up to 128 columns, two chunks per warp
 #pragma unroll
-      for (int u = 0; u < NT / 64; ++u, c0 += 64) {
-        if (c0 >= it.rows) break;
-        tmem_ld_wait(v[u & 1]);
-        if (u + 1 < NT / 64 && c0 + 64 < it.rows) tmem_ld32_async(t + c0 + 64, v[(u + 1) & 1]);
-        else {
-          tc_fence_before();
-          mbar_arrive(&c.acc_empty[b]);  // the last read of this thread
-        }
-        store_chunk(p, yp, v[u & 1], s, n, c0, it.rows, lane);
+      for (int part = 0; part < kParts; ++part) {
+        // the second part of the first accumulator is the first of the second
+        const int c0 = (kParts == 2 && part == b ? 128 : 0) + half * 32, c1 = c0 + 64;
+        uint32_t v[2][32];
+        if (c0 < it.rows) tmem_ld32_async(t + c0, v[0]);
+        if (NT > 64 && c1 < it.rows) tmem_ld32_async(t + c1, v[1]);
+        tmem_ld_wait(v[0]);
+        tmem_ld_wait(v[1]);
+        tc_fence_before();
+        if (Sh::kShared > 0 && part == 0) mbar_arrive(&c.edge[b]);
+        if (part == kParts - 1) mbar_arrive(&c.acc_empty[b]);
+        if (c0 < it.rows) store_chunk(p, yp, v[0], s, n, c0, it.rows, lane);
+        if (NT > 64 && c1 < it.rows) store_chunk(p, yp, v[1], s, n, c1, it.rows, lane);
       }
-      if (half * 32 >= it.rows) mbar_arrive(&c.acc_empty[b]);
     }
   }
   __syncwarp();
