@@ -14,8 +14,8 @@
 //   warp 0      loads: per K step of 256 columns one TMA box of W, one of A
 //               (128-byte rows, 128-byte swizzle) and the steps' scale atoms
 //               into a ring of stages
-//   warp 1      scales from the stage to TMEM (tcgen05.cp), then one MMA per
-//               64 columns
+//   warp 2      scales from the stage to TMEM (tcgen05.cp)
+//   warp 1      one MMA per 64 columns
 //   warps 4-11  accumulators from TMEM, scaled and rounded, to y
 #include <cudaTypedefs.h>
 
@@ -58,7 +58,7 @@ template <int NT, int FMT> struct Shape {
 };
 
 struct __align__(16) Ctl {
-  uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
+  uint64_t full[8], empty[8], scaled[8], acc_full[2], acc_empty[2];
   uint64_t edge[2];  // the columns shared with the other accumulator have been read
   uint32_t tmem;
   int abort;
@@ -227,6 +227,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
+      mbar_init(&c.scaled[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
@@ -308,32 +309,17 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(rows), 2);
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
-        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
-        // the MMAs that read this slot of scales have finished: with a slot
-        // per stage they had when the stage was free; with fewer slots wait
-        // for the step that used it last
-        if (Sh::kSlots < S && g >= Sh::kSlots)
-          ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns) && ok;
+        // the operands have landed, and their scales are in TMEM
+        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns) &&
+             mbar_wait(&c.scaled[st], (g / S) & 1, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sb = sb0 + st * Sh::kStride;
-        const uint32_t sf = sb + Sh::kWBytes + Sh::kABytes;
-        // the slot's cells: per atom four columns of W, then four per row block of A
         const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
         const uint32_t ta = tw + 4 * Sh::kAtoms;
-        const int na = p.atoms - k * Sh::kAtoms, nm = (p.cols - k * kKStep + 63) / 64;
+        const int nm = (p.cols - k * kKStep + 63) / 64;
         if (elect_one()) {
-#pragma unroll
-          for (int i = 0; i < Sh::kAtoms; ++i) {
-            if (i < na) {
-              copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
-#pragma unroll
-              for (int r = 0; r < Sh::kRowBlocks; ++r)
-                if (r * 128 < rows)
-                  copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
-            }
-          }
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int i = FMT == MLR_FP4_MX ? m >> 1 : m;
@@ -348,6 +334,47 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       }
       if (ok && elect_one()) mma_commit(&c.acc_full[b]);
       __syncwarp();
+    }
+  } else if (warp == 2) {
+    // ================================ scales ===============================
+    // A warp of its own: the copies' issue would hold up the MMAs'.
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint32_t sf0 = smem_u32(smem) + Sh::kWBytes + Sh::kABytes;
+    int g = 0, il = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
+      const int rows = walk.at(p, c, il, n_items, lane).rows;
+      for (int k = 0; k < p.ksteps; ++k, ++g) {
+        const int st = g % S;
+        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
+        // the MMAs that read this slot last have finished: with a slot per
+        // stage they had when the stage was free; with fewer slots wait for
+        // the step that used it
+        if (Sh::kSlots < S && g >= Sh::kSlots)
+          ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sf = sf0 + st * Sh::kStride;
+        // the slot's cells: per atom four columns of W, then four per row block of A
+        const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
+        const uint32_t ta = tw + 4 * Sh::kAtoms;
+        const int na = p.atoms - k * Sh::kAtoms;
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < Sh::kAtoms; ++i) {
+            if (i < na) {
+              copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
+#pragma unroll
+              for (int r = 0; r < Sh::kRowBlocks; ++r)
+                if (r * 128 < rows)
+                  copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
+            }
+          }
+          mma_commit(&c.scaled[st]);
+        }
+        __syncwarp();
+      }
     }
   } else if (warp >= 4) {
     // =============================== epilogue ==============================
