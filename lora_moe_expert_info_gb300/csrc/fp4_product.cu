@@ -11,10 +11,10 @@
 // of one expert (the MMA's N), so that few rows waste little of the tensor
 // core and every weight is read once per tile.  One persistent CTA per SM
 // walks a static share of the items; roles are warps:
-//   warp 0      loads: per K step of 256 columns one TMA box of W, one of A
-//               (128-byte rows, 128-byte swizzle) and the steps' scale atoms
-//               into a ring of stages
-//   warp 2      scales from the stage to TMEM (tcgen05.cp)
+//   warp 0      codes: per K step of 256 columns one TMA box of W and one of A
+//               (128-byte rows, 128-byte swizzle) into a ring of stages
+//   warp 3      the steps' scale atoms into a ring of their own
+//   warp 2      scales from there to TMEM (tcgen05.cp), ahead of the codes
 //   warp 1      one MMA per 64 columns
 //   warps 4-11  accumulators from TMEM, scaled and rounded, to y
 #include <cudaTypedefs.h>
@@ -33,32 +33,38 @@ constexpr uint64_t kGraceNs = 1000000;  // after an abort: time for issued copie
 
 template <int NT> struct ProductCfg;
 // few rows per expert: short row tiles leave room for a deeper ring
-template <> struct ProductCfg<64> { static constexpr int kStages = 7, kAcc1 = 64; };
+template <> struct ProductCfg<64> { static constexpr int kStages = 8, kScaleStages = 6, kAcc1 = 64; };
 // two accumulators of 256 columns and the scales do not fit TMEM: the second
 // accumulator begins 128 columns in, and the epilogue drains the shared half
 // first, so that the next tile's MMAs wait for half a drain only
-template <> struct ProductCfg<256> { static constexpr int kStages = 4, kAcc1 = 128; };
+template <> struct ProductCfg<256> { static constexpr int kStages = 4, kScaleStages = 4, kAcc1 = 128; };
 
 template <int NT, int FMT> struct Shape {
-  static constexpr int kAtoms = kKStep / (4 * fp4_block(FMT));  // scale atoms per stage and 128 rows
+  static constexpr int kAtoms = kKStep / (4 * fp4_block(FMT));  // scale atoms per step and 128 rows
   static constexpr int kRowBlocks = (NT + 127) / 128;
-  static constexpr int kWBytes = 128 * 128, kABytes = NT * 128;
-  static constexpr int kSfBytes = kAtoms * kAtomBytes;
-  static constexpr int kStageBytes = kWBytes + kABytes + (1 + kRowBlocks) * kSfBytes;
-  static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
-  static constexpr int S = ProductCfg<NT>::kStages;
+  static constexpr int S = ProductCfg<NT>::kStages, Q = ProductCfg<NT>::kScaleStages;
+  static constexpr int kWBytes = 128 * 128, kABytes = NT * 128;  // a stage of codes
+  static constexpr int kStride = kWBytes + kABytes;
+  static constexpr int kSfBytes = kAtoms * kAtomBytes;  // scales of 128 rows; a stage: W, then A's row blocks
+  static constexpr int kSfStride = (1 + kRowBlocks) * kSfBytes;
   static constexpr int kAcc1 = ProductCfg<NT>::kAcc1;  // TMEM column of the second accumulator
   static constexpr int kShared = NT - kAcc1;           // columns that both accumulators use
-  // TMEM columns after the accumulators: slots for a step's scales of W and A
+  // TMEM columns after the accumulators: slots for a step's scales of W and
+  // A.  A scale stage's barrier is not passed twice before the MMAs have seen
+  // it as long as there are no more slots than scale stages, and a stage's
+  // empty barrier not before the scales have as long as there are no more
+  // slots than stages.
   static constexpr int kSfCols = kAtoms * 4 * (1 + kRowBlocks);
   static constexpr int kSfCol0 = kAcc1 + NT;
-  static constexpr int kSlots = (512 - kSfCol0) / kSfCols < S ? (512 - kSfCol0) / kSfCols : S;
-  static_assert(kSlots >= 2, "TMEM columns");
+  static constexpr int kSlots = (512 - kSfCol0) / kSfCols < Q ? (512 - kSfCol0) / kSfCols : Q;
+  static_assert(kSlots >= 2 && kSlots <= Q && kSlots <= S && S <= 8 && Q <= 8, "slots");
   static_assert(kShared == 0 || (kShared == kAcc1 && kShared % 128 == 0), "halves of 128 columns");
 };
 
 struct __align__(16) Ctl {
-  uint64_t full[8], empty[8], scaled[8], acc_full[2], acc_empty[2];
+  uint64_t full[8], empty[8];      // a stage of codes has landed / its MMAs are done
+  uint64_t sf_full[8], scaled[8];  // a stage of scales has landed / is in TMEM
+  uint64_t acc_full[2], acc_empty[2];
   uint64_t edge[2];  // the columns shared with the other accumulator have been read
   uint32_t tmem;
   int abort;
@@ -67,7 +73,8 @@ struct __align__(16) Ctl {
 
 template <int NT, int FMT>
 constexpr int smem_bytes() {
-  return Shape<NT, FMT>::S * Shape<NT, FMT>::kStride + (int)sizeof(Ctl) + 1024;
+  return Shape<NT, FMT>::S * Shape<NT, FMT>::kStride + Shape<NT, FMT>::Q * Shape<NT, FMT>::kSfStride +
+         (int)sizeof(Ctl) + 1024;
 }
 
 struct Maps {
@@ -216,10 +223,11 @@ template <int NT, int FMT>
 __global__ void __launch_bounds__(kProductThreads, 1)
 product_kernel(const __grid_constant__ Maps maps, const Params p) {
   using Sh = Shape<NT, FMT>;
-  constexpr int S = Sh::S;
+  constexpr int S = Sh::S, Q = Sh::Q;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Ctl& c = *reinterpret_cast<Ctl*>(smem + S * Sh::kStride);
+  uint8_t* smem_sf = smem + S * Sh::kStride;
+  Ctl& c = *reinterpret_cast<Ctl*>(smem_sf + Q * Sh::kSfStride);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* abort = &c.abort;
 
@@ -227,7 +235,10 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&c.full[s], 1);
       mbar_init(&c.empty[s], 1);
-      mbar_init(&c.scaled[s], 1);
+    }
+    for (int q = 0; q < Q; ++q) {
+      mbar_init(&c.sf_full[q], 1);
+      mbar_init(&c.scaled[q], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
@@ -253,7 +264,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
   ItemWalk<NT> walk;
   walk.mine = Item{};
   if (warp == 0) {
-    // ================================ loads ================================
+    // ================================ codes ================================
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
@@ -261,27 +272,43 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       int bi = 0;  // the shortest box that holds the tile
       while ((16 << bi) < it.rows) ++bi;
       const CUtensorMap* ma = &maps.a[bi];
-      const int rblocks = (it.rows + 127) / 128;
       const int wrow = it.e * p.N + it.n0;
-      const uint8_t* sw = p.sw + ((int64_t)it.e * p.nblk + it.n0 / 128) * p.atoms * kAtomBytes;
-      const uint8_t* sa = p.sa + (int64_t)it.sblk * p.atoms * kAtomBytes;
-      const int64_t sa_block = (int64_t)p.atoms * kAtomBytes;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
         ok = __all_sync(0xffffffffu, mbar_wait(&c.empty[st], ((g / S) & 1) ^ 1, abort, p.wait_ns));
         if (!ok) break;
         uint8_t* sb = smem + st * Sh::kStride;
-        const uint32_t sf = smem_u32(sb) + Sh::kWBytes + Sh::kABytes;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128);
+          tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
+          tma_load_2d(sb + Sh::kWBytes, ma, &c.full[st], k * 128, it.row0);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 3) {
+    // ============================= scale loads =============================
+    int g = 0, il = 0;
+    bool ok = true;
+    for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
+      const Item it = walk.at(p, c, il, n_items, lane);
+      const int rblocks = (it.rows + 127) / 128;
+      const uint8_t* sw = p.sw + ((int64_t)it.e * p.nblk + it.n0 / 128) * p.atoms * kAtomBytes;
+      const uint8_t* sa = p.sa + (int64_t)it.sblk * p.atoms * kAtomBytes;
+      const int64_t sa_block = (int64_t)p.atoms * kAtomBytes;
+      for (int k = 0; k < p.ksteps; ++k, ++g) {
+        const int q = g % Q;
+        ok = __all_sync(0xffffffffu, mbar_wait(&c.scaled[q], ((g / Q) & 1) ^ 1, abort, p.wait_ns));
+        if (!ok) break;
+        const uint32_t sf = smem_u32(smem_sf) + q * Sh::kSfStride;
         const int a0 = k * Sh::kAtoms;
         const uint32_t abytes = (uint32_t)min(Sh::kAtoms, p.atoms - a0) * kAtomBytes;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128 + (1 + rblocks) * abytes);
-          tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
-          tma_load_2d(sb + Sh::kWBytes, ma, &c.full[st], k * 128, it.row0);
-          bulk_load(sf, sw + a0 * kAtomBytes, abytes, &c.full[st]);
-          bulk_load(sf + Sh::kSfBytes, sa + a0 * kAtomBytes, abytes, &c.full[st]);
+          mbar_arrive_expect_tx(&c.sf_full[q], (1 + rblocks) * abytes);
+          bulk_load(sf, sw + a0 * kAtomBytes, abytes, &c.sf_full[q]);
+          bulk_load(sf + Sh::kSfBytes, sa + a0 * kAtomBytes, abytes, &c.sf_full[q]);
           if (Sh::kRowBlocks > 1 && rblocks > 1)
-            bulk_load(sf + 2 * Sh::kSfBytes, sa + sa_block + a0 * kAtomBytes, abytes, &c.full[st]);
+            bulk_load(sf + 2 * Sh::kSfBytes, sa + sa_block + a0 * kAtomBytes, abytes, &c.sf_full[q]);
         }
         __syncwarp();
       }
@@ -309,9 +336,9 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(rows), 2);
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
-        // the operands have landed, and their scales are in TMEM
-        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns) &&
-             mbar_wait(&c.scaled[st], (g / S) & 1, abort, p.wait_ns);
+        // the codes have landed, and their scales are in TMEM
+        ok = mbar_wait(&c.scaled[g % Q], (g / Q) & 1, abort, p.wait_ns) &&
+             mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -336,26 +363,24 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       __syncwarp();
     }
   } else if (warp == 2) {
-    // ================================ scales ===============================
+    // ============================ scales to TMEM ===========================
     // A warp of its own: the copies' issue would hold up the MMAs'.
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t sf0 = smem_u32(smem) + Sh::kWBytes + Sh::kABytes;
+    const uint32_t sf0 = smem_u32(smem_sf);
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
       const int rows = walk.at(p, c, il, n_items, lane).rows;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
-        const int st = g % S;
-        ok = mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
-        // the MMAs that read this slot last have finished: with a slot per
-        // stage they had when the stage was free; with fewer slots wait for
-        // the step that used it
-        if (Sh::kSlots < S && g >= Sh::kSlots)
+        const int q = g % Q;
+        ok = mbar_wait(&c.sf_full[q], (g / Q) & 1, abort, p.wait_ns);
+        // the MMAs of the step that used this TMEM slot last are done
+        if (g >= Sh::kSlots)
           ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sf = sf0 + st * Sh::kStride;
+        const uint32_t sf = sf0 + q * Sh::kSfStride;
         // the slot's cells: per atom four columns of W, then four per row block of A
         const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
         const uint32_t ta = tw + 4 * Sh::kAtoms;
@@ -371,7 +396,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
                   copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
             }
           }
-          mma_commit(&c.scaled[st]);
+          mma_commit(&c.scaled[q]);
         }
         __syncwarp();
       }
