@@ -155,12 +155,11 @@ def _on_stream(fn):
     that the outputs, workspace and status word it allocates (and zeroes) are
     ordered on the stream the kernels are enqueued on, the caching allocator
     records them there, and the status read synchronises that stream."""
-    sig = inspect.signature(fn)
+    at = list(inspect.signature(fn).parameters).index("stream")
 
     @functools.wraps(fn)
     def run(*args, **kw):
-        bound = sig.bind(*args, **kw)
-        s = bound.arguments.get("stream")
+        s = kw.get("stream") if len(args) <= at else args[at]
         if s is None:
             return fn(*args, **kw)
         with torch.cuda.stream(s):
@@ -173,8 +172,15 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return ctypes.c_void_p(_stream_number(stream))
+
+
+def _stream_number(stream) -> int:
+    """The cudaStream_t of a torch stream; None: the current one (read without
+    building a stream object, which costs as much as a launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check_host(code: int, fn: str):

@@ -495,8 +495,14 @@ template <int NT, int FMT>
 int launch_product(const Maps& maps, const Params& p, cudaStream_t stream) {
   constexpr int smem = smem_bytes<NT, FMT>();
   static_assert(smem <= 227 * 1024, "shared memory per CTA");
-  if (cudaFuncSetAttribute(product_kernel<NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return MLR_ERR_CUDA;
+  static bool configured[64] = {};  // per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MLR_ERR_CUDA;
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    if (cudaFuncSetAttribute(product_kernel<NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return MLR_ERR_CUDA;
+    if (dev >= 0 && dev < 64) configured[dev] = true;
+  }
   // at most one partial tile per expert beyond the full ones
   const int64_t tiles = (p.P < p.E ? p.P : p.E) + (int64_t)p.P / NT;
   const int64_t items = tiles * p.nblk;

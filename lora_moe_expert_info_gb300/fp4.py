@@ -22,8 +22,8 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check_device, _check_host, _on_stream, _ptr, _req, _stream, library
-from .permute import DTYPES, _float, _out, moe_sort_pairs, moe_unpermute
+from . import _check_device, _check_host, _on_stream, _req, _stream_number, library
+from .permute import DTYPES, _address, _float, _out, moe_sort_pairs, moe_unpermute
 
 __all__ = ["fp4_quantize", "fp4_quantize_permuted", "fp4_quantize_swiglu", "fp4_dequantize", "fp4_expert_product",
            "fp4_moe_forward", "FORMATS"]
@@ -123,8 +123,9 @@ def fp4_quantize(x, fmt: str = "nvfp4", tensor_scale: Optional[torch.Tensor] = N
     _scale(tensor_scale, "tensor_scale", n, f, dev)
     codes, scales = _outputs(codes, scales, (*lead, rows), (*lead, (rows + 127) // 128), cols, f, dev)
     if n * rows:
-        _check_host(_lib().moe_fp4_quantize(_ptr(x), n, rows, cols, dtype, f, _ptr(tensor_scale), _ptr(codes),
-                                            _ptr(scales), _stream(stream)), "fp4_quantize")
+        _check_host(_lib().moe_fp4_quantize(x.data_ptr(), n, rows, cols, dtype, f, _address(tensor_scale),
+                                            codes.data_ptr(), scales.data_ptr(), _stream_number(stream)),
+                    "fp4_quantize")
     return codes, scales
 
 
@@ -154,9 +155,11 @@ def fp4_quantize_permuted(x, topk_ids, pair_pos, expert_offsets, fmt: str = "nvf
     codes, scales = _outputs(codes, scales, (T * K,), (T * K // 128 + E,), cols, f, dev)
     if T:
         status = _status(check, dev)
-        _done(_lib().moe_fp4_quantize_permuted(_ptr(x), _ptr(topk_ids), _ptr(pair_pos), _ptr(expert_offsets), T, K,
-                                               cols, E, dtype, f, _ptr(tensor_scale), _ptr(codes), _ptr(scales),
-                                               _ptr(status), _stream(stream)), status, "fp4_quantize_permuted")
+        _done(_lib().moe_fp4_quantize_permuted(x.data_ptr(), topk_ids.data_ptr(), pair_pos.data_ptr(),
+                                               expert_offsets.data_ptr(), T, K, cols, E, dtype, f,
+                                               _address(tensor_scale), codes.data_ptr(), scales.data_ptr(),
+                                               _address(status), _stream_number(stream)), status,
+              "fp4_quantize_permuted")
     return codes, scales
 
 
@@ -179,9 +182,9 @@ def fp4_quantize_swiglu(gate_up, expert_offsets, fmt: str = "nvfp4", tensor_scal
     codes, scales = _outputs(codes, scales, (P,), (P // 128 + E,), cols, f, dev)
     if P:
         status = _status(check, dev)
-        _done(_lib().moe_fp4_quantize_swiglu(_ptr(gate_up), _ptr(expert_offsets), P, cols, E, dtype, f,
-                                             _ptr(tensor_scale), _ptr(codes), _ptr(scales), _ptr(status),
-                                             _stream(stream)), status, "fp4_quantize_swiglu")
+        _done(_lib().moe_fp4_quantize_swiglu(gate_up.data_ptr(), expert_offsets.data_ptr(), P, cols, E, dtype, f,
+                                             _address(tensor_scale), codes.data_ptr(), scales.data_ptr(), _address(status),
+                                             _stream_number(stream)), status, "fp4_quantize_swiglu")
     return codes, scales
 
 
@@ -210,14 +213,14 @@ def fp4_dequantize(codes, scales, cols: int, fmt: str = "nvfp4", tensor_scale: O
     else:
         n = lead[0] if lead else 1
         blocks = (*lead, (rows + 127) // 128)
-    if codes.shape[-1] != _pitch(cols) or tuple(scales.shape) != (*blocks, _atoms(cols, f), 32, 4, 4):
+    if codes.shape[-1] != _pitch(cols) or scales.shape != (*blocks, _atoms(cols, f), 32, 4, 4):
         raise ValueError("fp4_dequantize: inconsistent shapes")
     _scale(tensor_scale, "tensor_scale", 1 if expert_offsets is not None else n, f, dev)
     out = _out(out, "out", (*lead, rows, cols), dtype, dev)
     if out.numel():
-        _check_host(_lib().moe_fp4_dequantize(_ptr(codes), _ptr(scales), _ptr(expert_offsets), n, rows, cols, f,
-                                              _ptr(tensor_scale), DTYPES[dtype], _ptr(out), _stream(stream)),
-                    "fp4_dequantize")
+        _check_host(_lib().moe_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), _address(expert_offsets), n, rows,
+                                              cols, f, _address(tensor_scale), DTYPES[dtype], out.data_ptr(),
+                                              _stream_number(stream)), "fp4_dequantize")
     return out
 
 
@@ -241,9 +244,9 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
         raise ValueError("fp4_expert_product: inconsistent shapes")
     P, N = a_codes.shape[0], w_codes.shape[1]
     pitch, atom = _pitch(cols), (_atoms(cols, f), 32, 4, 4)
-    if (a_codes.shape[1] != pitch or tuple(w_codes.shape) != (E, N, pitch)
-            or tuple(a_scales.shape) != (P // 128 + E, *atom)
-            or tuple(w_scales.shape) != (E, (N + 127) // 128, *atom)):
+    if (a_codes.shape[1] != pitch or w_codes.shape != (E, N, pitch)
+            or a_scales.shape != (P // 128 + E, *atom)
+            or w_scales.shape != (E, (N + 127) // 128, *atom)):
         raise ValueError("fp4_expert_product: inconsistent shapes")
     _scale(a_tensor_scale, "a_tensor_scale", 1, f, dev)
     _scale(w_tensor_scale, "w_tensor_scale", E, f, dev)
@@ -252,9 +255,10 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
         return y
     if check and status is None:
         status = _status(True, dev)
-    code = _lib().moe_fp4_expert_product(_ptr(a_codes), _ptr(a_scales), _ptr(a_tensor_scale), _ptr(w_codes),
-                                         _ptr(w_scales), _ptr(w_tensor_scale), _ptr(expert_offsets), P, E, N, cols, f,
-                                         _ptr(y), _ptr(status), _stream(stream))
+    code = _lib().moe_fp4_expert_product(a_codes.data_ptr(), a_scales.data_ptr(), _address(a_tensor_scale),
+                                         w_codes.data_ptr(), w_scales.data_ptr(), _address(w_tensor_scale),
+                                         expert_offsets.data_ptr(), P, E, N, cols, f, y.data_ptr(), _address(status),
+                                         _stream_number(stream))
     _done(code, status if check else None, "fp4_expert_product")
     return y
 

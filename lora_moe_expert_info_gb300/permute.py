@@ -21,7 +21,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check_device, _check_host, _on_stream, _ptr, _req, _stream, library
+from . import _check_device, _check_host, _on_stream, _req, _stream_number, library
 
 __all__ = ["moe_permute", "moe_sort_pairs", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
            "MoePermute", "MoeUnpermute"]
@@ -47,6 +47,10 @@ def _lib():
     return _typed
 
 
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _float(t: torch.Tensor, name: str, dev, ndim: int = 2) -> int:
     """Checks a contiguous bf16 or float32 tensor; its type number."""
     if not isinstance(t, torch.Tensor):
@@ -64,7 +68,7 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> torch.Tenso
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
     _req(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     return t
 
@@ -96,9 +100,9 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     # an empty tensor has no address: rows of no columns are only sorted
     copy = H > 0
-    code = lib.moe_permute(_ptr(x) if copy else None, _ptr(topk_ids), T, K, H, E, dtype, _ptr(rows) if copy else None,
-                           _ptr(pair_pos), _ptr(expert_offsets), _ptr(workspace), workspace.numel(), _ptr(status),
-                           _stream(stream))
+    code = lib.moe_permute(x.data_ptr() if copy else None, topk_ids.data_ptr(), T, K, H, E, dtype,
+                           rows.data_ptr() if copy else None, pair_pos.data_ptr(), expert_offsets.data_ptr(),
+                           workspace.data_ptr(), workspace.numel(), _address(status), _stream_number(stream))
     _check_host(code, fn)
     if check:
         _check_device(status, fn)
@@ -141,14 +145,14 @@ def _gather(rows, pair_pos, weights, y, stream, check, fn, rows_name):
     H = rows.shape[1]
     if weights is not None:
         _req(weights, "topk_weights", torch.float32, dev)
-    if rows.shape[0] != T * K or (weights is not None and tuple(weights.shape) != (T, K)):
+    if rows.shape[0] != T * K or (weights is not None and weights.shape != (T, K)):
         raise ValueError(f"{fn}: inconsistent shapes")
     y = _out(y, "y", (T, H), rows.dtype, dev)
     if T == 0 or H == 0:
         return y
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
-    code = lib.moe_unpermute(_ptr(rows), _ptr(pair_pos), _ptr(weights), T, K, H, dtype, _ptr(y), _ptr(status),
-                             _stream(stream))
+    code = lib.moe_unpermute(rows.data_ptr(), pair_pos.data_ptr(), _address(weights), T, K, H, dtype, y.data_ptr(),
+                             _address(status), _stream_number(stream))
     _check_host(code, fn)
     if check:
         _check_device(status, fn)
@@ -189,15 +193,16 @@ def moe_unpermute_backward(dy, rows, pair_pos, topk_weights, d_rows: Optional[to
     _req(topk_weights, "topk_weights", torch.float32, dev)
     T, K = pair_pos.shape
     H = rows.shape[1]
-    if rows.shape[0] != T * K or tuple(dy.shape) != (T, H) or tuple(topk_weights.shape) != (T, K):
+    if rows.shape[0] != T * K or dy.shape != (T, H) or topk_weights.shape != (T, K):
         raise ValueError("moe_unpermute_backward: inconsistent shapes")
     d_rows = _out(d_rows, "d_rows", (T * K, H), rows.dtype, dev)
     d_weights = _out(d_weights, "d_weights", (T, K), torch.float32, dev)
     if T == 0 or H == 0:
         return d_rows, d_weights.zero_()
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
-    code = lib.moe_unpermute_backward(_ptr(dy), _ptr(rows), _ptr(pair_pos), _ptr(topk_weights), T, K, H, dtype,
-                                      _ptr(d_rows), _ptr(d_weights), _ptr(status), _stream(stream))
+    code = lib.moe_unpermute_backward(dy.data_ptr(), rows.data_ptr(), pair_pos.data_ptr(), topk_weights.data_ptr(), T,
+                                      K, H, dtype, d_rows.data_ptr(), d_weights.data_ptr(), _address(status),
+                                      _stream_number(stream))
     _check_host(code, "moe_unpermute_backward")
     if check:
         _check_device(status, "moe_unpermute_backward")
