@@ -226,159 +226,175 @@ permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int 
 }
 
 // ------------------------------------------------------------ row vectors --
-// N consecutive elements of a row as fp32.
-template <int N> __device__ __forceinline__ void load_row(const float* p, float (&v)[N]) {
-  if (N == 4) {
-    const float4 q = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = q.x; v[1 % N] = q.y; v[2 % N] = q.z; v[3 % N] = q.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
-  }
+// N consecutive elements of a row: the raw load and its fp32 values.
+template <typename E_, int N> struct Vec;
+template <> struct Vec<float, 4> { using type = float4; };
+template <> struct Vec<float, 1> { using type = float; };
+template <> struct Vec<uint16_t, 8> { using type = uint4; };
+template <> struct Vec<uint16_t, 2> { using type = uint32_t; };
+template <> struct Vec<uint16_t, 1> { using type = uint16_t; };
+
+__device__ __forceinline__ void widen(const float4& q, float (&v)[4]) {
+  v[0] = q.x;
+  v[1] = q.y;
+  v[2] = q.z;
+  v[3] = q.w;
 }
+__device__ __forceinline__ void widen(const float& q, float (&v)[1]) { v[0] = q; }
 __device__ __forceinline__ void widen2(uint32_t w, float& a, float& b) {
   a = __uint_as_float(w << 16);
   b = __uint_as_float(w & 0xffff0000u);
 }
-template <int N> __device__ __forceinline__ void load_row(const uint16_t* p, float (&v)[N]) {
-  if (N == 8) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-    widen2(q.x, v[0], v[1 % N]);
-    widen2(q.y, v[2 % N], v[3 % N]);
-    widen2(q.z, v[4 % N], v[5 % N]);
-    widen2(q.w, v[6 % N], v[7 % N]);
-  } else if (N == 2) {
-    widen2(__ldg(reinterpret_cast<const uint32_t*>(p)), v[0], v[1 % N]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __uint_as_float((uint32_t)__ldg(p + i) << 16);
-  }
+__device__ __forceinline__ void widen(const uint4& q, float (&v)[8]) {
+  widen2(q.x, v[0], v[1]);
+  widen2(q.y, v[2], v[3]);
+  widen2(q.z, v[4], v[5]);
+  widen2(q.w, v[6], v[7]);
 }
-template <int N> __device__ __forceinline__ void store_row(float* p, const float (&v)[N]) {
-  if (N == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1 % N], v[2 % N], v[3 % N]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = v[i];
-  }
-}
+__device__ __forceinline__ void widen(const uint32_t& q, float (&v)[2]) { widen2(q, v[0], v[1]); }
+__device__ __forceinline__ void widen(const uint16_t& q, float (&v)[1]) { v[0] = __uint_as_float((uint32_t)q << 16); }
+
 __device__ __forceinline__ uint32_t narrow2(float a, float b) {
   uint32_t o;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(b), "f"(a));
   return o;
 }
-template <int N> __device__ __forceinline__ void store_row(uint16_t* p, const float (&v)[N]) {
-  if (N == 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(narrow2(v[0], v[1 % N]), narrow2(v[2 % N], v[3 % N]),
-                                              narrow2(v[4 % N], v[5 % N]), narrow2(v[6 % N], v[7 % N]));
-  } else if (N == 2) {
-    *reinterpret_cast<uint32_t*>(p) = narrow2(v[0], v[1 % N]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = f32_to_bf16_bits(v[i]);
-  }
+__device__ __forceinline__ void narrow(const float (&v)[4], float4& q) { q = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void narrow(const float (&v)[1], float& q) { q = v[0]; }
+__device__ __forceinline__ void narrow(const float (&v)[8], uint4& q) {
+  q = make_uint4(narrow2(v[0], v[1]), narrow2(v[2], v[3]), narrow2(v[4], v[5]), narrow2(v[6], v[7]));
+}
+__device__ __forceinline__ void narrow(const float (&v)[2], uint32_t& q) { q = narrow2(v[0], v[1]); }
+__device__ __forceinline__ void narrow(const float (&v)[1], uint16_t& q) { q = f32_to_bf16_bits(v[0]); }
+
+// The threads of a token: a power of two, so that short rows share a block.
+int row_threads(int nv, int most) {
+  int l = 8;
+  while (l < nv && l < most) l *= 2;
+  return l;
 }
 
 // y[t] = sum_k w[t, k] rows[pos]; w == nullptr: w = 1 (the gradient of permute).
-// One thread per N columns of a token, up to 8 rows in flight.
-template <typename E_, int N>
-__global__ void __launch_bounds__(256)
-unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos, const float* __restrict__ w,
-                 int64_t T, int K, int H, int nv, E_* __restrict__ y, int32_t* d_status) {
+// One thread per vector of a token; KU rows are loaded before any is added,
+// without branches, so that their loads are in flight together.
+constexpr int kSumThreads = 128;
+template <typename E_, int N, int KU>
+__global__ void __launch_bounds__(kSumThreads)
+unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos, const float* __restrict__ w, int T,
+                 int K, int H, int nv, int lpt_log2, unsigned col_blocks, E_* __restrict__ y, int32_t* d_status) {
+  using V = typename Vec<E_, N>::type;
   pdl_wait();
   pdl_trigger();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= T * nv) return;
-  const int64_t t = i / nv;
-  const int c = (int)(i - t * nv) * N;
-  const int64_t P = T * K;
+  const unsigned tb = blockIdx.x / col_blocks, cb = blockIdx.x - tb * col_blocks;
+  const int64_t t = ((int64_t)tb << (7 - lpt_log2)) + (threadIdx.x >> lpt_log2);
+  const int c = (int)(cb << lpt_log2) + (threadIdx.x & ((1 << lpt_log2) - 1));
+  if (t >= T || c >= nv) return;
+  const int64_t P = (int64_t)T * K;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += 8) {
-    float v[8][N];
-    float wk[8];
-    bool use[8];
+  for (int k0 = 0; k0 < K; k0 += KU) {
+    V v[KU];
+    float wk[KU];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int q = k0 + j < K ? __ldg(pair_pos + t * K + k0 + j) : -1;
-      use[j] = q >= 0 && q < P;
+    for (int j = 0; j < KU; ++j) {
+      const int64_t p = t * K + k0 + j;
+      const int q = k0 + j < K ? __ldg(pair_pos + p) : -1;
+      const bool use = q >= 0 && q < P;
       if (q >= P) set_status(d_status, MLR_STATUS_INDEX);
-      if (use[j]) {
-        wk[j] = w != nullptr ? __ldg(w + t * K + k0 + j) : 1.f;
-        load_row<N>(rows + (int64_t)q * H + c, v[j]);
-      }
+      wk[j] = !use ? 0.f : w != nullptr ? __ldg(w + p) : 1.f;
+      v[j] = use ? __ldg(reinterpret_cast<const V*>(rows + (int64_t)q * H) + c) : V{};
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (use[j])
+    for (int j = 0; j < KU; ++j) {
+      float f[N];
+      widen(v[j], f);
 #pragma unroll
-        for (int u = 0; u < N; ++u) acc[u] = fmaf(wk[j], v[j][u], acc[u]);
+      for (int u = 0; u < N; ++u) acc[u] = fmaf(wk[j], f[u], acc[u]);
+    }
   }
-  store_row<N>(y + t * H + c, acc);
+  V o;
+  narrow(acc, o);
+  reinterpret_cast<V*>(y + t * H)[c] = o;
 }
 
-// One block per token: the row gradients of its pairs and the dot products
-// that are the weights' gradients (per thread over its columns in increasing
-// order, then over lanes and warps in a fixed order).
+// The row gradients of a token's pairs and the dot products that are its
+// weights' gradients, by 2^lpt_log2 threads per token (per thread over its
+// columns in increasing order, then over lanes and warps in a fixed order).
 constexpr int kBackThreads = 256;
-template <typename E_, int N>
+template <typename E_, int N, int KU>
 __global__ void __launch_bounds__(kBackThreads)
 unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos,
-                          const float* __restrict__ w, int T, int K, int H, E_* __restrict__ d_rows,
-                          float* __restrict__ dw, int32_t* d_status) {
-  __shared__ float part[kBackThreads / 32][8];
+                          const float* __restrict__ w, int T, int K, int H, int nv, int lpt_log2,
+                          E_* __restrict__ d_rows, float* __restrict__ dw, int32_t* d_status) {
+  using V = typename Vec<E_, N>::type;
+  __shared__ float part[kBackThreads / 32][KU];
   pdl_wait();
   pdl_trigger();
-  const int64_t t = blockIdx.x;
+  const int lpt = 1 << lpt_log2, lt = threadIdx.x & (lpt - 1);
+  const int64_t t = ((int64_t)blockIdx.x << (8 - lpt_log2)) + (threadIdx.x >> lpt_log2);
   const int64_t P = (int64_t)T * K;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int k0 = 0; k0 < K; k0 += 8) {
-    int64_t at[8];
-    bool use[8], put[8];
-    float wk[8], dot[8];
+  const bool in = t < T;  // every thread stays for the exchanges
+  for (int k0 = 0; k0 < K; k0 += KU) {
+    int row[KU];  // -1: nothing to write
+    bool use[KU];
+    float wk[KU], dot[KU];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int q = k0 + j < K ? __ldg(pair_pos + t * K + k0 + j) : 0;
-      const int64_t r = q < 0 ? ~q : q;
-      put[j] = k0 + j < K && r < P;
-      use[j] = put[j] && q >= 0;
-      if (k0 + j < K && r >= P && threadIdx.x == 0) set_status(d_status, MLR_STATUS_INDEX);
-      at[j] = r * H;
+    for (int j = 0; j < KU; ++j) {
+      const bool have = in && k0 + j < K;
+      const int q = have ? __ldg(pair_pos + t * K + k0 + j) : 0;
+      const int r = q < 0 ? ~q : q;
+      const bool ok = have && r < P;
+      if (have && !ok && lt == 0) set_status(d_status, MLR_STATUS_INDEX);
+      row[j] = ok ? r : -1;
+      use[j] = ok && q >= 0;
       wk[j] = use[j] ? __ldg(w + t * K + k0 + j) : 0.f;
       dot[j] = 0.f;
     }
-    for (int c = threadIdx.x * N; c < H; c += kBackThreads * N) {
-      float g[N], v[8][N];
-      load_row<N>(dy + t * H + c, g);
+    if (in)
+      for (int c = lt; c < nv; c += lpt) {
+        float g[N];
+        V v[KU];
+        const V gv = __ldg(reinterpret_cast<const V*>(dy + t * H) + c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (use[j]) load_row<N>(rows + at[j] + c, v[j]);
+        for (int j = 0; j < KU; ++j)
+          v[j] = use[j] ? __ldg(reinterpret_cast<const V*>(rows + (int64_t)row[j] * H) + c) : V{};
+        widen(gv, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (!put[j]) continue;
-        float o[N];
+        for (int j = 0; j < KU; ++j) {
+          float f[N], o[N];
+          widen(v[j], f);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-          o[u] = use[j] ? wk[j] * g[u] : 0.f;
-          if (use[j]) dot[j] = fmaf(g[u], v[j][u], dot[j]);
+          for (int u = 0; u < N; ++u) {
+            o[u] = use[j] ? wk[j] * g[u] : 0.f;
+            dot[j] = use[j] ? fmaf(g[u], f[u], dot[j]) : 0.f;
+          }
+          V ov;
+          narrow(o, ov);
+          if (row[j] >= 0) reinterpret_cast<V*>(d_rows + (int64_t)row[j] * H)[c] = ov;
         }
-        store_row<N>(d_rows + at[j] + c, o);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < KU; ++j)
+      for (int o = min(lpt, 32) >> 1; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+    if (lpt <= 32) {
+      if (lt == 0 && in)
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
-      if (lane == 0) part[warp][j] = dot[j];
+        for (int j = 0; j < KU; ++j)
+          if (k0 + j < K) dw[t * K + k0 + j] = dot[j];
+    } else {
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < KU; ++j) part[warp][j] = dot[j];
+      __syncthreads();
+      if (lt < KU && in && k0 + lt < K) {
+        float s = 0.f;
+        for (int q = 0; q < lpt / 32; ++q) s += part[warp + q][lt];
+        dw[t * K + k0 + lt] = s;
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (threadIdx.x < 8 && k0 + (int)threadIdx.x < K) {
-      float s = 0.f;
-      for (int q = 0; q < kBackThreads / 32; ++q) s += part[q][threadIdx.x];
-      dw[t * K + k0 + threadIdx.x] = s;
-    }
-    __syncthreads();
   }
 }
 
@@ -414,26 +430,49 @@ int launch_permute(const SortPlan& s, const void* x, const int32_t* ids, int T, 
   return s.one ? run(permute_kernel<VB, true>) : run(permute_kernel<VB, false>);
 }
 
-template <typename E_, int N>
-int launch_unpermute(const void* rows, const int32_t* pos, const float* w, int64_t T, int K, int H, void* y,
-                     int32_t* d_status, cudaStream_t stream) {
-  const int nv = H / N;
-  if (launch_pdl(unpermute_kernel<E_, N>, dim3((unsigned)ceil_div(T * nv, 256)), dim3(256), 0, stream,
-                 static_cast<const E_*>(rows), pos, w, T, K, H, nv, static_cast<E_*>(y), d_status) != cudaSuccess)
+int log2_of(int n) {
+  int l = 0;
+  while ((1 << l) < n) ++l;
+  return l;
+}
+
+template <typename E_, int N, int KU>
+int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int T, int K, int H, void* y,
+                       int32_t* d_status, cudaStream_t stream) {
+  const int nv = H / N, lpt = row_threads(nv, kSumThreads);
+  const int64_t col_blocks = ceil_div(nv, lpt), blocks = ceil_div(T, kSumThreads / lpt) * col_blocks;
+  if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  if (launch_pdl(unpermute_kernel<E_, N, KU>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
+                 static_cast<const E_*>(rows), pos, w, T, K, H, nv, log2_of(lpt), (unsigned)col_blocks,
+                 static_cast<E_*>(y), d_status) != cudaSuccess)
     return MLR_ERR_CUDA;
   note_launch();
   return MLR_OK;
 }
 
-template <typename E_, int N>
-int launch_unpermute_backward(const void* dy, const void* rows, const int32_t* pos, const float* w, int T, int K,
-                              int H, void* d_rows, float* dw, int32_t* d_status, cudaStream_t stream) {
-  if (launch_pdl(unpermute_backward_kernel<E_, N>, dim3((unsigned)T), dim3(kBackThreads), 0, stream,
-                 static_cast<const E_*>(dy), static_cast<const E_*>(rows), pos, w, T, K, H,
-                 static_cast<E_*>(d_rows), dw, d_status) != cudaSuccess)
+// Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds K, so that
+// few experts per token cost no empty turns.
+template <typename E_, int N, typename... A>
+int launch_unpermute(int K, A... a) {
+  return K == 1 ? launch_unpermute_k<E_, N, 1>(a...) : K == 2 ? launch_unpermute_k<E_, N, 2>(a...)
+         : K <= 4 ? launch_unpermute_k<E_, N, 4>(a...) : launch_unpermute_k<E_, N, 8>(a...);
+}
+
+template <typename E_, int N, int KU>
+int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t* pos, const float* w, int T, int K,
+                                int H, void* d_rows, float* dw, int32_t* d_status, cudaStream_t stream) {
+  const int nv = H / N, lpt = row_threads(nv, kBackThreads);
+  if (launch_pdl(unpermute_backward_kernel<E_, N, KU>, dim3((unsigned)ceil_div(T, kBackThreads / lpt)),
+                 dim3(kBackThreads), 0, stream, static_cast<const E_*>(dy), static_cast<const E_*>(rows), pos, w, T, K,
+                 H, nv, log2_of(lpt), static_cast<E_*>(d_rows), dw, d_status) != cudaSuccess)
     return MLR_ERR_CUDA;
   note_launch();
   return MLR_OK;
+}
+template <typename E_, int N, typename... A>
+int launch_unpermute_backward(int K, A... a) {
+  return K == 1 ? launch_unpermute_backward_k<E_, N, 1>(a...) : K == 2 ? launch_unpermute_backward_k<E_, N, 2>(a...)
+         : K <= 4 ? launch_unpermute_backward_k<E_, N, 4>(a...) : launch_unpermute_backward_k<E_, N, 8>(a...);
 }
 
 // Common checks of the row operators; the row size in *es.
@@ -510,14 +549,14 @@ extern "C" int moe_unpermute(const void* rows, const int32_t* pair_pos, const fl
   if (num_tokens == 0) return MLR_OK;
   if (rows == nullptr || pair_pos == nullptr || y == nullptr || !aligned_to(rows, es) || !aligned_to(y, es))
     return MLR_ERR_INVALID;
-  if (ceil_div((int64_t)num_tokens * hidden, 256) > INT32_MAX) return MLR_ERR_UNSUPPORTED;
   auto fits = [&](int n) { return (int64_t)hidden * es % n == 0 && aligned_to(rows, n) && aligned_to(y, n); };
+  const int T = num_tokens, K = topk, H = hidden;
   if (dtype == MLR_DTYPE_F32)
-    return fits(16) ? launch_unpermute<float, 4>(rows, pair_pos, topk_weights, num_tokens, topk, hidden, y, d_status, stream)
-                    : launch_unpermute<float, 1>(rows, pair_pos, topk_weights, num_tokens, topk, hidden, y, d_status, stream);
-  return fits(16)  ? launch_unpermute<uint16_t, 8>(rows, pair_pos, topk_weights, num_tokens, topk, hidden, y, d_status, stream)
-         : fits(4) ? launch_unpermute<uint16_t, 2>(rows, pair_pos, topk_weights, num_tokens, topk, hidden, y, d_status, stream)
-                   : launch_unpermute<uint16_t, 1>(rows, pair_pos, topk_weights, num_tokens, topk, hidden, y, d_status, stream);
+    return fits(16) ? launch_unpermute<float, 4>(K, rows, pair_pos, topk_weights, T, K, H, y, d_status, stream)
+                    : launch_unpermute<float, 1>(K, rows, pair_pos, topk_weights, T, K, H, y, d_status, stream);
+  return fits(16)  ? launch_unpermute<uint16_t, 8>(K, rows, pair_pos, topk_weights, T, K, H, y, d_status, stream)
+         : fits(4) ? launch_unpermute<uint16_t, 2>(K, rows, pair_pos, topk_weights, T, K, H, y, d_status, stream)
+                   : launch_unpermute<uint16_t, 1>(K, rows, pair_pos, topk_weights, T, K, H, y, d_status, stream);
 }
 
 extern "C" int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair_pos,
@@ -538,9 +577,9 @@ extern "C" int moe_unpermute_backward(const void* dy, const void* rows, const in
   };
   const int T = num_tokens, K = topk, H = hidden;
   if (dtype == MLR_DTYPE_F32)
-    return fits(16) ? launch_unpermute_backward<float, 4>(dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
-                    : launch_unpermute_backward<float, 1>(dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
-  return fits(16)  ? launch_unpermute_backward<uint16_t, 8>(dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
-         : fits(4) ? launch_unpermute_backward<uint16_t, 2>(dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
-                   : launch_unpermute_backward<uint16_t, 1>(dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
+    return fits(16) ? launch_unpermute_backward<float, 4>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
+                    : launch_unpermute_backward<float, 1>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
+  return fits(16)  ? launch_unpermute_backward<uint16_t, 8>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
+         : fits(4) ? launch_unpermute_backward<uint16_t, 2>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
+                   : launch_unpermute_backward<uint16_t, 1>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
 }
