@@ -16,6 +16,8 @@
 // exchange their maxima), so a row is read once and nothing is kept outside
 // registers; bound by HBM: reads x, writes half a byte per value plus one byte
 // per block.
+#include <cuda_fp16.h>
+
 #include "mlr_fp4.cuh"
 #include "mlr_profile.cuh"
 
@@ -97,30 +99,58 @@ __device__ __forceinline__ Dest dest_of(const QuantParams& p, int64_t row, int k
   return e == p.E ? Dest{row, -1} : sorted_dest(p, row, e);
 }
 
-// 16 columns of a row as fp32, zeros past the end.  VEC: rows and base are
-// 16-byte aligned and the columns a multiple of 16 bytes.
-template <bool VEC>
+// 32 bytes at a 32-byte boundary, one instruction.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 16 columns of a row as fp32, zeros past the end.  VB: the bytes of a vector
+// that divide a row and the base's address (32, 16, or 0: single elements).
+template <int VB>
 __device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16]) {
-  if (VEC) {
+  if (VB > 0) {
+    uint32_t w[8] = {};
+    if (VB == 32) {
+      if (n > 0) load32(p, w);
+    } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 q = make_uint4(0, 0, 0, 0);
-      if (8 * h < n) q = __ldg(reinterpret_cast<const uint4*>(p) + h);
-      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      for (int h = 0; h < 2; ++h)
+        if (8 * h < n) {
+          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + h);
+          w[4 * h] = q.x;
+          w[4 * h + 1] = q.y;
+          w[4 * h + 2] = q.z;
+          w[4 * h + 3] = q.w;
+        }
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[8 * h + 2 * i] = __uint_as_float(w[i] << 16);
-        v[8 * h + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = i < n ? __uint_as_float((uint32_t)__ldg(p + i) << 16) : 0.f;
   }
 }
-template <bool VEC>
+template <int VB>
 __device__ __forceinline__ void load16(const float* p, int n, float (&v)[16]) {
-  if (VEC) {
+  if (VB == 32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[8] = {};
+      if (8 * h < n) load32(p + 8 * h, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * h + i] = __uint_as_float(w[i]);
+    }
+  } else if (VB == 16) {
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
       float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -143,6 +173,9 @@ __device__ __forceinline__ float swiglu(float g, float u) {
 
 // Eight values times r as E2M1 codes, value i in bits [4i, 4i + 4).
 __device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float r) {
+  float2 m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(r, r));
   uint32_t o;
   asm("{\n\t"
       ".reg .b8 b0, b1, b2, b3;\n\t"
@@ -153,8 +186,13 @@ __device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float r) {
       "mov.b32 %0, {b0, b1, b2, b3};\n\t"
       "}"
       : "=r"(o)
-      : "f"(v[0] * r), "f"(v[1] * r), "f"(v[2] * r), "f"(v[3] * r), "f"(v[4] * r), "f"(v[5] * r), "f"(v[6] * r),
-        "f"(v[7] * r));
+      : "f"(m[0].x), "f"(m[0].y), "f"(m[1].x), "f"(m[1].y), "f"(m[2].x), "f"(m[2].y), "f"(m[3].x), "f"(m[3].y));
+  return o;
+}
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float o;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(o) : "f"(a), "f"(b), "f"(c));
   return o;
 }
 
@@ -190,7 +228,7 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float* r) {
   return q;
 }
 
-template <typename E_, int FMT, int SRC, bool VEC>
+template <typename E_, int FMT, int SRC, int VB>
 __global__ void __launch_bounds__(kQThreads)
 quantize_kernel(const QuantParams p) {
   __shared__ Dest dest[kQDests];
@@ -215,16 +253,17 @@ quantize_kernel(const QuantParams p) {
     float v[16];
     if (SRC == kSwiglu) {
       float u[16];
-      load16<VEC>(x + row * 2 * p.cols + c, n, v);
-      load16<VEC>(x + row * 2 * p.cols + p.cols + c, n, u);
+      load16<VB>(x + row * 2 * p.cols + c, n, v);
+      load16<VB>(x + row * 2 * p.cols + p.cols + c, n, u);
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = swiglu(v[j], u[j]);
     } else {
-      load16<VEC>(x + row * p.cols + c, n, v);
+      load16<VB>(x + row * p.cols + c, n, v);
     }
-    uint32_t amax = 0;  // as bits: a NaN counts above infinity
+    float most = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7fffffffu);
+    for (int j = 0; j < 16; j += 2) most = max3_abs(most, v[j], v[j + 1]);
+    uint32_t amax = __float_as_uint(most);  // as bits a NaN counts above infinity
     if (FMT == MLR_FP4_MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     float r;
     uint32_t s;
@@ -274,9 +313,23 @@ struct DequantParams {
   void* out;
 };
 
+// Eight E2M1 codes as four pairs of halves (exact).
+__device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t (&f)[4]) {
+  asm("{\n\t"
+      ".reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t"
+      "}"
+      : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+      : "r"(w));
+}
+
 // value = (code x block scale) x tensor scale, rounded once to the output type
 // (code x block scale is exact).  Rows past the last expert's are zeros.
-template <typename O, int FMT, bool VEC>
+template <typename O, int FMT, int VB>
 __global__ void __launch_bounds__(kQThreads)
 dequantize_kernel(const DequantParams p) {
   __shared__ Dest src[kQDests];  // .scale as in the quantisation, .row: the matrix
@@ -327,35 +380,48 @@ dequantize_kernel(const DequantParams p) {
         if (p.tensor_scale != nullptr) ts = __ldg(p.tensor_scale + d.row);
       }
     }
-    float v[16];
+    float2 v[8];
+    const float2 s2 = make_float2(s, s), t2 = make_float2(ts, ts);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t w = h ? q.y : q.x;
+      uint32_t f[4];
+      from_e2m1x8(h ? q.y : q.x, f);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // E2M1 to fp32: sign, two exponent bits (bias 1), one fraction bit
-        const uint32_t m = (w >> (4 * j)) & 7u;
-        const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((m >> 1) + 126u) << 23 | (m & 1u) << 22);
-        const float z = __uint_as_float(__float_as_uint(a) | ((w >> (4 * j)) & 8u) << 28);
-        v[8 * h + j] = __fmul_rn(__fmul_rn(z, s), ts);
+      for (int j = 0; j < 4; ++j) {
+        v[4 * h + j] = __fmul2_rn(__half22float2(*reinterpret_cast<const __half2*>(&f[j])), s2);
+        if (FMT == MLR_FP4_NV) v[4 * h + j] = __fmul2_rn(v[4 * h + j], t2);
       }
     }
     O* o = out + row * p.cols + c;
     if constexpr (sizeof(O) == 4) {
-      if (VEC) {
+      if (VB == 32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[2 * j] = __float_as_uint(v[4 * h + j].x);
+            w[2 * j + 1] = __float_as_uint(v[4 * h + j].y);
+          }
+          if (8 * h < n) store32(o + 8 * h, w);
+        }
+      } else if (VB == 16) {
 #pragma unroll
         for (int h = 0; h < 4; ++h)
-          if (4 * h < n) reinterpret_cast<float4*>(o)[h] = make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
+          if (4 * h < n)
+            reinterpret_cast<float4*>(o)[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
       } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (j < n) o[j] = v[j];
+          if (j < n) o[j] = j & 1 ? v[j / 2].y : v[j / 2].x;
       }
     } else {
       uint32_t w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-      if (VEC) {
+      for (int j = 0; j < 8; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[j].y), "f"(v[j].x));
+      if (VB == 32) {
+        store32(o, w);
+      } else if (VB == 16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (8 * h < n) reinterpret_cast<uint4*>(o)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
@@ -385,13 +451,21 @@ bool dtype_ok(int32_t d) { return d == MLR_DTYPE_BF16 || d == MLR_DTYPE_F32; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int kMaxCols = 1 << 19;
 
+// The widest vector that divides a row and its base's address; one thread's 16
+// bf16 columns are 32 bytes, which one 32-byte access moves in whole sectors.
+int vector_bytes(const void* base, int64_t row_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(base) | (uintptr_t)row_bytes;
+  return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 0;
+}
+
 template <typename E_, int FMT, int SRC>
-int launch_quantize(const QuantParams& p, bool vec, cudaStream_t stream) {
+int launch_quantize(const QuantParams& p, int vb, cudaStream_t stream) {
   const int64_t blocks = ceil_div(p.rows, p.rpb);
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  const cudaError_t err =
-      vec ? launch_pdl(quantize_kernel<E_, FMT, SRC, true>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p)
-          : launch_pdl(quantize_kernel<E_, FMT, SRC, false>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p);
+  const dim3 grid((unsigned)blocks), block(kQThreads);
+  const cudaError_t err = vb == 32   ? launch_pdl(quantize_kernel<E_, FMT, SRC, 32>, grid, block, 0, stream, p)
+                          : vb == 16 ? launch_pdl(quantize_kernel<E_, FMT, SRC, 16>, grid, block, 0, stream, p)
+                                     : launch_pdl(quantize_kernel<E_, FMT, SRC, 0>, grid, block, 0, stream, p);
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MLR_ERR_CUDA;
@@ -415,12 +489,12 @@ int quantize(QuantParams& p, int32_t dtype, int32_t fmt, cudaStream_t stream) {
   p.block_bytes = (int64_t)atoms * kAtomBytes;
   p.rpb = rows_per_block(p.rows, p.nga, SRC == kTokens ? p.K : 1);
   p.ng_magic = (uint32_t)ceil_div(int64_t{1} << 32, p.nga);
-  const bool vec = (int64_t)p.cols * es % 16 == 0 && aligned16(p.x);
+  const int vb = vector_bytes(p.x, (int64_t)p.cols * es);
   if (dtype == MLR_DTYPE_BF16)
-    return fmt == MLR_FP4_MX ? launch_quantize<uint16_t, MLR_FP4_MX, SRC>(p, vec, stream)
-                             : launch_quantize<uint16_t, MLR_FP4_NV, SRC>(p, vec, stream);
-  return fmt == MLR_FP4_MX ? launch_quantize<float, MLR_FP4_MX, SRC>(p, vec, stream)
-                           : launch_quantize<float, MLR_FP4_NV, SRC>(p, vec, stream);
+    return fmt == MLR_FP4_MX ? launch_quantize<uint16_t, MLR_FP4_MX, SRC>(p, vb, stream)
+                             : launch_quantize<uint16_t, MLR_FP4_NV, SRC>(p, vb, stream);
+  return fmt == MLR_FP4_MX ? launch_quantize<float, MLR_FP4_MX, SRC>(p, vb, stream)
+                           : launch_quantize<float, MLR_FP4_NV, SRC>(p, vb, stream);
 }
 
 int check_quantize(int64_t cols, int32_t dtype, int32_t fmt, const float* tensor_scale) {
@@ -430,12 +504,13 @@ int check_quantize(int64_t cols, int32_t dtype, int32_t fmt, const float* tensor
 }
 
 template <typename O, int FMT>
-int launch_dequantize(const DequantParams& p, bool vec, cudaStream_t stream) {
+int launch_dequantize(const DequantParams& p, int vb, cudaStream_t stream) {
   const int64_t blocks = ceil_div(p.rows, p.rpb);
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  const cudaError_t err =
-      vec ? launch_pdl(dequantize_kernel<O, FMT, true>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p)
-          : launch_pdl(dequantize_kernel<O, FMT, false>, dim3((unsigned)blocks), dim3(kQThreads), 0, stream, p);
+  const dim3 grid((unsigned)blocks), block(kQThreads);
+  const cudaError_t err = vb == 32   ? launch_pdl(dequantize_kernel<O, FMT, 32>, grid, block, 0, stream, p)
+                          : vb == 16 ? launch_pdl(dequantize_kernel<O, FMT, 16>, grid, block, 0, stream, p)
+                                     : launch_pdl(dequantize_kernel<O, FMT, 0>, grid, block, 0, stream, p);
   if (err != cudaSuccess) {
     (void)cudaGetLastError();
     return MLR_ERR_CUDA;
@@ -553,10 +628,10 @@ extern "C" int moe_fp4_dequantize(const uint8_t* codes, const uint8_t* scales, c
   p.rpb = rows_per_block(p.rows, p.ng, 1);
   p.ng_magic = (uint32_t)ceil_div(int64_t{1} << 32, p.ng);
   p.out = out;
-  const bool vec = (int64_t)cols * es % 16 == 0 && aligned16(out);
+  const int vb = vector_bytes(out, (int64_t)cols * es);
   if (dtype == MLR_DTYPE_BF16)
-    return fmt == MLR_FP4_MX ? launch_dequantize<uint16_t, MLR_FP4_MX>(p, vec, stream)
-                             : launch_dequantize<uint16_t, MLR_FP4_NV>(p, vec, stream);
-  return fmt == MLR_FP4_MX ? launch_dequantize<float, MLR_FP4_MX>(p, vec, stream)
-                           : launch_dequantize<float, MLR_FP4_NV>(p, vec, stream);
+    return fmt == MLR_FP4_MX ? launch_dequantize<uint16_t, MLR_FP4_MX>(p, vb, stream)
+                             : launch_dequantize<uint16_t, MLR_FP4_NV>(p, vb, stream);
+  return fmt == MLR_FP4_MX ? launch_dequantize<float, MLR_FP4_MX>(p, vb, stream)
+                           : launch_dequantize<float, MLR_FP4_NV>(p, vb, stream);
 }

@@ -321,9 +321,13 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
 // The row gradients of a token's pairs and the dot products that are its
 // weights' gradients, by 2^lpt_log2 threads per token (per thread over its
 // columns in increasing order, then over lanes and warps in a fixed order).
-constexpr int kBackThreads = 256;
+// Bound by the bytes in flight: eight rows of a token are loaded at once, at
+// most 85 registers a thread for three blocks per SM.  8192 x 8 rows of 7168
+// bf16: 293 us at 85 registers, 530 at 110, 324 at 64 (spills); with 128
+// threads per token instead of 256, 4096 x 8 rows of 2048 take 48 instead of 53.
+constexpr int kBackThreads = 256, kBackLanes = 128;
 template <typename E_, int N, int KU>
-__global__ void __launch_bounds__(kBackThreads)
+__global__ void __launch_bounds__(kBackThreads, 3)
 unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos,
                           const float* __restrict__ w, int T, int K, int H, int nv, int lpt_log2,
                           E_* __restrict__ d_rows, float* __restrict__ dw, int32_t* d_status) {
@@ -461,7 +465,7 @@ int launch_unpermute(int K, A... a) {
 template <typename E_, int N, int KU>
 int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t* pos, const float* w, int T, int K,
                                 int H, void* d_rows, float* dw, int32_t* d_status, cudaStream_t stream) {
-  const int nv = H / N, lpt = row_threads(nv, kBackThreads);
+  const int nv = H / N, lpt = row_threads(nv, kBackLanes);
   if (launch_pdl(unpermute_backward_kernel<E_, N, KU>, dim3((unsigned)ceil_div(T, kBackThreads / lpt)),
                  dim3(kBackThreads), 0, stream, static_cast<const E_*>(dy), static_cast<const E_*>(rows), pos, w, T, K,
                  H, nv, log2_of(lpt), static_cast<E_*>(d_rows), dw, d_status) != cudaSuccess)
