@@ -111,10 +111,38 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// Rows that no vector divides: a warp's 32 groups of 16 columns go element by
+// element through shared memory, half a warp to a group, so that each access
+// covers whole sectors.  p: this lane's group, n its columns (none if <= 0).
+template <typename T>
+__device__ __forceinline__ void load_staged(const T* p, int n, T* stage /* [32][16], the warp's */, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int owner = 2 * i + (lane >> 4), j = lane & 15;
+    const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), owner));
+    const int m = __shfl_sync(0xffffffffu, n, owner);
+    stage[owner * 16 + j] = j < m ? __ldg(q + j) : T{};
+  }
+  __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ void store_staged(T* p, int n, const T* stage, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int owner = 2 * i + (lane >> 4), j = lane & 15;
+    T* q = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), owner));
+    const int m = __shfl_sync(0xffffffffu, n, owner);
+    if (j < m) q[j] = stage[owner * 16 + j];
+  }
+  __syncwarp();
+}
+
 // 16 columns of a row as fp32, zeros past the end.  VB: the bytes of a vector
-// that divide a row and the base's address (32, 16, or 0: single elements).
+// that divide a row and the base's address (32, 16, or 0: through `stage`).
 template <int VB>
-__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16]) {
+__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16], uint16_t* stage) {
   if (VB > 0) {
     uint32_t w[8] = {};
     if (VB == 32) {
@@ -136,12 +164,26 @@ __device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16])
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
+    const int lane = threadIdx.x & 31;
+    load_staged(p, n, stage, lane);
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? __uint_as_float((uint32_t)__ldg(p + i) << 16) : 0.f;
+    for (int h = 0; h < 2; ++h) {
+      const uint4 q = reinterpret_cast<const uint4*>(stage + lane * 16)[h];
+      w[4 * h] = q.x;
+      w[4 * h + 1] = q.y;
+      w[4 * h + 2] = q.z;
+      w[4 * h + 3] = q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
   }
 }
 template <int VB>
-__device__ __forceinline__ void load16(const float* p, int n, float (&v)[16]) {
+__device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], float* stage) {
   if (VB == 32) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -161,14 +203,46 @@ __device__ __forceinline__ void load16(const float* p, int n, float (&v)[16]) {
       v[4 * h + 3] = q.w;
     }
   } else {
+    const int lane = threadIdx.x & 31;
+    load_staged(p, n, stage, lane);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = i < n ? __ldg(p + i) : 0.f;
+    for (int h = 0; h < 4; ++h) {
+      const float4 q = reinterpret_cast<const float4*>(stage + lane * 16)[h];
+      v[4 * h] = q.x;
+      v[4 * h + 1] = q.y;
+      v[4 * h + 2] = q.z;
+      v[4 * h + 3] = q.w;
+    }
   }
 }
 
-// u * SiLU(g) with the roundings of the separate operations (no contraction).
-__device__ __forceinline__ float swiglu(float g, float u) {
-  return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.f, expf(-g))), u);
+// v[j] = u[j] * (v[j] / (1 + min(exp(-v[j]), 2^125))), each operation rounded to
+// fp32.
+//
+// The quotient g / d, d = 1 + exp(-g) >= 1, is one approximate reciprocal r and
+// one residual step with fused multiply-adds (Markstein's division): q = g r,
+// q + (g - d q) r, where g - d q is exact.  r is within 1 ulp, so the result is
+// the correctly rounded quotient but for about one in 10^6, which are one ulp
+// off.  It needs 1 / d to be a normal number, hence the bound on exp(-g): it
+// acts below g = -86.6, where g / d is under 3e-36 either way.  8192 x 8 rows of
+// 7168 bf16 take 584 us with __fdiv_rn, 406 us so; without any division or
+// exponential 300 us, what their bytes take.
+constexpr float kMaxExp = 0x1p125f;
+__device__ __forceinline__ void swiglu16(float (&v)[16], const float (&u)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    const float2 ng = make_float2(-v[j], -v[j + 1]);
+    const float2 d = __fadd2_rn(make_float2(fminf(expf(ng.x), kMaxExp), fminf(expf(ng.y), kMaxExp)),
+                                make_float2(1.f, 1.f));
+    float2 r;  // -1 / d
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-d.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-d.y));
+    const float2 q = __fmul2_rn(ng, r);
+    const float2 m = __ffma2_rn(d, q, ng);  // d q - g
+    const float2 h = __fmul2_rn(__ffma2_rn(m, r, q), make_float2(u[j], u[j + 1]));
+    v[j] = h.x;
+    v[j + 1] = h.y;
+  }
 }
 
 // Eight values times r as E2M1 codes, value i in bits [4i, 4i + 4).
@@ -228,10 +302,14 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float* r) {
   return q;
 }
 
+// Five blocks per SM (at most 51 registers): the exponentials of the SwiGLU form
+// need the warps (8192 x 8 rows of 7168: 406 us against 422 unbounded).
 template <typename E_, int FMT, int SRC, int VB>
-__global__ void __launch_bounds__(kQThreads)
+__global__ void __launch_bounds__(kQThreads, 5)
 quantize_kernel(const QuantParams p) {
   __shared__ Dest dest[kQDests];
+  __shared__ __align__(16) E_ stages[VB == 0 ? kQThreads * 16 : 1];
+  E_* stage = stages + (VB == 0 ? (threadIdx.x >> 5) * 512 : 0);
   pdl_wait();
   pdl_trigger();
   const int K = SRC == kTokens ? p.K : 1;
@@ -253,12 +331,11 @@ quantize_kernel(const QuantParams p) {
     float v[16];
     if (SRC == kSwiglu) {
       float u[16];
-      load16<VB>(x + row * 2 * p.cols + c, n, v);
-      load16<VB>(x + row * 2 * p.cols + p.cols + c, n, u);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = swiglu(v[j], u[j]);
+      load16<VB>(x + row * 2 * p.cols + c, n, v, stage);
+      load16<VB>(x + row * 2 * p.cols + p.cols + c, n, u, stage);
+      swiglu16(v, u);
     } else {
-      load16<VB>(x + row * p.cols + c, n, v);
+      load16<VB>(x + row * p.cols + c, n, v, stage);
     }
     float most = 0.f;
 #pragma unroll
@@ -355,18 +432,21 @@ dequantize_kernel(const DequantParams p) {
     src[i] = d;
   }
   __syncthreads();
+  __shared__ __align__(16) O stages[VB == 0 ? kQThreads * 16 : 1];
+  O* stage = stages + (VB == 0 ? (threadIdx.x >> 5) * 512 : 0);
   O* out = static_cast<O*>(p.out);
   const int total = nr * p.ng;
-  for (int i = threadIdx.x; i < total; i += kQThreads) {
-    const int lr = (int)__umulhi((uint32_t)i, p.ng_magic);
-    const int g = i - lr * p.ng;
+  for (int i0 = 0; i0 < total; i0 += kQThreads) {  // whole warps: they stage together
+    const int i = i0 + threadIdx.x;
+    const bool in = i < total;
+    const int lr = in ? (int)__umulhi((uint32_t)i, p.ng_magic) : 0;
+    const int g = in ? i - lr * p.ng : 0;
     const int64_t row = r0 + lr;
-    const int c = 16 * g, n = min(16, p.cols - c);
-    if (n <= 0) continue;
+    const int c = 16 * g, n = in ? min(16, p.cols - c) : 0;
     const Dest d = src[lr];
     float s = 0.f, ts = 1.f;
     uint2 q = make_uint2(0, 0);
-    if (d.scale >= 0) {
+    if (d.scale >= 0 && n > 0) {
       q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * p.pitch + 8 * g));
       const int b = FMT == MLR_FP4_MX ? g / 2 : g;
       const uint32_t sb = __ldg(p.scales + d.scale + (int64_t)(b / 4) * kAtomBytes + b % 4);
@@ -411,39 +491,50 @@ dequantize_kernel(const DequantParams p) {
           if (4 * h < n)
             reinterpret_cast<float4*>(o)[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
       } else {
+        float4* mine = reinterpret_cast<float4*>(stage + (threadIdx.x & 31) * 16);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < n) o[j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+        for (int h = 0; h < 4; ++h) mine[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+        store_staged(o, n, stage, threadIdx.x & 31);
       }
     } else {
       uint32_t w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[j].y), "f"(v[j].x));
       if (VB == 32) {
-        store32(o, w);
+        if (n > 0) store32(o, w);
       } else if (VB == 16) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (8 * h < n) reinterpret_cast<uint4*>(o)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
       } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (j < n) o[j] = (O)(w[j / 2] >> (16 * (j % 2)));
+        uint4* mine = reinterpret_cast<uint4*>(stage + (threadIdx.x & 31) * 16);
+        mine[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        mine[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        store_staged(o, n, stage, threadIdx.x & 31);
       }
     }
   }
 }
 
 // ------------------------------------------------------------------ host side --
-// Source rows per block: about four passes of the block, fewer when that would
-// leave SMs without a block, and at most kQDests destinations.
+// Source rows per block: of at most eight passes of the block (and few enough
+// to leave every SM its blocks, at most kQDests destinations) the count that
+// leaves the fewest threads idle in the last pass.
 int rows_per_block(int64_t rows, int groups, int K) {
-  int64_t r = ceil_div(4 * kQThreads, groups);
-  const int64_t spread = ceil_div(rows, 4 * 152);
-  if (r > spread) r = spread;
-  if (r > kQDests / K) r = kQDests / K;
-  if (r > 65535 / groups) r = 65535 / groups;  // the row division by multiplication holds below 2^16
-  return r < 1 ? 1 : (int)r;
+  int64_t most = 8 * kQThreads / groups;
+  const int64_t spread = ceil_div(rows, 16 * 152);
+  if (most > spread) most = spread;
+  if (most > kQDests / K) most = kQDests / K;
+  int best = 1;
+  double used = 0;
+  for (int r = 1; r <= most; ++r) {
+    const double u = (double)(r * groups) / (double)round_up(r * groups, kQThreads);
+    if (u >= used - 0.01) {  // of equals the larger: the destinations are looked up once per block
+      used = u > used ? u : used;
+      best = r;
+    }
+  }
+  return best;
 }
 
 bool fmt_ok(int32_t fmt) { return fmt == MLR_FP4_MX || fmt == MLR_FP4_NV; }
