@@ -95,6 +95,7 @@ struct Params {
 struct Item {
   int e, row0, rows;  // expert, first sorted row, rows of the tile
   int sblk;           // 128-row scale block of row0
+  int sf0;            // where row0 begins in that block: TMEM columns of 32 rows
   int n0;             // first output
 };
 
@@ -114,6 +115,7 @@ __device__ __forceinline__ Item item_of(const Params& p, const Ctl& c, int item)
   it.row0 = o0 + j0;
   it.rows = min(NT, o1 - it.row0);
   it.sblk = o0 / 128 + lo + j0 / 128;
+  it.sf0 = j0 % 128 / 32;
   it.n0 = (item - t * p.nblk) * 128;
   return it;
 }
@@ -132,6 +134,7 @@ struct ItemWalk {
     it.row0 = __shfl_sync(0xffffffffu, mine.row0, i & 31);
     it.rows = __shfl_sync(0xffffffffu, mine.rows, i & 31);
     it.sblk = __shfl_sync(0xffffffffu, mine.sblk, i & 31);
+    it.sf0 = __shfl_sync(0xffffffffu, mine.sf0, i & 31);
     it.n0 = __shfl_sync(0xffffffffu, mine.n0, i & 31);
     return it;
   }
@@ -324,7 +327,8 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
-      const int rows = walk.at(p, c, il, n_items, lane).rows;
+      const Item it = walk.at(p, c, il, n_items, lane);
+      const int rows = it.rows;
       const int b = il & 1;
       ok = mbar_wait(&c.acc_empty[b], ((il >> 1) & 1) ^ 1, abort, p.wait_ns);
       if (Sh::kShared > 0 && il > 0)
@@ -344,7 +348,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         tc_fence_after();
         const uint32_t sb = sb0 + st * Sh::kStride;
         const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
-        const uint32_t ta = tw + 4 * Sh::kAtoms;
+        const uint32_t ta = tw + 4 * Sh::kAtoms + it.sf0;
         const int nm = (p.cols - k * kKStep + 63) / 64;
         if (elect_one()) {
 #pragma unroll

@@ -237,6 +237,19 @@ def test_product_with_empty_experts(cuda_device, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [65, 128, 129, 192, 200, 257, 700])
+def test_product_with_one_long_expert(cuda_device, fmt, rows):
+    """Few rows per expert on average, many for one: its row tiles begin inside
+    the 128-row blocks of its scales."""
+    E = 40
+    ids = torch.cat([torch.arange(E), torch.full((rows,), 7)]).to(torch.int32).cuda().view(-1, 1)
+    pos, off = pm.moe_sort_pairs(ids, E)
+    x = randn(ids.shape[0], 320, seed=rows)
+    w = randn(E, 136, 320, seed=rows + 1)
+    check_product(off, *fp4.fp4_quantize_permuted(x, ids, pos, off, fmt), *fp4.fp4_quantize(w, fmt), None, None, 320, fmt)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("T,E,N,C", [(1, 1, 256, 4096), (33, 2, 300, 1000), (400, 1, 130, 544), (1000, 3, 257, 2048)])
 def test_product_exact_sums(cuda_device, fmt, T, E, N, C):
     """Scales 2^-1..2^1 and codes give products that are multiples of 2^-4 and
