@@ -516,7 +516,8 @@ int32_t moe_lora_deterministic(void);
  *   rows [P, hidden], y and dy [num_tokens, hidden] of type `dtype`; weights float32 [P].
  * A pair_pos beyond P sets MLR_STATUS_INDEX and is skipped.  Results are
  * bit-identical between runs.
- * Limits: topk <= 256 and num_experts <= 16384 (moe_permute), P < 2^31.
+ * Limits: topk <= 256 and num_experts <= 16384 (moe_permute), hidden <= 2^24,
+ *   P < 2^31 - 1.
  */
 size_t moe_permute_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts);
 int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_tokens, int32_t topk, int32_t hidden,
@@ -561,7 +562,7 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *   as moe_permute leaves them); tensor_scale null or [1].  A masked pair's
  *   row has zero codes.  Limit: topk <= 512.
  * moe_fp4_quantize_swiglu: sorted rows [num_rows, 2 cols], gate then up, to
- *   the codes of up * gate / (1 + exp(-gate)), all in fp32.  Rows past
+ *   the codes of up * gate / (1 + min(exp(-gate), 2^125)), all in fp32.  Rows past
  *   expert_offsets[num_experts] have zero codes.
  * moe_fp4_dequantize: (code * block scale) * tensor scale, rounded once to
  *   `dtype`.  expert_offsets null: a stack of num_matrices; else sorted rows of

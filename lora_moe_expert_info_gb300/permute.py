@@ -20,6 +20,7 @@ import ctypes
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _check_device, _check_host, _on_stream, _req, _stream_number, library
 
@@ -220,6 +221,7 @@ class MoePermute(torch.autograd.Function):
         return rows, pair_pos, expert_offsets
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_rows, *_):
         return moe_permute_backward(d_rows.contiguous(), *ctx.saved_tensors), None, None
 
@@ -233,6 +235,7 @@ class MoeUnpermute(torch.autograd.Function):
         return moe_unpermute(rows, pair_pos, topk_weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         d_rows, d_weights = moe_unpermute_backward(dy.contiguous(), *ctx.saved_tensors)
         return d_rows, None, d_weights
