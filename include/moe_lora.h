@@ -506,7 +506,8 @@ int32_t moe_lora_deterministic(void);
  *   pair_pos        out [P]: pos(p), or ~pos(p) (negative) for a masked pair
  *   expert_offsets  out [num_experts + 1]: first row of each expert, then the
  *                   number of rows that belong to one
- *   workspace       moe_permute_workspace_bytes(...), 256-byte aligned
+ *   workspace       moe_permute_workspace_bytes(...), 256-byte aligned; null is
+ *                   taken where that is 1 (up to 8192 pairs, sorted in one launch)
  * moe_unpermute: y[t] = sum_k topk_weights[t, k] * rows[pos(t, k)], in
  *   increasing k, in fp32; topk_weights null: weights of 1, which is the
  *   gradient of moe_permute (rows = the gradient of its rows).

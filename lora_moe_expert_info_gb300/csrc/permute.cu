@@ -56,7 +56,7 @@ SortPlan sort_plan(int32_t T, int32_t K, int32_t E) {
   s.tpb = (int)(want < 1 ? 1 : want > most ? most : want);
   s.G = ceil_div(T, s.tpb);
   s.o_tot = round_up((int64_t)(E + 1) * s.G * 4, 256);
-  s.bytes = s.one ? 256 : s.o_tot + round_up((int64_t)(E + 1) * 4, 256);
+  s.bytes = s.one ? 1 : s.o_tot + round_up((int64_t)(E + 1) * 4, 256);  // one launch: nothing is kept
   s.ok = true;
   s.code = MLR_OK;
   return s;
@@ -342,6 +342,30 @@ __device__ __forceinline__ uint4 load_piece(const char* a, const E_* base, const
   }
   return q;
 }
+// How a thread takes 16 bytes of a row.  kWhole: rows and bases are multiples of
+// 16 bytes.  kPieces (bf16 rows off that grid): in the two aligned pieces that
+// they lie in, the second one mostly from L1, and shifted.  kStrided (float32
+// rows off it): four elements a row of threads apart, each access of a warp
+// being 128 bytes in a row.
+enum RowAccess { kWhole, kPieces, kStrided };
+template <typename E_> constexpr RowAccess kOffGrid = sizeof(E_) == 2 ? kPieces : kStrided;
+
+// Elements c, c + step, ... of a row of H float32, zeros past its end; and back.
+__device__ __forceinline__ uint4 load_strided(const float* r, int c, int step, int H) {
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = c + i * step < H ? __ldg(r + c + i * step) : 0.f;
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ uint4 load_strided(const uint16_t*, int, int, int) { return make_uint4(0, 0, 0, 0); }
+__device__ __forceinline__ void store_strided(float* r, int c, int step, int H, const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i * step < H) r[c + i * step] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void store_strided(uint16_t*, int, int, int, const uint4&) {}
+
 // Bytes s to s + 16 of a and b one after the other (s a multiple of the element).
 template <typename E_>
 __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) {
@@ -365,11 +389,9 @@ int row_threads(int nv, int most) {
 
 // y[t] = sum_k w[t, k] rows[pos]; w == nullptr: w = 1 (the gradient of permute).
 // One thread per 16 bytes of a token; KU rows are loaded before any is added,
-// without branches, so that their loads are in flight together.  ALIGNED: rows
-// and bases are multiples of 16 bytes; else each row is read in the two aligned
-// pieces that its 16 bytes lie in (the second one mostly from L1) and shifted.
+// without branches, so that their loads are in flight together.
 constexpr int kSumThreads = 128;
-template <typename E_, int KU, bool ALIGNED>
+template <typename E_, int KU, RowAccess A>
 __global__ void __launch_bounds__(kSumThreads)
 unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos, const float* __restrict__ w, int T,
                  int K, int H, int lpt_log2, unsigned col_blocks, E_* __restrict__ y, int32_t* d_status) {
@@ -378,15 +400,16 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
   pdl_trigger();
   const unsigned tb = blockIdx.x / col_blocks, cb = blockIdx.x - tb * col_blocks;
   const int64_t t = ((int64_t)tb << (7 - lpt_log2)) + (threadIdx.x >> lpt_log2);
-  const int c = ((int)(cb << lpt_log2) + (threadIdx.x & ((1 << lpt_log2) - 1))) * N;  // first column
+  const int lpt = 1 << lpt_log2, lt = threadIdx.x & (lpt - 1);
+  const int c = A == kStrided ? (int)cb * N * lpt + lt : ((int)cb * lpt + lt) * N;  // first column
   if (t >= T || c >= H) return;
   const int64_t P = (int64_t)T * K;
   float acc[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) acc[j] = 0.f;
   for (int k0 = 0; k0 < K; k0 += KU) {
-    uint4 v[KU], v2[ALIGNED ? 1 : KU];
-    int shift[ALIGNED ? 1 : KU];
+    uint4 v[KU], v2[A == kPieces ? KU : 1];
+    int shift[A == kPieces ? KU : 1];
     float wk[KU];
 #pragma unroll
     for (int j = 0; j < KU; ++j) {
@@ -396,8 +419,10 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
       if (q >= P) set_status(d_status, MLR_STATUS_INDEX);
       wk[j] = !use ? 0.f : w != nullptr ? __ldg(w + p) : 1.f;
       const E_* r = rows + (int64_t)q * H + c;
-      if constexpr (ALIGNED) {
+      if constexpr (A == kWhole) {
         v[j] = use ? __ldg(reinterpret_cast<const uint4*>(r)) : make_uint4(0, 0, 0, 0);
+      } else if constexpr (A == kStrided) {
+        v[j] = load_strided(rows + (int64_t)q * H, c, lpt, use ? H : 0);
       } else {
         const int s = (int)(reinterpret_cast<uintptr_t>(r) & 15);
         const char* a = reinterpret_cast<const char*>(r) - s;
@@ -410,8 +435,8 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
 #pragma unroll
     for (int j = 0; j < KU; ++j) {
       float f[N];
-      if constexpr (ALIGNED) widen(v[j], f);
-      else widen(shifted<E_>(v[j], v2[j], shift[j]), f);
+      if constexpr (A == kPieces) widen(shifted<E_>(v[j], v2[j], shift[j]), f);
+      else widen(v[j], f);
 #pragma unroll
       for (int u = 0; u < N; ++u) acc[u] = fmaf(wk[j], f[u], acc[u]);
     }
@@ -419,8 +444,10 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
   uint4 o;
   narrow(acc, o);
   E_* out = y + t * H + c;
-  if constexpr (ALIGNED) {
+  if constexpr (A == kWhole) {
     *reinterpret_cast<uint4*>(out) = o;
+  } else if constexpr (A == kStrided) {
+    store_strided(y + t * H, c, lpt, H, o);
   } else {
     const E_* e = reinterpret_cast<const E_*>(&o);
 #pragma unroll
@@ -485,7 +512,7 @@ __device__ __forceinline__ Pair load_pair(const int32_t* __restrict__ pair_pos, 
   return o;
 }
 
-template <typename E_, int KU>
+template <typename E_, int KU, RowAccess A>
 __global__ void __launch_bounds__(kBackThreads, 3)
 unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos,
                           const float* __restrict__ w, int T, int K, int H, int lpt_log2, E_* __restrict__ d_rows,
@@ -506,14 +533,20 @@ unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows
       dot[j] = 0.f;
     }
     if (in)
-      for (int c = lt * N; c < H; c += lpt * N) {
+      for (int c = A == kStrided ? lt : lt * N; c < H; c += lpt * N) {
         uint4 v[KU];
         float g[N];
-        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(dy + t * H + c));
+        uint4 gv;
+        if constexpr (A == kStrided) gv = load_strided(dy + t * H, c, lpt, H);
+        else gv = __ldg(reinterpret_cast<const uint4*>(dy + t * H + c));
 #pragma unroll
-        for (int j = 0; j < KU; ++j)
-          v[j] = pr[j].use ? __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pr[j].row * H + c))
-                           : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < KU; ++j) {
+          if constexpr (A == kStrided)
+            v[j] = load_strided(rows + (int64_t)pr[j].row * H, c, lpt, pr[j].use ? H : 0);
+          else
+            v[j] = pr[j].use ? __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pr[j].row * H + c))
+                             : make_uint4(0, 0, 0, 0);
+        }
         widen(gv, g);
 #pragma unroll
         for (int j = 0; j < KU; ++j) {
@@ -526,14 +559,18 @@ unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows
           }
           uint4 ov;
           narrow(o, ov);
-          if (pr[j].row >= 0) *reinterpret_cast<uint4*>(d_rows + (int64_t)pr[j].row * H + c) = ov;
+          if constexpr (A == kStrided) {
+            store_strided(d_rows + (int64_t)pr[j].row * H, c, lpt, pr[j].row >= 0 ? H : 0, ov);
+          } else {
+            if (pr[j].row >= 0) *reinterpret_cast<uint4*>(d_rows + (int64_t)pr[j].row * H + c) = ov;
+          }
         }
       }
     store_dots<KU>(dot, part, lpt, lt, in, t, K, k0, dw);
   }
 }
 
-// The same for rows off the 16-byte grid: each row of d_rows is written in its
+// The same for bf16 rows off the 16-byte grid: each row of d_rows is written in its
 // own aligned 16-byte pieces, with the row of rows (in the same pieces, unless
 // the two bases differ) and the token's dy from shared memory at the piece's
 // columns; the ends that share 16 bytes with another row go element by element.
@@ -670,13 +707,13 @@ int log2_of(int n) {
   return l;
 }
 
-template <typename E_, int KU, bool ALIGNED>
+template <typename E_, int KU, RowAccess A>
 int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int T, int K, int H, void* y,
                        int32_t* d_status, cudaStream_t stream) {
   const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16), lpt = row_threads(nv, kSumThreads);
   const int64_t col_blocks = ceil_div(nv, lpt), blocks = ceil_div(T, kSumThreads / lpt) * col_blocks;
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  if (launch_pdl(unpermute_kernel<E_, KU, ALIGNED>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
+  if (launch_pdl(unpermute_kernel<E_, KU, A>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
                  static_cast<const E_*>(rows), pos, w, T, K, H, log2_of(lpt), (unsigned)col_blocks,
                  static_cast<E_*>(y), d_status) != cudaSuccess)
     return MLR_ERR_CUDA;
@@ -685,26 +722,27 @@ int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int
 }
 
 // Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds K, so that
-// few experts per token cost no empty turns; at most 4 of unaligned rows, which
-// take twice the registers.
-template <typename E_, typename... A>
-int launch_unpermute(bool aligned, int K, A... a) {
-  if (!aligned)
-    return K == 1 ? launch_unpermute_k<E_, 1, false>(a...) : K == 2 ? launch_unpermute_k<E_, 2, false>(a...)
-                                                                    : launch_unpermute_k<E_, 4, false>(a...);
-  return K == 1 ? launch_unpermute_k<E_, 1, true>(a...) : K == 2 ? launch_unpermute_k<E_, 2, true>(a...)
-         : K <= 4 ? launch_unpermute_k<E_, 4, true>(a...) : launch_unpermute_k<E_, 8, true>(a...);
+// few experts per token cost no empty turns; at most 4 of rows off the grid,
+// which take more registers or loads.
+template <typename E_, typename... Args>
+int launch_unpermute(bool whole, int K, Args... a) {
+  constexpr RowAccess O = kOffGrid<E_>;
+  if (!whole)
+    return K == 1 ? launch_unpermute_k<E_, 1, O>(a...) : K == 2 ? launch_unpermute_k<E_, 2, O>(a...)
+                                                                : launch_unpermute_k<E_, 4, O>(a...);
+  return K == 1 ? launch_unpermute_k<E_, 1, kWhole>(a...) : K == 2 ? launch_unpermute_k<E_, 2, kWhole>(a...)
+         : K <= 4 ? launch_unpermute_k<E_, 4, kWhole>(a...) : launch_unpermute_k<E_, 8, kWhole>(a...);
 }
 
-template <typename E_, int KU, bool ALIGNED>
+template <typename E_, int KU, RowAccess A>
 int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t* pos, const float* w, int T, int K,
                                 int H, void* d_rows, float* dw, int32_t* d_status, cudaStream_t stream) {
   const E_ *dyp = static_cast<const E_*>(dy), *rp = static_cast<const E_*>(rows);
   E_* dp = static_cast<E_*>(d_rows);
   cudaError_t err;
-  if (ALIGNED) {
+  if constexpr (A != kPieces) {
     const int lpt = row_threads((int)ceil_div((int64_t)H * sizeof(E_), 16), kBackLanes);
-    err = launch_pdl(unpermute_backward_kernel<E_, KU>, dim3((unsigned)ceil_div(T, kBackThreads / lpt)),
+    err = launch_pdl(unpermute_backward_kernel<E_, KU, A>, dim3((unsigned)ceil_div(T, kBackThreads / lpt)),
                      dim3(kBackThreads), 0, stream, dyp, rp, pos, w, T, K, H, log2_of(lpt), dp, dw, d_status);
   } else {
     auto run = [&](auto kernel, int threads) {
@@ -717,10 +755,14 @@ int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t*
   note_launch();
   return MLR_OK;
 }
-template <typename E_, bool ALIGNED, typename... A>
-int launch_unpermute_backward(int K, A... a) {
-  return K == 1 ? launch_unpermute_backward_k<E_, 1, ALIGNED>(a...) : K == 2 ? launch_unpermute_backward_k<E_, 2, ALIGNED>(a...)
-         : K <= 4 || !ALIGNED ? launch_unpermute_backward_k<E_, 4, ALIGNED>(a...) : launch_unpermute_backward_k<E_, 8, ALIGNED>(a...);
+template <typename E_, typename... Args>
+int launch_unpermute_backward(bool whole, int K, Args... a) {
+  constexpr RowAccess O = kOffGrid<E_>;
+  if (!whole)
+    return K == 1 ? launch_unpermute_backward_k<E_, 1, O>(a...) : K == 2 ? launch_unpermute_backward_k<E_, 2, O>(a...)
+                                                                         : launch_unpermute_backward_k<E_, 4, O>(a...);
+  return K == 1 ? launch_unpermute_backward_k<E_, 1, kWhole>(a...) : K == 2 ? launch_unpermute_backward_k<E_, 2, kWhole>(a...)
+         : K <= 4 ? launch_unpermute_backward_k<E_, 4, kWhole>(a...) : launch_unpermute_backward_k<E_, 8, kWhole>(a...);
 }
 
 // Common checks of the row operators; the row size in *es.
@@ -757,7 +799,7 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
     return cudaMemsetAsync(expert_offsets, 0, (size_t)(num_experts + 1) * 4, stream) == cudaSuccess ? MLR_OK
                                                                                                      : MLR_ERR_CUDA;
   if (topk_ids == nullptr || pair_pos == nullptr) return MLR_ERR_INVALID;
-  if (workspace == nullptr || ws_bytes < (size_t)s.bytes) return MLR_ERR_CAPACITY;
+  if (!(s.one && workspace == nullptr) && (workspace == nullptr || ws_bytes < (size_t)s.bytes)) return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
   char* ws = static_cast<char*>(workspace);
   if (!s.one) {
@@ -817,9 +859,7 @@ extern "C" int moe_unpermute_backward(const void* dy, const void* rows, const in
   if (pair_pos == nullptr || topk_weights == nullptr || d_weights == nullptr) return MLR_ERR_INVALID;
   const bool al = (int64_t)hidden * es % 16 == 0 && aligned_to(dy, 16) && aligned_to(rows, 16) && aligned_to(d_rows, 16);
   const int T = num_tokens, K = topk, H = hidden;
-  if (dtype == MLR_DTYPE_F32)
-    return al ? launch_unpermute_backward<float, true>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
-              : launch_unpermute_backward<float, false>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
-  return al ? launch_unpermute_backward<uint16_t, true>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
-            : launch_unpermute_backward<uint16_t, false>(K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
+  return dtype == MLR_DTYPE_F32
+             ? launch_unpermute_backward<float>(al, K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream)
+             : launch_unpermute_backward<uint16_t>(al, K, dy, rows, pair_pos, topk_weights, T, K, H, d_rows, d_weights, d_status, stream);
 }

@@ -96,14 +96,15 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
         raise ValueError(f"{fn}: unsupported sizes")
     pair_pos = _out(pair_pos, "pair_pos", (T, K), torch.int32, dev)
     expert_offsets = _out(expert_offsets, "expert_offsets", (E + 1,), torch.int32, dev)
-    if workspace is None:
+    if workspace is None and wsb > 1:
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     # an empty tensor has no address: rows of no columns are only sorted
     copy = H > 0
     code = lib.moe_permute(x.data_ptr() if copy else None, topk_ids.data_ptr(), T, K, H, E, dtype,
                            rows.data_ptr() if copy else None, pair_pos.data_ptr(), expert_offsets.data_ptr(),
-                           workspace.data_ptr(), workspace.numel(), _address(status), _stream_number(stream))
+                           _address(workspace), 0 if workspace is None else workspace.numel(), _address(status),
+                           _stream_number(stream))
     _check_host(code, fn)
     if check:
         _check_device(status, fn)
