@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kSortThreads = 256;
 constexpr int kChunkPairs = 256;     // pairs of one block, ranked by comparison in shared memory
+constexpr int kCountChunks = 8;      // chunks counted by one block, a warp each
 constexpr int kMaxSortTopk = 256;    // one token's pairs fit a chunk
 constexpr int kMaxSortExperts = 16384;
 constexpr int kMaxHidden = 1 << 24;
@@ -33,7 +34,7 @@ struct SortPlan {
   int code;
   int64_t P;
   int tpb;        // tokens per block
-  int64_t G;      // blocks (chunks)
+  int64_t G, Gp;  // blocks (chunks), and their number rounded up to whole 32-byte sectors of counts
   bool one;       // a single launch
   int64_t o_tot;  // workspace: counts [E+1][G], then totals [E+1]
   int64_t bytes;
@@ -55,7 +56,8 @@ SortPlan sort_plan(int32_t T, int32_t K, int32_t E) {
   const int most = kChunkPairs / K;
   s.tpb = (int)(want < 1 ? 1 : want > most ? most : want);
   s.G = ceil_div(T, s.tpb);
-  s.o_tot = round_up((int64_t)(E + 1) * s.G * 4, 256);
+  s.Gp = round_up(s.G, kCountChunks);
+  s.o_tot = round_up((int64_t)(E + 1) * s.Gp * 4, 256);
   s.bytes = s.one ? 1 : s.o_tot + round_up((int64_t)(E + 1) * 4, 256);  // one launch: nothing is kept
   s.ok = true;
   s.code = MLR_OK;
@@ -91,35 +93,50 @@ __device__ void block_scan(int* s, int n) {
   __syncthreads();
 }
 
-// Counts of one chunk's pairs per expert (masked pairs as expert E):
-// cnt[e][g].
+// Counts of eight chunks' pairs per expert (masked pairs as expert E), a warp
+// per chunk: cnt[e][g], whole sectors at a time.  WIDE: the histograms of eight
+// warps fit shared memory; else the chunks are counted one after another.
+template <bool WIDE>
 __global__ void __launch_bounds__(kSortThreads)
-sort_count_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int chunk, int64_t G, int32_t* __restrict__ cnt) {
-  extern __shared__ int hist[];  // [E + 1]
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) hist[e] = 0;
+sort_count_kernel(const int32_t* __restrict__ ids, int64_t P, int E, int chunk, int64_t Gp, int32_t* __restrict__ cnt) {
+  extern __shared__ int hist[];  // [WIDE ? 8 : 1][E + 1]
+  constexpr int kHist = WIDE ? kCountChunks : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  __syncthreads();
-  const int64_t p = (int64_t)blockIdx.x * chunk + threadIdx.x;
-  if ((int)threadIdx.x < chunk && p < P) atomicAdd(&hist[sort_key(__ldg(ids + p), E)], 1);
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kSortThreads) cnt[(int64_t)e * G + blockIdx.x] = hist[e];
+  for (int c0 = 0; c0 < kCountChunks; c0 += kHist) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kHist * (E + 1); i += kSortThreads) hist[i] = 0;
+    __syncthreads();
+    const int64_t g = (int64_t)blockIdx.x * kCountChunks + c0 + (WIDE ? warp : 0);
+    int* h = hist + (WIDE ? warp * (E + 1) : 0);
+    for (int i = WIDE ? lane : threadIdx.x; i < chunk; i += WIDE ? 32 : kSortThreads) {
+      const int64_t p = g * chunk + i;
+      if (p < P) atomicAdd(&h[sort_key(__ldg(ids + p), E)], 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kHist * (E + 1); i += kSortThreads) {
+      const int e = i / kHist, c = i - e * kHist;
+      cnt[(int64_t)e * Gp + (int64_t)blockIdx.x * kCountChunks + c0 + c] = hist[c * (E + 1) + e];
+    }
+  }
 }
 
-// One block per expert: the exclusive scan of its chunk counts, in place, and
-// its total.
+// One block per expert: the exclusive scan of its chunk counts, in place, four
+// to a thread, and its total.
 __global__ void __launch_bounds__(kSortThreads)
-sort_scan_kernel(int32_t* __restrict__ cnt, int64_t G, int32_t* __restrict__ tot) {
+sort_scan_kernel(int32_t* __restrict__ cnt, int64_t Gp, int32_t* __restrict__ tot) {
   __shared__ int warp_tot[kSortThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t* c = cnt + (int64_t)blockIdx.x * G;
+  int4* c = reinterpret_cast<int4*>(cnt + (int64_t)blockIdx.x * Gp);
   pdl_wait();
   pdl_trigger();
   int carry = 0;
-  for (int64_t g0 = 0; g0 < G; g0 += kSortThreads) {
+  for (int64_t g0 = 0; g0 < Gp / 4; g0 += kSortThreads) {
     const int64_t g = g0 + threadIdx.x;
-    const int v = g < G ? c[g] : 0;
-    int inc = v;
+    const int4 v = g < Gp / 4 ? c[g] : make_int4(0, 0, 0, 0);
+    const int mine = v.x + v.y + v.z + v.w;
+    int inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
@@ -127,13 +144,12 @@ sort_scan_kernel(int32_t* __restrict__ cnt, int64_t G, int32_t* __restrict__ tot
     }
     if (lane == 31) warp_tot[warp] = inc;
     __syncthreads();
-    int before = carry, all = 0;
+    int run = carry + inc - mine;
     for (int w = 0; w < kSortThreads / 32; ++w) {
-      if (w < warp) before += warp_tot[w];
-      all += warp_tot[w];
+      if (w < warp) run += warp_tot[w];
+      carry += warp_tot[w];
     }
-    if (g < G) c[g] = before + inc - v;
-    carry += all;
+    if (g < Gp / 4) c[g] = make_int4(run, run + v.x, run + v.x + v.y, run + v.x + v.y + v.z);
     __syncthreads();
   }
   if (threadIdx.x == 0) tot[blockIdx.x] = carry;
@@ -202,14 +218,15 @@ __device__ void copy_unaligned(const char* __restrict__ src, int64_t bytes, char
 // Places the pairs of one chunk of tokens and copies this block's column slice
 // of their rows.  The rank of a pair inside the chunk is the number of earlier
 // chunk pairs with the same key, counted by comparison.  VB: 16 where rows and
-// bases are multiples of 16 bytes, else the element's size.
+// bases are multiples of 16 bytes, 32 for long ones of them, else the element's
+// size.
 template <int VB> struct CopyElement;
 template <> struct CopyElement<4> { using type = uint32_t; };
 template <> struct CopyElement<2> { using type = uint16_t; };
 
 template <int VB, bool ONE>
 __global__ void __launch_bounds__(kSortThreads)
-permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int T, int K, int E, int tpb, int64_t G,
+permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int T, int K, int E, int tpb, int64_t Gp,
                int64_t row_bytes /* 0: sort only */, void* __restrict__ rows,
                int32_t* __restrict__ pair_pos, int32_t* __restrict__ offsets, const int32_t* __restrict__ cnt,
                const int32_t* __restrict__ tot, int32_t* d_status) {
@@ -250,7 +267,7 @@ permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int 
   if (tid < np) {
     int r = 0;
     for (int j = 0; j < tid; ++j) r += key[j] == mine;
-    r += start[mine] + (ONE ? before[mine] : __ldg(cnt + (int64_t)mine * G + blockIdx.x));
+    r += start[mine] + (ONE ? before[mine] : __ldg(cnt + (int64_t)mine * Gp + blockIdx.x));
     const int at = mine == E ? ~r : r;
     place[tid] = at;
     if (blockIdx.y == 0) pair_pos[p0 + tid] = at;
@@ -259,8 +276,7 @@ permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int 
     for (int e = tid; e <= E; e += kSortThreads) offsets[e] = start[e];
   if (row_bytes == 0) return;
   __syncthreads();
-  // one warp per token and pass: each piece of its row is read once and
-  // written to its K rows
+  // each piece of a token's row is read once and written to its K rows
   const int lane = tid & 31, warp = tid >> 5;
   if constexpr (VB < 16) {
     using V = typename CopyElement<VB>::type;
@@ -270,13 +286,17 @@ permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int 
                         place + i * K, K, seg[warp], blockIdx.y, gridDim.y, lane);
   } else {
     const int64_t nvec = row_bytes / 16;
+    // a warp per token, or for long rows the block, so that their copies are
+    // written in long runs (8192 x 8 rows of 14 KB: 183 us, by warps 197;
+    // 16384 x 4 rows of 2 KB: 50 us, by warps 38)
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* rv = static_cast<uint4*>(rows);
-    const int64_t step = (int64_t)gridDim.y * 32;
-    for (int i = warp; i < nt; i += kSortThreads / 32) {
+    constexpr int kLanes = VB == 32 ? kSortThreads : 32;
+    const int64_t step = (int64_t)gridDim.y * kLanes;
+    for (int i = tid / kLanes; i < nt; i += kSortThreads / kLanes) {
       const uint4* src = xv + (t0 + i) * nvec;
       const int* pl = place + i * K;
-      for (int64_t c = (int64_t)blockIdx.y * 32 + lane; c < nvec; c += 4 * step) {
+      for (int64_t c = (int64_t)blockIdx.y * kLanes + tid % kLanes; c < nvec; c += 4 * step) {
         uint4 v[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -692,7 +712,7 @@ int launch_permute(const SortPlan& s, const void* x, const int32_t* ids, int T, 
     if (smem > 24 * 1024 &&  // with the segments past the 48 KB that need no opt-in
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
       return MLR_ERR_CUDA;
-    if (launch_pdl(kernel, grid, dim3(kSortThreads), smem, stream, x, ids, T, K, E, s.tpb, s.G, row_bytes, rows, pair_pos,
+    if (launch_pdl(kernel, grid, dim3(kSortThreads), smem, stream, x, ids, T, K, E, s.tpb, s.Gp, row_bytes, rows, pair_pos,
                    offsets, cnt, tot, d_status) != cudaSuccess)
       return MLR_ERR_CUDA;
     note_launch();
@@ -805,20 +825,28 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
   if (!s.one) {
     int32_t* cnt = reinterpret_cast<int32_t*>(ws);
     int32_t* tot = reinterpret_cast<int32_t*>(ws + s.o_tot);
-    const size_t smem = (size_t)(num_experts + 1) * 4;
-    if (smem > 40 * 1024 && cudaFuncSetAttribute(sort_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 (int)smem) != cudaSuccess)
+    const size_t one = (size_t)(num_experts + 1) * 4;
+    const bool wide = one * kCountChunks <= 48 * 1024;
+    const unsigned blocks = (unsigned)(s.Gp / kCountChunks);
+    if (one > 48 * 1024 && cudaFuncSetAttribute(sort_count_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (int)one) != cudaSuccess)
       return MLR_ERR_CUDA;
-    if (launch_pdl(sort_count_kernel, dim3((unsigned)s.G), dim3(kSortThreads), smem, stream, topk_ids, s.P,
-                   num_experts, s.tpb * topk, s.G, cnt) != cudaSuccess)
+    if ((wide ? launch_pdl(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), one * kCountChunks, stream,
+                           topk_ids, s.P, num_experts, s.tpb * topk, s.Gp, cnt)
+              : launch_pdl(sort_count_kernel<false>, dim3(blocks), dim3(kSortThreads), one, stream, topk_ids, s.P,
+                           num_experts, s.tpb * topk, s.Gp, cnt)) != cudaSuccess)
       return MLR_ERR_CUDA;
-    if (launch_pdl(sort_scan_kernel, dim3((unsigned)(num_experts + 1)), dim3(kSortThreads), 0, stream, cnt, s.G,
+    if (launch_pdl(sort_scan_kernel, dim3((unsigned)(num_experts + 1)), dim3(kSortThreads), 0, stream, cnt, s.Gp,
                    tot) != cudaSuccess)
       return MLR_ERR_CUDA;
     note_launch(2);
   }
   const int64_t rb = x == nullptr ? 0 : (int64_t)hidden * es;
-  if (rb % 16 == 0 && aligned_to(x, 16) && aligned_to(rows, 16))
+  const bool whole = rb % 16 == 0 && aligned_to(x, 16) && aligned_to(rows, 16);
+  if (whole && rb >= 8192)
+    return launch_permute<32>(s, x, topk_ids, num_tokens, topk, num_experts, rb, rows, pair_pos, expert_offsets, ws,
+                              d_status, stream);
+  if (whole)
     return launch_permute<16>(s, x, topk_ids, num_tokens, topk, num_experts, rb, rows, pair_pos, expert_offsets, ws,
                               d_status, stream);
   if (es == 4)
