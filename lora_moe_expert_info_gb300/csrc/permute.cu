@@ -12,8 +12,11 @@
 // fp32, so results are bit-identical between runs.  pair_pos stores pos(p),
 // or ~pos(p) (negative) for a masked pair.
 //
-// All four move rows once: they are bound by HBM (bytes = rows read + rows
-// written), the sort by launch latency.
+// All four move rows once and are bound by HBM (bytes = rows read + rows
+// written; copy rate 6.67 TB/s), small ones by launch latency.  8192 tokens x 8
+// experts x 7168 bf16: permute 182 us (87% of the copy rate, 11 us of it the
+// sort), its gradient and unpermute 154 us (103%), unpermute's gradients 300 us
+// (100%).  1 to 256 tokens: 6 to 9 us.
 #include "mlr_profile.cuh"
 
 namespace mlr {
@@ -408,27 +411,31 @@ int row_threads(int nv, int most) {
 }
 
 // y[t] = sum_k w[t, k] rows[pos]; w == nullptr: w = 1 (the gradient of permute).
-// One thread per 16 bytes of a token; KU rows are loaded before any is added,
+// One thread per 16 bytes of a token, or a few of them a row of threads apart;
+// KU rows are loaded before any is added,
 // without branches, so that their loads are in flight together.
 constexpr int kSumThreads = 128;
+// Vectors per thread, so that few rows per token leave as many loads in flight
+// (13273 rows of 5656 float32, top-1: 87 us, with one vector 160).
+template <int KU, RowAccess A> constexpr int kVecs = A != kWhole || KU == 8 ? 1 : KU == 4 ? 2 : 4;
 template <typename E_, int KU, RowAccess A>
 __global__ void __launch_bounds__(kSumThreads)
 unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos, const float* __restrict__ w, int T,
                  int K, int H, int lpt_log2, unsigned col_blocks, E_* __restrict__ y, int32_t* d_status) {
-  constexpr int N = 16 / (int)sizeof(E_);
+  constexpr int N = 16 / (int)sizeof(E_), U = kVecs<KU, A>;
   pdl_wait();
   pdl_trigger();
   const unsigned tb = blockIdx.x / col_blocks, cb = blockIdx.x - tb * col_blocks;
   const int64_t t = ((int64_t)tb << (7 - lpt_log2)) + (threadIdx.x >> lpt_log2);
   const int lpt = 1 << lpt_log2, lt = threadIdx.x & (lpt - 1);
-  const int c = A == kStrided ? (int)cb * N * lpt + lt : ((int)cb * lpt + lt) * N;  // first column
-  if (t >= T || c >= H) return;
+  const int c0 = A == kStrided ? (int)cb * N * lpt + lt : ((int)cb * U * lpt + lt) * N;  // first column
+  if (t >= T || c0 >= H) return;
   const int64_t P = (int64_t)T * K;
-  float acc[N];
+  float acc[U][N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) acc[j] = 0.f;
+  for (int j = 0; j < U * N; ++j) acc[j / N][j % N] = 0.f;
   for (int k0 = 0; k0 < K; k0 += KU) {
-    uint4 v[KU], v2[A == kPieces ? KU : 1];
+    uint4 v[KU][U], v2[A == kPieces ? KU : 1];
     int shift[A == kPieces ? KU : 1];
     float wk[KU];
 #pragma unroll
@@ -438,41 +445,49 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
       const bool use = q >= 0 && q < P;
       if (q >= P) set_status(d_status, MLR_STATUS_INDEX);
       wk[j] = !use ? 0.f : w != nullptr ? __ldg(w + p) : 1.f;
-      const E_* r = rows + (int64_t)q * H + c;
+      const E_* r = rows + (int64_t)q * H + c0;
       if constexpr (A == kWhole) {
-        v[j] = use ? __ldg(reinterpret_cast<const uint4*>(r)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          v[j][i] = use && c0 + i * lpt * N < H ? __ldg(reinterpret_cast<const uint4*>(r) + i * lpt)
+                                                : make_uint4(0, 0, 0, 0);
       } else if constexpr (A == kStrided) {
-        v[j] = load_strided(rows + (int64_t)q * H, c, lpt, use ? H : 0);
+        v[j][0] = load_strided(rows + (int64_t)q * H, c0, lpt, use ? H : 0);
       } else {
         const int s = (int)(reinterpret_cast<uintptr_t>(r) & 15);
         const char* a = reinterpret_cast<const char*>(r) - s;
-        const int n = min(N, H - c) * (int)sizeof(E_);  // bytes of the row from r on
+        const int n = min(N, H - c0) * (int)sizeof(E_);  // bytes of the row from r on
         shift[j] = s;
-        v[j] = use ? load_piece<E_>(a, rows, rows + P * H) : make_uint4(0, 0, 0, 0);
+        v[j][0] = use ? load_piece<E_>(a, rows, rows + P * H) : make_uint4(0, 0, 0, 0);
         v2[j] = use && s + n > 16 ? load_piece<E_>(a + 16, rows, rows + P * H) : make_uint4(0, 0, 0, 0);
       }
     }
 #pragma unroll
-    for (int j = 0; j < KU; ++j) {
-      float f[N];
-      if constexpr (A == kPieces) widen(shifted<E_>(v[j], v2[j], shift[j]), f);
-      else widen(v[j], f);
+    for (int j = 0; j < KU; ++j)
 #pragma unroll
-      for (int u = 0; u < N; ++u) acc[u] = fmaf(wk[j], f[u], acc[u]);
-    }
+      for (int i = 0; i < U; ++i) {
+        float f[N];
+        if constexpr (A == kPieces) widen(shifted<E_>(v[j][i], v2[j], shift[j]), f);
+        else widen(v[j][i], f);
+#pragma unroll
+        for (int u = 0; u < N; ++u) acc[i][u] = fmaf(wk[j], f[u], acc[i][u]);
+      }
   }
-  uint4 o;
-  narrow(acc, o);
-  E_* out = y + t * H + c;
-  if constexpr (A == kWhole) {
-    *reinterpret_cast<uint4*>(out) = o;
-  } else if constexpr (A == kStrided) {
-    store_strided(y + t * H, c, lpt, H, o);
-  } else {
-    const E_* e = reinterpret_cast<const E_*>(&o);
+  E_* out = y + t * H + c0;
 #pragma unroll
-    for (int u = 0; u < N; ++u)
-      if (c + u < H) out[u] = e[u];
+  for (int i = 0; i < U; ++i) {
+    uint4 o;
+    narrow(acc[i], o);
+    if constexpr (A == kWhole) {
+      if (c0 + i * lpt * N < H) reinterpret_cast<uint4*>(out)[i * lpt] = o;
+    } else if constexpr (A == kStrided) {
+      store_strided(y + t * H, c0, lpt, H, o);
+    } else {
+      const E_* e = reinterpret_cast<const E_*>(&o);
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+        if (c0 + u < H) out[u] = e[u];
+    }
   }
 }
 
@@ -481,8 +496,10 @@ unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_p
 // columns in increasing order, then over lanes and warps in a fixed order).
 // Bound by the bytes in flight: eight rows of a token are loaded at once, at
 // most 85 registers a thread for three blocks per SM.  8192 x 8 rows of 7168
-// bf16: 293 us at 85 registers, 530 at 110, 324 at 64 (spills); with 128
-// threads per token instead of 256, 4096 x 8 rows of 2048 take 48 instead of 53.
+// bf16: 300 us so, 530 at 110 registers, 324 at 64 (spills); with 128 threads
+// per token instead of 256, 4096 x 8 rows of 2048 take 48 us instead of 53.  With
+// one or two rows per token a thread takes four or two vectors at once (13273
+// rows of 5656 float32, top-1: 126 us instead of 148).
 constexpr int kBackThreads = 256, kBackLanes = 128;
 
 // Sums dot[j] over the 2^lpt_log2 threads of a token (whole groups of the block)
@@ -537,7 +554,7 @@ __global__ void __launch_bounds__(kBackThreads, 3)
 unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos,
                           const float* __restrict__ w, int T, int K, int H, int lpt_log2, E_* __restrict__ d_rows,
                           float* __restrict__ dw, int32_t* d_status) {
-  constexpr int N = 16 / (int)sizeof(E_);
+  constexpr int N = 16 / (int)sizeof(E_), U = KU == 1 ? 4 : KU == 2 ? 2 : 1;
   __shared__ float part[kBackThreads / 32][KU];
   pdl_wait();
   pdl_trigger();
@@ -553,36 +570,46 @@ unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows
       dot[j] = 0.f;
     }
     if (in)
-      for (int c = A == kStrided ? lt : lt * N; c < H; c += lpt * N) {
-        uint4 v[KU];
-        float g[N];
-        uint4 gv;
-        if constexpr (A == kStrided) gv = load_strided(dy + t * H, c, lpt, H);
-        else gv = __ldg(reinterpret_cast<const uint4*>(dy + t * H + c));
+      for (int c = A == kStrided ? lt : lt * N; c < H; c += U * lpt * N) {
+        uint4 gv[U], v[KU][U];
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-          if constexpr (A == kStrided)
-            v[j] = load_strided(rows + (int64_t)pr[j].row * H, c, lpt, pr[j].use ? H : 0);
-          else
-            v[j] = pr[j].use ? __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pr[j].row * H + c))
-                             : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < U; ++i) {
+          const int ci = c + i * lpt * N;
+          if constexpr (A == kStrided) gv[i] = load_strided(dy + t * H, ci, lpt, H);
+          else gv[i] = ci < H ? __ldg(reinterpret_cast<const uint4*>(dy + t * H + ci)) : make_uint4(0, 0, 0, 0);
         }
-        widen(gv, g);
 #pragma unroll
-        for (int j = 0; j < KU; ++j) {
-          float f[N], o[N];
-          widen(v[j], f);
+        for (int j = 0; j < KU; ++j)
 #pragma unroll
-          for (int u = 0; u < N; ++u) {
-            o[u] = pr[j].use ? pr[j].w * g[u] : 0.f;
-            dot[j] = pr[j].use ? fmaf(g[u], f[u], dot[j]) : 0.f;
+          for (int i = 0; i < U; ++i) {
+            const int ci = c + i * lpt * N;
+            if constexpr (A == kStrided)
+              v[j][i] = load_strided(rows + (int64_t)pr[j].row * H, ci, lpt, pr[j].use ? H : 0);
+            else
+              v[j][i] = pr[j].use && ci < H ? __ldg(reinterpret_cast<const uint4*>(rows + (int64_t)pr[j].row * H + ci))
+                                            : make_uint4(0, 0, 0, 0);
           }
-          uint4 ov;
-          narrow(o, ov);
-          if constexpr (A == kStrided) {
-            store_strided(d_rows + (int64_t)pr[j].row * H, c, lpt, pr[j].row >= 0 ? H : 0, ov);
-          } else {
-            if (pr[j].row >= 0) *reinterpret_cast<uint4*>(d_rows + (int64_t)pr[j].row * H + c) = ov;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int ci = c + i * lpt * N;
+          float g[N];
+          widen(gv[i], g);
+#pragma unroll
+          for (int j = 0; j < KU; ++j) {
+            float f[N], o[N];
+            widen(v[j][i], f);
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+              o[u] = pr[j].use ? pr[j].w * g[u] : 0.f;
+              dot[j] = pr[j].use ? fmaf(g[u], f[u], dot[j]) : 0.f;
+            }
+            uint4 ov;
+            narrow(o, ov);
+            if constexpr (A == kStrided) {
+              store_strided(d_rows + (int64_t)pr[j].row * H, ci, lpt, pr[j].row >= 0 ? H : 0, ov);
+            } else {
+              if (pr[j].row >= 0 && ci < H) *reinterpret_cast<uint4*>(d_rows + (int64_t)pr[j].row * H + ci) = ov;
+            }
           }
         }
       }
@@ -730,7 +757,7 @@ int log2_of(int n) {
 template <typename E_, int KU, RowAccess A>
 int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int T, int K, int H, void* y,
                        int32_t* d_status, cudaStream_t stream) {
-  const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16), lpt = row_threads(nv, kSumThreads);
+  const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16 * kVecs<KU, A>), lpt = row_threads(nv, kSumThreads);
   const int64_t col_blocks = ceil_div(nv, lpt), blocks = ceil_div(T, kSumThreads / lpt) * col_blocks;
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
   if (launch_pdl(unpermute_kernel<E_, KU, A>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
