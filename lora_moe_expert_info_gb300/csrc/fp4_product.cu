@@ -17,6 +17,15 @@
 //   warp 2      scales from there to TMEM (tcgen05.cp), ahead of the codes
 //   warp 1      one MMA per 64 columns
 //   warps 4-11  accumulators from TMEM, scaled and rounded, to y
+//
+// Few rows are bound by HBM (each expert's weights once), many by the pace of
+// the K steps: a step of 256 columns is four MMAs of 128 cycles, next to them in
+// the tensor pipe 6 (MXFP4) or 12 (NVFP4) scale copies of about 25, and 48 KB
+// through shared memory twice.  Measured, device time: 32768 rows x 128 experts
+// x 1536 x 2048 NVFP4 73 us (5.0 TB/s of what it has to move, 75% of the copy
+// rate; 2.8 PFLOP/s), 8192 rows x 32 experts x 4096 x 7168 MXFP4 121 us (74%; 4.0
+// PFLOP/s), 2048 rows x 128 experts x 2048 x 768 MXFP4 23.6 us (74%), one token's
+// 8 rows 7.2 us, 2 us of it bytes.
 #include <cudaTypedefs.h>
 
 #include "mlr_fp4.cuh"
