@@ -11,21 +11,22 @@
 // of one expert (the MMA's N), so that few rows waste little of the tensor
 // core and every weight is read once per tile.  One persistent CTA per SM
 // walks a static share of the items; roles are warps:
-//   warp 0      codes: per K step of 256 columns one TMA box of W and one of A
-//               (128-byte rows, 128-byte swizzle) into a ring of stages
-//   warp 3      the steps' scale atoms into a ring of their own
-//   warp 2      scales from there to TMEM (tcgen05.cp), ahead of the codes
+//   warp 0, 3   codes: per K step of 256 columns one TMA box of W (warp 0) and
+//               one of A (warp 3), rows of 128 bytes in 128-byte swizzle, into
+//               a ring of stages
+//   warp 2      the steps' scale atoms into a ring of their own
+//   warps 12-15 scales from there to TMEM, ahead of the codes
 //   warp 1      one MMA per 64 columns
 //   warps 4-11  accumulators from TMEM, scaled and rounded, to y
 //
 // Few rows are bound by HBM (each expert's weights once), many by the pace of
-// the K steps: a step of 256 columns is four MMAs of 128 cycles, next to them in
-// the tensor pipe 6 (MXFP4) or 12 (NVFP4) scale copies of about 25, and 48 KB
-// through shared memory twice.  Measured, device time: 32768 rows x 128 experts
-// x 1536 x 2048 NVFP4 73 us (5.0 TB/s of what it has to move, 75% of the copy
-// rate; 2.8 PFLOP/s), 8192 rows x 32 experts x 4096 x 7168 MXFP4 121 us (74%; 4.0
-// PFLOP/s), 2048 rows x 128 experts x 2048 x 768 MXFP4 23.6 us (74%), one token's
-// 8 rows 7.2 us, 2 us of it bytes.
+// the K steps: four MMAs of 128 cycles, and the time from a stage's release to
+// its next load, which four stages of 48 KB hide in part.  Measured, device
+// time: 32768 rows x 128 experts x 1536 x 2048 NVFP4 69 us (5.3 TB/s of what it
+// has to move, 79% of the copy rate; 3.0 PFLOP/s), 8192 rows x 32 experts x 4096 x
+// 7168 MXFP4 120 us (74%; 4.0 PFLOP/s), 4096 rows x one 4096 x 7168 matrix 47 us (5.1
+// PFLOP/s), 2048 rows x 128 experts x 2048 x 768 MXFP4 24 us (73%), one token's 8
+// rows 6.9 us, 2 us of it bytes.
 #include <cudaTypedefs.h>
 
 #include "mlr_fp4.cuh"
@@ -34,7 +35,7 @@
 namespace mlr {
 namespace {
 
-constexpr int kProductThreads = 384;
+constexpr int kProductThreads = 512;
 constexpr int kEpilogueThreads = 256;  // warps 4-11: two per TMEM lane quarter
 constexpr int kMaxProductExperts = 2048;
 constexpr int kKStep = 256;      // columns per ring stage: 128 bytes of codes per row
@@ -58,21 +59,20 @@ template <int NT, int FMT> struct Shape {
   static constexpr int kSfStride = (1 + kRowBlocks) * kSfBytes;
   static constexpr int kAcc1 = ProductCfg<NT>::kAcc1;  // TMEM column of the second accumulator
   static constexpr int kShared = NT - kAcc1;           // columns that both accumulators use
-  // TMEM columns after the accumulators: slots for a step's scales of W and
-  // A.  A scale stage's barrier is not passed twice before the MMAs have seen
-  // it as long as there are no more slots than scale stages, and a stage's
-  // empty barrier not before the scales have as long as there are no more
-  // slots than stages.
+  // TMEM columns after the accumulators: slots for a step's scales of W and A.
+  // With no more slots than stages, a warp that finds its slot free (the MMAs
+  // of that many steps ago are done) also finds its stage's barrier past the
+  // step before.
   static constexpr int kSfCols = kAtoms * 4 * (1 + kRowBlocks);
   static constexpr int kSfCol0 = kAcc1 + NT;
-  static constexpr int kSlots = (512 - kSfCol0) / kSfCols < Q ? (512 - kSfCol0) / kSfCols : Q;
-  static_assert(kSlots >= 2 && kSlots <= Q && kSlots <= S && S <= 8 && Q <= 8, "slots");
+  static constexpr int kSlots = (512 - kSfCol0) / kSfCols < S ? (512 - kSfCol0) / kSfCols : S;
+  static_assert(kSlots >= 2 && S <= 8 && Q <= 8 && kSfCols % 8 == 0, "slots");
   static_assert(kShared == 0 || (kShared == kAcc1 && kShared % 128 == 0), "halves of 128 columns");
 };
 
 struct __align__(16) Ctl {
-  uint64_t full[8], empty[8];      // a stage of codes has landed / its MMAs are done
-  uint64_t sf_full[8], scaled[8];  // a stage of scales has landed / is in TMEM
+  uint64_t full[8], empty[8];        // a step's codes and scales are there / its MMAs are done
+  uint64_t sf_full[8], sf_empty[8];  // a stage of scales has landed / has been read
   uint64_t acc_full[2], acc_empty[2];
   uint64_t edge[2];  // the columns shared with the other accumulator have been read
   uint32_t tmem;
@@ -87,12 +87,13 @@ constexpr int smem_bytes() {
 }
 
 struct Maps {
-  CUtensorMap w;     // [E * N, pitch] in boxes of 128 rows
-  CUtensorMap a[5];  // [P, pitch] in boxes of 16 << i rows
+  CUtensorMap w;      // [E * N, pitch] in boxes of 128 rows
+  CUtensorMap a[5];   // [P, pitch] in boxes of 16 << i rows
+  CUtensorMap sw;     // W's scales, a row per 128-row block, one step per box
+  CUtensorMap sa[2];  // A's scales, the same in boxes of one and two row blocks
 };
 
 struct Params {
-  const uint8_t *sa, *sw;
   const float *ga, *gw;
   const int32_t* offsets;
   int P, E, N, nblk, ksteps, cols, atoms;
@@ -231,6 +232,19 @@ __device__ __forceinline__ void store_chunk(const Params& p, uint16_t* yp, const
   }
 }
 
+// One arrival for the warp, after all its lanes are done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+// Registers -> TMEM: this warp's 32 lanes, 8 columns; tmem_st_wait waits for all.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 template <int NT, int FMT>
 __global__ void __launch_bounds__(kProductThreads, 1)
 product_kernel(const __grid_constant__ Maps maps, const Params p) {
@@ -245,17 +259,17 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&c.full[s], 1);
+      mbar_init(&c.full[s], 6);  // W's load, A's load, four warps of scales
       mbar_init(&c.empty[s], 1);
     }
     for (int q = 0; q < Q; ++q) {
       mbar_init(&c.sf_full[q], 1);
-      mbar_init(&c.scaled[q], 1);
+      mbar_init(&c.sf_empty[q], 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.acc_full[b], 1);
-      mbar_init(&c.acc_empty[b], kEpilogueThreads);
-      mbar_init(&c.edge[b], kEpilogueThreads);
+      mbar_init(&c.acc_empty[b], kEpilogueThreads / 32);
+      mbar_init(&c.edge[b], kEpilogueThreads / 32);
     }
     c.abort = 0;
     fence_mbar_init();
@@ -275,52 +289,46 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
 
   ItemWalk<NT> walk;
   walk.mine = Item{};
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ================================ codes ================================
+    // W by one warp, A by the other: a stage's loads are issued side by side.
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
       const Item it = walk.at(p, c, il, n_items, lane);
       int bi = 0;  // the shortest box that holds the tile
       while ((16 << bi) < it.rows) ++bi;
-      const CUtensorMap* ma = &maps.a[bi];
-      const int wrow = it.e * p.N + it.n0;
+      const CUtensorMap* map = warp == 0 ? &maps.w : &maps.a[bi];
+      const int row = warp == 0 ? it.e * p.N + it.n0 : it.row0;
+      const uint32_t bytes = warp == 0 ? Sh::kWBytes : (16 << bi) * 128;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
         ok = __all_sync(0xffffffffu, mbar_wait(&c.empty[st], ((g / S) & 1) ^ 1, abort, p.wait_ns));
         if (!ok) break;
-        uint8_t* sb = smem + st * Sh::kStride;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&c.full[st], Sh::kWBytes + (16 << bi) * 128);
-          tma_load_2d(sb, &maps.w, &c.full[st], k * 128, wrow);
-          tma_load_2d(sb + Sh::kWBytes, ma, &c.full[st], k * 128, it.row0);
+          mbar_arrive_expect_tx(&c.full[st], bytes);
+          tma_load_2d(smem + st * Sh::kStride + (warp == 0 ? 0 : Sh::kWBytes), map, &c.full[st], k * 128, row);
         }
         __syncwarp();
       }
     }
-  } else if (warp == 3) {
+  } else if (warp == 2) {
     // ============================= scale loads =============================
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
       const Item it = walk.at(p, c, il, n_items, lane);
-      const int rblocks = (it.rows + 127) / 128;
-      const uint8_t* sw = p.sw + ((int64_t)it.e * p.nblk + it.n0 / 128) * p.atoms * kAtomBytes;
-      const uint8_t* sa = p.sa + (int64_t)it.sblk * p.atoms * kAtomBytes;
-      const int64_t sa_block = (int64_t)p.atoms * kAtomBytes;
+      const int two = Sh::kRowBlocks > 1 && it.rows > 128;
+      const int wb = it.e * p.nblk + it.n0 / 128;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int q = g % Q;
-        ok = __all_sync(0xffffffffu, mbar_wait(&c.scaled[q], ((g / Q) & 1) ^ 1, abort, p.wait_ns));
+        ok = __all_sync(0xffffffffu, mbar_wait(&c.sf_empty[q], ((g / Q) & 1) ^ 1, abort, p.wait_ns));
         if (!ok) break;
-        const uint32_t sf = smem_u32(smem_sf) + q * Sh::kSfStride;
-        const int a0 = k * Sh::kAtoms;
-        const uint32_t abytes = (uint32_t)min(Sh::kAtoms, p.atoms - a0) * kAtomBytes;
+        uint8_t* sf = smem_sf + q * Sh::kSfStride;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&c.sf_full[q], (1 + rblocks) * abytes);
-          bulk_load(sf, sw + a0 * kAtomBytes, abytes, &c.sf_full[q]);
-          bulk_load(sf + Sh::kSfBytes, sa + a0 * kAtomBytes, abytes, &c.sf_full[q]);
-          if (Sh::kRowBlocks > 1 && rblocks > 1)
-            bulk_load(sf + 2 * Sh::kSfBytes, sa + sa_block + a0 * kAtomBytes, abytes, &c.sf_full[q]);
+          mbar_arrive_expect_tx(&c.sf_full[q], (2 + two) * Sh::kSfBytes);
+          tma_load_2d(sf, &maps.sw, &c.sf_full[q], k * Sh::kAtoms * (kAtomBytes / 8), wb);
+          tma_load_2d(sf + Sh::kSfBytes, &maps.sa[two], &c.sf_full[q], k * Sh::kAtoms * (kAtomBytes / 8), it.sblk);
         }
         __syncwarp();
       }
@@ -329,15 +337,13 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     // ================================= MMA =================================
     // The whole warp walks the steps, so that every operand is uniform over it
     // and stays in uniform registers; one elected lane issues.  (With a single
-    // lane in the loop each MMA took 240 cycles to issue whatever its N, each
-    // scale copy 95.)
+    // lane in the loop each MMA took 240 cycles to issue whatever its N.)
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint32_t sb0 = smem_u32(smem);
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
       const Item it = walk.at(p, c, il, n_items, lane);
-      const int rows = it.rows;
       const int b = il & 1;
       ok = mbar_wait(&c.acc_empty[b], ((il >> 1) & 1) ^ 1, abort, p.wait_ns);
       if (Sh::kShared > 0 && il > 0)
@@ -346,13 +352,11 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tm + b * Sh::kAcc1;
-      const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(rows), 2);
+      const uint32_t id0 = idesc_fp4<FMT>(128, mma_rows(it.rows), 0), id2 = idesc_fp4<FMT>(128, mma_rows(it.rows), 2);
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int st = g % S;
         // the codes have landed, and their scales are in TMEM
-        ok = mbar_wait(&c.scaled[g % Q], (g / Q) & 1, abort, p.wait_ns) &&
-             mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns);
-        ok = __all_sync(0xffffffffu, ok);
+        ok = __all_sync(0xffffffffu, mbar_wait(&c.full[st], (g / S) & 1, abort, p.wait_ns));
         if (!ok) break;
         tc_fence_after();
         const uint32_t sb = sb0 + st * Sh::kStride;
@@ -365,8 +369,8 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
             const int i = FMT == MLR_FP4_MX ? m >> 1 : m;
             if (m < nm)
               mma_fp4<FMT>(acc, sdesc_sw128(sb + m * 32), sdesc_sw128(sb + Sh::kWBytes + m * 32),
-                           FMT == MLR_FP4_MX && (m & 1) ? id2 : id0, tw + 4 * i, ta + 4 * Sh::kRowBlocks * i,
-                           (k > 0 || m > 0) ? 1u : 0u);
+                                 FMT == MLR_FP4_MX && (m & 1) ? id2 : id0, tw + 4 * i, ta + 4 * Sh::kRowBlocks * i,
+                                 (k > 0 || m > 0) ? 1u : 0u);
           }
           mma_commit(&c.empty[st]);
         }
@@ -375,46 +379,63 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (ok && elect_one()) mma_commit(&c.acc_full[b]);
       __syncwarp();
     }
-  } else if (warp == 2) {
+  } else if (warp >= 12) {
     // ============================ scales to TMEM ===========================
-    // A warp of its own: the copies' issue would hold up the MMAs'.
-    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint32_t sf0 = smem_u32(smem_sf);
+    // Each of the four warps writes its own lane quarter, a repetition of the
+    // same 32 lanes: lane l holds bytes 16 l to 16 l + 15 of every atom, four
+    // columns of it.  (Copies by tcgen05.cp take about 28 cycles each in the
+    // tensor pipe, between the MMAs: 12 a step for NVFP4; 4096 rows x 4096 x 7168
+    // took 57 us with them, 47 us so.)
+    const uint32_t t0 = tmem + Sh::kSfCol0 + ((uint32_t)(warp & 3) << 21);
+    const uint32_t sf0 = smem_u32(smem_sf) + lane * 16;
     int g = 0, il = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_items && ok; item += gridDim.x, ++il) {
-      const int rows = walk.at(p, c, il, n_items, lane).rows;
+      const bool two = Sh::kRowBlocks > 1 && walk.at(p, c, il, n_items, lane).rows > 128;
       for (int k = 0; k < p.ksteps; ++k, ++g) {
         const int q = g % Q;
         ok = mbar_wait(&c.sf_full[q], (g / Q) & 1, abort, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t sf = sf0 + q * Sh::kSfStride;
+        uint32_t v[Sh::kSfCols];  // per atom W's four columns; then per atom those of A's row blocks
+#pragma unroll
+        for (int i = 0; i < Sh::kAtoms; ++i) {
+          const uint4 w = lds128(sf + i * kAtomBytes);
+          v[4 * i] = w.x;
+          v[4 * i + 1] = w.y;
+          v[4 * i + 2] = w.z;
+          v[4 * i + 3] = w.w;
+#pragma unroll
+          for (int r = 0; r < Sh::kRowBlocks; ++r) {
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (r == 0 || two) a = lds128(sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
+            const int o = 4 * Sh::kAtoms + 4 * (Sh::kRowBlocks * i + r);
+            v[o] = a.x;
+            v[o + 1] = a.y;
+            v[o + 2] = a.z;
+            v[o + 3] = a.w;
+          }
+        }
         // the MMAs of the step that used this TMEM slot last are done
         if (g >= Sh::kSlots)
-          ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns) && ok;
+          ok = mbar_wait(&c.empty[(g - Sh::kSlots) % S], ((g - Sh::kSlots) / S) & 1, abort, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sf = sf0 + q * Sh::kSfStride;
-        // the slot's cells: per atom four columns of W, then four per row block of A
-        const uint32_t tw = tm + Sh::kSfCol0 + (g % Sh::kSlots) * Sh::kSfCols;
-        const uint32_t ta = tw + 4 * Sh::kAtoms;
-        const int na = p.atoms - k * Sh::kAtoms;
-        if (elect_one()) {
+        const uint32_t t = t0 + (g % Sh::kSlots) * Sh::kSfCols;
 #pragma unroll
-          for (int i = 0; i < Sh::kAtoms; ++i) {
-            if (i < na) {
-              copy_scale_atom(tw + 4 * i, sf + i * kAtomBytes);
-#pragma unroll
-              for (int r = 0; r < Sh::kRowBlocks; ++r)
-                if (r * 128 < rows)
-                  copy_scale_atom(ta + 4 * (Sh::kRowBlocks * i + r), sf + (1 + r) * Sh::kSfBytes + i * kAtomBytes);
-            }
-          }
-          mma_commit(&c.scaled[q]);
-        }
+        for (int i = 0; i < Sh::kSfCols; i += 8) tmem_st8(t + i, v + i);
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&c.sf_empty[q]);
+          mbar_arrive(&c.full[g % S]);
+        }
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4) {  // 4 to 11
     // =============================== epilogue ==============================
     // Two warps per lane quarter take alternate chunks of 32 accumulator
     // columns (rows of y), first those that the next tile's accumulator shares.
@@ -447,8 +468,8 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         tmem_ld_wait(v[0]);
         tmem_ld_wait(v[1]);
         tc_fence_before();
-        if (Sh::kShared > 0 && part == 0) mbar_arrive(&c.edge[b]);
-        if (part == kParts - 1) mbar_arrive(&c.acc_empty[b]);
+        if (Sh::kShared > 0 && part == 0) warp_arrive(&c.edge[b], lane);
+        if (part == kParts - 1) warp_arrive(&c.acc_empty[b], lane);
         if (c0 < it.rows) store_chunk(p, yp, v[0], s, n, c0, it.rows, lane);
         if (NT > 64 && c1 < it.rows) store_chunk(p, yp, v[1], s, n, c1, it.rows, lane);
       }
@@ -460,8 +481,8 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
   if (*abort) {
     if (tid == 0) set_status(p.status, MLR_STATUS_TIMEOUT);
     sleep_for_ns(kGraceNs);  // copies and MMAs already issued finish before the teardown
-    __syncthreads();
   }
+  __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
@@ -492,36 +513,58 @@ bool code_map(CUtensorMap* m, const void* base, uint64_t pitch, uint64_t rows, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scales as rows of 128-row blocks, in boxes of one step of `boxes` row blocks;
+// atoms past the last one read as zeros.
+bool scale_map(CUtensorMap* m, const void* base, uint64_t atoms, uint64_t blocks, uint32_t box_atoms, uint32_t boxes) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {atoms * (kAtomBytes / 8), blocks};  // in 8-byte elements: a box has at most 256 a side
+  cuuint64_t strides[1] = {atoms * kAtomBytes};
+  cuuint32_t box[2] = {box_atoms * (kAtomBytes / 8), boxes};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_INT64, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// SMs of the current device, after opting the kernel in to its shared memory;
+// kept per device.  0: an error.
+template <int NT, int FMT>
 int product_sms() {
-  static int n[64] = {};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (n[dev] == 0) {
-    int v = 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0) v = 148;
-    n[dev] = v;
-  }
-  return n[dev];
+  constexpr int smem = smem_bytes<NT, FMT>();
+  static_assert(smem <= 227 * 1024, "shared memory per CTA");
+  static int sms[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (sms[dev] != 0) return sms[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0 ||
+      cudaFuncSetAttribute(product_kernel<NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return 0;
+  sms[dev] = n;
+  return n;
 }
 
 template <int NT, int FMT>
-int launch_product(const Maps& maps, const Params& p, cudaStream_t stream) {
-  constexpr int smem = smem_bytes<NT, FMT>();
-  static_assert(smem <= 227 * 1024, "shared memory per CTA");
-  static bool configured[64] = {};  // per device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MLR_ERR_CUDA;
-  if (dev < 0 || dev >= 64 || !configured[dev]) {
-    if (cudaFuncSetAttribute(product_kernel<NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    if (dev >= 0 && dev < 64) configured[dev] = true;
-  }
+int launch_product(Maps& maps, Params& p, const uint8_t* a, const uint8_t* sa, const uint8_t* sw, uint64_t pitch,
+                   cudaStream_t stream) {
+  using Sh = Shape<NT, FMT>;
   // at most one partial tile per expert beyond the full ones
   const int64_t tiles = (p.P < p.E ? p.P : p.E) + (int64_t)p.P / NT;
   const int64_t items = tiles * p.nblk;
   if (items > INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  const int grid = (int)(items < product_sms() ? items : product_sms());
-  if (launch_pdl(product_kernel<NT, FMT>, dim3(grid), dim3(kProductThreads), smem, stream, maps, p) != cudaSuccess) {
+  const int sms = product_sms<NT, FMT>();
+  if (sms == 0) {
+    (void)cudaGetLastError();
+    return MLR_ERR_CUDA;
+  }
+  bool ok = scale_map(&maps.sw, sw, p.atoms, (uint64_t)p.E * p.nblk, Sh::kAtoms, 1);
+  for (int i = 0; i < Sh::kRowBlocks; ++i)
+    ok = ok && scale_map(&maps.sa[i], sa, p.atoms, (uint64_t)p.P / 128 + p.E, Sh::kAtoms, i + 1);
+  for (uint32_t i = 0, rows = 16; rows <= NT; ++i, rows *= 2)
+    ok = ok && code_map(&maps.a[i], a, pitch, (uint64_t)p.P, rows);
+  if (!ok) return MLR_ERR_CUDA;
+  if (launch_pdl(product_kernel<NT, FMT>, dim3((unsigned)(items < sms ? items : sms)), dim3(kProductThreads),
+                 smem_bytes<NT, FMT>(), stream, maps, p) != cudaSuccess) {
     (void)cudaGetLastError();
     return MLR_ERR_CUDA;
   }
@@ -550,16 +593,14 @@ extern "C" int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_s
     if (q == nullptr || (reinterpret_cast<uintptr_t>(q) & 15) != 0) return MLR_ERR_INVALID;
   if (expert_offsets == nullptr || y == nullptr) return MLR_ERR_INVALID;
   const uint64_t pitch = (uint64_t)fp4_pitch(cols);
-  Maps maps;
-  bool ok = code_map(&maps.w, w_codes, pitch, (uint64_t)num_experts * outputs, 128);
-  for (int i = 0; i < 5; ++i) ok = ok && code_map(&maps.a[i], a_codes, pitch, (uint64_t)num_rows, 16u << i);
-  if (!ok) return MLR_ERR_CUDA;
-  Params p{a_scales, w_scales, a_tensor_scale, w_tensor_scale, expert_offsets, num_rows, num_experts, outputs,
+  Maps maps = {};
+  if (!code_map(&maps.w, w_codes, pitch, (uint64_t)num_experts * outputs, 128)) return MLR_ERR_CUDA;
+  Params p{a_tensor_scale, w_tensor_scale, expert_offsets, num_rows, num_experts, outputs,
            (int)ceil_div(outputs, 128), (int)ceil_div(cols, kKStep), cols, fp4_atoms(cols, fmt), y, d_status,
            wait_limit_ns()};
   // an average expert of at most 32 rows rarely needs a second 64-row tile
   const bool small = num_rows <= 32 * (int64_t)num_experts || num_rows <= 64;
-  if (fmt == MLR_FP4_MX)
-    return small ? launch_product<64, MLR_FP4_MX>(maps, p, stream) : launch_product<256, MLR_FP4_MX>(maps, p, stream);
-  return small ? launch_product<64, MLR_FP4_NV>(maps, p, stream) : launch_product<256, MLR_FP4_NV>(maps, p, stream);
+  auto run = [&](auto launch) { return launch(maps, p, a_codes, a_scales, w_scales, pitch, stream); };
+  if (fmt == MLR_FP4_MX) return small ? run(launch_product<64, MLR_FP4_MX>) : run(launch_product<256, MLR_FP4_MX>);
+  return small ? run(launch_product<64, MLR_FP4_NV>) : run(launch_product<256, MLR_FP4_NV>);
 }

@@ -6,8 +6,8 @@
 // its columns past the last one hold zero codes.  Block scales lie in 512-byte
 // atoms of 128 rows x 4 scale blocks, row r of the atom and block c at byte
 // 16 (r % 32) + 4 (r / 32) + c -- the order in which the tensor cores take
-// them from TMEM after one copy of the atom -- with the atoms of a 128-row
-// block one after another along the columns.
+// them from TMEM, 16 bytes a lane -- with the atoms of a 128-row block one after
+// another along the columns.
 #pragma once
 #include "mlr_common.cuh"
 
@@ -53,24 +53,11 @@ __device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
-// One scale atom (512 bytes: 32 rows of 16) from shared memory to four TMEM
-// columns, repeated in every lane quarter.  Ordered before later MMAs of the
-// same thread.
-__device__ __forceinline__ void copy_scale_atom(uint32_t taddr, uint32_t saddr) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc_noswz(saddr, 16, 128))
-               : "memory");
-}
 // One lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n}" : "=r"(r));
   return r != 0;
-}
-// Untiled bulk copy (16-byte aligned addresses, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
 }
 
 }  // namespace mlr
