@@ -307,6 +307,31 @@ def test_product_bad_blocks_stay_in_their_rows(cuda_device, fmt):
     assert torch.equal(y.isnan(), want) and torch.equal(y[~want], y0[~want])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_swiglu_of_bad_and_extreme_values(cuda_device, fmt, bad):
+    """A block with an infinity or a NaN is NaN and leaves its neighbours alone;
+    gates far below zero give zeros, far above the other factor."""
+    P, C = 6, 64
+    gu = torch.ones(P, 2 * C)
+    gu[0, 5] = bad
+    gu[1, C + 40] = bad
+    gu[2, :C], gu[2, C:] = -200.0, 3.0   # SiLU -> 0
+    gu[3, :C], gu[3, C:] = -88.0, 3.0
+    gu[4, :C], gu[4, C:] = 100.0, 0.0    # u = 0
+    gu[5, :C], gu[5, C:] = 96.0, 0.5     # 48 in float32
+    off = torch.tensor([0, P], dtype=torch.int32, device="cuda")
+    codes, scales = fp4.fp4_quantize_swiglu(gu.cuda(), off, fmt, check=True)
+    y = fp4.fp4_dequantize(codes, scales, C, fmt, expert_offsets=off, dtype=F32).cpu()
+    n = 16 if fmt == "nvfp4" else 32
+    want = torch.zeros(P, C, dtype=torch.bool)
+    # -inf as a gate: -inf / inf is NaN as well
+    want[0, 0:n] = True
+    want[1, 40 // n * n:40 // n * n + n] = True
+    assert torch.equal(y.isnan(), want)
+    assert (y[2:5].abs() < 1e-30).all() and (y[5] == 48).all()
+
+
 def test_product_rejects_bad_offsets(cuda_device):
     off, a, sa, qw, sw, _, _ = product_case(20, 1, 3, 128, 64, "mxfp4")
     for bad in ([0, 5, 3, 20], [-1, 5, 9, 20], [0, 5, 9, 21]):

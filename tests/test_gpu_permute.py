@@ -68,6 +68,39 @@ def test_permute_and_back(cuda_device, T, K, E, H, dtype, masked):
     assert np.all(np.abs(f64(dw) - rw) <= (H + 1) * 2.0 ** -23 * mag)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,K,E,H,masked", [(2000, 8, 60, 72, 0.1), (2000, 8, 60, 71, 0.1), (1500, 6, 7, 4200, 0.05),
+                                            (9000, 1, 5, 1, 0.0), (9000, 1, 5, 2, 0.1), (1100, 8, 3, 2083, 0.0),
+                                            (50, 2, 3, 5000, 0.2), (50, 3, 3, 4099, 0.2)])
+def test_rows_of_large_batches_and_long_rows(cuda_device, T, K, E, H, dtype, masked):
+    """Past the single launch, long rows and rows off the 16-byte grid, against
+    indexing and 64-bit sums on the device."""
+    x, ids, w = case(T, K, E, H, dtype, seed=T + H, masked=masked)
+    rows, pos, off = pm.moe_permute(x, ids, E)
+    at, held = torch.where(pos < 0, ~pos, pos).long(), pos >= 0
+    want = torch.zeros_like(rows)
+    want[at.reshape(-1)] = torch.where(held[..., None], x[:, None].expand(-1, K, -1), 0).reshape(T * K, H)
+    assert torch.equal(rows, want)
+    assert int(off[-1]) == int(held.sum())
+
+    r = torch.randn(T * K, H, generator=torch.Generator().manual_seed(5)).to(dtype).cuda()
+    g = torch.where(held[..., None], r[at].double(), 0)
+    wd = w.double()[..., None]
+    u = U[dtype]
+
+    def near(got, ref, mag, terms):
+        return bool(((got.double() - ref).abs() <= u * ref.abs() + (terms + 1) * 2.0 ** -23 * mag).all())
+
+    assert near(pm.moe_unpermute(r, pos, w, check=True), (g * wd).sum(1), (g * wd).abs().sum(1), K)
+    assert near(pm.moe_permute_backward(r, pos, check=True), g.sum(1), g.abs().sum(1), K)
+    d_rows, dw = pm.moe_unpermute_backward(x, r, pos, w, check=True)
+    ref = torch.zeros(T * K, H, dtype=torch.float64, device="cuda")
+    ref[at.reshape(-1)] = torch.where(held[..., None], x.double()[:, None] * wd, 0).reshape(T * K, H)
+    assert bool(((d_rows.double() - ref).abs() <= (u + 2.0 ** -23) * ref.abs()).all())
+    t = g * x.double()[:, None]
+    assert bool(((dw.double() - t.sum(-1)).abs() <= (H + 1) * 2.0 ** -23 * t.abs().sum(-1)).all())
+
+
 @pytest.mark.parametrize("T,K,E,masked,skew", [(1024, 8, 128, 0.0, 0.0), (1025, 8, 128, 0.1, 0.0), (5000, 8, 256, 0.0, 0.9),
                                                (40000, 3, 17, 0.05, 0.0), (9000, 1, 4000, 0.0, 0.0),
                                                (300, 100, 7, 0.2, 0.0), (2, 256, 16384, 0.0, 0.0),
