@@ -15,8 +15,8 @@
 // One thread holds 16 consecutive columns of a row (MXFP4: two neighbours
 // exchange their maxima), so a row is read once and nothing is kept outside
 // registers; bound by HBM: reads x, writes half a byte per value plus one byte
-// per block.  65536 rows of 7168 bf16, MXFP4: quantised 170 us (105% of the copy
-// rate), back 179 us (99%), from [gate | up] 362 us (88%, the rest the
+// per block.  65536 rows of 7168 bf16, MXFP4: quantised 169 us (105% of the copy
+// rate), back 181 us (98%), from [gate | up] 359 us (89%, the rest the
 // exponential's and the division's instructions), 8192 tokens to those 65536
 // sorted rows 80 us (69%: each row's scales are scattered four bytes at a time).
 #include <cuda_fp16.h>
@@ -27,7 +27,7 @@
 namespace mlr {
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 128;
 constexpr int kQDests = 512;  // (row, destination) pairs a block keeps in shared memory
 enum Source { kMatrix, kTokens, kSwiglu };
 
@@ -228,7 +228,7 @@ __device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], fl
 // the correctly rounded quotient but for about one in 10^6, which are one ulp
 // off.  It needs 1 / d to be a normal number, hence the bound on exp(-g): it
 // acts below g = -86.6, where g / d is under 3e-36 either way.  8192 x 8 rows of
-// 7168 bf16 take 584 us with __fdiv_rn, 406 us so; without any division or
+// 7168 bf16 took 584 us with __fdiv_rn, 406 us so; without any division or
 // exponential 300 us, what their bytes take.
 constexpr float kMaxExp = 0x1p125f;
 __device__ __forceinline__ void swiglu16(float (&v)[16], const float (&u)[16]) {
@@ -305,10 +305,10 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float* r) {
   return q;
 }
 
-// Five blocks per SM (at most 51 registers): the exponentials of the SwiGLU form
-// need the warps (8192 x 8 rows of 7168: 406 us against 422 unbounded).
+// Ten blocks per SM (at most 51 registers): the exponentials of the SwiGLU form
+// need the warps (8192 x 8 rows of 7168: 359 us, 386 with twelve).
 template <typename E_, int FMT, int SRC, int VB>
-__global__ void __launch_bounds__(kQThreads, 5)
+__global__ void __launch_bounds__(kQThreads, 10)
 quantize_kernel(const QuantParams p) {
   __shared__ Dest dest[kQDests];
   __shared__ __align__(16) E_ stages[VB == 0 ? kQThreads * 16 : 1];

@@ -788,7 +788,9 @@ int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t*
   E_* dp = static_cast<E_*>(d_rows);
   cudaError_t err;
   if constexpr (A != kPieces) {
-    const int lpt = row_threads((int)ceil_div((int64_t)H * sizeof(E_), 16), kBackLanes);
+    // strided rows take four times the loads: fewer threads per token leave more
+    // tokens in flight (1531 x 6 rows of 1111 float32: 24 us, with 128 28 us)
+    const int lpt = row_threads((int)ceil_div((int64_t)H * sizeof(E_), 16), A == kStrided ? kBackLanes / 2 : kBackLanes);
     err = launch_pdl(unpermute_backward_kernel<E_, KU, A>, dim3((unsigned)ceil_div(T, kBackThreads / lpt)),
                      dim3(kBackThreads), 0, stream, dyp, rp, pos, w, T, K, H, log2_of(lpt), dp, dw, d_status);
   } else {
