@@ -550,8 +550,8 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *           moe_fp4_pitch(cols) bytes (a multiple of 16), zero past cols
  *   scales  per 128 rows moe_fp4_scale_atoms(cols, fmt) atoms of 512 bytes; an
  *           atom holds 128 rows x 4 blocks, row r and block c at byte
- *           16 (r % 32) + 4 (r / 32) + c.  Blocks past cols are zero; rows
- *           past the last one are not written.
+ *           16 (r % 32) + 4 (r / 32) + c.  Blocks past cols are zero; what
+ *           stands for rows past the last one is undefined.
  * A stack of matrices has ceil(rows / 128) such row blocks for each.  Rows
  * sorted by expert have num_rows / 128 + num_experts (integer division) row
  * blocks, expert e's rows beginning at row block expert_offsets[e] / 128 + e.

@@ -18,7 +18,7 @@
 // per block.  65536 rows of 7168 bf16, MXFP4: quantised 169 us (105% of the copy
 // rate), back 181 us (98%), from [gate | up] 359 us (89%, the rest the
 // exponential's and the division's instructions), 8192 tokens to those 65536
-// sorted rows 80 us (69%: each row's scales are scattered four bytes at a time).
+// sorted rows 73 us (76%: their scales go through arrange_kernel).
 #include <cuda_fp16.h>
 
 #include "mlr_fp4.cuh"
@@ -49,6 +49,7 @@ struct QuantParams {
   uint8_t* codes;
   uint8_t* scales;
   int64_t pitch, block_bytes;  // bytes of a code row; of a 128-row block's atoms
+  int arrange;                 // kTokens: a row's scales one after another, for arrange_kernel
   int32_t* status;
 };
 
@@ -58,6 +59,7 @@ struct Dest {
   int64_t row, scale;
 };
 
+template <int SRC>
 __device__ __forceinline__ Dest sorted_dest(const QuantParams& p, int64_t r, int e) {
   const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
   if (o0 < 0 || r < o0 || r >= o1 || r >= p.P) {
@@ -65,7 +67,8 @@ __device__ __forceinline__ Dest sorted_dest(const QuantParams& p, int64_t r, int
     return Dest{-1, -1};
   }
   const int j = (int)r - o0;
-  return Dest{r, (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j)};
+  const int in_block = SRC == kTokens && p.arrange ? (j & 127) * (int)(p.block_bytes / 128) : fp4_scale_byte(j);
+  return Dest{r, (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + in_block};
 }
 
 // The expert of sorted row r: the last e with offsets[e] <= r; E if r is past
@@ -96,10 +99,10 @@ __device__ __forceinline__ Dest dest_of(const QuantParams& p, int64_t row, int k
       set_status(p.status, MLR_STATUS_INDEX);
       return Dest{-1, -1};
     }
-    return sorted_dest(p, q, e);
+    return sorted_dest<SRC>(p, q, e);
   }
   const int e = row_expert(p.offsets, p.E, row);
-  return e == p.E ? Dest{row, -1} : sorted_dest(p, row, e);
+  return e == p.E ? Dest{row, -1} : sorted_dest<SRC>(p, row, e);
 }
 
 // 32 bytes at a 32-byte boundary, one instruction.
@@ -369,14 +372,62 @@ quantize_kernel(const QuantParams p) {
     }
     if (!in) continue;
     constexpr int kLanes = FMT == MLR_FP4_MX ? 8 : 4;  // 16-column groups per atom
+    const int step = SRC == kTokens && p.arrange ? 4 : kAtomBytes;
     for (int k = 0; k < K; ++k) {
       const Dest d = dest[lr * K + k];
       if (d.row < 0) continue;
       if (g < p.ng)
         *reinterpret_cast<uint2*>(p.codes + d.row * p.pitch + 8 * g) = d.scale < 0 ? make_uint2(0, 0) : q;
       if (g % kLanes == 0 && d.scale >= 0)
-        *reinterpret_cast<uint32_t*>(p.scales + d.scale + (int64_t)(g / kLanes) * kAtomBytes) = s;
+        *reinterpret_cast<uint32_t*>(p.scales + d.scale + (int64_t)(g / kLanes) * step) = s;
     }
+  }
+}
+
+// Sorted rows' scales from row after row to atoms, in place, a 128-row block at
+// a time: through shared memory (rows an odd number of words apart), 512 bytes
+// a warp's store.
+//
+// Written straight to the atoms, each word of four scales of a token's K rows is
+// a 32-byte sector of its own in L2: of 8192 x 8 rows of 7168 bf16 in MXFP4 17 of
+// 80 us, in NVFP4, with twice the scales, 44 of 107.  Row after row and arranged
+// here it is 73 and 83 us (with 256 threads 80 and 84, with 1024 78 and 85).
+constexpr int kArrangeThreads = 512;
+
+__global__ void __launch_bounds__(kArrangeThreads)
+arrange_kernel(const QuantParams p, int atoms, uint32_t atoms_magic) {
+  extern __shared__ uint32_t words[];  // [128][atoms | 1]
+  __shared__ int rows;                 // of block b; 0: none
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.x;
+  if (threadIdx.x == 0) rows = 0;
+  __syncthreads();
+  // the expert whose row blocks hold b: all of them at once, a search takes their latency in turn
+  for (int e = threadIdx.x; e < p.E; e += kArrangeThreads) {
+    const int o0 = __ldg(p.offsets + e), o1 = __ldg(p.offsets + e + 1);
+    const int64_t left = (int64_t)o1 - o0 - 128 * ((int64_t)b - (o0 / 128 + e));
+    if (b >= o0 / 128 + e && b < o1 / 128 + e + 1 && left > 0) rows = (int)min(left, (int64_t)128);
+  }
+  __syncthreads();
+  const int n = rows;
+  if (n == 0) return;
+  uint32_t* const scales = reinterpret_cast<uint32_t*>(p.scales + b * p.block_bytes);
+  const int pitch = atoms | 1;
+  for (int i = threadIdx.x; i < n * atoms; i += kArrangeThreads) {
+    const int r = (int)__umulhi((uint32_t)i, atoms_magic);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(words + r * pitch + (i - r * atoms))),
+                 "l"(scales + i)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  for (int a = threadIdx.x >> 5; a < atoms; a += kArrangeThreads / 32) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = lane + 32 * i < n ? words[(lane + 32 * i) * pitch + a] : 0;
+    reinterpret_cast<uint4*>(scales + a * (kAtomBytes / 4))[lane] = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -545,6 +596,19 @@ bool dtype_ok(int32_t d) { return d == MLR_DTYPE_BF16 || d == MLR_DTYPE_F32; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 constexpr int kMaxCols = 1 << 19;
 
+// Whether tokens' scales take the way through arrange_kernel: only many words
+// repay its launch and its pass (8 rows per token, NVFP4: 1.8 M words 33.5 -> 30.1
+// us, 1.0 M 16.7 -> 17.3), and only where a token's words are written several
+// times (2 rows per token, 2.1 M words: 43 -> 49 us; 4 rows, 1.8 M: 45 -> 43).  A
+// block's words have to fit into shared memory (up to 25536 columns in NVFP4).
+constexpr int64_t kArrangeWords = 3 << 19;
+constexpr int kArrangeTopk = 4;
+constexpr int kArrangeSmem = 200 << 10;
+int arrange_smem(int atoms) { return 128 * 4 * (atoms | 1); }
+bool arranged(int64_t P, int K, int atoms) {
+  return K >= kArrangeTopk && P * atoms >= kArrangeWords && arrange_smem(atoms) <= kArrangeSmem;
+}
+
 // The widest vector that divides a row and its base's address; one thread's 16
 // bf16 columns are 32 bytes, which one 32-byte access moves in whole sectors.
 int vector_bytes(const void* base, int64_t row_bytes) {
@@ -568,6 +632,20 @@ int launch_quantize(const QuantParams& p, int vb, cudaStream_t stream) {
   return MLR_OK;
 }
 
+int launch_arrange(const QuantParams& p, int atoms, cudaStream_t stream) {
+  const int smem = arrange_smem(atoms);
+  cudaError_t err = cudaFuncSetAttribute(arrange_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kArrangeSmem);
+  if (err == cudaSuccess)
+    err = launch_pdl(arrange_kernel, dim3((unsigned)(p.P / 128 + p.E)), dim3(kArrangeThreads), smem, stream, p, atoms,
+                     (uint32_t)ceil_div(int64_t{1} << 32, atoms));
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();
+    return MLR_ERR_CUDA;
+  }
+  note_launch();
+  return MLR_OK;
+}
+
 // Fills the layout fields and launches; p has its source and destination set.
 template <int SRC>
 int quantize(QuantParams& p, int32_t dtype, int32_t fmt, cudaStream_t stream) {
@@ -583,12 +661,16 @@ int quantize(QuantParams& p, int32_t dtype, int32_t fmt, cudaStream_t stream) {
   p.block_bytes = (int64_t)atoms * kAtomBytes;
   p.rpb = rows_per_block(p.rows, p.nga, SRC == kTokens ? p.K : 1);
   p.ng_magic = (uint32_t)ceil_div(int64_t{1} << 32, p.nga);
+  p.arrange = SRC == kTokens && arranged(p.P, p.K, atoms);
   const int vb = vector_bytes(p.x, (int64_t)p.cols * es);
+  int code;
   if (dtype == MLR_DTYPE_BF16)
-    return fmt == MLR_FP4_MX ? launch_quantize<uint16_t, MLR_FP4_MX, SRC>(p, vb, stream)
+    code = fmt == MLR_FP4_MX ? launch_quantize<uint16_t, MLR_FP4_MX, SRC>(p, vb, stream)
                              : launch_quantize<uint16_t, MLR_FP4_NV, SRC>(p, vb, stream);
-  return fmt == MLR_FP4_MX ? launch_quantize<float, MLR_FP4_MX, SRC>(p, vb, stream)
-                           : launch_quantize<float, MLR_FP4_NV, SRC>(p, vb, stream);
+  else
+    code = fmt == MLR_FP4_MX ? launch_quantize<float, MLR_FP4_MX, SRC>(p, vb, stream)
+                             : launch_quantize<float, MLR_FP4_NV, SRC>(p, vb, stream);
+  return code == MLR_OK && p.arrange ? launch_arrange(p, atoms, stream) : code;
 }
 
 int check_quantize(int64_t cols, int32_t dtype, int32_t fmt, const float* tensor_scale) {

@@ -143,6 +143,41 @@ def test_quantize_permuted(cuda_device, fmt, dtype, T, K, E, C, masked):
     assert torch.equal(y, pm.moe_permute(direct, ids, E)[0])
 
 
+def scale_bytes(scales, block, row, count):
+    """[rows, count] scale bytes of rows `row` of row blocks `block`."""
+    c = torch.arange(count, device=scales.device)
+    at = (c // 4) * 512 + (16 * (row % 32) + 4 * (row // 32))[:, None] + c % 4
+    return scales.view(scales.shape[0], -1)[block[:, None], at]
+
+
+@pytest.mark.parametrize("fmt,dtype,T,K,E,C,masked", [
+    ("nvfp4", BF, 2100, 8, 40, 7168, 0.0), ("nvfp4", F32, 1300, 12, 300, 7001, 0.1), ("mxfp4", BF, 3300, 9, 7, 7168, 0.3),
+    ("mxfp4", F32, 900, 40, 3, 6000, 0.0), ("nvfp4", BF, 4100, 4, 700, 6500, 0.02), ("mxfp4", BF, 80, 200, 5, 16384, 0.0),
+    ("nvfp4", BF, 900, 8, 40, 25500, 0.0), ("nvfp4", BF, 900, 8, 40, 25600, 0.0), ("nvfp4", BF, 4000, 8, 2, 3200, 1.0)])
+def test_quantize_many_tokens(cuda_device, fmt, dtype, T, K, E, C, masked):
+    """Rows of many tokens hold the codes and scales of their tokens quantised
+    as a matrix; one expert has no row and one few."""
+    x = randn(T, C, seed=T, dtype=dtype)
+    ids = routing(T, K, E, seed=C, masked=masked, empty=(1,))
+    pos, off = pm.moe_sort_pairs(ids, E)
+    g = scale_of(x, fmt)
+    codes, scales = fp4.fp4_quantize_permuted(x, ids, pos, off, fmt, g, check=True)
+    ref_codes, ref_scales = fp4.fp4_quantize(x, fmt, g)
+    n = int(off[-1])
+    flat = pos.flatten().long()
+    token = torch.arange(T * K, device="cuda") // K
+    live = flat >= 0
+    src = torch.empty(T * K, dtype=torch.long, device="cuda")
+    src[torch.where(live, flat, ~flat)] = token
+    assert torch.equal(codes[:n], ref_codes[src[:n]]) and not codes[n:].any()
+    r, o = torch.arange(n, device="cuda"), off.long()
+    e = torch.searchsorted(o[1:], r, right=True)
+    j = r - o[e]
+    count = scales.shape[1] * 4
+    have = scale_bytes(scales, o[e] // 128 + e + j // 128, j % 128, count)
+    assert torch.equal(have, scale_bytes(ref_scales, src[:n] // 128, src[:n] % 128, count))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,K,E,C,masked", [(1, 1, 1, 16, 0.0), (50, 3, 4, 90, 0.2), (200, 2, 3, 64, 0.0), (9, 1, 2, 1001, 0.0)])
