@@ -34,6 +34,7 @@ enum Source { kMatrix, kTokens, kSwiglu };
 // What a block's rows are and where their codes and scales go.
 struct QuantParams {
   const void* x;
+  const void* x_end;
   int64_t rows;        // source rows
   int cols, ng, nga;   // columns; 16-column groups of the code pitch; of the atoms
   int rpb;             // source rows per block
@@ -117,79 +118,79 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-// Rows that no vector divides: a warp's 32 groups of 16 columns go element by
-// element through shared memory, half a warp to a group, so that each access
-// covers whole sectors.  p: this lane's group, n its columns (none if <= 0).
-template <typename T>
-__device__ __forceinline__ void load_staged(const T* p, int n, T* stage /* [32][16], the warp's */, int lane) {
-  __syncwarp();
+// The 32-bit words of n bytes at p, which no vector divides, from the 16-byte
+// vectors that hold them: W words, moved down by the misalignment in two steps
+// of words and one of bytes.  The caller sees to it that the vectors lie in the
+// tensor; words past the n bytes hold whatever follows.  50440 rows of 900 bf16
+// to NVFP4: 33 us, from [gate | up] 66 (element by element through shared
+// memory, half a warp to a group of 16 columns, 44 and 90).
+template <int W>
+__device__ __forceinline__ void load_shifted(const void* p, int n, uint32_t (&w)[W]) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  const uint4* base = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+  uint32_t t[W + 4] = {};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int owner = 2 * i + (lane >> 4), j = lane & 15;
-    const T* q = reinterpret_cast<const T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), owner));
-    const int m = __shfl_sync(0xffffffffu, n, owner);
-    stage[owner * 16 + j] = j < m ? __ldg(q + j) : T{};
-  }
-  __syncwarp();
+  for (int i = 0; i < W / 4 + 1; ++i)
+    if (16 * i < off + n) {
+      const uint4 q = __ldg(base + i);
+      t[4 * i] = q.x;
+      t[4 * i + 1] = q.y;
+      t[4 * i + 2] = q.z;
+      t[4 * i + 3] = q.w;
+    }
+#pragma unroll
+  for (int i = 0; i < W + 2; ++i) t[i] = off & 8 ? t[i + 2] : t[i];
+#pragma unroll
+  for (int i = 0; i < W + 1; ++i) t[i] = off & 4 ? t[i + 1] : t[i];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(t[i], t[i + 1], 8 * (off & 3));
 }
-template <typename T>
-__device__ __forceinline__ void store_staged(T* p, int n, const T* stage, int lane) {
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int owner = 2 * i + (lane >> 4), j = lane & 15;
-    T* q = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), owner));
-    const int m = __shfl_sync(0xffffffffu, n, owner);
-    if (j < m) q[j] = stage[owner * 16 + j];
-  }
-  __syncwarp();
+// Whether all those vectors lie in the tensor [lo, hi).
+__device__ __forceinline__ bool vectors_inside(const void* p, int n, const void* lo, const void* hi) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return (a & ~(uintptr_t)15) >= reinterpret_cast<uintptr_t>(lo) &&
+         ((a + n + 15) & ~(uintptr_t)15) <= reinterpret_cast<uintptr_t>(hi);
 }
 
 // 16 columns of a row as fp32, zeros past the end.  VB: the bytes of a vector
-// that divide a row and the base's address (32, 16, or 0: through `stage`).
+// that divide a row and the base's address (32, 16, or 0: none, the vectors
+// around them, and element by element at the ends of the tensor [lo, hi)).
 template <int VB>
-__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16], uint16_t* stage) {
-  if (VB > 0) {
-    uint32_t w[8] = {};
-    if (VB == 32) {
-      if (n > 0) load32(p, w);
+__device__ __forceinline__ void load16(const uint16_t* p, int n, float (&v)[16], const void* lo, const void* hi) {
+  uint32_t w[8] = {};
+  if (VB == 32) {
+    if (n > 0) load32(p, w);
+  } else if (VB == 16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (8 * h < n) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + h);
+        w[4 * h] = q.x;
+        w[4 * h + 1] = q.y;
+        w[4 * h + 2] = q.z;
+        w[4 * h + 3] = q.w;
+      }
+  } else if (n > 0) {
+    if (vectors_inside(p, 2 * n, lo, hi)) {
+      load_shifted(p, 2 * n, w);
+      if (n < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 2 * i + 1 < n ? w[i] : 2 * i < n ? w[i] & 0xffffu : 0u;
+      }
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (8 * h < n) {
-          const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + h);
-          w[4 * h] = q.x;
-          w[4 * h + 1] = q.y;
-          w[4 * h + 2] = q.z;
-          w[4 * h + 3] = q.w;
-        }
+      for (int i = 0; i < 16; ++i)
+        if (i < n) w[i / 2] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  } else {
-    const int lane = threadIdx.x & 31;
-    load_staged(p, n, stage, lane);
-    uint32_t w[8];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 q = reinterpret_cast<const uint4*>(stage + lane * 16)[h];
-      w[4 * h] = q.x;
-      w[4 * h + 1] = q.y;
-      w[4 * h + 2] = q.z;
-      w[4 * h + 3] = q.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
 template <int VB>
-__device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], float* stage) {
+__device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], const void* lo, const void* hi) {
   if (VB == 32) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -209,16 +210,18 @@ __device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], fl
       v[4 * h + 3] = q.w;
     }
   } else {
-    const int lane = threadIdx.x & 31;
-    load_staged(p, n, stage, lane);
+    uint32_t w[16] = {};
+    if (n > 0) {
+      if (vectors_inside(p, 4 * n, lo, hi)) {
+        load_shifted(p, 4 * n, w);
+      } else {
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const float4 q = reinterpret_cast<const float4*>(stage + lane * 16)[h];
-      v[4 * h] = q.x;
-      v[4 * h + 1] = q.y;
-      v[4 * h + 2] = q.z;
-      v[4 * h + 3] = q.w;
+        for (int i = 0; i < 16; ++i)
+          if (i < n) w[i] = __float_as_uint(__ldg(p + i));
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = i < n ? __uint_as_float(w[i]) : 0.f;
   }
 }
 
@@ -314,8 +317,6 @@ template <typename E_, int FMT, int SRC, int VB>
 __global__ void __launch_bounds__(kQThreads, 10)
 quantize_kernel(const QuantParams p) {
   __shared__ Dest dest[kQDests];
-  __shared__ __align__(16) E_ stages[VB == 0 ? kQThreads * 16 : 1];
-  E_* stage = stages + (VB == 0 ? (threadIdx.x >> 5) * 512 : 0);
   pdl_wait();
   pdl_trigger();
   const int K = SRC == kTokens ? p.K : 1;
@@ -337,11 +338,11 @@ quantize_kernel(const QuantParams p) {
     float v[16];
     if (SRC == kSwiglu) {
       float u[16];
-      load16<VB>(x + row * 2 * p.cols + c, n, v, stage);
-      load16<VB>(x + row * 2 * p.cols + p.cols + c, n, u, stage);
+      load16<VB>(x + row * 2 * p.cols + c, n, v, p.x, p.x_end);
+      load16<VB>(x + row * 2 * p.cols + p.cols + c, n, u, p.x, p.x_end);
       swiglu16(v, u);
     } else {
-      load16<VB>(x + row * p.cols + c, n, v, stage);
+      load16<VB>(x + row * p.cols + c, n, v, p.x, p.x_end);
     }
     float most = 0.f;
 #pragma unroll
@@ -458,61 +459,117 @@ __device__ __forceinline__ void from_e2m1x8(uint32_t w, uint32_t (&f)[4]) {
       : "r"(w));
 }
 
+// The number of a scale byte.
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  if (FMT == MLR_FP4_MX) return __uint_as_float(b == 0 ? 0x00400000u : b == 255 ? 0x7fc00000u : b << 23);
+  float s;
+  asm("{\n\t.reg .b32 p;\n\t.reg .f16 a, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 p, %1;\n\tmov.b32 {a, b}, p;\n\tcvt.f32.f16 %0, a;\n\t}"
+      : "=f"(s)
+      : "h"((uint16_t)b));
+  return s;
+}
+
+// Where the scales of a row are (.scale, -1: past the last expert's rows) and
+// the matrix whose tensor scale it has (.row).
+__device__ __forceinline__ Dest row_source(const DequantParams& p, int64_t row) {
+  if (p.offsets == nullptr) {
+    const int64_t g = row / p.group_rows, r = row - g * p.group_rows;
+    return Dest{g, (g * p.group_blocks + r / 128) * p.block_bytes + fp4_scale_byte((int)(r & 127))};
+  }
+  Dest d{0, -1};
+  const int e = row_expert(p.offsets, p.E, row);
+  if (e < p.E) {
+    const int o0 = __ldg(p.offsets + e);
+    const int j = (int)row - o0;
+    if (o0 >= 0 && j >= 0) d.scale = (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j);
+  }
+  return d;
+}
+template <int FMT>
+__device__ __forceinline__ float source_scale(const DequantParams& p, const Dest& d, int block) {
+  return scale_value<FMT>(__ldg(p.scales + d.scale + (int64_t)(block / 4) * kAtomBytes + block % 4));
+}
+template <int FMT>
+__device__ __forceinline__ float matrix_scale(const DequantParams& p, const Dest& d) {
+  return FMT == MLR_FP4_NV && p.tensor_scale != nullptr ? __ldg(p.tensor_scale + d.row) : 1.f;
+}
+// n bytes in W words to p, which no vector divides, as the 16-byte vectors from
+// p's next boundary on: the last one takes its rest from the next lane, if that
+// lane's bytes follow.  What no vector covers (at the ends of a warp's or a
+// row's run) goes value by value.  T: the values' unsigned type; n = 0: none.
+// All lanes of the warp call it.  50440 rows of 900 bf16 from NVFP4: 34 us
+// (value by value through shared memory 42; a thread to eight values from a
+// boundary on, whatever their blocks and rows, 46).
+template <typename T, int W>
+__device__ __forceinline__ void store_shifted(void* p, int n, const uint32_t (&w)[W]) {
+  const unsigned long long a = reinterpret_cast<unsigned long long>(p);
+  const int lane = threadIdx.x & 31;
+  const int next_n = __shfl_down_sync(0xffffffffu, n, 1);
+  const bool joined = __shfl_down_sync(0xffffffffu, a, 1) == a + n && n == 4 * W && lane < 31;
+  const bool follows = __shfl_up_sync(0xffffffffu, joined, 1) && lane > 0;
+  uint32_t t[W + 4];
+#pragma unroll
+  for (int i = 0; i < W; ++i) t[i] = w[i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[W + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  const int head = (int)(-a & 15), held = n + (joined ? min(next_n, 16) : 0);
+#pragma unroll
+  for (int i = 0; i < W + 2; ++i) t[i] = head & 8 ? t[i + 2] : t[i];
+#pragma unroll
+  for (int i = 0; i < W + 1; ++i) t[i] = head & 4 ? t[i + 1] : t[i];
+  uint4* const base = reinterpret_cast<uint4*>(a + head);
+  int done = min(head, n);  // the bytes from `done` on are neither the head nor in a vector
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i)
+    if (head + 16 * (i + 1) <= held) {
+      uint32_t u[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = __funnelshift_r(t[4 * i + j], t[4 * i + j + 1], 8 * (head & 3));
+      base[i] = make_uint4(u[0], u[1], u[2], u[3]);
+      done = head + 16 * (i + 1);
+    }
+  const int skip = follows && n >= head ? head : 0;  // the lane before has written the head
+  if (skip < min(head, n) || done < n) {
+#pragma unroll
+    for (int i = 0; i < 4 * W / (int)sizeof(T); ++i) {
+      const int b = i * (int)sizeof(T);
+      if (b < n && b >= skip && (b < head || b >= done))
+        reinterpret_cast<T*>(p)[i] = (T)(sizeof(T) == 4 ? w[i * sizeof(T) / 4] : w[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
 // value = (code x block scale) x tensor scale, rounded once to the output type
 // (code x block scale is exact).  Rows past the last expert's are zeros.
 template <typename O, int FMT, int VB>
 __global__ void __launch_bounds__(kQThreads)
 dequantize_kernel(const DequantParams p) {
-  __shared__ Dest src[kQDests];  // .scale as in the quantisation, .row: the matrix
+  __shared__ Dest src[kQDests];
   pdl_wait();
   pdl_trigger();
   const int64_t r0 = (int64_t)blockIdx.x * p.rpb;
   const int nr = (int)min((int64_t)p.rpb, p.rows - r0);
-  for (int i = threadIdx.x; i < nr; i += kQThreads) {
-    const int64_t row = r0 + i;
-    Dest d{0, -1};
-    if (p.offsets == nullptr) {
-      const int64_t g = row / p.group_rows, r = row - g * p.group_rows;
-      d = Dest{g, (g * p.group_blocks + r / 128) * p.block_bytes + fp4_scale_byte((int)(r & 127))};
-    } else {
-      const int e = row_expert(p.offsets, p.E, row);
-      if (e < p.E) {
-        const int o0 = __ldg(p.offsets + e);
-        const int j = (int)row - o0;
-        if (o0 >= 0 && j >= 0)
-          d.scale = (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + fp4_scale_byte(j);
-      }
-    }
-    src[i] = d;
-  }
+  for (int i = threadIdx.x; i < nr; i += kQThreads) src[i] = row_source(p, r0 + i);
   __syncthreads();
-  __shared__ __align__(16) O stages[VB == 0 ? kQThreads * 16 : 1];
-  O* stage = stages + (VB == 0 ? (threadIdx.x >> 5) * 512 : 0);
   O* out = static_cast<O*>(p.out);
   const int total = nr * p.ng;
-  for (int i0 = 0; i0 < total; i0 += kQThreads) {  // whole warps: they stage together
+  for (int i0 = 0; i0 < total; i0 += kQThreads) {  // whole warps: store_shifted
     const int i = i0 + threadIdx.x;
     const bool in = i < total;
     const int lr = in ? (int)__umulhi((uint32_t)i, p.ng_magic) : 0;
     const int g = in ? i - lr * p.ng : 0;
     const int64_t row = r0 + lr;
-    const int c = 16 * g, n = in ? min(16, p.cols - c) : 0;
+    const int c = 16 * g, n = in ? max(0, min(16, p.cols - c)) : 0;
     const Dest d = src[lr];
     float s = 0.f, ts = 1.f;
     uint2 q = make_uint2(0, 0);
     if (d.scale >= 0 && n > 0) {
       q = __ldg(reinterpret_cast<const uint2*>(p.codes + row * p.pitch + 8 * g));
       const int b = FMT == MLR_FP4_MX ? g / 2 : g;
-      const uint32_t sb = __ldg(p.scales + d.scale + (int64_t)(b / 4) * kAtomBytes + b % 4);
-      if (FMT == MLR_FP4_MX) {
-        s = __uint_as_float(sb == 0 ? 0x00400000u : sb == 255 ? 0x7fc00000u : sb << 23);
-      } else {
-        asm("{\n\t.reg .b32 p;\n\t.reg .f16 a, b;\n\t"
-            "cvt.rn.f16x2.e4m3x2 p, %1;\n\tmov.b32 {a, b}, p;\n\tcvt.f32.f16 %0, a;\n\t}"
-            : "=f"(s)
-            : "h"((uint16_t)sb));
-        if (p.tensor_scale != nullptr) ts = __ldg(p.tensor_scale + d.row);
-      }
+      s = source_scale<FMT>(p, d, b);
+      ts = matrix_scale<FMT>(p, d);
     }
     float2 v[8];
     const float2 s2 = make_float2(s, s), t2 = make_float2(ts, ts);
@@ -539,16 +596,19 @@ dequantize_kernel(const DequantParams p) {
           }
           if (8 * h < n) store32(o + 8 * h, w);
         }
-      } else if (VB == 16) {
+      } else if (VB == 0) {
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          w[2 * j] = __float_as_uint(v[j].x);
+          w[2 * j + 1] = __float_as_uint(v[j].y);
+        }
+        store_shifted<uint32_t>(o, 4 * n, w);
+      } else {
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           if (4 * h < n)
             reinterpret_cast<float4*>(o)[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
-      } else {
-        float4* mine = reinterpret_cast<float4*>(stage + (threadIdx.x & 31) * 16);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) mine[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
-        store_staged(o, n, stage, threadIdx.x & 31);
       }
     } else {
       uint32_t w[8];
@@ -556,15 +616,12 @@ dequantize_kernel(const DequantParams p) {
       for (int j = 0; j < 8; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[j].y), "f"(v[j].x));
       if (VB == 32) {
         if (n > 0) store32(o, w);
-      } else if (VB == 16) {
+      } else if (VB == 0) {
+        store_shifted<uint16_t>(o, 2 * n, w);
+      } else {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
           if (8 * h < n) reinterpret_cast<uint4*>(o)[h] = make_uint4(w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]);
-      } else {
-        uint4* mine = reinterpret_cast<uint4*>(stage + (threadIdx.x & 31) * 16);
-        mine[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        mine[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        store_staged(o, n, stage, threadIdx.x & 31);
       }
     }
   }
@@ -654,6 +711,7 @@ int quantize(QuantParams& p, int32_t dtype, int32_t fmt, cudaStream_t stream) {
   if (p.x == nullptr || p.codes == nullptr || p.scales == nullptr ||
       (reinterpret_cast<uintptr_t>(p.x) & (es - 1)) != 0 || !aligned16(p.codes) || !aligned16(p.scales))
     return MLR_ERR_INVALID;
+  p.x_end = static_cast<const char*>(p.x) + p.rows * p.cols * (SRC == kSwiglu ? 2 : 1) * es;
   p.pitch = fp4_pitch(p.cols);
   p.ng = (int)(p.pitch / 8);
   const int atoms = fp4_atoms(p.cols, fmt);

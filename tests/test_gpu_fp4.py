@@ -143,6 +143,40 @@ def test_quantize_permuted(cuda_device, fmt, dtype, T, K, E, C, masked):
     assert torch.equal(y, pm.moe_permute(direct, ids, E)[0])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 2), (70, 3), (9, 8), (33, 17), (130, 48), (40, 90), (5, 1001), (300, 96)])
+def test_any_address(cuda_device, fmt, dtype, rows, cols):
+    """Rows at every address their type allows give what rows at a 512-byte
+    boundary give, read nothing and write nothing around them."""
+    x = randn(rows, cols, seed=cols, dtype=dtype)
+    gu = randn(rows, 2 * cols, seed=rows, dtype=dtype)
+    off = torch.tensor([0, rows // 3, rows // 3, rows], dtype=torch.int32, device="cuda")
+    g = scale_of(x, fmt)
+    codes, scales = fp4.fp4_quantize(x, fmt, g)
+    back = fp4.fp4_dequantize(codes, scales, cols, fmt, g, dtype=dtype)
+    h = fp4.fp4_dequantize(*fp4.fp4_quantize_swiglu(gu, off, fmt, g), cols, fmt, g, expert_offsets=off, dtype=dtype)
+
+    def at(t, k):  # t's values k elements past a boundary, NaN around them
+        buf = torch.full((t.numel() + 32,), math.nan, dtype=dtype, device="cuda")
+        view = buf[k:k + t.numel()].view(t.shape)
+        view.copy_(t)
+        return buf, view
+
+    for k in range(16 // x.element_size() + 1):
+        c, s = fp4.fp4_quantize(at(x, k)[1], fmt, g)
+        assert torch.equal(c, codes)
+        r = torch.arange(rows, device="cuda")
+        n = scales.shape[1] * 4
+        assert torch.equal(scale_bytes(s, r // 128, r % 128, n), scale_bytes(scales, r // 128, r % 128, n))
+        buf, out = at(torch.zeros_like(x), k)
+        fp4.fp4_dequantize(c, s, cols, fmt, g, dtype=dtype, out=out)
+        assert torch.equal(out, back)
+        assert buf[:k].isnan().all() and buf[k + x.numel():].isnan().all()
+        hk = fp4.fp4_quantize_swiglu(at(gu, k)[1], off, fmt, g)
+        assert torch.equal(fp4.fp4_dequantize(*hk, cols, fmt, g, expert_offsets=off, dtype=dtype), h)
+
+
 def scale_bytes(scales, block, row, count):
     """[rows, count] scale bytes of rows `row` of row blocks `block`."""
     c = torch.arange(count, device=scales.device)
