@@ -158,62 +158,87 @@ sort_scan_kernel(int32_t* __restrict__ cnt, int64_t Gp, int32_t* __restrict__ to
   if (threadIdx.x == 0) tot[blockIdx.x] = carry;
 }
 
-// A row off the 16-byte grid, copied to its K rows by one warp: a segment of it
-// goes through shared memory in the source's alignment, from where every
-// destination takes 16-byte pieces in its own; the ends that share 16 bytes
-// with another row go element by element.  Copied element by element
-// throughout, 8192 x 6 rows of 1111 bf16 took 61 us (sort included).
-constexpr int kSegBytes = 2048;
-struct __align__(16) Segment {
-  uint32_t w[(kSegBytes + 48) / 4];
-};
+// The aligned 16 bytes at a of the array [base, end); where they reach past one
+// of its ends, the elements inside, zeros elsewhere.
 template <typename E_>
-__device__ void copy_unaligned(const char* __restrict__ src, int64_t bytes, char* __restrict__ rows,
-                               const int* __restrict__ place, int K, Segment& sm, int64_t seg0, int64_t seg_step,
+__device__ __forceinline__ uint4 load_piece(const char* a, const E_* base, const E_* end) {
+  if (a >= reinterpret_cast<const char*>(base) && a + 16 <= reinterpret_cast<const char*>(end))
+    return __ldg(reinterpret_cast<const uint4*>(a));
+  uint4 q = make_uint4(0, 0, 0, 0);
+  E_* e = reinterpret_cast<E_*>(&q);
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(E_); ++i) {
+    const E_* p = reinterpret_cast<const E_*>(a) + i;
+    if (p >= base && p < end) e[i] = __ldg(p);
+  }
+  return q;
+}
+// Bytes s to s + 16 of a and b one after the other (s a multiple of the element).
+template <typename E_>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
+  if (sizeof(E_) == 2)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (s & 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The part of a row that a warp copies at a time.
+constexpr int kItemBytes = 2048;
+
+// One such part (its aligned pieces from byte b on) of a row off the 16-byte
+// grid, copied to the K rows by a warp: a lane holds four pieces and what follows
+// each, of which every destination takes 16-byte pieces in its own alignment;
+// the row's ends, which share 16 bytes with another row, go element by element.
+// [x, end): the array; bytes: of the row, at most 2^26.  8192 x 6 rows of 1111
+// bf16, sort included: 34 us (through shared memory 41, element by element 61);
+// 3000 x 2 of 7001 float32: 53 us (77).
+template <typename E_>
+__device__ void copy_unaligned(const char* __restrict__ src, int bytes, char* __restrict__ rows,
+                               const int* __restrict__ place, int K, const E_* x, const E_* end, int b,
                                int lane) {
-  char* sb = reinterpret_cast<char*>(sm.w);
+  constexpr int kVec = kItemBytes / 512, es = (int)sizeof(E_);
   const int ps = (int)(reinterpret_cast<uintptr_t>(src) & 15);
-  for (int64_t b0 = seg0 * kSegBytes; b0 < bytes; b0 += seg_step * kSegBytes) {
-    const int span = (int)min(bytes - b0, (int64_t)kSegBytes + 16);
-    __syncwarp();
-    for (int i = lane; 16 * i < ps + span; i += 32) {
-      const char* q = src + b0 - ps + 16 * i;
-      if (q >= src && q + 16 <= src + bytes) {
-        reinterpret_cast<uint4*>(sb)[i] = __ldg(reinterpret_cast<const uint4*>(q));
-      } else {
-        for (int e = 0; e < 16; e += (int)sizeof(E_))
-          if (q + e >= src && q + e < src + bytes)
-            *reinterpret_cast<E_*>(sb + 16 * i + e) = __ldg(reinterpret_cast<const E_*>(q + e));
-      }
+  uint4 v[kVec], next[kVec];
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) {
+    const int at = b + 16 * (32 * u + lane);
+    v[u] = at < ps + bytes ? load_piece<E_>(src - ps + at, x, end) : make_uint4(0, 0, 0, 0);
+  }
+  uint4 past = make_uint4(0, 0, 0, 0);
+  if (lane == 31 && b + kVec * 512 < ps + bytes) past = load_piece<E_>(src - ps + b + kVec * 512, x, end);
+#pragma unroll
+  for (int u = 0; u < kVec; ++u) {
+    const uint4 t = v[u], f = u + 1 < kVec ? v[u + 1 < kVec ? u + 1 : 0] : past;
+    // lane 31's neighbour is lane 0 of the next 32 pieces
+    const uint4 give = lane == 0 && u + 1 < kVec ? f : t;
+    next[u].x = __shfl_sync(0xffffffffu, give.x, (lane + 1) & 31);
+    next[u].y = __shfl_sync(0xffffffffu, give.y, (lane + 1) & 31);
+    next[u].z = __shfl_sync(0xffffffffu, give.z, (lane + 1) & 31);
+    next[u].w = __shfl_sync(0xffffffffu, give.w, (lane + 1) & 31);
+    if (u + 1 == kVec && lane == 31) next[u] = past;
+  }
+  for (int k = 0; k < K; ++k) {
+    const int at = place[k];
+    char* dst = rows + (int64_t)(at < 0 ? ~at : at) * bytes;
+    const int off = (int)(-reinterpret_cast<uintptr_t>(dst) & 15);  // to the first 16-byte piece
+    const int r = (ps + off) & 15;
+#pragma unroll
+    for (int u = 0; u < kVec; ++u) {
+      if (b + 512 * u >= ps + bytes) break;
+      const int d = b + 16 * (32 * u + lane) + r - ps;
+      if (d >= 0 && d + 16 <= bytes)
+        *reinterpret_cast<uint4*>(dst + d) = at < 0 ? make_uint4(0, 0, 0, 0) : shifted<E_>(v[u], next[u], r);
     }
-    __syncwarp();
-    for (int k = 0; k < K; ++k) {
-      const int at = place[k];
-      char* dst = rows + (int64_t)(at < 0 ? ~at : at) * bytes;
-      const int off = (int)(-reinterpret_cast<uintptr_t>(dst) & 15);  // to the first 16-byte piece
-      const int m = (ps + off) & 3, w0 = (ps + off) >> 2;
-      for (int i = lane; 16 * i < kSegBytes && b0 + off + 16 * i + 16 <= bytes; i += 32) {
-        const uint32_t* w = sm.w + w0 + 4 * i;
-        uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-        if (m != 0) {
-          v.x = __funnelshift_r(v.x, v.y, 16);
-          v.y = __funnelshift_r(v.y, v.z, 16);
-          v.z = __funnelshift_r(v.z, v.w, 16);
-          v.w = __funnelshift_r(v.w, w[4], 16);
-        }
-        *reinterpret_cast<uint4*>(dst + b0 + off + 16 * i) = at < 0 ? make_uint4(0, 0, 0, 0) : v;
-      }
-      // the row's first bytes, and its last ones
-      constexpr int es = (int)sizeof(E_);
-      const int head = b0 == 0 ? (int)min((int64_t)off, bytes) : 0;
-      if (lane * es < head)
-        *reinterpret_cast<E_*>(dst + lane * es) = at < 0 ? E_{} : *reinterpret_cast<const E_*>(sb + ps + lane * es);
-      const int64_t t0 = bytes <= off ? bytes : off + (bytes - off) / 16 * 16;  // end of the 16-byte pieces
-      if (t0 >= b0 && t0 < b0 + kSegBytes) {
-        const int64_t t = t0 + lane * es;
-        if (t < bytes)
-          *reinterpret_cast<E_*>(dst + t) = at < 0 ? E_{} : *reinterpret_cast<const E_*>(sb + ps + (t - b0));
-      }
+    if (b == 0) {  // the row's first bytes (lanes 0 to 7), and its last ones (16 to 23)
+      const int tail = bytes <= off ? bytes : off + (bytes - off) / 16 * 16;  // end of the 16-byte pieces
+      const int t = lane < 16 ? lane * es : tail + (lane - 16) * es;
+      if (t < (lane < 16 ? min(off, bytes) : bytes))
+        *reinterpret_cast<E_*>(dst + t) = at < 0 ? E_{} : __ldg(reinterpret_cast<const E_*>(src + t));
     }
   }
 }
@@ -227,8 +252,9 @@ template <int VB> struct CopyElement;
 template <> struct CopyElement<4> { using type = uint32_t; };
 template <> struct CopyElement<2> { using type = uint16_t; };
 
+// Rows off the grid: four blocks per SM (9836 x 5 rows of 1513 bf16: 46 us, three 52).
 template <int VB, bool ONE>
-__global__ void __launch_bounds__(kSortThreads)
+__global__ void __launch_bounds__(kSortThreads, VB < 16 ? 4 : 1)
 permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int T, int K, int E, int tpb, int64_t Gp,
                int64_t row_bytes /* 0: sort only */, void* __restrict__ rows,
                int32_t* __restrict__ pair_pos, int32_t* __restrict__ offsets, const int32_t* __restrict__ cnt,
@@ -279,38 +305,54 @@ permute_kernel(const void* __restrict__ x, const int32_t* __restrict__ ids, int 
     for (int e = tid; e <= E; e += kSortThreads) offsets[e] = start[e];
   if (row_bytes == 0) return;
   __syncthreads();
-  // each piece of a token's row is read once and written to its K rows
+  // each piece of a token's row is read once and written to its K rows; a warp
+  // takes a part of 2 KB at a time, as a block may have fewer tokens than warps
+  // (4096 x 8 rows of 4 KB: 31.5 us, a token to a warp 36)
+  auto row_items = [&](int64_t bytes) {
+    return (int)ceil_div(ceil_div(bytes, kItemBytes) - (int64_t)blockIdx.y, (int64_t)gridDim.y);
+  };
   const int lane = tid & 31, warp = tid >> 5;
   if constexpr (VB < 16) {
     using V = typename CopyElement<VB>::type;
-    __shared__ Segment seg[kSortThreads / 32];
-    for (int i = warp; i < nt; i += kSortThreads / 32)
-      copy_unaligned<V>(static_cast<const char*>(x) + (t0 + i) * row_bytes, row_bytes, static_cast<char*>(rows),
-                        place + i * K, K, seg[warp], blockIdx.y, gridDim.y, lane);
+    const V* end = static_cast<const V*>(x) + T * (row_bytes / (int)sizeof(V));
+    const int items = row_items(row_bytes + 15);
+    for (int it = warp; it < nt * items; it += kSortThreads / 32) {
+      const int i = it / items;
+      const int b = ((it - i * items) * (int)gridDim.y + (int)blockIdx.y) * kItemBytes;
+      copy_unaligned<V>(static_cast<const char*>(x) + (t0 + i) * row_bytes, (int)row_bytes, static_cast<char*>(rows),
+                        place + i * K, K, static_cast<const V*>(x), end, b, lane);
+    }
   } else {
-    const int64_t nvec = row_bytes / 16;
-    // a warp per token, or for long rows the block, so that their copies are
+    // a warp per part, or for long rows the block, so that their copies are
     // written in long runs (8192 x 8 rows of 14 KB: 183 us, by warps 197;
     // 16384 x 4 rows of 2 KB: 50 us, by warps 38)
+    const int64_t nvec = row_bytes / 16;
     const uint4* xv = static_cast<const uint4*>(x);
     uint4* rv = static_cast<uint4*>(rows);
-    constexpr int kLanes = VB == 32 ? kSortThreads : 32;
-    const int64_t step = (int64_t)gridDim.y * kLanes;
-    for (int i = tid / kLanes; i < nt; i += kSortThreads / kLanes) {
+    // vectors c, c + step, c + 2 step and c + 3 step of the block's token i
+    auto copy = [&](int i, int64_t c, int64_t step) {
       const uint4* src = xv + (t0 + i) * nvec;
-      const int* pl = place + i * K;
-      for (int64_t c = (int64_t)blockIdx.y * kLanes + tid % kLanes; c < nvec; c += 4 * step) {
-        uint4 v[4];
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (c + u * step < nvec) v[u] = __ldg(src + c + u * step);
+      for (int k = 0; k < K; ++k) {
+        const int at = place[i * K + k];
+        uint4* dst = rv + (int64_t)(at < 0 ? ~at : at) * nvec;
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-          if (c + u * step < nvec) v[u] = __ldg(src + c + u * step);
-        for (int k = 0; k < K; ++k) {
-          const int at = pl[k];
-          uint4* dst = rv + (int64_t)(at < 0 ? ~at : at) * nvec;
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (c + u * step < nvec) dst[c + u * step] = at < 0 ? make_uint4(0, 0, 0, 0) : v[u];
-        }
+          if (c + u * step < nvec) dst[c + u * step] = at < 0 ? make_uint4(0, 0, 0, 0) : v[u];
+      }
+    };
+    if (VB == 32) {
+      const int64_t step = (int64_t)gridDim.y * kSortThreads;
+      for (int i = 0; i < nt; ++i)
+        for (int64_t c = (int64_t)blockIdx.y * kSortThreads + tid; c < nvec; c += 4 * step) copy(i, c, step);
+    } else {
+      const int items = row_items(row_bytes);
+      for (int it = warp; it < nt * items; it += kSortThreads / 32) {
+        const int i = it / items;
+        copy(i, ((int64_t)(it - i * items) * gridDim.y + blockIdx.y) * (kItemBytes / 16) + lane, 32);
       }
     }
   }
@@ -350,21 +392,6 @@ __device__ __forceinline__ float widen1(uint16_t v) { return __uint_as_float((ui
 __device__ __forceinline__ void narrow1(float v, float& q) { q = v; }
 __device__ __forceinline__ void narrow1(float v, uint16_t& q) { q = f32_to_bf16_bits(v); }
 
-// The aligned 16 bytes at a of the array [base, end); where they reach past one
-// of its ends, the elements inside, zeros elsewhere.
-template <typename E_>
-__device__ __forceinline__ uint4 load_piece(const char* a, const E_* base, const E_* end) {
-  if (a >= reinterpret_cast<const char*>(base) && a + 16 <= reinterpret_cast<const char*>(end))
-    return __ldg(reinterpret_cast<const uint4*>(a));
-  uint4 q = make_uint4(0, 0, 0, 0);
-  E_* e = reinterpret_cast<E_*>(&q);
-#pragma unroll
-  for (int i = 0; i < 16 / (int)sizeof(E_); ++i) {
-    const E_* p = reinterpret_cast<const E_*>(a) + i;
-    if (p >= base && p < end) e[i] = __ldg(p);
-  }
-  return q;
-}
 // How a thread takes 16 bytes of a row.  kWhole: rows and bases are multiples of
 // 16 bytes.  kPieces (bf16 rows off that grid): in the two aligned pieces that
 // they lie in, the second one mostly from L1, and shifted.  kStrided (float32
@@ -388,20 +415,6 @@ __device__ __forceinline__ void store_strided(float* r, int c, int step, int H, 
     if (c + i * step < H) r[c + i * step] = __uint_as_float(w[i]);
 }
 __device__ __forceinline__ void store_strided(uint16_t*, int, int, int, const uint4&) {}
-
-// Bytes s to s + 16 of a and b one after the other (s a multiple of the element).
-template <typename E_>
-__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int s) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = s & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = s & 4 ? w[i + 1] : w[i];
-  if (sizeof(E_) == 2)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8 * (s & 2));
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // The threads of a token: a power of two, so that short rows share a block.
 int row_threads(int nv, int most) {
@@ -736,7 +749,7 @@ int launch_permute(const SortPlan& s, const void* x, const int32_t* ids, int T, 
   const dim3 grid((unsigned)s.G, (unsigned)slices);
   const size_t smem = (size_t)(E + 2) * 4 + (s.one ? (size_t)(E + 1) * 4 : 0);
   auto run = [&](auto kernel) {
-    if (smem > 24 * 1024 &&  // with the segments past the 48 KB that need no opt-in
+    if (smem > 40 * 1024 &&  // with the static part past the 48 KB that need no opt-in
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
       return MLR_ERR_CUDA;
     if (launch_pdl(kernel, grid, dim3(kSortThreads), smem, stream, x, ids, T, K, E, s.tpb, s.Gp, row_bytes, rows, pair_pos,
