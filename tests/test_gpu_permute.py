@@ -4,6 +4,8 @@ The order and the copied rows are exact.  Tolerances: an output rounded once to
 type u (2^-8 bf16, 2^-24 float32, relative) after a float32 sum of n terms is
 within u |ref| + (n + 1) 2^-23 sum|terms| of the exact sum, whatever the order.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -195,6 +197,32 @@ def test_unaligned_views(cuda_device):
     a, b = pm.moe_unpermute_backward(x, rows, pos, w), pm.moe_unpermute_backward(xu, ru, pos, w)
     assert torch.equal(a[0], b[0])
     assert torch.allclose(a[1], b[1], rtol=1e-5, atol=(H + 1) * 2.0 ** -23 * H)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,K,E,H", [(3, 2, 4, 1), (70, 3, 5, 3), (9, 4, 3, 8), (600, 2, 7, 64), (300, 3, 9, 256),
+                                     (21, 5, 6, 1111), (5, 2, 3, 1024), (1100, 8, 20, 37)])
+def test_copies_at_any_address(cuda_device, dtype, T, K, E, H):
+    """x and rows at every address their type allows, NaN around both: the rows
+    are those at 512-byte boundaries, nothing around x is read into them and
+    nothing around rows is written."""
+    x, ids, _ = case(T, K, E, H, dtype, seed=H, masked=0.1)
+    want, pos, off = pm.moe_permute(x, ids, E)
+
+    def at(shape, k):  # a view k elements past a boundary, NaN around it
+        n = math.prod(shape)
+        buf = torch.full((n + 32,), math.nan, dtype=dtype, device="cuda")
+        return buf, buf[k:k + n].view(shape)
+
+    per = 16 // x.element_size()
+    for k in range(per + 1):
+        for j in range(per):
+            _, xk = at(x.shape, k)
+            xk.copy_(x)
+            buf, rows = at(want.shape, j)
+            pm.moe_permute(xk, ids, E, rows=rows)
+            assert torch.equal(rows, want)
+            assert buf[:j].isnan().all() and buf[j + rows.numel():].isnan().all()
 
 
 def test_buffers_streams_and_repeats(cuda_device):
