@@ -443,9 +443,17 @@ int row_threads(int nv, int most) {
 // KU rows are loaded before any is added,
 // without branches, so that their loads are in flight together.
 constexpr int kSumThreads = 128;
+// As many that fewest of the last ones have nothing to do (8192 x 6 rows of 1111
+// bf16, 139 vectors: 34 us with 16, 41 with 128; 14599 x 4 of 640, 80: 18 and 21).
+int sum_threads(int nv) {
+  int best = row_threads(nv, kSumThreads);
+  for (int l = best / 2; l >= 8; l /= 2)
+    if (10 * round_up(nv, l) <= 9 * round_up(nv, best)) best = l;
+  return best;
+}
 // Vectors per thread, so that few rows per token leave as many loads in flight
 // (13273 rows of 5656 float32, top-1: 87 us, with one vector 160).
-template <int KU, RowAccess A> constexpr int kVecs = A != kWhole || KU == 8 ? 1 : KU == 4 ? 2 : 4;
+template <int KU, RowAccess A> constexpr int kVecs = A != kWhole || KU >= 6 ? 1 : KU == 4 ? 2 : 4;
 template <typename E_, int KU, RowAccess A>
 __global__ void __launch_bounds__(kSumThreads)
 unpermute_kernel(const E_* __restrict__ rows, const int32_t* __restrict__ pair_pos, const float* __restrict__ w, int T,
@@ -649,8 +657,9 @@ unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows
 // own aligned 16-byte pieces, with the row of rows (in the same pieces, unless
 // the two bases differ) and the token's dy from shared memory at the piece's
 // columns; the ends that share 16 bytes with another row go element by element.
-// One block per token, a warp for rows of up to 512 bytes, four rows in flight (8192 x 6
-// rows of 1111 bf16: 84 us, with eight rows 109 us, element by element 144 us).
+// One block per token, 64 threads or for rows of up to 1 KB a warp (8192 x 6 rows
+// of 1111 bf16: 62 us, with 128 threads 68, element by element 144; 10000 x 6 of
+// 461: 40, with 64 threads 42).
 constexpr int kBackSegBytes = 4096;
 template <typename E_, int KU, int LANES>
 __global__ void __launch_bounds__(LANES)
@@ -681,7 +690,7 @@ unpermute_backward_unaligned_kernel(const E_* __restrict__ dy, const E_* __restr
       __syncthreads();
       for (int i = lt; i < span; i += LANES) seg[i] = __ldg(dy + t * H + b0 + i);
       __syncthreads();
-      for (int i = lt * N; i < kSegCols; i += LANES * N) {
+      for (int i = lt * N; i < min(H - b0, kSegCols); i += LANES * N) {
         uint4 v[KU];
         bool piece[KU];
 #pragma unroll
@@ -785,7 +794,7 @@ int log2_of(int n) {
 template <typename E_, int KU, RowAccess A>
 int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int T, int K, int H, void* y,
                        int32_t* d_status, cudaStream_t stream) {
-  const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16 * kVecs<KU, A>), lpt = row_threads(nv, kSumThreads);
+  const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16 * kVecs<KU, A>), lpt = sum_threads(nv);
   const int64_t col_blocks = ceil_div(nv, lpt), blocks = ceil_div(T, kSumThreads / lpt) * col_blocks;
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
   if (launch_pdl(unpermute_kernel<E_, KU, A>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
@@ -796,17 +805,22 @@ int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int
   return MLR_OK;
 }
 
-// Rows in flight per thread: the smallest of 1, 2, 4, 8 that holds K, so that
-// few experts per token cost no empty turns; at most 4 of rows off the grid,
-// which take more registers or loads.
+// Rows in flight per thread: K in as few equal turns as there are of at most eight
+// rows (four of rows off the grid, which take more registers or loads), as an
+// empty place costs its instructions all the same (8479 x 5 rows of 2144 bf16:
+// 42 us in eight places, 39 in six; 9836 x 5 rows of 1513: 54 and 46 in four and
+// three; but on the grid three rows take 22.5 us in four places and 23.4 in three).
 template <typename E_, typename... Args>
 int launch_unpermute(bool whole, int K, Args... a) {
   constexpr RowAccess O = kOffGrid<E_>;
+  const int most = whole ? 8 : 4;
+  const int64_t ku = ceil_div(K, ceil_div(K, most));
   if (!whole)
-    return K == 1 ? launch_unpermute_k<E_, 1, O>(a...) : K == 2 ? launch_unpermute_k<E_, 2, O>(a...)
-                                                                : launch_unpermute_k<E_, 4, O>(a...);
-  return K == 1 ? launch_unpermute_k<E_, 1, kWhole>(a...) : K == 2 ? launch_unpermute_k<E_, 2, kWhole>(a...)
-         : K <= 4 ? launch_unpermute_k<E_, 4, kWhole>(a...) : launch_unpermute_k<E_, 8, kWhole>(a...);
+    return ku == 1 ? launch_unpermute_k<E_, 1, O>(a...) : ku == 2 ? launch_unpermute_k<E_, 2, O>(a...)
+           : ku == 3 ? launch_unpermute_k<E_, 3, O>(a...) : launch_unpermute_k<E_, 4, O>(a...);
+  return ku == 1 ? launch_unpermute_k<E_, 1, kWhole>(a...) : ku == 2 ? launch_unpermute_k<E_, 2, kWhole>(a...)
+         : ku <= 4 ? launch_unpermute_k<E_, 4, kWhole>(a...) : ku <= 6 ? launch_unpermute_k<E_, 6, kWhole>(a...)
+                                                                       : launch_unpermute_k<E_, 8, kWhole>(a...);
 }
 
 template <typename E_, int KU, RowAccess A>
@@ -825,19 +839,22 @@ int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t*
     auto run = [&](auto kernel, int threads) {
       return launch_pdl(kernel, dim3((unsigned)T), dim3(threads), 0, stream, dyp, rp, pos, w, T, K, H, dp, dw, d_status);
     };
-    err = H * (int)sizeof(E_) <= 512 ? run(unpermute_backward_unaligned_kernel<E_, KU, 32>, 32)
-                                     : run(unpermute_backward_unaligned_kernel<E_, KU, 128>, 128);
+    err = H * (int)sizeof(E_) <= 1024 ? run(unpermute_backward_unaligned_kernel<E_, KU, 32>, 32)
+                                     : run(unpermute_backward_unaligned_kernel<E_, KU, 64>, 64);
   }
   if (err != cudaSuccess) return MLR_ERR_CUDA;
   note_launch();
   return MLR_OK;
 }
+// Rows in flight as above, but on the grid always four places or eight (8479 x 5
+// rows of 2144 bf16: 89 us in eight, 102 in six).
 template <typename E_, typename... Args>
 int launch_unpermute_backward(bool whole, int K, Args... a) {
   constexpr RowAccess O = kOffGrid<E_>;
+  const int64_t ku = ceil_div(K, ceil_div(K, 4));
   if (!whole)
-    return K == 1 ? launch_unpermute_backward_k<E_, 1, O>(a...) : K == 2 ? launch_unpermute_backward_k<E_, 2, O>(a...)
-                                                                         : launch_unpermute_backward_k<E_, 4, O>(a...);
+    return ku == 1 ? launch_unpermute_backward_k<E_, 1, O>(a...) : ku == 2 ? launch_unpermute_backward_k<E_, 2, O>(a...)
+           : ku == 3 ? launch_unpermute_backward_k<E_, 3, O>(a...) : launch_unpermute_backward_k<E_, 4, O>(a...);
   return K == 1 ? launch_unpermute_backward_k<E_, 1, kWhole>(a...) : K == 2 ? launch_unpermute_backward_k<E_, 2, kWhole>(a...)
          : K <= 4 ? launch_unpermute_backward_k<E_, 4, kWhole>(a...) : launch_unpermute_backward_k<E_, 8, kWhole>(a...);
 }
