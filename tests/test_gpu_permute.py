@@ -120,6 +120,23 @@ def test_order_of_large_batches(cuda_device, T, K, E, masked, skew):
     assert torch.equal(off.cpu(), torch.searchsorted(by, torch.arange(E + 1)).int())
 
 
+@pytest.mark.parametrize("T,K,E,masked", [(1025, 8, 128, 0.1), (2048, 8, 60, 0.0), (2049, 8, 60, 0.1), (1366, 12, 16000, 0.1),
+                                          (70, 200, 3, 0.0), (16384, 1, 1, 0.5), (16385, 1, 5, 0.0)])
+def test_order_with_and_without_rows(cuda_device, T, K, E, masked):
+    """Sorting alone takes one launch for larger batches than sorting with rows;
+    both orders are the stable sort's."""
+    x, ids, _ = case(T, K, E, 8, F32, seed=T, masked=masked)
+    rows, pos, off = pm.moe_permute(x, ids, E)
+    pos2, off2 = pm.moe_sort_pairs(ids, E)
+    assert torch.equal(pos, pos2) and torch.equal(off, off2)
+    key = torch.where(ids < 0, E, ids).reshape(-1).long()
+    by, order = key.sort(stable=True)
+    want = torch.empty_like(order)
+    want[order] = torch.arange(order.numel(), device="cuda")
+    assert torch.equal(torch.where(pos < 0, ~pos, pos).reshape(-1), want.int())
+    assert torch.equal(off, torch.searchsorted(by, torch.arange(E + 1, device="cuda")).int())
+
+
 def test_no_tokens_and_no_columns(cuda_device):
     x = torch.empty(0, 16, device="cuda", dtype=BF)
     ids = torch.empty(0, 4, device="cuda", dtype=torch.int32)
