@@ -574,7 +574,9 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *   [1], w_tensor_scale null or [num_experts] (NVFP4 only).  Rows past the
  *   last expert's are zeros.  Offsets that are not 0 <= o[e] <= o[e + 1] <=
  *   num_rows set MLR_STATUS_INDEX and y is not written.
- * Codes and scales are 16-byte aligned.  Limits: cols <= 524288; the product:
+ * Codes and scales are 16-byte aligned, other tensors as their elements are (y
+ * of the product is written in words where outputs is even and y lies on a
+ * 4-byte boundary, in single elements elsewhere).  Limits: cols <= 524288; the product:
  *   num_experts <= 2048, num_experts * outputs < 2^31.
  */
 #define MLR_FP4_MX 0

@@ -98,6 +98,7 @@ struct Params {
   const int32_t* offsets;
   int P, E, N, nblk, ksteps, cols, atoms;
   uint16_t* y;
+  bool pairs;  // two outputs of a row are one aligned word of y
   int32_t* status;
   uint64_t wait_ns;
 };
@@ -210,10 +211,12 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
 }
 
 // 32 rows of y from c0 of the tile, this lane's output n.  Neighbouring lanes
-// trade values so that each stores two outputs of one row at once.
+// trade values so that each stores two outputs of one row at once, where those
+// are a word of y; an odd number of outputs, or a y that begins between two
+// words, takes single ones.
 __device__ __forceinline__ void store_chunk(const Params& p, uint16_t* yp, const uint32_t (&v)[32], float s, int n,
                                             int c0, int rows, int lane) {
-  if ((p.N & 1) == 0) {
+  if (p.pairs) {
     const int odd = lane & 1;
     uint16_t* q = yp + (int64_t)(c0 + odd) * p.N - odd;
 #pragma unroll
@@ -591,13 +594,14 @@ extern "C" int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_s
   for (const void* q : {static_cast<const void*>(a_codes), static_cast<const void*>(a_scales),
                         static_cast<const void*>(w_codes), static_cast<const void*>(w_scales)})
     if (q == nullptr || (reinterpret_cast<uintptr_t>(q) & 15) != 0) return MLR_ERR_INVALID;
-  if (expert_offsets == nullptr || y == nullptr) return MLR_ERR_INVALID;
+  const uintptr_t ya = reinterpret_cast<uintptr_t>(y);
+  if (expert_offsets == nullptr || y == nullptr || (ya & 1) != 0) return MLR_ERR_INVALID;
   const uint64_t pitch = (uint64_t)fp4_pitch(cols);
   Maps maps = {};
   if (!code_map(&maps.w, w_codes, pitch, (uint64_t)num_experts * outputs, 128)) return MLR_ERR_CUDA;
   Params p{a_tensor_scale, w_tensor_scale, expert_offsets, num_rows, num_experts, outputs,
-           (int)ceil_div(outputs, 128), (int)ceil_div(cols, kKStep), cols, fp4_atoms(cols, fmt), y, d_status,
-           wait_limit_ns()};
+           (int)ceil_div(outputs, 128), (int)ceil_div(cols, kKStep), cols, fp4_atoms(cols, fmt), y,
+           outputs % 2 == 0 && ya % 4 == 0, d_status, wait_limit_ns()};
   // an average expert of at most 32 rows rarely needs a second 64-row tile
   const bool small = num_rows <= 32 * (int64_t)num_experts || num_rows <= 64;
   auto run = [&](auto launch) { return launch(maps, p, a_codes, a_scales, w_scales, pitch, stream); };
