@@ -217,6 +217,16 @@ def _req(t: torch.Tensor, name: str, dtype, dev):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _launch_device(dev: torch.device, fn: str):
+    """Refuses tensors that the kernels cannot take: they are launched on the
+    current device's stream, so the tensors have to be on that device."""
+    if dev.type != "cuda":
+        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors are on {dev}, the current device (or the stream's) is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 @_on_stream
 def moe_lora_batch_info(seg_indptr: torch.Tensor, weight_indices: torch.Tensor,
                         lora_ranks: torch.Tensor, num_tokens: int, max_len: int = 0,

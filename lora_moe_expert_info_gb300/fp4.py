@@ -13,7 +13,8 @@ of 16, E4M3 scales under a float32 tensor scale).  Codes are uint8 [..., 16 *
 ceil(cols / 32)], two per byte; scales uint8 [row blocks, atoms, 32, 4, 4] in
 512-byte atoms of 128 rows by 4 blocks (see the C header).  Rows sorted by expert
 come from permute.moe_sort_pairs or permute.moe_permute.  Every step runs in the
-library's kernels; nothing here synchronises unless check=True.
+library's kernels; nothing here synchronises unless check=True.  All tensors are
+on the current CUDA device.
 """
 from __future__ import annotations
 
@@ -22,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check_device, _check_host, _on_stream, _req, _stream_number, library
+from . import _check_device, _check_host, _launch_device, _on_stream, _req, _stream_number, library
 from .permute import DTYPES, _address, _float, _out, moe_sort_pairs, moe_unpermute
 
 __all__ = ["fp4_quantize", "fp4_quantize_permuted", "fp4_quantize_swiglu", "fp4_dequantize", "fp4_expert_product",
@@ -121,6 +122,7 @@ def fp4_quantize(x, fmt: str = "nvfp4", tensor_scale: Optional[torch.Tensor] = N
     if cols == 0:
         raise ValueError("x has no columns")
     _scale(tensor_scale, "tensor_scale", n, f, dev)
+    _launch_device(dev, "fp4_quantize")
     codes, scales = _outputs(codes, scales, (*lead, rows), (*lead, (rows + 127) // 128), cols, f, dev)
     if n * rows:
         _check_host(_lib().moe_fp4_quantize(x.data_ptr(), n, rows, cols, dtype, f, _address(tensor_scale),
@@ -152,6 +154,7 @@ def fp4_quantize_permuted(x, topk_ids, pair_pos, expert_offsets, fmt: str = "nvf
         raise ValueError("x has no columns")
     K = topk_ids.shape[1]
     _scale(tensor_scale, "tensor_scale", 1, f, dev)
+    _launch_device(dev, "fp4_quantize_permuted")
     codes, scales = _outputs(codes, scales, (T * K,), (T * K // 128 + E,), cols, f, dev)
     if T:
         status = _status(check, dev)
@@ -179,6 +182,7 @@ def fp4_quantize_swiglu(gate_up, expert_offsets, fmt: str = "nvfp4", tensor_scal
     if gate_up.shape[1] % 2 or cols == 0:
         raise ValueError("gate_up must have an even number of columns")
     _scale(tensor_scale, "tensor_scale", 1, f, dev)
+    _launch_device(dev, "fp4_quantize_swiglu")
     codes, scales = _outputs(codes, scales, (P,), (P // 128 + E,), cols, f, dev)
     if P:
         status = _status(check, dev)
@@ -216,6 +220,7 @@ def fp4_dequantize(codes, scales, cols: int, fmt: str = "nvfp4", tensor_scale: O
     if codes.shape[-1] != _pitch(cols) or scales.shape != (*blocks, _atoms(cols, f), 32, 4, 4):
         raise ValueError("fp4_dequantize: inconsistent shapes")
     _scale(tensor_scale, "tensor_scale", 1 if expert_offsets is not None else n, f, dev)
+    _launch_device(dev, "fp4_dequantize")
     out = _out(out, "out", (*lead, rows, cols), dtype, dev)
     if out.numel():
         _check_host(_lib().moe_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), _address(expert_offsets), n, rows,
@@ -250,6 +255,9 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
         raise ValueError("fp4_expert_product: inconsistent shapes")
     _scale(a_tensor_scale, "a_tensor_scale", 1, f, dev)
     _scale(w_tensor_scale, "w_tensor_scale", E, f, dev)
+    if status is not None:
+        _req(status, "status", torch.int32, dev)
+    _launch_device(dev, "fp4_expert_product")
     y = _out(y, "y", (P, N), torch.bfloat16, dev)
     if P == 0 or N == 0:
         return y

@@ -12,7 +12,7 @@ stable in p.  A pair whose id is not in [0, num_experts) -- -1 to mask it -- com
 last with a zero row, and pair_pos holds ~row for it.  Tensors are bf16 or
 float32; sums run in increasing k in float32, so results are bit-identical
 between runs.  Every step runs in the library's kernels; nothing here
-synchronises unless check=True.
+synchronises unless check=True.  All tensors are on the current CUDA device.
 """
 from __future__ import annotations
 
@@ -22,7 +22,7 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check_device, _check_host, _on_stream, _req, _stream_number, library
+from . import _check_device, _check_host, _launch_device, _on_stream, _req, _stream_number, library
 
 __all__ = ["moe_permute", "moe_sort_pairs", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
            "MoePermute", "MoeUnpermute"]
@@ -90,20 +90,24 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
         H = x.shape[1]
         if x.shape[0] != T:
             raise ValueError(f"{fn}: inconsistent shapes")
+    _launch_device(dev, fn)
+    if x is not None:
         rows = _out(rows, "rows", (T * K, H), x.dtype, dev)
     wsb = lib.moe_permute_workspace_bytes(T, K, E)
     if wsb == 0:
         raise ValueError(f"{fn}: unsupported sizes")
     pair_pos = _out(pair_pos, "pair_pos", (T, K), torch.int32, dev)
     expert_offsets = _out(expert_offsets, "expert_offsets", (E + 1,), torch.int32, dev)
-    if workspace is None and wsb > 1:
+    if workspace is not None:
+        _req(workspace, "workspace", getattr(workspace, "dtype", None), dev)  # of any type
+    elif wsb > 1:
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     # an empty tensor has no address: rows of no columns are only sorted
     copy = H > 0
     code = lib.moe_permute(x.data_ptr() if copy else None, topk_ids.data_ptr(), T, K, H, E, dtype,
                            rows.data_ptr() if copy else None, pair_pos.data_ptr(), expert_offsets.data_ptr(),
-                           _address(workspace), 0 if workspace is None else workspace.numel(), _address(status),
+                           _address(workspace), 0 if workspace is None else workspace.nbytes, _address(status),
                            _stream_number(stream))
     _check_host(code, fn)
     if check:
@@ -149,6 +153,7 @@ def _gather(rows, pair_pos, weights, y, stream, check, fn, rows_name):
         _req(weights, "topk_weights", torch.float32, dev)
     if rows.shape[0] != T * K or (weights is not None and weights.shape != (T, K)):
         raise ValueError(f"{fn}: inconsistent shapes")
+    _launch_device(dev, fn)
     y = _out(y, "y", (T, H), rows.dtype, dev)
     if T == 0 or H == 0:
         return y
@@ -197,6 +202,7 @@ def moe_unpermute_backward(dy, rows, pair_pos, topk_weights, d_rows: Optional[to
     H = rows.shape[1]
     if rows.shape[0] != T * K or dy.shape != (T, H) or topk_weights.shape != (T, K):
         raise ValueError("moe_unpermute_backward: inconsistent shapes")
+    _launch_device(dev, "moe_unpermute_backward")
     d_rows = _out(d_rows, "d_rows", (T * K, H), rows.dtype, dev)
     d_weights = _out(d_weights, "d_weights", (T, K), torch.float32, dev)
     if T == 0 or H == 0:

@@ -2,11 +2,13 @@
 import ctypes
 
 import pytest
+import torch
 
 import __graft_entry__
 import lora_moe_expert_info_gb300 as mlr
 from lora_moe_expert_info_gb300 import fp4, permute as pm
 
+BF = torch.bfloat16
 FAKE = ctypes.c_void_p(0x1000)
 ODD = ctypes.c_void_p(0x1001)
 
@@ -18,8 +20,58 @@ def lib():
     return mlr.library()
 
 
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+def u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
 @pytest.mark.parametrize("outputs", [127, 128])
 def test_product_refuses_half_an_element(lib, outputs):
     """y between two bf16 elements is not an address of a bf16 tensor."""
     assert lib.moe_fp4_expert_product(FAKE, FAKE, None, FAKE, FAKE, None, FAKE, 4, 2, outputs, 64, 0, ODD, None,
                                       None) == mlr.MLR_ERR_INVALID
+
+
+def calls():
+    """Every entry point with tensors of the right types and shapes, on the host;
+    an empty batch as well, which launches nothing."""
+    E, P, N, C = 2, 8, 128, 64
+    x, ids, rows, w = torch.zeros(4, C, dtype=BF), i32(4, 2), torch.zeros(8, C, dtype=BF), torch.zeros(4, 2)
+    off, codes, scales = i32(E + 1), u8(P, 32), u8(P // 128 + E, 1, 32, 4, 4)
+    wc, ws = u8(E, N, 32), u8(E, 1, 1, 32, 4, 4)
+    dc, ds = u8(E, C, 32), u8(E, 1, 1, 32, 4, 4)
+    return {
+        "moe_permute": lambda: pm.moe_permute(x, ids, E),
+        "moe_permute unchecked": lambda: pm.moe_permute(x, ids, E, check=False),
+        "moe_permute empty": lambda: pm.moe_permute(x[:0], ids[:0], E),
+        "moe_sort_pairs": lambda: pm.moe_sort_pairs(ids, E),
+        "moe_permute_backward": lambda: pm.moe_permute_backward(rows, ids),
+        "moe_unpermute": lambda: pm.moe_unpermute(rows, ids, w),
+        "moe_unpermute empty": lambda: pm.moe_unpermute(rows[:0], ids[:0], w[:0]),
+        "moe_unpermute_backward": lambda: pm.moe_unpermute_backward(x, rows, ids, w),
+        "MoePermute": lambda: pm.MoePermute.apply(x, ids, E),
+        "MoeUnpermute": lambda: pm.MoeUnpermute.apply(rows, ids, w),
+        "fp4_quantize": lambda: fp4.fp4_quantize(x),
+        "fp4_quantize_permuted": lambda: fp4.fp4_quantize_permuted(x, ids, ids, off),
+        "fp4_quantize_swiglu": lambda: fp4.fp4_quantize_swiglu(torch.zeros(P, 2 * C), off),
+        "fp4_dequantize": lambda: fp4.fp4_dequantize(codes, scales, C, expert_offsets=off),
+        "fp4_expert_product": lambda: fp4.fp4_expert_product(codes, scales, off, wc, ws, C),
+        "fp4_moe_forward": lambda: fp4.fp4_moe_forward(x, ids, w, wc, ws, dc, ds),
+    }
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_host_tensors_are_refused(name):
+    with pytest.raises(ValueError, match="must be on a CUDA device"):
+        calls()[name]()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The kernels go to the current device's stream."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    mlr._launch_device(torch.device("cuda", 0), "call")
+    with pytest.raises(ValueError, match="cuda:1"):
+        mlr._launch_device(torch.device("cuda", 1), "call")

@@ -1,11 +1,12 @@
 """Corners of the expert operators' arguments: buffers at every address their type
-allows."""
+allows, buffers of the caller that the kernels cannot write."""
 import math
 
 import pytest
 import torch
 
-from lora_moe_expert_info_gb300 import fp4
+import lora_moe_expert_info_gb300 as mlr
+from lora_moe_expert_info_gb300 import fp4, permute as pm
 from test_gpu_fp4 import FMTS, product_case
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,26 @@ def test_product_into_any_address(cuda_device, fmt, T, K, E, N, C, masked):
         out = fp4.fp4_expert_product(a, sa, off, qw, sw, C, fmt, ga, gw, y=y)
         assert out is y and torch.equal(y, want), k
         assert buf[:k].isnan().all() and buf[k + n:].isnan().all(), k
+
+
+def test_buffers_of_the_caller_on_the_host_are_refused(cuda_device):
+    """A workspace or a status word that the kernels would write, on the host, with
+    holes or too small; a workspace may have any type."""
+    ids = torch.zeros(9000, 2, dtype=torch.int32, device="cuda")
+    n = pm._lib().moe_permute_workspace_bytes(9000, 2, 4)
+    want = pm.moe_sort_pairs(ids, 4)
+    got = pm.moe_sort_pairs(ids, 4, workspace=torch.empty((n + 3) // 4, device="cuda"))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    for ws, error in ((torch.empty(n, dtype=torch.uint8), ValueError), (n, TypeError),
+                      (torch.empty(n - 1, dtype=torch.uint8, device="cuda"), mlr.MoeLoraError),
+                      (torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2], ValueError)):
+        with pytest.raises(error):
+            pm.moe_sort_pairs(ids, 4, workspace=ws)
+    off, a, sa, qw, sw, ga, gw = product_case(20, 1, 3, 128, 64, "mxfp4")
+    with pytest.raises(ValueError):
+        fp4.fp4_expert_product(a, sa, off, qw, sw, 64, "mxfp4", status=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        fp4.fp4_expert_product(a, sa, off, qw, sw, 64, "mxfp4", status=torch.zeros(1, device="cuda"))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    fp4.fp4_expert_product(a, sa, off, qw, sw, 64, "mxfp4", status=status, check=False)
+    assert int(status) == 0
