@@ -39,7 +39,6 @@ constexpr int kProductThreads = 512;
 constexpr int kEpilogueThreads = 256;  // warps 4-11: two per TMEM lane quarter
 constexpr int kMaxProductExperts = 2048;
 constexpr int kKStep = 256;      // columns per ring stage: 128 bytes of codes per row
-constexpr uint64_t kGraceNs = 1000000;  // after an abort: time for issued copies to land
 
 template <int NT> struct ProductCfg;
 // few rows per expert: short row tiles leave room for a deeper ring
@@ -75,6 +74,8 @@ struct __align__(16) Ctl {
   uint64_t sf_full[8], sf_empty[8];  // a stage of scales has landed / has been read
   uint64_t acc_full[2], acc_empty[2];
   uint64_t edge[2];  // the columns shared with the other accumulator have been read
+  uint64_t drain;    // every MMA issued is done
+  int steps[7];      // steps that warps 0, 3, 12 to 15 (arrivals on full) and 2 (on sf_full) have arrived for
   uint32_t tmem;
   int abort;
   int tiles[kMaxProductExperts + 1];  // row tiles of all earlier experts
@@ -274,6 +275,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       mbar_init(&c.acc_empty[b], kEpilogueThreads / 32);
       mbar_init(&c.edge[b], kEpilogueThreads / 32);
     }
+    mbar_init(&c.drain, 1);
     c.abort = 0;
     fence_mbar_init();
   }
@@ -315,6 +317,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
       }
     }
+    if (lane == 0) c.steps[warp == 0 ? 0 : 1] = g;
   } else if (warp == 2) {
     // ============================= scale loads =============================
     int g = 0, il = 0;
@@ -336,6 +339,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         __syncwarp();
       }
     }
+    if (lane == 0) c.steps[6] = g;
   } else if (warp == 1) {
     // ================================= MMA =================================
     // The whole warp walks the steps, so that every operand is uniform over it
@@ -382,6 +386,11 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
       if (ok && elect_one()) mma_commit(&c.acc_full[b]);
       __syncwarp();
     }
+    // the MMAs read shared memory and write TMEM: whatever has given up, all that
+    // were issued are done before either is freed
+    if (elect_one()) mma_commit(&c.drain);
+    __syncwarp();
+    if (!mbar_wait_for(&c.drain, 0, kWaitLimitNs)) *abort = 1;
   } else if (warp >= 12) {
     // ============================ scales to TMEM ===========================
     // Each of the four warps writes its own lane quarter, a repetition of the
@@ -438,6 +447,7 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
         }
       }
     }
+    if (lane == 0) c.steps[warp - 10] = g;
   } else if (warp >= 4) {  // 4 to 11
     // =============================== epilogue ==============================
     // Two warps per lane quarter take alternate chunks of 32 accumulator
@@ -483,7 +493,23 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
   __syncthreads();  // every role has left: the abort flag is final
   if (*abort) {
     if (tid == 0) set_status(p.status, MLR_STATUS_TIMEOUT);
-    sleep_for_ns(kGraceNs);  // copies and MMAs already issued finish before the teardown
+    // Copies already issued land before their shared memory is given up.  A stage
+    // has at most one step whose copies may be under way, the last that a loader
+    // arrived for (it found the MMAs of the step before done): roles that did not
+    // come to that step are stood in for, so that its barrier completes with its
+    // bytes.  Scales have their loader's arrival only.
+    if (tid < S) {
+      const int last = c.steps[0] > c.steps[1] ? c.steps[0] : c.steps[1];
+      if (last > tid) {
+        const int g = tid + (last - 1 - tid) / S * S;
+        for (int r = 0; r < 6; ++r)
+          if (c.steps[r] <= g) mbar_arrive(&c.full[tid]);
+        mbar_wait_for(&c.full[tid], (g / S) & 1, kWaitLimitNs);
+      }
+    } else if (tid >= 32 && tid - 32 < Q && c.steps[6] > tid - 32) {
+      const int q = tid - 32, g = q + (c.steps[6] - 1 - q) / Q * Q;
+      mbar_wait_for(&c.sf_full[q], (g / Q) & 1, kWaitLimitNs);
+    }
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, 512);

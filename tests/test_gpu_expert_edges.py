@@ -1,6 +1,7 @@
 """Corners of the expert operators' arguments: buffers at every address their type
-allows, buffers of the caller that the kernels cannot write."""
+allows, buffers of the caller that the kernels cannot write, waits that give up."""
 import math
+import time
 
 import pytest
 import torch
@@ -52,3 +53,45 @@ def test_buffers_of_the_caller_on_the_host_are_refused(cuda_device):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     fp4.fp4_expert_product(a, sa, off, qw, sw, 64, "mxfp4", status=status, check=False)
     assert int(status) == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,experts", [(1200, 40), (5000, 40)])
+def test_product_that_gives_up_leaves_nothing_behind(cuda_device, fmt, rows, experts):
+    """Waits that give up anywhere between the first step and the last: what was
+    issued by then is waited for, which takes microseconds (the waits of the
+    teardown, for copies and MMAs, run out after two seconds each: a call that
+    needs one of them is a failure), and a product launched right behind, into
+    the same shared memory and TMEM, is right."""
+    C, N = 7168, 2048
+    g = torch.Generator("cuda").manual_seed(0)
+
+    def random(rows, blocks):
+        codes = torch.randint(0, 256, (*rows, C // 2), generator=g, device="cuda", dtype=torch.uint8)
+        byte = 56 if fmt == "nvfp4" else 127
+        return codes, torch.full((*blocks, C // (64 if fmt == "nvfp4" else 128), 32, 4, 4), byte, device="cuda",
+                                 dtype=torch.uint8)
+
+    off = (torch.arange(experts + 1, device="cuda", dtype=torch.int32) * (rows // experts)).contiguous()
+    args = (*random((rows,), (rows // 128 + experts,)), off, *random((experts, N), (experts, N // 128)), C, fmt)
+    want = fp4.fp4_expert_product(*args)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gave_up = 0
+    default = mlr.wait_limit_ns()
+    try:
+        for limit in (0, 300, 600, 1000, 1500, 2000, 3000, 5000, 8000, 20000) * 3:
+            status.zero_()
+            torch.cuda.synchronize()
+            t0 = time.monotonic()
+            mlr.set_wait_limit_ns(limit)
+            y = fp4.fp4_expert_product(*args, status=status, check=False)
+            mlr.set_wait_limit_ns(default)
+            behind = fp4.fp4_expert_product(*args, check=False)
+            bits = int(status)
+            assert time.monotonic() - t0 < 1
+            assert bits in (0, 0x10) and torch.equal(behind, want)
+            assert bits or torch.equal(y, want)
+            gave_up += bits != 0
+    finally:
+        mlr.set_wait_limit_ns(default)
+    assert gave_up
