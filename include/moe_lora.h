@@ -506,8 +506,10 @@ int32_t moe_lora_deterministic(void);
  *   pair_pos        out [P]: pos(p), or ~pos(p) (negative) for a masked pair
  *   expert_offsets  out [num_experts + 1]: first row of each expert, then the
  *                   number of rows that belong to one
- *   workspace       moe_permute_workspace_bytes(...), 256-byte aligned; null is
- *                   taken where that is 1 (up to 8192 pairs, sorted in one launch)
+ *   workspace       moe_permute_workspace_bytes(...), or without x and rows
+ *                   moe_sort_pairs_workspace_bytes(...) is enough, 256-byte
+ *                   aligned; null is taken where that is 1 (pairs sorted in one
+ *                   launch: up to 8192, without rows up to 16384)
  * moe_unpermute: y[t] = sum_k topk_weights[t, k] * rows[pos(t, k)], in
  *   increasing k, in fp32; topk_weights null: weights of 1, which is the
  *   gradient of moe_permute (rows = the gradient of its rows).
@@ -521,6 +523,7 @@ int32_t moe_lora_deterministic(void);
  *   P < 2^31 - 1.
  */
 size_t moe_permute_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts);
+size_t moe_sort_pairs_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts);
 int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_tokens, int32_t topk, int32_t hidden,
                 int32_t num_experts, int32_t dtype, void* rows, int32_t* pair_pos, int32_t* expert_offsets,
                 void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);

@@ -46,7 +46,7 @@ struct SortPlan {
   int64_t bytes;
 };
 
-SortPlan sort_plan(int32_t T, int32_t K, int32_t E, int64_t one_launch = kOneLaunchPairs) {
+SortPlan sort_plan(int32_t T, int32_t K, int32_t E, int64_t one_launch) {
   SortPlan s{};
   s.code = MLR_ERR_INVALID;
   if (T < 0 || K < 1 || E < 1) return s;
@@ -874,7 +874,12 @@ int check_rows(int32_t T, int32_t K, int32_t H, int32_t dtype, int* es) {
 }  // namespace mlr
 
 extern "C" size_t moe_permute_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts) {
-  const mlr::SortPlan s = mlr::sort_plan(num_tokens, topk, num_experts);
+  const mlr::SortPlan s = mlr::sort_plan(num_tokens, topk, num_experts, mlr::kOneLaunchPairs);
+  return s.ok ? (size_t)s.bytes : 0;
+}
+
+extern "C" size_t moe_sort_pairs_workspace_bytes(int32_t num_tokens, int32_t topk, int32_t num_experts) {
+  const mlr::SortPlan s = mlr::sort_plan(num_tokens, topk, num_experts, mlr::kOneLaunchSorted);
   return s.ok ? (size_t)s.bytes : 0;
 }
 
@@ -883,7 +888,7 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
                            void* workspace, size_t ws_bytes, int32_t* d_status, void* stream_) {
   using namespace mlr;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  SortPlan s = sort_plan(num_tokens, topk, num_experts);
+  const SortPlan s = sort_plan(num_tokens, topk, num_experts, x == nullptr ? kOneLaunchSorted : kOneLaunchPairs);
   if (!s.ok) return s.code;
   if ((x == nullptr) != (rows == nullptr) || expert_offsets == nullptr) return MLR_ERR_INVALID;
   int es = 0;
@@ -898,7 +903,6 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
   if (topk_ids == nullptr || pair_pos == nullptr) return MLR_ERR_INVALID;
   if (!(s.one && workspace == nullptr) && (workspace == nullptr || ws_bytes < (size_t)s.bytes)) return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
-  if (x == nullptr) s = sort_plan(num_tokens, topk, num_experts, kOneLaunchSorted);
   char* ws = static_cast<char*>(workspace);
   if (!s.one) {
     int32_t* cnt = reinterpret_cast<int32_t*>(ws);

@@ -36,8 +36,9 @@ def _lib():
     if _typed is None:
         lib = library()
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-        lib.moe_permute_workspace_bytes.restype = sz
-        lib.moe_permute_workspace_bytes.argtypes = [i32] * 3
+        for f in (lib.moe_permute_workspace_bytes, lib.moe_sort_pairs_workspace_bytes):
+            f.restype = sz
+            f.argtypes = [i32] * 3
         lib.moe_permute.restype = ctypes.c_int
         lib.moe_permute.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp, vp]
         lib.moe_unpermute.restype = ctypes.c_int
@@ -93,7 +94,9 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
     _launch_device(dev, fn)
     if x is not None:
         rows = _out(rows, "rows", (T * K, H), x.dtype, dev)
-    wsb = lib.moe_permute_workspace_bytes(T, K, E)
+    # an empty tensor has no address: rows of no columns are only sorted
+    copy = H > 0
+    wsb = (lib.moe_permute_workspace_bytes if copy else lib.moe_sort_pairs_workspace_bytes)(T, K, E)
     if wsb == 0:
         raise ValueError(f"{fn}: unsupported sizes")
     pair_pos = _out(pair_pos, "pair_pos", (T, K), torch.int32, dev)
@@ -103,8 +106,6 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
     elif wsb > 1:
         workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
-    # an empty tensor has no address: rows of no columns are only sorted
-    copy = H > 0
     code = lib.moe_permute(x.data_ptr() if copy else None, topk_ids.data_ptr(), T, K, H, E, dtype,
                            rows.data_ptr() if copy else None, pair_pos.data_ptr(), expert_offsets.data_ptr(),
                            _address(workspace), 0 if workspace is None else workspace.nbytes, _address(status),

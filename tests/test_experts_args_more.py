@@ -75,3 +75,16 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     mlr._launch_device(torch.device("cuda", 0), "call")
     with pytest.raises(ValueError, match="cuda:1"):
         mlr._launch_device(torch.device("cuda", 1), "call")
+
+
+def test_workspace_of_sorts_with_and_without_rows(lib):
+    """One launch, which keeps nothing, sorts 8192 pairs with rows and 16384 without."""
+    rows, order = lib.moe_permute_workspace_bytes, lib.moe_sort_pairs_workspace_bytes
+    for T, K in ((1, 1), (1024, 8), (8192, 1)):
+        assert rows(T, K, 60) == 1 and order(T, K, 60) == 1
+    for T, K in ((1025, 8), (2048, 8), (16384, 1)):
+        assert rows(T, K, 60) > 4 * 61 and order(T, K, 60) == 1
+    for T, K in ((2049, 8), (16385, 1), (1 << 20, 8)):
+        assert order(T, K, 60) == rows(T, K, 60) > 4 * 61
+    for bad in ((-1, 2, 3), (4, 257, 3), (4, 2, 16385), (4, 2, 0)):
+        assert order(*bad) == 0

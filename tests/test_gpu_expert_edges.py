@@ -95,3 +95,24 @@ def test_product_that_gives_up_leaves_nothing_behind(cuda_device, fmt, rows, exp
     finally:
         mlr.set_wait_limit_ns(default)
     assert gave_up
+
+
+@pytest.mark.parametrize("T,K,E", [(1025, 8, 60), (2048, 8, 60), (16384, 1, 16384)])
+def test_order_alone_needs_no_workspace(cuda_device, T, K, E):
+    """Between the largest single launch with rows and without: null is taken for
+    the order alone, nothing is allocated for it, and rows still need theirs."""
+    ids = torch.randint(-1, E, (T, K), generator=torch.Generator().manual_seed(T), dtype=torch.int32).cuda()
+    x = torch.zeros(T, 8, device="cuda")
+    rows, want, first = pm.moe_permute(x, ids, E)
+    pos, off = torch.empty_like(want), torch.empty_like(first)
+    f = pm._lib().moe_permute
+    stream = torch.cuda.current_stream().cuda_stream
+    assert f(None, ids.data_ptr(), T, K, 0, E, 0, None, pos.data_ptr(), off.data_ptr(), None, 0, None, stream) == mlr.MLR_OK
+    assert torch.equal(pos, want) and torch.equal(off, first)
+    assert f(x.data_ptr(), ids.data_ptr(), T, K, 8, E, 1, rows.data_ptr(), pos.data_ptr(), off.data_ptr(), None, 0, None,
+             stream) == mlr.MLR_ERR_CAPACITY
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    pm.moe_sort_pairs(ids, E, pair_pos=pos, expert_offsets=off, check=False)
+    assert torch.cuda.max_memory_allocated() == before
