@@ -566,8 +566,8 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *   as moe_permute leaves them); tensor_scale null or [1].  A masked pair's
  *   row has zero codes.  Limit: topk <= 512.
  * moe_fp4_quantize_swiglu: sorted rows [num_rows, 2 cols], gate then up, to
- *   the codes of up * gate / (1 + min(exp(-gate), 2^125)), all in fp32.  Rows past
- *   expert_offsets[num_experts] have zero codes.
+ *   the codes of up * (gate / (1 + exp(-gate))), held in fp32 (a few ulp, for
+ *   any finite gate).  Rows past expert_offsets[num_experts] have zero codes.
  * moe_fp4_dequantize: (code * block scale) * tensor scale, rounded once to
  *   `dtype`.  expert_offsets null: a stack of num_matrices; else sorted rows of
  *   num_matrices experts (tensor_scale [1]), zeros past the last expert's.

@@ -16,9 +16,9 @@
 // exchange their maxima), so a row is read once and nothing is kept outside
 // registers; bound by HBM: reads x, writes half a byte per value plus one byte
 // per block.  65536 rows of 7168 bf16, MXFP4: quantised 169 us (105% of the copy
-// rate), back 181 us (98%), from [gate | up] 359 us (89%, the rest the
-// exponential's and the division's instructions), 8192 tokens to those 65536
-// sorted rows 73 us (76%: their scales go through arrange_kernel).
+// rate), back 181 us (98%), from [gate | up] 367 us (87%; without exponential
+// and division 300), 8192 tokens to those 65536 sorted rows 73 us (76%: their
+// scales go through arrange_kernel).
 #include <cuda_fp16.h>
 
 #include "mlr_fp4.cuh"
@@ -225,24 +225,23 @@ __device__ __forceinline__ void load16(const float* p, int n, float (&v)[16], co
   }
 }
 
-// v[j] = u[j] * (v[j] / (1 + min(exp(-v[j]), 2^125))), each operation rounded to
-// fp32.
+// v[j] = 4 u[j] (v[j] / (1 + exp(-v[j]))), each operation rounded to fp32; not
+// finite where exp(-v[j]), 4 v[j] or the result overflows.
 //
 // The quotient g / d, d = 1 + exp(-g) >= 1, is one approximate reciprocal r and
 // one residual step with fused multiply-adds (Markstein's division): q = g r,
 // q + (g - d q) r, where g - d q is exact.  r is within 1 ulp, so the result is
-// the correctly rounded quotient but for about one in 10^6, which are one ulp
-// off.  It needs 1 / d to be a normal number, hence the bound on exp(-g): it
-// acts below g = -86.6, where g / d is under 3e-36 either way.  8192 x 8 rows of
-// 7168 bf16 took 584 us with __fdiv_rn, 406 us so; without any division or
-// exponential 300 us, what their bytes take.
-constexpr float kMaxExp = 0x1p125f;
+// within 1 ulp of the quotient.  d is taken a quarter as large, which keeps 1 / d
+// a normal number as long as exp(-g) is finite; the quotient's factor of 4 is
+// left to the block's scale.  8192 x 8 rows of 7168 bf16 took 584 us with
+// __fdiv_rn, 406 us so; without any division or exponential 300 us, what their
+// bytes take.
 __device__ __forceinline__ void swiglu16(float (&v)[16], const float (&u)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
     const float2 ng = make_float2(-v[j], -v[j + 1]);
-    const float2 d = __fadd2_rn(make_float2(fminf(expf(ng.x), kMaxExp), fminf(expf(ng.y), kMaxExp)),
-                                make_float2(1.f, 1.f));
+    const float2 d = __ffma2_rn(make_float2(expf(ng.x), expf(ng.y)), make_float2(0.25f, 0.25f),
+                                make_float2(0.25f, 0.25f));
     float2 r;  // -1 / d
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(-d.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(-d.y));
@@ -253,6 +252,18 @@ __device__ __forceinline__ void swiglu16(float (&v)[16], const float (&u)[16]) {
     v[j + 1] = h.y;
   }
 }
+// u g / (1 + exp(-g)) of any g and u.  Where exp(-g) may overflow (from about
+// g = -88.7 down) it is u g exp(g) in three factors,
+//   (u w) (g / exp(80)) w,  w = exp((g + 80) / 2),
+// none above 1 and none that underflows but where the result does.
+__device__ __forceinline__ float swiglu1(float g, float u) {
+  if (!(g < -80.f)) return u * __fdiv_rn(g, 1.f + expf(-g));
+  constexpr float kExp = 1.8048513878454153e-35f;  // exp(-80)
+  const float w = expf(0.5f * (g + 80.f));
+  return u * w * (g * kExp) * w;
+}
+__device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
 
 // Eight values times r as E2M1 codes, value i in bits [4i, 4i + 4).
 __device__ __forceinline__ uint32_t to_e2m1x8(const float* v, float r) {
@@ -311,21 +322,14 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float g, float* r) {
   return q;
 }
 
-// Ten blocks per SM (at most 51 registers): the exponentials of the SwiGLU form
-// need the warps (8192 x 8 rows of 7168: 359 us, 386 with twelve).
+// A block's rows.  SwiGLU: whether the thread met a block of columns that holds a
+// value that swiglu16 does not give, or an infinity or a NaN; it has a NaN scale.
 template <typename E_, int FMT, int SRC, int VB>
-__global__ void __launch_bounds__(kQThreads, 10)
-quantize_kernel(const QuantParams p) {
-  __shared__ Dest dest[kQDests];
-  pdl_wait();
-  pdl_trigger();
+__device__ __forceinline__ bool quantize_rows(const QuantParams& p, const Dest* dest, int64_t r0, int nr) {
   const int K = SRC == kTokens ? p.K : 1;
-  const int64_t r0 = (int64_t)blockIdx.x * p.rpb;
-  const int nr = (int)min((int64_t)p.rpb, p.rows - r0);
-  for (int i = threadIdx.x; i < nr * K; i += kQThreads) dest[i] = dest_of<SRC>(p, r0 + i / K, i % K);
-  __syncthreads();
   const E_* x = static_cast<const E_*>(p.x);
   const int total = nr * p.nga;
+  bool beyond = false;
   // whole warps stay in the loop: neighbours exchange maxima and scales
   for (int i0 = 0; i0 < total; i0 += kQThreads) {
     const int i = i0 + threadIdx.x;
@@ -335,6 +339,8 @@ quantize_kernel(const QuantParams p) {
     const int64_t row = r0 + lr;
     const int c = 16 * g;
     const int n = in ? min(16, p.cols - c) : 0;  // <= 0 past the last column
+    // v holds `unit` times the values
+    constexpr float unit = SRC == kSwiglu ? 4.f : 1.f;
     float v[16];
     if (SRC == kSwiglu) {
       float u[16];
@@ -347,7 +353,7 @@ quantize_kernel(const QuantParams p) {
     float most = 0.f;
 #pragma unroll
     for (int j = 0; j < 16; j += 2) most = max3_abs(most, v[j], v[j + 1]);
-    uint32_t amax = __float_as_uint(most);  // as bits a NaN counts above infinity
+    uint32_t amax = __float_as_uint(most * (1.f / unit));  // as bits a NaN counts above infinity
     if (FMT == MLR_FP4_MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     float r;
     uint32_t s;
@@ -357,10 +363,12 @@ quantize_kernel(const QuantParams p) {
       const float ts = p.tensor_scale == nullptr ? 1.f : __ldg(p.tensor_scale + (SRC == kMatrix ? row / p.group_rows : 0));
       s = nv_scale(__uint_as_float(amax), ts, &r);
     }
+    r *= 1.f / unit;
     uint2 q = make_uint2(to_e2m1x8(v, r), to_e2m1x8(v + 8, r));
     if (amax >= 0x7f800000u) {
       s = FMT == MLR_FP4_MX ? 0xffu : 0x7fu;
       q = make_uint2(0, 0);
+      beyond = true;
     }
     if (n <= 0) s = 0;  // scale blocks past the last column
     // four scales of the row's atom in one word
@@ -383,6 +391,68 @@ quantize_kernel(const QuantParams p) {
         *reinterpret_cast<uint32_t*>(p.scales + d.scale + (int64_t)(g / kLanes) * step) = s;
     }
   }
+  return beyond;
+}
+
+// The blocks of columns of the warp's rows that have a NaN scale once more, value
+// by value, any gate.  A pass of its own and short, for the sake of the first
+// one's registers: 8192 x 8 rows of 7168 take 367 us (MXFP4) and 363 (NVFP4) so,
+// 376 and 393 where the first pass turns to such values itself in a branch that
+// is not taken, 360 and 393 with this pass unrolled as the first.
+template <typename E_, int FMT>
+__device__ __forceinline__ void swiglu_rows_again(const QuantParams& p, const Dest* dest, int64_t r0, int nr) {
+  const E_* x = static_cast<const E_*>(p.x);
+  const int total = nr * p.nga;
+  __syncwarp();  // the scales of the first pass
+#pragma unroll 1
+  for (int i0 = 0; i0 < total; i0 += kQThreads) {
+    const int i = i0 + threadIdx.x;
+    const int lr = i < total ? (int)__umulhi((uint32_t)i, p.ng_magic) : 0;
+    const int g = i < total ? i - lr * p.nga : 0;
+    const int n = i < total ? min(16, p.cols - 16 * g) : 0;
+    const E_* gate = x + (r0 + lr) * 2 * p.cols + 16 * g;
+    const Dest d = dest[lr];
+    const int b = FMT == MLR_FP4_MX ? g / 2 : g;
+    uint8_t* const scale = p.scales + d.scale + (int64_t)(b / 4) * kAtomBytes + b % 4;
+    constexpr uint32_t kNan = FMT == MLR_FP4_MX ? 0xffu : 0x7fu;
+    const bool again = n > 0 && d.row >= 0 && d.scale >= 0 && *scale == kNan;
+    float most = 0.f;
+#pragma unroll 1
+    for (int j = 0; again && j < n; ++j) most = max3_abs(most, swiglu1(load1(gate + j), load1(gate + p.cols + j)), 0.f);
+    uint32_t amax = __float_as_uint(most);
+    if (FMT == MLR_FP4_MX) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    if (!again || amax >= 0x7f800000u) continue;
+    float r;
+    uint32_t s;
+    if (FMT == MLR_FP4_MX) s = mx_scale(amax, &r);
+    else s = nv_scale(most, p.tensor_scale == nullptr ? 1.f : __ldg(p.tensor_scale), &r);
+    uint64_t q = 0;
+#pragma unroll 1
+    for (int j = 0; j < n; ++j) {
+      const float h[8] = {swiglu1(load1(gate + j), load1(gate + p.cols + j))};
+      q |= (uint64_t)(to_e2m1x8(h, r) & 15u) << (4 * j);
+    }
+    *reinterpret_cast<uint64_t*>(p.codes + d.row * p.pitch + 8 * g) = q;
+    *scale = (uint8_t)s;
+  }
+}
+
+// Ten blocks per SM (at most 51 registers): the exponentials of the SwiGLU form
+// need the warps (8192 x 8 rows of 7168, before the pass above: 359 us, 386 with twelve).
+template <typename E_, int FMT, int SRC, int VB>
+__global__ void __launch_bounds__(kQThreads, 10)
+quantize_kernel(const QuantParams p) {
+  __shared__ Dest dest[kQDests];
+  pdl_wait();
+  pdl_trigger();
+  const int K = SRC == kTokens ? p.K : 1;
+  const int64_t r0 = (int64_t)blockIdx.x * p.rpb;
+  const int nr = (int)min((int64_t)p.rpb, p.rows - r0);
+  for (int i = threadIdx.x; i < nr * K; i += kQThreads) dest[i] = dest_of<SRC>(p, r0 + i / K, i % K);
+  __syncthreads();
+  const bool beyond = quantize_rows<E_, FMT, SRC, VB>(p, dest, r0, nr);
+  if constexpr (SRC == kSwiglu)
+    if (__any_sync(0xffffffffu, beyond)) swiglu_rows_again<E_, FMT>(p, dest, r0, nr);
 }
 
 // Sorted rows' scales from row after row to atoms, in place, a 128-row block at

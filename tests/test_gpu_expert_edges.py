@@ -1,8 +1,10 @@
 """Corners of the expert operators' arguments: buffers at every address their type
-allows, buffers of the caller that the kernels cannot write, waits that give up."""
+allows, buffers of the caller that the kernels cannot write, waits that give up, gates far
+below zero."""
 import math
 import time
 
+import numpy as np
 import pytest
 import torch
 
@@ -116,3 +118,63 @@ def test_order_alone_needs_no_workspace(cuda_device, T, K, E):
     torch.cuda.reset_peak_memory_stats()
     pm.moe_sort_pairs(ids, E, pair_pos=pos, expert_offsets=off, check=False)
     assert torch.cuda.max_memory_allocated() == before
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("gate,up", [(-85.9, 3e38), (-86.1, 3e38), (-86.5, 1e38), (-88.0, 3e38), (-89.0, -3e38), (-95.0, 3e38),
+                                     (-100.0, 3e38), (-103.5, 3e38), (-120.0, 3e38), (-168.0, 3e38), (-1e4, 3e38),
+                                     (-1e30, 3e38), (-3e38, 1.0), (-3e38, -3e38), (-88.0, 1.0), (-100.0, 1.0)])
+def test_swiglu_of_gates_far_below_zero(cuda_device, fmt, gate, up):
+    """u g / (1 + exp(-g)) where 1 / (1 + exp(-g)) is no normal float, or none at
+    all: blocks of one value, whose 4-bit number is within a fifth of it (the value
+    5 between the codes 4 and 6; float32 steps add less than a hundredth of that)
+    or, below the smallest scale, half of its smallest code (MXFP4) or that scale
+    (NVFP4).  Gates of zero among them give zeros."""
+    g32 = float(np.float32(gate))
+    h = g32 * math.exp(g32) / (1 + math.exp(g32)) * float(np.float32(up))
+    block = 16 if fmt == "nvfp4" else 32
+    most = max(abs(h), 1e-30)
+    scale = torch.tensor([most / 2688], device="cuda") if fmt == "nvfp4" else None
+    gu = torch.full((2, 4 * block), 0.0)
+    gu[0, :2 * block], gu[0, 2 * block:] = gate, up
+    gu[1, 0:2 * block:2], gu[1, 1:2 * block:2] = gate, 0.0   # beside gates of 0
+    gu[1, 2 * block::2], gu[1, 2 * block + 1::2] = up, 1.0
+    off = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    codes, scales = fp4.fp4_quantize_swiglu(gu.cuda(), off, fmt, scale, check=True)
+    y = fp4.fp4_dequantize(codes, scales, 2 * block, fmt, scale, expert_offsets=off, dtype=torch.float32)
+    y = y.cpu().double().numpy()
+    floor = 2.0 ** -127 / 4 if fmt == "mxfp4" else 2.0 ** -9 * float(scale)
+    assert (np.abs(y[0] - h) <= 0.202 * abs(h) + 1.01 * floor).all(), (y[0, 0], h)
+    assert (np.abs(y[1, 0::2] - h) <= 0.202 * abs(h) + 1.01 * floor).all()
+    assert not y[1, 1::2].any()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(70, 128), (33, 90), (5, 7168), (9, 1001)])
+def test_swiglu_blocks_with_far_gates_leave_the_others_alone(cuda_device, fmt, dtype, rows, cols):
+    """Some blocks hold a far gate, an infinity or a NaN: all others have the codes
+    and scales that they have without those, whatever the row's vectors."""
+    g = torch.Generator().manual_seed(cols)
+    gu = torch.randn(rows, 2 * cols, generator=g)
+    bad = gu.clone()
+    n = 16 if fmt == "nvfp4" else 32
+    touched = torch.zeros(rows, -(-cols // n) * n, dtype=torch.bool)
+    for value in (-90.0, -3e38, math.inf, math.nan):
+        for _ in range(3):
+            r, c = (int(torch.randint(m, (1,), generator=g)) for m in (rows, cols))
+            bad[r, c] = value
+            touched[r, c // n * n:c // n * n + n] = True
+    far = touched & (torch.nn.functional.pad(bad[:, :cols], (0, touched.shape[1] - cols)).isfinite().view(rows, -1, n)
+                     .all(-1, keepdim=True).expand(-1, -1, n).reshape(touched.shape))
+    off = torch.tensor([0, rows // 3, rows // 3, rows], dtype=torch.int32, device="cuda")
+    y = [fp4.fp4_dequantize(*fp4.fp4_quantize_swiglu(t.to(dtype).cuda(), off, fmt, check=True), cols, fmt, expert_offsets=off,
+                            dtype=torch.float32).cpu() for t in (gu, bad)]
+    touched, far = touched[:, :cols], far[:, :cols]
+    assert torch.equal(y[0][~touched], y[1][~touched])
+    assert torch.equal(y[1].isnan(), touched & ~far)
+    # in blocks with far gates those are zero and the others within half a code's step of the block's scale
+    h = torch.nn.functional.silu(bad[:, :cols].to(dtype).double()) * bad[:, cols:].to(dtype).double()
+    most = torch.nn.functional.pad(h.abs(), (0, -cols % n)).view(rows, -1, n).amax(-1, keepdim=True)
+    step = (most / 3).expand(-1, -1, n).reshape(rows, -1)[:, :cols]
+    assert bool(((y[1] - h).abs()[far] <= step[far] + 2.0 ** -9).all())
