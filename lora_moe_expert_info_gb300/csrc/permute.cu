@@ -757,6 +757,23 @@ unpermute_backward_unaligned_kernel(const E_* __restrict__ dy, const E_* __restr
   }
 }
 
+// Opts a kernel in to the most dynamic shared memory that any call of it needs,
+// not to what this one does: a call of fewer experts in another thread would
+// lower the limit again before this one's launch.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t need, int most) {
+  if (need <= 40 * 1024) return cudaSuccess;  // with the static part within the 48 KB that need no opt-in
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+int launched(cudaError_t err, int kernels) {
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();  // not left for the next call to find
+    return MLR_ERR_CUDA;
+  }
+  note_launch(kernels);
+  return MLR_OK;
+}
+
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <int VB>
@@ -776,14 +793,11 @@ int launch_permute(const SortPlan& s, const void* x, const int32_t* ids, int T, 
   const dim3 grid((unsigned)s.G, (unsigned)slices);
   const size_t smem = (size_t)(E + 2) * 4 + (s.one ? (size_t)(E + 1) * 4 : 0);
   auto run = [&](auto kernel) {
-    if (smem > 40 * 1024 &&  // with the static part past the 48 KB that need no opt-in
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    if (launch_pdl(kernel, grid, dim3(kSortThreads), smem, stream, x, ids, T, K, E, s.tpb, s.Gp, row_bytes, rows, pair_pos,
-                   offsets, cnt, tot, d_status) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    note_launch();
-    return MLR_OK;
+    cudaError_t err = allow_smem(kernel, smem, (2 * kMaxSortExperts + 3) * 4);
+    if (err == cudaSuccess)
+      err = launch_pdl(kernel, grid, dim3(kSortThreads), smem, stream, x, ids, T, K, E, s.tpb, s.Gp, row_bytes, rows,
+                       pair_pos, offsets, cnt, tot, d_status);
+    return launched(err, 1);
   };
   return s.one ? run(permute_kernel<VB, true>) : run(permute_kernel<VB, false>);
 }
@@ -800,12 +814,9 @@ int launch_unpermute_k(const void* rows, const int32_t* pos, const float* w, int
   const int nv = (int)ceil_div((int64_t)H * sizeof(E_), 16 * kVecs<KU, A>), lpt = sum_threads(nv);
   const int64_t col_blocks = ceil_div(nv, lpt), blocks = ceil_div(T, kSumThreads / lpt) * col_blocks;
   if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  if (launch_pdl(unpermute_kernel<E_, KU, A>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
-                 static_cast<const E_*>(rows), pos, w, T, K, H, log2_of(lpt), (unsigned)col_blocks,
-                 static_cast<E_*>(y), d_status) != cudaSuccess)
-    return MLR_ERR_CUDA;
-  note_launch();
-  return MLR_OK;
+  return launched(launch_pdl(unpermute_kernel<E_, KU, A>, dim3((unsigned)blocks), dim3(kSumThreads), 0, stream,
+                             static_cast<const E_*>(rows), pos, w, T, K, H, log2_of(lpt), (unsigned)col_blocks,
+                             static_cast<E_*>(y), d_status), 1);
 }
 
 // Rows in flight per thread: K in as few equal turns as there are of at most eight
@@ -845,9 +856,7 @@ int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t*
     err = H * (int)sizeof(E_) <= 1024 ? run(unpermute_backward_unaligned_kernel<E_, KU, 32>, 32)
                                      : run(unpermute_backward_unaligned_kernel<E_, KU, 64>, 64);
   }
-  if (err != cudaSuccess) return MLR_ERR_CUDA;
-  note_launch();
-  return MLR_OK;
+  return launched(err, 1);
 }
 // Rows in flight as above, but on the grid always four places or eight (8479 x 5
 // rows of 2144 bf16: 89 us in eight, 102 in six).
@@ -898,8 +907,7 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
     if (!aligned_to(x, es) || !aligned_to(rows, es)) return MLR_ERR_INVALID;
   }
   if (s.P == 0)
-    return cudaMemsetAsync(expert_offsets, 0, (size_t)(num_experts + 1) * 4, stream) == cudaSuccess ? MLR_OK
-                                                                                                     : MLR_ERR_CUDA;
+    return launched(cudaMemsetAsync(expert_offsets, 0, (size_t)(num_experts + 1) * 4, stream), 0);
   if (topk_ids == nullptr || pair_pos == nullptr) return MLR_ERR_INVALID;
   if (!(s.one && workspace == nullptr) && (workspace == nullptr || ws_bytes < (size_t)s.bytes)) return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
@@ -910,18 +918,17 @@ extern "C" int moe_permute(const void* x, const int32_t* topk_ids, int32_t num_t
     const size_t one = (size_t)(num_experts + 1) * 4;
     const bool wide = one * kCountChunks <= 48 * 1024;
     const unsigned blocks = (unsigned)(s.Gp / kCountChunks);
-    if (one > 48 * 1024 && cudaFuncSetAttribute(sort_count_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                (int)one) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    if ((wide ? launch_pdl(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), one * kCountChunks, stream,
-                           topk_ids, s.P, num_experts, s.tpb * topk, s.Gp, cnt)
-              : launch_pdl(sort_count_kernel<false>, dim3(blocks), dim3(kSortThreads), one, stream, topk_ids, s.P,
-                           num_experts, s.tpb * topk, s.Gp, cnt)) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    if (launch_pdl(sort_scan_kernel, dim3((unsigned)(num_experts + 1)), dim3(kSortThreads), 0, stream, cnt, s.Gp,
-                   tot) != cudaSuccess)
-      return MLR_ERR_CUDA;
-    note_launch(2);
+    cudaError_t err = wide ? cudaSuccess : allow_smem(sort_count_kernel<false>, one, (kMaxSortExperts + 1) * 4);
+    if (err == cudaSuccess)
+      err = wide ? launch_pdl(sort_count_kernel<true>, dim3(blocks), dim3(kSortThreads), one * kCountChunks, stream,
+                              topk_ids, s.P, num_experts, s.tpb * topk, s.Gp, cnt)
+                 : launch_pdl(sort_count_kernel<false>, dim3(blocks), dim3(kSortThreads), one, stream, topk_ids, s.P,
+                              num_experts, s.tpb * topk, s.Gp, cnt);
+    int code = launched(err, 1);
+    if (code != MLR_OK) return code;
+    code = launched(launch_pdl(sort_scan_kernel, dim3((unsigned)(num_experts + 1)), dim3(kSortThreads), 0, stream, cnt,
+                               s.Gp, tot), 1);
+    if (code != MLR_OK) return code;
   }
   const int64_t rb = x == nullptr ? 0 : (int64_t)hidden * es;
   const bool whole = rb % 16 == 0 && aligned_to(x, 16) && aligned_to(rows, 16);

@@ -2,6 +2,7 @@
 allows, buffers of the caller that the kernels cannot write, waits that give up, gates far
 below zero."""
 import math
+import threading
 import time
 
 import numpy as np
@@ -178,3 +179,30 @@ def test_swiglu_blocks_with_far_gates_leave_the_others_alone(cuda_device, fmt, d
     most = torch.nn.functional.pad(h.abs(), (0, -cols % n)).view(rows, -1, n).amax(-1, keepdim=True)
     step = (most / 3).expand(-1, -1, n).reshape(rows, -1)[:, :cols]
     assert bool(((y[1] - h).abs()[far] <= step[far] + 2.0 ** -9).all())
+
+
+@pytest.mark.parametrize("T,experts", [(40, (16384, 5200)), (9000, (16384, 12500))])
+def test_sorts_of_different_experts_in_two_threads(cuda_device, T, experts):
+    """Each thread's launches need another amount of shared memory of the same
+    kernels (in one launch, and counted first); none takes the other's away."""
+    lib = pm._lib()
+    codes, done = [], []
+
+    def sort(E):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            ids = (torch.arange(T, dtype=torch.int32, device="cuda") * 7 % E).view(T, 1)
+            x = torch.arange(T, dtype=torch.float32, device="cuda").view(T, 1).expand(T, 8).contiguous()
+            rows, pos = torch.empty_like(x), torch.empty_like(ids)
+            off = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+            ws = torch.empty(lib.moe_permute_workspace_bytes(T, 1, E), dtype=torch.uint8, device="cuda")
+            for _ in range(3000):
+                codes.append(lib.moe_permute(x.data_ptr(), ids.data_ptr(), T, 1, 8, E, 1, rows.data_ptr(), pos.data_ptr(),
+                                             off.data_ptr(), ws.data_ptr(), ws.nbytes, None, s.cuda_stream))
+            s.synchronize()
+            done.append(torch.equal(rows[pos.view(-1).long()], x))
+
+    threads = [threading.Thread(target=sort, args=(E,)) for E in experts]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert codes == [mlr.MLR_OK] * 6000 and done == [True, True]
