@@ -567,20 +567,22 @@ int moe_unpermute_backward(const void* dy, const void* rows, const int32_t* pair
  *   row has zero codes.  Limit: topk <= 512.
  * moe_fp4_quantize_swiglu: sorted rows [num_rows, 2 cols], gate then up, to
  *   the codes of up * (gate / (1 + exp(-gate))), held in fp32 (a few ulp, for
- *   any finite gate).  Rows past expert_offsets[num_experts] have zero codes.
+ *   any finite gate).  Rows that are no expert's have zero codes.
  * moe_fp4_dequantize: (code * block scale) * tensor scale, rounded once to
  *   `dtype`.  expert_offsets null: a stack of num_matrices; else sorted rows of
- *   num_matrices experts (tensor_scale [1]), zeros past the last expert's.
+ *   num_matrices experts (tensor_scale [1]), zeros in rows that are no expert's.
  * moe_fp4_expert_product: y[r, n] = g_a g_w[e] sum_c A[r, c] W[e, n, c] for
  *   each sorted row r and its expert e, summed in fp32, bf16 out [num_rows,
  *   outputs]; w a stack [num_experts, outputs, cols]; a_tensor_scale null or
- *   [1], w_tensor_scale null or [num_experts] (NVFP4 only).  Rows past the
- *   last expert's are zeros.  Offsets that are not 0 <= o[e] <= o[e + 1] <=
- *   num_rows set MLR_STATUS_INDEX and y is not written.
+ *   [1], w_tensor_scale null or [num_experts] (NVFP4 only).  Rows that are no
+ *   expert's are zeros.  Offsets that are not 0 <= o[e] <= o[e + 1] <= num_rows
+ *   set MLR_STATUS_INDEX and y is not written.
+ * Rows before expert_offsets[0] and from expert_offsets[num_experts] on are no
+ *   expert's.
  * Codes and scales are 16-byte aligned, other tensors as their elements are (y
  * of the product is written in words where outputs is even and y lies on a
- * 4-byte boundary, in single elements elsewhere).  Limits: cols <= 524288; the product:
- *   num_experts <= 2048, num_experts * outputs < 2^31.
+ * 4-byte boundary, in single elements elsewhere).  Limits: cols <= 524288; the
+ *   product: num_experts <= 2048, num_experts * outputs < 2^31.
  */
 #define MLR_FP4_MX 0
 #define MLR_FP4_NV 1

@@ -4,8 +4,8 @@
 //
 // with A and W given as E2M1 codes and block scales (mlr_fp4.cuh), on the
 // block-scaled FP4 tensor cores: the scales are applied inside the MMA, sums
-// are held in fp32 and y is rounded once to bf16.  Rows past the last expert's
-// are zeros.
+// are held in fp32 and y is rounded once to bf16.  Rows before the first expert's
+// and past the last one's are zeros.
 //
 // An item is 128 outputs (rows of W, the MMA's M) by one tile of up to NT rows
 // of one expert (the MMA's N), so that few rows waste little of the tensor
@@ -454,10 +454,12 @@ product_kernel(const __grid_constant__ Maps maps, const Params p) {
     // columns (rows of y), first those that the next tile's accumulator shares.
     const int m = (warp & 3) * 32 + lane;  // output of the item; TMEM lane
     const int half = (warp - 4) >> 2;
-    if (ok_offsets)
-      for (int64_t i = (int64_t)__ldg(p.offsets + p.E) * p.N + (int64_t)blockIdx.x * kEpilogueThreads + tid - 128;
-           i < (int64_t)p.P * p.N; i += (int64_t)gridDim.x * kEpilogueThreads)
-        p.y[i] = 0;
+    if (ok_offsets) {
+      const int64_t first = (int64_t)blockIdx.x * kEpilogueThreads + tid - 128;
+      const int64_t step = (int64_t)gridDim.x * kEpilogueThreads;
+      for (int64_t i = first; i < (int64_t)__ldg(p.offsets) * p.N; i += step) p.y[i] = 0;
+      for (int64_t i = (int64_t)__ldg(p.offsets + p.E) * p.N + first; i < (int64_t)p.P * p.N; i += step) p.y[i] = 0;
+    }
     int il = 0;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x, ++il) {
       const Item it = walk.at(p, c, il, n_items, lane);

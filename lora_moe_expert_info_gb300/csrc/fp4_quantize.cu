@@ -72,10 +72,10 @@ __device__ __forceinline__ Dest sorted_dest(const QuantParams& p, int64_t r, int
   return Dest{r, (int64_t)(o0 / 128 + e + j / 128) * p.block_bytes + in_block};
 }
 
-// The expert of sorted row r: the last e with offsets[e] <= r; E if r is past
-// the last expert's rows.
+// The expert of sorted row r: the last e with offsets[e] <= r; E if r is before
+// the first expert's rows or past the last one's.
 __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets, int E, int64_t r) {
-  if (r >= __ldg(offsets + E)) return E;
+  if (r < __ldg(offsets) || r >= __ldg(offsets + E)) return E;
   int lo = 0, hi = E;  // offsets[lo] <= r < offsets[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -541,7 +541,7 @@ __device__ __forceinline__ float scale_value(uint32_t b) {
   return s;
 }
 
-// Where the scales of a row are (.scale, -1: past the last expert's rows) and
+// Where the scales of a row are (.scale, -1: the row is no expert's) and
 // the matrix whose tensor scale it has (.row).
 __device__ __forceinline__ Dest row_source(const DequantParams& p, int64_t row) {
   if (p.offsets == nullptr) {
@@ -612,7 +612,7 @@ __device__ __forceinline__ void store_shifted(void* p, int n, const uint32_t (&w
 }
 
 // value = (code x block scale) x tensor scale, rounded once to the output type
-// (code x block scale is exact).  Rows past the last expert's are zeros.
+// (code x block scale is exact).  Rows that are no expert's are zeros.
 template <typename O, int FMT, int VB>
 __global__ void __launch_bounds__(kQThreads)
 dequantize_kernel(const DequantParams p) {

@@ -198,7 +198,7 @@ def fp4_dequantize(codes, scales, cols: int, fmt: str = "nvfp4", tensor_scale: O
                    out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The numbers of codes [rows, .] or [E, rows, .], in bf16 or float32.  With
     expert_offsets the rows are sorted by expert (their scales lie by expert, one
-    tensor scale) and rows past the last expert's are zeros."""
+    tensor scale) and rows that are no expert's are zeros."""
     f = _format(fmt)
     if dtype not in DTYPES:
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
@@ -236,7 +236,8 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
                        status: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [P, N] bf16 of sorted rows (a_codes [P, .], scales by expert) times their
     expert's matrix (w_codes [E, N, .]), both with `cols` columns; tensor scales
-    float32 [1] and [E] (nvfp4).  Rows past the last expert's are zeros."""
+    float32 [1] and [E] (nvfp4).  Rows that are no expert's (before
+    expert_offsets[0], from expert_offsets[E] on) are zeros."""
     f = _format(fmt)
     if not isinstance(a_codes, torch.Tensor):
         raise TypeError("a_codes must be a torch.Tensor")

@@ -206,3 +206,27 @@ def test_sorts_of_different_experts_in_two_threads(cuda_device, T, experts):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert codes == [mlr.MLR_OK] * 6000 and done == [True, True]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("P,E,N,first,last", [(40, 3, 128, 7, 33), (700, 2, 129, 130, 700), (9, 4, 64, 9, 9), (2000, 2, 72, 1000, 1999)])
+def test_rows_before_the_first_expert(cuda_device, fmt, P, E, N, first, last):
+    """Offsets need not begin at 0: rows before the first expert's are no expert's,
+    as are those past the last one's.  Their codes and results are zeros, and
+    the others are those of the same rows alone."""
+    C = 96
+    off = torch.linspace(first, last, E + 1).int().cuda()
+    gu = torch.randn(P, 2 * C, generator=torch.Generator().manual_seed(P)).cuda()
+    codes = torch.full((P, 48), 255, dtype=torch.uint8, device="cuda")
+    codes, scales = fp4.fp4_quantize_swiglu(gu, off, fmt, codes=codes, check=True)
+    assert not codes[:first].any() and not codes[last:].any()
+    h = fp4.fp4_dequantize(codes, scales, C, fmt, expert_offsets=off, dtype=torch.float32)
+    assert not h[:first].any() and not h[last:].any()
+    qw, sw = fp4.fp4_quantize(torch.randn(E, N, C, generator=torch.Generator().manual_seed(N)).cuda(), fmt)
+    y = torch.full((P, N), 7.0, dtype=BF, device="cuda")
+    fp4.fp4_expert_product(codes, scales, off, qw, sw, C, fmt, y=y)
+    assert not y[:first].any() and not y[last:].any()
+    if first < last:
+        part = fp4.fp4_quantize_swiglu(gu[first:last].contiguous(), off - first, fmt, check=True)
+        assert torch.equal(part[0], codes[first:last])
+        assert torch.equal(fp4.fp4_expert_product(*part, off - first, qw, sw, C, fmt), y[first:last])
