@@ -405,10 +405,7 @@ __device__ __forceinline__ void narrow(const float (&v)[4], uint4& q) {
 __device__ __forceinline__ void narrow(const float (&v)[8], uint4& q) {
   q = make_uint4(narrow2(v[0], v[1]), narrow2(v[2], v[3]), narrow2(v[4], v[5]), narrow2(v[6], v[7]));
 }
-__device__ __forceinline__ float widen1(float v) { return v; }
 __device__ __forceinline__ float widen1(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
-__device__ __forceinline__ void narrow1(float v, float& q) { q = v; }
-__device__ __forceinline__ void narrow1(float v, uint16_t& q) { q = f32_to_bf16_bits(v); }
 
 // How a thread takes 16 bytes of a row.  kWhole: rows and bases are multiples of
 // 16 bytes.  kPieces (bf16 rows off that grid): in the two aligned pieces that
@@ -425,14 +422,12 @@ __device__ __forceinline__ uint4 load_strided(const float* r, int c, int step, i
   for (int i = 0; i < 4; ++i) v[i] = c + i * step < H ? __ldg(r + c + i * step) : 0.f;
   return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
 }
-__device__ __forceinline__ uint4 load_strided(const uint16_t*, int, int, int) { return make_uint4(0, 0, 0, 0); }
 __device__ __forceinline__ void store_strided(float* r, int c, int step, int H, const uint4& q) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (c + i * step < H) r[c + i * step] = __uint_as_float(w[i]);
 }
-__device__ __forceinline__ void store_strided(uint16_t*, int, int, int, const uint4&) {}
 
 // The threads of a token: a power of two, so that short rows share a block.
 int row_threads(int nv, int most) {
@@ -664,11 +659,12 @@ unpermute_backward_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows
 // of 1111 bf16: 62 us, with 128 threads 68, element by element 144; 10000 x 6 of
 // 461: 40, with 64 threads 42).
 constexpr int kBackSegBytes = 4096;
-template <typename E_, int KU, int LANES>
+template <int KU, int LANES>
 __global__ void __launch_bounds__(LANES)
-unpermute_backward_unaligned_kernel(const E_* __restrict__ dy, const E_* __restrict__ rows,
+unpermute_backward_unaligned_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ rows,
                                     const int32_t* __restrict__ pair_pos, const float* __restrict__ w, int T, int K,
-                                    int H, E_* __restrict__ d_rows, float* __restrict__ dw, int32_t* d_status) {
+                                    int H, uint16_t* __restrict__ d_rows, float* __restrict__ dw, int32_t* d_status) {
+  using E_ = uint16_t;
   constexpr int es = (int)sizeof(E_), N = 16 / es;
   __shared__ float part[LANES / 32][KU];
   __shared__ __align__(16) E_ seg[(kBackSegBytes + 32) / es];  // dy columns [b0, b0 + span)
@@ -712,14 +708,12 @@ unpermute_backward_unaligned_kernel(const E_* __restrict__ dy, const E_* __restr
           widen(v[j], f);
           const uint32_t* sw = reinterpret_cast<const uint32_t*>(seg) + (off[j] + i) * es / 4;
           uint4 q = make_uint4(sw[0], sw[1], sw[2], sw[3]);
-          if (es == 2) {  // dy's columns may begin inside a word
-            const uint32_t last = sw[4];
-            const int m = 16 * (off[j] & 1);
-            q.x = __funnelshift_r(q.x, q.y, m);
-            q.y = __funnelshift_r(q.y, q.z, m);
-            q.z = __funnelshift_r(q.z, q.w, m);
-            q.w = __funnelshift_r(q.w, last, m);
-          }
+          const uint32_t last = sw[4];  // dy's columns may begin inside a word
+          const int m = 16 * (off[j] & 1);
+          q.x = __funnelshift_r(q.x, q.y, m);
+          q.y = __funnelshift_r(q.y, q.z, m);
+          q.z = __funnelshift_r(q.z, q.w, m);
+          q.w = __funnelshift_r(q.w, last, m);
           widen(q, g);
 #pragma unroll
           for (int u = 0; u < N; ++u) {
@@ -748,7 +742,7 @@ unpermute_backward_unaligned_kernel(const E_* __restrict__ dy, const E_* __restr
         for (int j = 0; j < KU; ++j) {
           if (c[j] < 0) continue;
           const float g = widen1(seg[c[j] - b0]);
-          narrow1(pr[j].use ? pr[j].w * g : 0.f, d_rows[(int64_t)pr[j].row * H + c[j]]);
+          d_rows[(int64_t)pr[j].row * H + c[j]] = f32_to_bf16_bits(pr[j].use ? pr[j].w * g : 0.f);
           if (pr[j].use) dot[j] = fmaf(g, widen1(e[j]), dot[j]);
         }
       }
@@ -853,8 +847,8 @@ int launch_unpermute_backward_k(const void* dy, const void* rows, const int32_t*
     auto run = [&](auto kernel, int threads) {
       return launch_pdl(kernel, dim3((unsigned)T), dim3(threads), 0, stream, dyp, rp, pos, w, T, K, H, dp, dw, d_status);
     };
-    err = H * (int)sizeof(E_) <= 1024 ? run(unpermute_backward_unaligned_kernel<E_, KU, 32>, 32)
-                                     : run(unpermute_backward_unaligned_kernel<E_, KU, 64>, 64);
+    err = H * (int)sizeof(E_) <= 1024 ? run(unpermute_backward_unaligned_kernel<KU, 32>, 32)
+                                     : run(unpermute_backward_unaligned_kernel<KU, 64>, 64);
   }
   return launched(err, 1);
 }
