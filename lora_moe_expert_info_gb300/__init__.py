@@ -217,14 +217,15 @@ def _req(t: torch.Tensor, name: str, dtype, dev):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _launch_device(dev: torch.device, fn: str):
-    """Refuses tensors that the kernels cannot take: they are launched on the
-    current device's stream, so the tensors have to be on that device."""
-    if dev.type != "cuda":
-        raise ValueError(f"{fn}: tensors must be on a CUDA device, got {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: tensors are on {dev}, the current device (or the stream's) is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _launch_stream(t: torch.Tensor, fn: str) -> int:
+    """The cudaStream_t that kernels on t are launched on: the current one, which
+    _on_stream makes the caller's.  Refuses a t that is not on its device."""
+    if t.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        if t.get_device() == dev:
+            return torch._C._cuda_getCurrentRawStream(dev)
+        raise ValueError(f"{fn}: tensors are on {t.device}, the current device (or the stream's) is cuda:{dev}")
+    raise ValueError(f"{fn}: tensors must be on a CUDA device, got {t.device}")
 
 
 @_on_stream

@@ -23,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import _check_device, _check_host, _launch_device, _on_stream, _req, _stream_number, library
+from . import _check_device, _check_host, _launch_stream, _on_stream, _req, library
 from .permute import DTYPES, _address, _float, _out, moe_sort_pairs, moe_unpermute
 
 __all__ = ["fp4_quantize", "fp4_quantize_permuted", "fp4_quantize_swiglu", "fp4_dequantize", "fp4_expert_product",
@@ -122,12 +122,11 @@ def fp4_quantize(x, fmt: str = "nvfp4", tensor_scale: Optional[torch.Tensor] = N
     if cols == 0:
         raise ValueError("x has no columns")
     _scale(tensor_scale, "tensor_scale", n, f, dev)
-    _launch_device(dev, "fp4_quantize")
+    on = _launch_stream(x, "fp4_quantize")
     codes, scales = _outputs(codes, scales, (*lead, rows), (*lead, (rows + 127) // 128), cols, f, dev)
     if n * rows:
         _check_host(_lib().moe_fp4_quantize(x.data_ptr(), n, rows, cols, dtype, f, _address(tensor_scale),
-                                            codes.data_ptr(), scales.data_ptr(), _stream_number(stream)),
-                    "fp4_quantize")
+                                            codes.data_ptr(), scales.data_ptr(), on), "fp4_quantize")
     return codes, scales
 
 
@@ -154,14 +153,14 @@ def fp4_quantize_permuted(x, topk_ids, pair_pos, expert_offsets, fmt: str = "nvf
         raise ValueError("x has no columns")
     K = topk_ids.shape[1]
     _scale(tensor_scale, "tensor_scale", 1, f, dev)
-    _launch_device(dev, "fp4_quantize_permuted")
+    on = _launch_stream(x, "fp4_quantize_permuted")
     codes, scales = _outputs(codes, scales, (T * K,), (T * K // 128 + E,), cols, f, dev)
     if T:
         status = _status(check, dev)
         _done(_lib().moe_fp4_quantize_permuted(x.data_ptr(), topk_ids.data_ptr(), pair_pos.data_ptr(),
                                                expert_offsets.data_ptr(), T, K, cols, E, dtype, f,
                                                _address(tensor_scale), codes.data_ptr(), scales.data_ptr(),
-                                               _address(status), _stream_number(stream)), status,
+                                               _address(status), on), status,
               "fp4_quantize_permuted")
     return codes, scales
 
@@ -182,13 +181,13 @@ def fp4_quantize_swiglu(gate_up, expert_offsets, fmt: str = "nvfp4", tensor_scal
     if gate_up.shape[1] % 2 or cols == 0:
         raise ValueError("gate_up must have an even number of columns")
     _scale(tensor_scale, "tensor_scale", 1, f, dev)
-    _launch_device(dev, "fp4_quantize_swiglu")
+    on = _launch_stream(gate_up, "fp4_quantize_swiglu")
     codes, scales = _outputs(codes, scales, (P,), (P // 128 + E,), cols, f, dev)
     if P:
         status = _status(check, dev)
         _done(_lib().moe_fp4_quantize_swiglu(gate_up.data_ptr(), expert_offsets.data_ptr(), P, cols, E, dtype, f,
-                                             _address(tensor_scale), codes.data_ptr(), scales.data_ptr(), _address(status),
-                                             _stream_number(stream)), status, "fp4_quantize_swiglu")
+                                             _address(tensor_scale), codes.data_ptr(), scales.data_ptr(),
+                                             _address(status), on), status, "fp4_quantize_swiglu")
     return codes, scales
 
 
@@ -220,12 +219,12 @@ def fp4_dequantize(codes, scales, cols: int, fmt: str = "nvfp4", tensor_scale: O
     if codes.shape[-1] != _pitch(cols) or scales.shape != (*blocks, _atoms(cols, f), 32, 4, 4):
         raise ValueError("fp4_dequantize: inconsistent shapes")
     _scale(tensor_scale, "tensor_scale", 1 if expert_offsets is not None else n, f, dev)
-    _launch_device(dev, "fp4_dequantize")
+    on = _launch_stream(codes, "fp4_dequantize")
     out = _out(out, "out", (*lead, rows, cols), dtype, dev)
     if out.numel():
         _check_host(_lib().moe_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), _address(expert_offsets), n, rows,
-                                              cols, f, _address(tensor_scale), DTYPES[dtype], out.data_ptr(),
-                                              _stream_number(stream)), "fp4_dequantize")
+                                              cols, f, _address(tensor_scale), DTYPES[dtype], out.data_ptr(), on),
+                    "fp4_dequantize")
     return out
 
 
@@ -258,7 +257,7 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
     _scale(w_tensor_scale, "w_tensor_scale", E, f, dev)
     if status is not None:
         _req(status, "status", torch.int32, dev)
-    _launch_device(dev, "fp4_expert_product")
+    on = _launch_stream(a_codes, "fp4_expert_product")
     y = _out(y, "y", (P, N), torch.bfloat16, dev)
     if P == 0 or N == 0:
         return y
@@ -266,8 +265,7 @@ def fp4_expert_product(a_codes, a_scales, expert_offsets, w_codes, w_scales, col
         status = _status(True, dev)
     code = _lib().moe_fp4_expert_product(a_codes.data_ptr(), a_scales.data_ptr(), _address(a_tensor_scale),
                                          w_codes.data_ptr(), w_scales.data_ptr(), _address(w_tensor_scale),
-                                         expert_offsets.data_ptr(), P, E, N, cols, f, y.data_ptr(), _address(status),
-                                         _stream_number(stream))
+                                         expert_offsets.data_ptr(), P, E, N, cols, f, y.data_ptr(), _address(status), on)
     _done(code, status if check else None, "fp4_expert_product")
     return y
 

@@ -22,7 +22,7 @@ from typing import Optional, Tuple
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _check_device, _check_host, _launch_device, _on_stream, _req, _stream_number, library
+from . import _check_device, _check_host, _launch_stream, _on_stream, _req, library
 
 __all__ = ["moe_permute", "moe_sort_pairs", "moe_permute_backward", "moe_unpermute", "moe_unpermute_backward",
            "MoePermute", "MoeUnpermute"]
@@ -75,7 +75,7 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype, dev) -> torch.Tenso
     return t
 
 
-def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, stream, check, fn):
+def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, check, fn):
     lib = _lib()
     if not isinstance(topk_ids, torch.Tensor):
         raise TypeError("topk_ids must be a torch.Tensor")
@@ -91,7 +91,7 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
         H = x.shape[1]
         if x.shape[0] != T:
             raise ValueError(f"{fn}: inconsistent shapes")
-    _launch_device(dev, fn)
+    on = _launch_stream(topk_ids, fn)
     if x is not None:
         rows = _out(rows, "rows", (T * K, H), x.dtype, dev)
     # an empty tensor has no address: rows of no columns are only sorted
@@ -108,8 +108,7 @@ def _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, s
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     code = lib.moe_permute(x.data_ptr() if copy else None, topk_ids.data_ptr(), T, K, H, E, dtype,
                            rows.data_ptr() if copy else None, pair_pos.data_ptr(), expert_offsets.data_ptr(),
-                           _address(workspace), 0 if workspace is None else workspace.nbytes, _address(status),
-                           _stream_number(stream))
+                           _address(workspace), 0 if workspace is None else workspace.nbytes, _address(status), on)
     _check_host(code, fn)
     if check:
         _check_device(status, fn)
@@ -127,7 +126,7 @@ def moe_permute(x, topk_ids, num_experts: int, rows: Optional[torch.Tensor] = No
     other than -1 outside [0, num_experts) raise."""
     if x is None:
         raise TypeError("x must be a torch.Tensor")
-    return _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, stream, check, "moe_permute")
+    return _sort(x, topk_ids, num_experts, rows, pair_pos, expert_offsets, workspace, check, "moe_permute")
 
 
 @_on_stream
@@ -135,11 +134,10 @@ def moe_sort_pairs(topk_ids, num_experts: int, pair_pos: Optional[torch.Tensor] 
                    expert_offsets: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                    stream=None, check: bool = True) -> Tuple[torch.Tensor, torch.Tensor]:
     """The order alone: (pair_pos, expert_offsets) of moe_permute."""
-    return _sort(None, topk_ids, num_experts, None, pair_pos, expert_offsets, workspace, stream, check,
-                 "moe_sort_pairs")[1:]
+    return _sort(None, topk_ids, num_experts, None, pair_pos, expert_offsets, workspace, check, "moe_sort_pairs")[1:]
 
 
-def _gather(rows, pair_pos, weights, y, stream, check, fn, rows_name):
+def _gather(rows, pair_pos, weights, y, check, fn, rows_name):
     lib = _lib()
     if not isinstance(pair_pos, torch.Tensor):
         raise TypeError("pair_pos must be a torch.Tensor")
@@ -154,13 +152,13 @@ def _gather(rows, pair_pos, weights, y, stream, check, fn, rows_name):
         _req(weights, "topk_weights", torch.float32, dev)
     if rows.shape[0] != T * K or (weights is not None and weights.shape != (T, K)):
         raise ValueError(f"{fn}: inconsistent shapes")
-    _launch_device(dev, fn)
+    on = _launch_stream(pair_pos, fn)
     y = _out(y, "y", (T, H), rows.dtype, dev)
     if T == 0 or H == 0:
         return y
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     code = lib.moe_unpermute(rows.data_ptr(), pair_pos.data_ptr(), _address(weights), T, K, H, dtype, y.data_ptr(),
-                             _address(status), _stream_number(stream))
+                             _address(status), on)
     _check_host(code, fn)
     if check:
         _check_device(status, fn)
@@ -171,7 +169,7 @@ def _gather(rows, pair_pos, weights, y, stream, check, fn, rows_name):
 def moe_permute_backward(d_rows, pair_pos, dx: Optional[torch.Tensor] = None, stream=None,
                          check: bool = False) -> torch.Tensor:
     """The gradient of moe_permute's x: dx[t] = sum over k of d_rows[pair_pos[t, k]]."""
-    return _gather(d_rows, pair_pos, None, dx, stream, check, "moe_permute_backward", "d_rows")
+    return _gather(d_rows, pair_pos, None, dx, check, "moe_permute_backward", "d_rows")
 
 
 @_on_stream
@@ -180,7 +178,7 @@ def moe_unpermute(rows, pair_pos, topk_weights, y: Optional[torch.Tensor] = None
     """y[t] = sum over k of topk_weights[t, k] * rows[pair_pos[t, k]], masked pairs skipped."""
     if topk_weights is None:
         raise TypeError("topk_weights must be a torch.Tensor")
-    return _gather(rows, pair_pos, topk_weights, y, stream, check, "moe_unpermute", "rows")
+    return _gather(rows, pair_pos, topk_weights, y, check, "moe_unpermute", "rows")
 
 
 @_on_stream
@@ -203,15 +201,14 @@ def moe_unpermute_backward(dy, rows, pair_pos, topk_weights, d_rows: Optional[to
     H = rows.shape[1]
     if rows.shape[0] != T * K or dy.shape != (T, H) or topk_weights.shape != (T, K):
         raise ValueError("moe_unpermute_backward: inconsistent shapes")
-    _launch_device(dev, "moe_unpermute_backward")
+    on = _launch_stream(pair_pos, "moe_unpermute_backward")
     d_rows = _out(d_rows, "d_rows", (T * K, H), rows.dtype, dev)
     d_weights = _out(d_weights, "d_weights", (T, K), torch.float32, dev)
     if T == 0 or H == 0:
         return d_rows, d_weights.zero_()
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     code = lib.moe_unpermute_backward(dy.data_ptr(), rows.data_ptr(), pair_pos.data_ptr(), topk_weights.data_ptr(), T,
-                                      K, H, dtype, d_rows.data_ptr(), d_weights.data_ptr(), _address(status),
-                                      _stream_number(stream))
+                                      K, H, dtype, d_rows.data_ptr(), d_weights.data_ptr(), _address(status), on)
     _check_host(code, "moe_unpermute_backward")
     if check:
         _check_device(status, "moe_unpermute_backward")

@@ -69,12 +69,23 @@ def test_host_tensors_are_refused(name):
         calls()[name]()
 
 
+class On:
+    """As much of a tensor as tells where it is."""
+
+    def __init__(self, index):
+        self.device, self.is_cuda = torch.device("cuda", index), True
+
+    def get_device(self):
+        return self.device.index
+
+
 def test_tensors_of_another_device_are_refused(monkeypatch):
     """The kernels go to the current device's stream."""
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    mlr._launch_device(torch.device("cuda", 0), "call")
-    with pytest.raises(ValueError, match="cuda:1"):
-        mlr._launch_device(torch.device("cuda", 1), "call")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d, raising=False)
+    assert mlr._launch_stream(On(1), "call") == 71
+    with pytest.raises(ValueError, match="tensors are on cuda:0, .* is cuda:1"):
+        mlr._launch_stream(On(0), "call")
 
 
 def test_workspace_of_sorts_with_and_without_rows(lib):
