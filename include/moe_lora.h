@@ -55,6 +55,7 @@ extern "C" {
 #define MLR_STATUS_CAPACITY 0x08     /* padded length exceeded capacity (truncated)     */
 #define MLR_STATUS_TIMEOUT 0x10      /* a pipeline wait gave up; results are invalid    */
 #define MLR_STATUS_RANK 0x20         /* lora_ranks[l] outside [0, max_rank]             */
+#define MLR_STATUS_VALUE 0x40        /* a logit is NaN or +inf (taken as -inf)          */
 
 typedef uint16_t mlr_bf16; /* bfloat16 bit pattern */
 
@@ -604,6 +605,75 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
                            const uint8_t* w_codes, const uint8_t* w_scales, const float* w_tensor_scale,
                            const int32_t* expert_offsets, int32_t num_rows, int32_t num_experts, int32_t outputs,
                            int32_t cols, int32_t fmt, mlr_bf16* y, int32_t* d_status, void* stream);
+
+/*
+ * Before the experts: the norm, and the router's choice.
+ *
+ * moe_rms_norm: per row of `hidden` columns, r = x + residual rounded to `dtype`
+ *   (r = x without a residual), y = r weight / sqrt(mean(r^2) + eps), rounded.
+ *   x, residual, y, residual_out (r) [num_tokens, hidden] of type `dtype`; residual and
+ *   residual_out both or neither; weight [hidden] of type `weight_dtype`.
+ *   codes, exps (both or neither): y in 8 bits as the W8A8 layer quantises its x:
+ *   per group of 128 columns the scale 2^s, s the smallest integer >= -127 with
+ *   max|y| <= 448 * 2^s (0 for zeros), codes [num_tokens, hidden] the nearest E4M3
+ *   values of y * 2^-s for y as rounded to `dtype` (infinities saturate, NaN stays),
+ *   exps [num_tokens, ceil(hidden / 128)] the bytes s + 127.  y null: codes alone.
+ *   y may be x, residual_out may be residual.
+ * moe_fp8_dequantize: code * 2^(exp - 127) of codes [rows, cols], rounded to `dtype`
+ *   (bf16 holds every such number that is not below its range); an exp byte of 255: NaN.
+ * moe_rms_norm_backward: with m = 1 / sqrt(mean(r^2) + eps) and h = dy weight
+ *   dx = m (h - r m^2 mean(h r)) + d_r, the gradient of both x and residual (d_r: what
+ *   reaches r otherwise, null for none), and d_weight[c] = sum over rows of dy r m,
+ *   float32.  dx may be dy or d_r.  workspace of moe_rms_norm_backward_workspace_bytes.
+ * Sums are held in fp32 in a fixed order: results are bit-identical between runs.
+ * Limit: hidden <= 32768.
+ *
+ * moe_route: each token's topk experts from logits [num_tokens, num_experts].
+ *   A logit that is not finite counts as -inf (NaN and +inf also set MLR_STATUS_VALUE);
+ *   such an expert is never chosen.  Choice scores: the logits; with a bias (sigmoid
+ *   only) or groups under MLR_SCORE_SIGMOID sigmoid(logit) + bias.  num_groups > 1: only
+ *   the experts of the topk_groups best groups (num_experts / num_groups consecutive
+ *   experts each) stand to choice; a group's score is its best choice score under
+ *   softmax, the sum of its two best under sigmoid.  Scores are compared as the numbers
+ *   they stand for (in 64 bits where 32 do not tell), ties go to the lowest index.
+ *   topk_ids int32, topk_weights float32 [num_tokens, topk]: the best first, weights
+ *   softmax(logits) or sigmoid(logits) of the chosen, divided by their sum where
+ *   `renormalize` (0 where that is 0), times `scale`.  Places that no expert is left
+ *   for have id -1 and weight 0, and so have the tokens whose token_mask (nullable, a
+ *   byte per token) is 0; their logits are not read.
+ * moe_balance_loss: loss[0] = E / (K N^2) sum_e c_e sum_t p_te, with N the tokens that
+ *   are not masked, c_e their pairs of expert e and p = softmax(logits), or
+ *   sigmoid(logits) over their sum.  counts int32 [num_experts + 1]: c, then N.  Ids
+ *   other than -1 outside [0, num_experts) set MLR_STATUS_INDEX; neither counts.
+ * moe_route_backward: d_logits of type `dtype` from d_weights [num_tokens, topk]
+ *   (nullable) and, given counts and d_loss[1] (both or neither), from the balance loss;
+ *   zeros in masked tokens.  The same id twice in a token: both gradients are added.
+ *   topk, scoring, renormalize and scale as in the forward calls.
+ * Limits: num_experts <= 4096, topk <= 32, num_groups <= 256, num_tokens * topk < 2^31 - 1.
+ */
+#define MLR_SCORE_SOFTMAX 0
+#define MLR_SCORE_SIGMOID 1
+int moe_rms_norm(const void* x, const void* residual, const void* weight, int32_t num_tokens, int32_t hidden,
+                 int32_t dtype, int32_t weight_dtype, float eps, void* y, void* residual_out, uint8_t* codes,
+                 uint8_t* exps, void* stream);
+int moe_fp8_dequantize(const uint8_t* codes, const uint8_t* exps, int32_t rows, int32_t cols, int32_t dtype, void* out,
+                       void* stream);
+size_t moe_rms_norm_backward_workspace_bytes(int32_t num_tokens, int32_t hidden, int32_t dtype);
+int moe_rms_norm_backward(const void* dy, const void* r, const void* weight, const void* d_r, int32_t num_tokens,
+                          int32_t hidden, int32_t dtype, int32_t weight_dtype, float eps, void* dx, float* d_weight,
+                          void* workspace, size_t ws_bytes, void* stream);
+int moe_route(const void* logits, const float* bias, const uint8_t* token_mask, int32_t num_tokens,
+              int32_t num_experts, int32_t topk, int32_t num_groups, int32_t topk_groups, int32_t dtype,
+              int32_t scoring, int32_t renormalize, float scale, int32_t* topk_ids, float* topk_weights,
+              int32_t* d_status, void* stream);
+size_t moe_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts);
+int moe_balance_loss(const void* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t num_tokens,
+                     int32_t num_experts, int32_t topk, int32_t dtype, int32_t scoring, float* loss, int32_t* counts,
+                     void* workspace, size_t ws_bytes, int32_t* d_status, void* stream);
+int moe_route_backward(const void* logits, const int32_t* topk_ids, const float* d_weights, const int32_t* counts,
+                       const float* d_loss, const uint8_t* token_mask, int32_t num_tokens, int32_t num_experts,
+                       int32_t topk, int32_t dtype, int32_t scoring, int32_t renormalize, float scale, void* d_logits,
+                       int32_t* d_status, void* stream);
 
 int moe_lora_profile_stages(uint32_t mask);
 int moe_lora_profile_begin(int32_t max_calls);

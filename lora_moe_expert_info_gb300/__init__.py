@@ -43,7 +43,7 @@ MLR_ERR_UNSUPPORTED = -8
 
 STATUS_BITS = {0x01: "bad seg_indptr", 0x02: "under-covers tokens", 0x04: "id out of range",
                0x08: "capacity exceeded", 0x10: "device wait timed out",
-               0x20: "rank out of range"}
+               0x20: "rank out of range", 0x40: "a logit is NaN or +inf"}
 
 _lock = threading.Lock()
 _lib = None
@@ -203,6 +203,8 @@ def _check_device(status: torch.Tensor, fn: str):
         raise AssertionError(f"{fn}: kernel under-covers tokens ({names})")
     if bits & 0x10:
         raise MoeLoraError(MLR_ERR_TIMEOUT, f"{fn}: {names}")
+    if bits & 0x40:
+        raise MoeLoraError(MLR_ERR_INVALID, f"{fn}: {names}")
     raise MoeLoraError(MLR_ERR_INDEX if bits & 0x24 else MLR_ERR_CAPACITY, f"{fn}: {names}")
 
 
