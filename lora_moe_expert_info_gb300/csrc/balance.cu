@@ -1,0 +1,467 @@
+// balance.cu -- the balance loss over a batch with the tokens per expert, and the
+// gradient of the router's logits.
+//
+// With s = softmax(logits) or sigmoid(logits) (a logit that is not finite counts as
+// -inf), p = s [/ its sum over e (sigmoid)], N unmasked tokens and c_e pairs of
+// expert e:
+//   loss = E / (K N^2) sum_e c_e sum_t p_te
+// Gradients, with a_e = dloss E / (K N^2) c_e and g_k what reaches weight k:
+//   softmax  dl_e = p_e (a_e - sum_j p_j a_j)           + g's part
+//   sigmoid  dl_e = p_e (1 - s_e) (a_e - sum_j p_j a_j) + g's part
+// where g's part is, for a chosen expert with weight w = scale s / total,
+//   w (g - sum g w / scale) [(1 - s) for sigmoid]       renormalised
+//   scale g s (1 - s)                                   sigmoid
+//   p (scale g - sum scale g p), of all experts         softmax
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
+#include "mlr_router.cuh"
+
+namespace mlr {
+namespace {
+
+constexpr int kBalanceThreads = 256;
+
+// A sum over the block, the same in every thread (E > 1024: a token per block).
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBalanceThreads / 32; ++i) v += red[i];
+  return v;
+}
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = warp_max(v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < kBalanceThreads / 32; ++i) v = fmaxf(v, red[i]);
+  return v;
+}
+
+// How the threads hold a token's logits.  LPT lanes of a warp with V each (E up to
+// 1024), or the block (LPT = 256).
+template <int LPT> constexpr bool kBlockTokens = LPT == kBalanceThreads;
+template <int LPT> constexpr int kTeams = kBalanceThreads / LPT;
+template <int LPT>
+__device__ __forceinline__ float team_sum(float v, float* red) {
+  if constexpr (kBlockTokens<LPT>) return block_sum(v, red);
+  else return part_sum<LPT>(v);
+}
+template <int LPT>
+__device__ __forceinline__ float team_max(float v, float* red) {
+  if constexpr (kBlockTokens<LPT>) return block_max(v, red);
+  else return part_max<LPT>(v);
+}
+template <int LPT>
+__device__ __forceinline__ void team_sync() {
+  if constexpr (kBlockTokens<LPT>) __syncthreads();
+  else __syncwarp();
+}
+
+// v: logits to s, zeros past E, in tokens that are not active and for logits that are
+// not finite.  Returns 1 / sum of s, 0 where that is 0.  Every thread of the warp
+// (the block) calls it.
+template <int VEC, int LPT, int V, typename E_>
+__device__ __forceinline__ float scores(const E_* row, int E, bool sigmoid, int ll, bool active, float* red, float (&v)[V]) {
+  const float check = load_logits<VEC, LPT>(row, E, ll, active, v);
+  if (__any_sync(0xffffffffu, !(check == 0.f)))
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = finite_logit(v[i]);
+  close_past<VEC, LPT>(E, ll, v);
+  float sum = 0.f;
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += v[i] = quick_sigmoid(v[i]);
+  } else {
+    float most = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
+    most = team_max<LPT>(most, red);
+    most = most > -CUDART_INF_F ? most : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += v[i] = __expf(v[i] - most);
+  }
+  sum = team_sum<LPT>(sum, red);
+  return active && sum > 0.f ? 1.f / sum : 0.f;
+}
+
+// Sums of shares and pairs per expert over the block's tokens: part [blocks][E]
+// and count [blocks][E + 1] (the last one: tokens).
+template <int VEC, int LPT, int V, typename E_>
+__global__ void __launch_bounds__(kBalanceThreads)
+balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
+               int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, int32_t* status) {
+  extern __shared__ int hist[];  // [E + 1] pairs, then float [warps (1 for a block's token)][E] shares
+  __shared__ float red[kBalanceThreads / 32];
+  constexpr int TEAMS = kTeams<LPT>, ROWS = kBlockTokens<LPT> ? 1 : kBalanceThreads / 32;
+  float* sums = reinterpret_cast<float*>(hist + E + 1);
+  const int team = threadIdx.x / LPT, ll = threadIdx.x % LPT;
+  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  float acc[V] = {};
+  int tokens = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += (int64_t)gridDim.x * TEAMS) {
+    const int64_t t = t0 + team;
+    const bool active = t < T && (mask == nullptr || mask[t]);
+    float v[V];
+    const float inv = scores<VEC, LPT>(logits + (active ? t : 0) * E, E, sigmoid, ll, active, red, v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+    if (active) {
+      ++tokens;
+      for (int k = ll; k < K; k += LPT) {
+        const int id = __ldg(ids + t * K + k);
+        if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+        else if (id != -1) set_status(status, MLR_STATUS_INDEX);
+      }
+    }
+  }
+  if (ll == 0) atomicAdd(&hist[E], tokens);
+  if constexpr (!kBlockTokens<LPT>)
+#pragma unroll
+    for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+  if (kBlockTokens<LPT> || (threadIdx.x & 31) < LPT)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
+      if (e < E) sums[(kBlockTokens<LPT> ? 0 : threadIdx.x >> 5) * E + e] = acc[i];
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
+    count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+    if (e == E) continue;
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) v += sums[i * E + e];
+    part[(int64_t)blockIdx.x * E + e] = v;
+  }
+}
+
+// The blocks' sums added in order, by one cluster: a block takes every eighth run of
+// 32 experts, a warp every 32nd row; then the loss, over distributed shared memory.
+constexpr int kTotalThreads = 1024, kTotalCluster = 8;
+__global__ void __cluster_dims__(kTotalCluster, 1, 1) __launch_bounds__(kTotalThreads)
+balance_total_kernel(const float* __restrict__ part, const int32_t* __restrict__ count, int blocks, int E, int K,
+                     float* __restrict__ loss, int32_t* __restrict__ counts) {
+  namespace cg = cooperative_groups;
+  __shared__ float sums[32][33];
+  __shared__ int pairs[32][33];
+  __shared__ double total;   // of this block's experts
+  __shared__ int tokens;     // in the block that has column E
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double mine = 0.0;  // warp 0
+  pdl_wait();
+  pdl_trigger();
+  for (int e0 = blockIdx.x * 32; e0 <= E; e0 += kTotalCluster * 32) {
+    const int e = e0 + lane;
+    float s = 0.f;  // of a few hundred positive terms; fp64 takes 16 cycles an instruction
+    int c = 0;
+    if (e <= E)
+#pragma unroll 4
+      for (int b = warp; b < blocks; b += 32) {
+        c += count[(int64_t)b * (E + 1) + e];
+        if (e < E) s += part[(int64_t)b * E + e];
+      }
+    __syncthreads();
+    sums[warp][lane] = s;
+    pairs[warp][lane] = c;
+    __syncthreads();
+    if (warp == 0 && e <= E) {
+      s = 0.f;
+      c = 0;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        s += sums[i][lane];
+        c += pairs[i][lane];
+      }
+      counts[e] = c;
+      if (e == E) tokens = c;
+      else mine += (double)s * c;
+    }
+  }
+  if (warp == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) total = mine;
+  }
+  cluster.sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    double v = 0.0;
+    for (int i = 0; i < kTotalCluster; ++i) v += *cluster.map_shared_rank(&total, i);
+    const int n = *cluster.map_shared_rank(&tokens, E / 32 % kTotalCluster);
+    const double d = n > 0 ? n : 1;
+    *loss = (float)(v * E / (K * d * d));
+  }
+  cluster.sync();  // the blocks' shared memory is read until here
+}
+
+struct GradArgs {
+  const int32_t* ids;
+  const float* d_weights;  // nullable: no gradient of the weights
+  const int32_t* counts;   // nullable: none of the loss
+  const float* d_loss;
+  const uint8_t* mask;
+  int T, E, K;
+  bool sigmoid, renormalize;
+  float scale;
+};
+
+// Gradient of the logits.  What comes by the weights is put together by lanes that
+// take a place each (place ll + LPT c; in a block's token: its first warp) and laid
+// in a row of shared memory, zero elsewhere, from where the experts' lanes take it.
+template <int VEC, int LPT, int V, typename E_>
+__global__ void __launch_bounds__(kBalanceThreads)
+route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ GradArgs a, E_* __restrict__ d_logits,
+                      int32_t* status) {
+  extern __shared__ float rows[];  // [teams][E], zero but for the chosen experts while a token is in work
+  __shared__ float red[kBalanceThreads / 32];
+  constexpr int TEAMS = kTeams<LPT>;
+  constexpr int PL = kBlockTokens<LPT> ? 32 : LPT;  // lanes that take places
+  constexpr int CP = kMaxRouteTopk / PL;
+  const int team = threadIdx.x / LPT, ll = threadIdx.x % LPT;
+  const int E = a.E, K = a.K;
+  const bool by_weights = a.d_weights != nullptr, all_chosen = by_weights && !a.sigmoid && !a.renormalize;
+  const bool shares = a.counts != nullptr || all_chosen;
+  float* row_s = rows + team * E;
+  if (by_weights) {
+    for (int e = ll; e < E; e += LPT) row_s[e] = 0.f;
+    team_sync<LPT>();
+  }
+  pdl_wait();
+  pdl_trigger();
+  float coef[V] = {};
+  if (a.counts != nullptr) {
+    const double n = max(1, __ldg(a.counts + E));
+    const double f = (double)__ldg(a.d_loss) * E / (K * n * n);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
+      if (e < E) coef[i] = (float)(f * __ldg(a.counts + e));
+    }
+  }
+  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < a.T; t0 += (int64_t)gridDim.x * TEAMS) {
+    const int64_t t = t0 + team;
+    const bool active = t < a.T && (a.mask == nullptr || a.mask[t]);
+    const E_* row = logits + (active ? t : 0) * E;
+    float v[V] = {};
+    float inv = 0.f;
+    if (shares) inv = scores<VEC, LPT>(row, E, a.sigmoid, ll, active, red, v);
+    int id[CP];
+    if (by_weights) {
+      if (!kBlockTokens<LPT> || threadIdx.x < 32) {
+        float dl[CP], s[CP], g[CP];
+        float total = 0.f, mean = 0.f, most = -CUDART_INF_F;
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+          const int k = ll + c * PL;
+          id[c] = active && k < K ? __ldg(a.ids + t * K + k) : -1;
+          if (id[c] < -1 || id[c] >= E) {
+            set_status(status, MLR_STATUS_INDEX);
+            id[c] = -1;
+          }
+          s[c] = id[c] >= 0 ? finite_logit(row + id[c]) : -CUDART_INF_F;
+          if (!(s[c] > -CUDART_INF_F)) id[c] = -1;
+          g[c] = id[c] >= 0 ? a.scale * __ldg(a.d_weights + t * K + k) : 0.f;
+          most = fmaxf(most, s[c]);
+        }
+        if (all_chosen) {
+#pragma unroll
+          for (int c = 0; c < CP; ++c) dl[c] = g[c];  // times p below
+        } else {
+          if (!a.sigmoid) most = part_max<PL>(most);
+#pragma unroll
+          for (int c = 0; c < CP; ++c) {
+            s[c] = id[c] < 0 ? 0.f : a.sigmoid ? sigmoid_f(s[c]) : expf(s[c] - most);
+            total += s[c];
+            mean = fmaf(g[c], s[c], mean);
+          }
+          if (a.renormalize) {
+            total = part_sum<PL>(total);
+            mean = part_sum<PL>(mean);
+            total = total > 0.f ? 1.f / total : 0.f;
+            mean *= total;
+          } else {
+            total = 1.f;
+            mean = 0.f;
+          }
+#pragma unroll
+          for (int c = 0; c < CP; ++c) dl[c] = s[c] * total * (g[c] - mean) * (a.sigmoid ? 1.f - s[c] : 1.f);
+        }
+        // an expert that a token holds twice gets both, in order
+        bool twice = K > PL;
+        if (!twice) {
+          const uint32_t same = __match_any_sync(0xffffffffu, id[0] < 0 ? ~(int)threadIdx.x : id[0] + (team % (32 / PL)) * E);
+          twice = __any_sync(0xffffffffu, (same & (same - 1)) != 0);
+        }
+        if (!twice) {
+          if (id[0] >= 0) row_s[id[0]] = dl[0];
+        } else {
+#pragma unroll
+          for (int c = 0; c < CP; ++c)
+            for (int l = 0; l < PL; ++l) {
+              if (ll == l && id[c] >= 0) row_s[id[c]] += dl[c];
+              __syncwarp();
+            }
+        }
+      }
+      team_sync<LPT>();
+    }
+    // d: what the place's lane has left of an expert
+    float dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < V / VEC; ++j) {
+      const int e = (ll + LPT * j) * VEC;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int n = j * VEC + i;
+        float q = coef[n];
+        if (all_chosen && e < E) q += row_s[e + i];
+        dot = fmaf(v[n], q, dot);
+      }
+    }
+    if (shares) dot = team_sum<LPT>(dot, red) * inv;
+#pragma unroll
+    for (int j = 0; j < V / VEC; ++j) {
+      const int e = (ll + LPT * j) * VEC;
+      if (e >= E) continue;
+      float o[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int n = j * VEC + i;
+        const float d = by_weights ? row_s[e + i] : 0.f;
+        const float p = v[n] * inv;
+        if (all_chosen) o[i] = p * (coef[n] + d - dot);
+        else o[i] = fmaf(a.sigmoid ? p * (1.f - v[n]) : p, coef[n] - dot, d);
+      }
+      if (t < a.T) {
+        if constexpr (VEC == 1) {
+          row_narrow(o[0], d_logits[t * E + e]);
+        } else {
+          uint4 q;
+          row_narrow(o, q);
+          *reinterpret_cast<uint4*>(d_logits + t * E + e) = q;
+        }
+      }
+    }
+    if (by_weights) {
+      team_sync<LPT>();
+      if (!kBlockTokens<LPT> || threadIdx.x < 32)
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+          if (id[c] >= 0) row_s[id[c]] = 0.f;
+      team_sync<LPT>();
+    }
+  }
+}
+
+// f<LPT, V>() for E experts.
+template <typename F>
+int by_experts(int E, F f) {
+  using std::integral_constant;
+  if (E <= 64) return f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+  if (E <= 128) return f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+  if (E <= 256) return f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+  if (E <= 512) return f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+  if (E <= kPartExperts) return f(integral_constant<int, 32>{}, integral_constant<int, 32>{});
+  return f(integral_constant<int, kBalanceThreads>{}, integral_constant<int, 16>{});
+}
+int lanes_of(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : E <= kPartExperts ? 32 : kBalanceThreads; }
+
+int64_t balance_blocks(int32_t T, int32_t E) {
+  const int64_t want = ceil_div(T, kBalanceThreads / lanes_of(E)), most = 2 * (int64_t)current_sms();
+  return want < 1 ? 1 : want < most ? want : most;
+}
+
+template <int VEC, typename E_>
+int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int K, bool sigmoid, float* part,
+                int32_t* count, int32_t* status, cudaStream_t stream) {
+  const unsigned blocks = (unsigned)balance_blocks(T, E);
+  return by_experts(E, [&](auto lpt, auto v) {
+    const size_t smem = (size_t)(E + 1) * 4 + (size_t)(kBlockTokens<lpt.value> ? 1 : kBalanceThreads / 32) * E * 4;
+    return launched(launch_pdl(balance_kernel<VEC, lpt.value, v.value, E_>, dim3(blocks), dim3(kBalanceThreads), smem, stream,
+                               static_cast<const E_*>(logits), ids, mask, T, E, K, sigmoid, part, count, status));
+  });
+}
+
+template <int VEC, typename E_>
+int run_backward(const void* logits, const GradArgs& a, void* d_logits, int32_t* status, cudaStream_t stream) {
+  return by_experts(a.E, [&](auto lpt, auto v) {
+    constexpr int teams = kTeams<lpt.value>;
+    const int64_t want = ceil_div(a.T, teams), most = 2 * (int64_t)current_sms();
+    return launched(launch_pdl(route_backward_kernel<VEC, lpt.value, v.value, E_>, dim3((unsigned)(want < most ? want : most)),
+                               dim3(kBalanceThreads), (size_t)teams * a.E * 4, stream, static_cast<const E_*>(logits), a,
+                               static_cast<E_*>(d_logits), status));
+  });
+}
+
+// f<VEC, E_>() for logits (and their gradient) of a type, in vectors where they lie on the 16-byte grid.
+template <typename F>
+int by_type(int dtype, int E, const void* logits, const void* d_logits, F f) {
+  const bool bf16 = dtype == MLR_DTYPE_BF16;
+  const bool whole = E % (bf16 ? 8 : 4) == 0 && aligned_to(logits, 16) && aligned_to(d_logits, 16);
+  using std::integral_constant;
+  if (bf16) return whole ? f(integral_constant<int, 8>{}, uint16_t{}) : f(integral_constant<int, 1>{}, uint16_t{});
+  return whole ? f(integral_constant<int, 4>{}, float{}) : f(integral_constant<int, 1>{}, float{});
+}
+
+}  // namespace
+}  // namespace mlr
+
+extern "C" size_t moe_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts) {
+  using namespace mlr;
+  if (num_tokens < 0 || num_experts < 1 || num_experts > kMaxRouteExperts) return 0;
+  return (size_t)balance_blocks(num_tokens, num_experts) * (2 * num_experts + 1) * 4;
+}
+
+extern "C" int moe_balance_loss(const void* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t num_tokens,
+                                int32_t num_experts, int32_t topk, int32_t dtype, int32_t scoring, float* loss, int32_t* counts,
+                                void* workspace, size_t ws_bytes, int32_t* d_status, void* stream_) {
+  using namespace mlr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
+  if (code != MLR_OK) return code;
+  if (loss == nullptr || counts == nullptr || (num_tokens > 0 && topk_ids == nullptr)) return MLR_ERR_INVALID;
+  if (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)) return MLR_ERR_CAPACITY;
+  if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
+  const int blocks = (int)balance_blocks(num_tokens, num_experts);
+  float* part = static_cast<float*>(workspace);
+  int32_t* count = reinterpret_cast<int32_t*>(part + (int64_t)blocks * num_experts);
+  const int c = by_type(dtype, num_experts, logits, nullptr, [&](auto vec, auto e) {
+    return run_balance<vec.value, decltype(e)>(logits, topk_ids, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
+                                               part, count, d_status, stream);
+  });
+  if (c != MLR_OK) return c;
+  return launched(launch_pdl(balance_total_kernel, dim3(kTotalCluster), dim3(kTotalThreads), 0, stream, (const float*)part,
+                             (const int32_t*)count, blocks, (int)num_experts, (int)topk, loss, counts));
+}
+
+extern "C" int moe_route_backward(const void* logits, const int32_t* topk_ids, const float* d_weights, const int32_t* counts,
+                                  const float* d_loss, const uint8_t* token_mask, int32_t num_tokens, int32_t num_experts,
+                                  int32_t topk, int32_t dtype, int32_t scoring, int32_t renormalize, float scale, void* d_logits,
+                                  int32_t* d_status, void* stream_) {
+  using namespace mlr;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
+  if (code != MLR_OK) return code;
+  if (num_tokens == 0) return MLR_OK;  // empty tensors may have no address
+  if ((counts == nullptr) != (d_loss == nullptr) || (d_weights == nullptr && counts == nullptr)) return MLR_ERR_INVALID;
+  if (d_logits == nullptr || !aligned_to(d_logits, dtype == MLR_DTYPE_BF16 ? 2 : 4) || (d_weights != nullptr && topk_ids == nullptr))
+    return MLR_ERR_INVALID;
+  const GradArgs a{topk_ids, d_weights, counts, d_loss, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
+                   renormalize != 0, scale};
+  return by_type(dtype, num_experts, logits, d_logits, [&](auto vec, auto e) {
+    return run_backward<vec.value, decltype(e)>(logits, a, d_logits, d_status, stream);
+  });
+}

@@ -1,0 +1,101 @@
+// mlr_router.cuh -- what the router's choice and the balance loss have in common:
+// logits as fp32, and a token's logits in the lanes of a part of a warp.
+#pragma once
+#include <math_constants.h>
+
+#include "mlr_profile.cuh"
+#include "mlr_rows.cuh"
+
+namespace mlr {
+
+constexpr int kMaxRouteExperts = 4096;
+constexpr int kMaxRouteTopk = 32;
+constexpr int kPartExperts = 1024;  // a part of a warp holds a token of up to this many experts
+
+enum Scoring { kSoftmax = 0, kSigmoid = 1 };
+
+// A logit as fp32, -inf where it is not finite.
+__device__ __forceinline__ float finite_logit(float v) { return fabsf(v) < CUDART_INF_F ? v : -CUDART_INF_F; }
+template <typename E_>
+__device__ __forceinline__ float finite_logit(const E_* p) {
+  return finite_logit(row_widen(*p));
+}
+__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + expf(-v)); }
+// The same with the hardware's exponential and reciprocal: relative error below
+// (|v| + 5) 2^-23, at most 2.25 2^-23 as a difference.
+__device__ __forceinline__ float quick_sigmoid(float v) {
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return r;
+}
+
+// A token's logits in LPT lanes, V each: unit j of lane ll is number ll + LPT j, VEC
+// logits (16 bytes, or one where rows lie off that grid).
+template <typename E_, int VEC>
+__device__ __forceinline__ void load_unit(const E_* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) v[0] = row_widen(__ldg(p));
+  else row_widen(__ldg(reinterpret_cast<const uint4*>(p)), v);
+}
+// Loads them: zeros past E, and all where `active` is not set.  Returns NaN if one is
+// not finite, else 0.
+template <int VEC, int LPT, int V, typename E_>
+__device__ __forceinline__ float load_logits(const E_* row, int E, int ll, bool active, float (&v)[V]) {
+#pragma unroll
+  for (int j = 0; j < V / VEC; ++j) {
+    const int e = (ll + LPT * j) * VEC;
+    float u[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) u[i] = 0.f;
+    if (active && e < E) load_unit<E_, VEC>(row + e, u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
+  }
+  float check = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) check = fmaf(v[i], 0.f, check);
+  return check;
+}
+// -inf past E.
+template <int VEC, int LPT, int V>
+__device__ __forceinline__ void close_past(int E, int ll, float (&v)[V]) {
+  if (E < LPT * V)
+#pragma unroll
+    for (int j = 0; j < V / VEC; ++j)
+      if ((ll + LPT * j) * VEC >= E)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j * VEC + i] = -CUDART_INF_F;
+}
+
+template <int LPT>
+__device__ __forceinline__ float part_sum(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LPT>
+__device__ __forceinline__ float part_max(float v) {
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+inline int launched(cudaError_t err) {
+  if (err != cudaSuccess) {
+    (void)cudaGetLastError();  // not left for the next call to find
+    return MLR_ERR_CUDA;
+  }
+  note_launch();
+  return MLR_OK;
+}
+
+inline int check_logits(const void* logits, int32_t T, int32_t E, int32_t K, int32_t dtype, int32_t scoring) {
+  if (T < 0 || E < 1 || K < 1 || (dtype != MLR_DTYPE_BF16 && dtype != MLR_DTYPE_F32) ||
+      (scoring != kSoftmax && scoring != kSigmoid))
+    return MLR_ERR_INVALID;
+  if (E > kMaxRouteExperts || K > kMaxRouteTopk || (int64_t)T * K >= INT32_MAX) return MLR_ERR_UNSUPPORTED;
+  if (T > 0 && (logits == nullptr || !aligned_to(logits, dtype == MLR_DTYPE_BF16 ? 2 : 4))) return MLR_ERR_INVALID;
+  return MLR_OK;
+}
+
+}  // namespace mlr

@@ -1,47 +1,25 @@
-// router.cu -- the router's choice of experts from its logits, the balance loss
-// over a batch, and their gradients.
+// router.cu -- the router's choice of experts from its logits.
 //
 // Logits [T, E]; one that is not finite counts as -inf, and its expert is never
 // chosen.  An expert's choice score is its logit, or with a bias or (sigmoid)
 // groups sigmoid(logit) + bias.  With groups only the experts of the topk_groups
 // best groups stand to choice; a group's score is its best choice score (softmax)
 // or the sum of its two best (sigmoid).  Ties go to the lowest index.  With s =
-// softmax(logits) or sigmoid(logits):
-//   w_k = scale s_k [/ sum of the chosen s]
-//   loss = E / (K N^2) sum_e c_e sum_t p_te,  p = s [/ its sum over e (sigmoid)]
-// for N unmasked tokens and c_e pairs of expert e.  Gradients, with a_e = dloss
-// E / (K N^2) c_e and g_k what reaches w_k:
-//   softmax  dl_e = p_e (q_e - sum_j p_j q_j), q = a plus g's part
-//   sigmoid  dl_e = p_e (1 - s_e) (a_e - sum_j p_j a_j) + g's part
+// softmax(logits) or sigmoid(logits): w_k = scale s_k [/ sum of the chosen s].
 //
 // The choice is decided by the real numbers that the scores stand for: where
 // 32 bits do not tell two of them apart, they are computed in 64.
-#include <math_constants.h>
+#include <float.h>
 
-#include <type_traits>
-
-#include "mlr_profile.cuh"
-#include "mlr_rows.cuh"
+#include "mlr_router.cuh"
 
 namespace mlr {
 namespace {
 
-constexpr int kMaxRouteExperts = 4096;
-constexpr int kMaxRouteTopk = 32;  // a lane per place
 constexpr int kMaxGroups = 256;
 
-enum Scoring { kSoftmax = 0, kSigmoid = 1 };
-
-// A logit as fp32, -inf where it is not finite.
-template <typename E_>
-__device__ __forceinline__ float finite_logit(const E_* p) {
-  const float v = row_widen(*p);
-  return fabsf(v) < CUDART_INF_F ? v : -CUDART_INF_F;
-}
 // Whether a logit is one that the caller hears of: NaN or +inf.
 __device__ __forceinline__ bool bad_logit(float v) { return !(v < CUDART_INF_F); }
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + expf(-v)); }
-
 struct RouteArgs {
   const float* bias;
   const uint8_t* mask;
@@ -52,6 +30,11 @@ struct RouteArgs {
   float* weights;
   int32_t* status;
 };
+
+// sigmoid(logit) + bias in 64 bits.
+__device__ __noinline__ double exact_score(float l, const float* bias, int e) {
+  return 1.0 / (1.0 + exp(-(double)l)) + (bias != nullptr ? (double)__ldg(bias + e) : 0.0);
+}
 
 // The larger of two (score, index) pairs over the warp: the larger score, the
 // lower index of equal ones.
@@ -99,13 +82,13 @@ __device__ __forceinline__ void write_choice(const RouteArgs& a, const E_* row, 
 // One token by one warp, every score in 64 bits: keys [E] and group scores [groups]
 // in shared memory.
 template <typename E_>
-__device__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, double* key, double* group, int lane) {
+__device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, double* key, double* group, int lane) {
   const bool logit_key = !a.sigmoid || (a.bias == nullptr && a.groups == 1);
   for (int e = lane; e < a.E; e += 32) {
     const float l = finite_logit(row + e);
     double k = (double)l;
     if (!logit_key && l > -CUDART_INF_F) {
-      k = 1.0 / (1.0 + exp(-k)) + (a.bias != nullptr ? (double)__ldg(a.bias + e) : 0.0);
+      k = exact_score(l, a.bias, e);
       if (!(k < CUDART_INF)) k = -CUDART_INF;  // a bias that is NaN or +inf
     }
     key[e] = k;
@@ -157,7 +140,7 @@ __device__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, dou
 constexpr int kRouteThreads = 128;
 template <typename E_>
 __global__ void __launch_bounds__(kRouteThreads)
-route_kernel(const E_* __restrict__ logits, RouteArgs a) {
+route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a) {
   extern __shared__ double smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   double* key = smem + (size_t)warp * (a.E + a.groups);
@@ -182,327 +165,361 @@ route_kernel(const E_* __restrict__ logits, RouteArgs a) {
   }
 }
 
-// ------------------------------------------------- balance loss, gradients --
-// A token is taken by TPT threads (a warp, or for more than 512 experts a block
-// of 256), thread i holding experts i, i + TPT, ...
-template <int TPT>
-__device__ __forceinline__ float team_sum(float v, float* red) {
-  v = warp_sum(v);
-  if (TPT == 32) return v;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < TPT / 32; ++i) v += red[i];
-  return v;
-}
-template <int TPT>
-__device__ __forceinline__ float team_max(float v, float* red) {
-  v = warp_max(v);
-  if (TPT == 32) return v;
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int i = 1; i < TPT / 32; ++i) v = fmaxf(v, red[i]);
-  return v;
-}
+// ------------------------------------------------------- the choice, fast --
+// LPT lanes take a token, V logits each (in units of VEC: unit number lane + LPT j),
+// so a warp has 32 / LPT tokens at once.  The K-th largest of 4 L block maxima (L >= K
+// the length of the sorted lists) is a lower bound of the K-th largest score; the
+// few scores above it -- 1.15 L of them where scores are in no order -- are the
+// candidates, which are ranked against one another.  Where two candidates are nearer
+// than their 32 bits tell, the candidates alone are computed in 64; where there are
+// more than 2 L of them, or two groups are that near, the token goes through
+// choose_exactly.
+//
+// A warp's time goes to the ALU pipe (maxima, comparisons), which takes an
+// instruction every two cycles.
 
-// The shares p of a token's experts and (sigmoid) s, zeros without finite logits.
-template <int TPT, int VPL, typename E_>
-__device__ __forceinline__ void shares(const E_* row, int E, bool sigmoid, int lt, float* red, float (&p)[VPL], float (&s)[VPL]) {
-  float l[VPL];
-  float most = -CUDART_INF_F;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) {
-    const int e = lt + j * TPT;
-    l[j] = e < E ? finite_logit(row + e) : -CUDART_INF_F;
-    most = fmaxf(most, l[j]);
-  }
-  float sum = 0.f;
-  if (sigmoid) {
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) sum += s[j] = l[j] > -CUDART_INF_F ? sigmoid_f(l[j]) : 0.f;
-  } else {
-    most = team_max<TPT>(most, red);
-#pragma unroll
-    for (int j = 0; j < VPL; ++j) sum += s[j] = l[j] > -CUDART_INF_F ? expf(l[j] - most) : 0.f;
-  }
-  sum = team_sum<TPT>(sum, red);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int j = 0; j < VPL; ++j) p[j] = s[j] * inv;
+// How near two sigmoid + bias may be in fp32 and still be in either order: each is
+// off by at most 2.25 2^-23 (ex2 2^-22 and its argument |l| 2^-23, both times s (1 -
+// s); 1 + e 2^-24; rcp 2^-23) and the sum's 2^-24 |c|; twice that, rounded up.
+__device__ __forceinline__ float near_score(float c) { return fmaf(fabsf(c), 0x1p-22f, 0x1p-20f); }
+__device__ __forceinline__ void order_desc(float& a, float& b) {
+  const float hi = fmaxf(a, b), lo = fminf(a, b);
+  a = hi;
+  b = lo;
 }
-
-constexpr int kBalanceThreads = 256;
-
-// Sums of shares and pairs per expert over the block's tokens: part [blocks][E]
-// and count [blocks][E + 1] (the last one: tokens).
-template <int TPT, int VPL, typename E_>
-__global__ void __launch_bounds__(kBalanceThreads)
-balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
-               int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, int32_t* status) {
-  extern __shared__ int hist[];  // [E + 1] pairs, then float [teams][E] shares
-  __shared__ float red[kBalanceThreads / 32];
-  constexpr int TEAMS = kBalanceThreads / TPT;
-  float* sums = reinterpret_cast<float*>(hist + E + 1);
-  const int team = threadIdx.x / TPT, lt = threadIdx.x - team * TPT;
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) hist[e] = 0;
-  __syncthreads();
-  pdl_wait();
-  pdl_trigger();
-  float acc[VPL] = {};
-  int tokens = 0;
-  for (int64_t t = (int64_t)blockIdx.x * TEAMS + team; t < T; t += (int64_t)gridDim.x * TEAMS) {
-    if (mask != nullptr && !mask[t]) continue;  // the same for the whole team
-    ++tokens;
-    float p[VPL], s[VPL];
-    shares<TPT, VPL>(logits + t * E, E, sigmoid, lt, red, p, s);
+// A bitonic sequence of N in descending order.
+template <int N, int M>
+__device__ __forceinline__ void bitonic_desc(float (&x)[M]) {
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) acc[j] += p[j];
-    for (int k = lt; k < K; k += TPT) {
-      const int id = __ldg(ids + t * K + k);
-      if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
-      else if (id != -1) set_status(status, MLR_STATUS_INDEX);
+  for (int s = N / 2; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & s) == 0) order_desc(x[i], x[i + s]);
+}
+// x[0..N) in descending order (odd-even merge sort).
+template <int N, int M>
+__device__ __forceinline__ void sort_desc(float (&x)[M]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k > 0; k >>= 1)
+#pragma unroll
+      for (int j = k & (p - 1); j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order_desc(x[i + j], x[i + j + k]);
+}
+// The L largest of the lists x[0..N) of LPT lanes, in descending order in each.
+template <int N, int L, int LPT, int O>
+__device__ __forceinline__ void merge_lists(float (&x)[L]) {
+  if constexpr (O < LPT) {
+    float y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = __shfl_xor_sync(0xffffffffu, x[i], O);
+    if constexpr (N < L) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[2 * N - 1 - i] = y[i];
+      bitonic_desc<2 * N>(x);
+      merge_lists<2 * N, L, LPT, 2 * O>(x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = fmaxf(x[i], y[N - 1 - i]);
+      bitonic_desc<N>(x);
+      merge_lists<N, L, LPT, 2 * O>(x);
     }
   }
-  if (lt == 0) atomicAdd(&hist[E], tokens);
-#pragma unroll
-  for (int j = 0; j < VPL; ++j)
-    if (lt + j * TPT < E) sums[team * E + lt + j * TPT] = acc[j];
-  __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
-    count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
-    if (e == E) continue;
-    float v = 0.f;
-#pragma unroll
-    for (int i = 0; i < TEAMS; ++i) v += sums[i * E + e];
-    part[(int64_t)blockIdx.x * E + e] = v;
-  }
 }
 
-constexpr int kTotalThreads = 1024;
-// The blocks' sums added in order, in one block: counts, and the loss.
-__global__ void __launch_bounds__(kTotalThreads)
-balance_total_kernel(const float* __restrict__ part, const int32_t* __restrict__ count, int blocks, int E, int K,
-                     float* __restrict__ loss, int32_t* __restrict__ counts) {
-  __shared__ double red[kTotalThreads / 32];
-  __shared__ int tokens;
-  pdl_wait();
-  pdl_trigger();
-  double v = 0.0;
-  for (int e = threadIdx.x; e <= E; e += kTotalThreads) {
-    int c = 0;
-    double s = 0.0;
-    for (int b = 0; b < blocks; ++b) {
-      c += count[(int64_t)b * (E + 1) + e];
-      if (e < E) s += part[(int64_t)b * E + e];
-    }
-    counts[e] = c;
-    if (e == E) tokens = c;
-    else v += s * c;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    v = 0.0;
-    for (int i = 0; i < kTotalThreads / 32; ++i) v += red[i];
-    const double n = tokens > 0 ? tokens : 1;
-    *loss = (float)(v * E / (K * n * n));
-  }
-}
+constexpr int kFastThreads = 128;
+constexpr int kFastTopk = 16;
 
-struct GradArgs {
-  const int32_t* ids;
-  const float* d_weights;  // nullable: no gradient of the weights
-  const int32_t* counts;   // nullable: none of the loss
-  const float* d_loss;
-  const uint8_t* mask;
-  int T, E, K;
-  bool sigmoid, renormalize;
-  float scale;
+// Shared memory of a warp: keys in 64 bits for choose_exactly, the same bytes for
+// the groups' two best of each unit; the candidates' keys (32 and 64 bits) and ids.
+template <int LPT, int L>
+struct alignas(16) Candidates {
+  double exact[2 * L];
+  float key[2 * L];
+  int id[2 * L];
 };
+__host__ __device__ constexpr int64_t fast_scratch(int E, int groups, int vec, int tokens) {
+  const int64_t slow = (int64_t)(E + groups) * 8, best = groups > 1 ? (int64_t)tokens * (E / vec) * 8 : 0;
+  return round_up(slow > best ? slow : best, 16);
+}
 
-// Gradient of the logits.  The part that comes by the weights is put together by
-// the token's first warp (lane k place k) in a row of shared memory, from where
-// the experts' threads take it.
-template <int TPT, int VPL, typename E_>
-__global__ void __launch_bounds__(kBalanceThreads)
-route_backward_kernel(const E_* __restrict__ logits, GradArgs a, E_* __restrict__ d_logits, int32_t* status) {
-  extern __shared__ float rows[];  // [teams][E]
-  __shared__ float red[kBalanceThreads / 32];
-  constexpr int TEAMS = kBalanceThreads / TPT;
-  const int team = threadIdx.x / TPT, lt = threadIdx.x - team * TPT;
+template <typename E_, int VEC, int LPT, int V, int L>
+__global__ void __launch_bounds__(kFastThreads)
+route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a, int scratch_bytes) {
+  constexpr int NU = V / VEC;               // units of a lane
+  constexpr int TPW = 32 / LPT;             // tokens of a warp
+  constexpr int NB = 4 * L / LPT;           // block maxima of a lane
+  constexpr int CPL = (2 * L + LPT - 1) / LPT;  // candidates of a lane
+  static_assert(NB >= 1 && NB <= V && NB <= L && LPT * NB >= L, "lists grow to L");
+  extern __shared__ char fast_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPT, ll = lane % LPT;
+  const uint32_t team = (LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1) << (sub * LPT));
+  char* mine = fast_smem + (size_t)warp * (scratch_bytes + TPW * sizeof(Candidates<LPT, L>));
+  double* slow_key = reinterpret_cast<double*>(mine);
+  Candidates<LPT, L>& cand = reinterpret_cast<Candidates<LPT, L>*>(mine + scratch_bytes)[sub];
   const int E = a.E, K = a.K;
-  float* row_s = rows + team * E;
+  const bool biased = a.sigmoid && (a.bias != nullptr || a.groups > 1);
   pdl_wait();
   pdl_trigger();
-  float coef[VPL] = {};
-  if (a.counts != nullptr) {
-    const double n = max(1, __ldg(a.counts + E));
-    const double f = (double)__ldg(a.d_loss) * E / (K * n * n);
+  const int64_t t0 = ((int64_t)blockIdx.x * (kFastThreads / 32) + warp) * TPW;
+  if (t0 >= a.T) return;
+  const int64_t t = t0 + sub;
+  const bool token = t < a.T, active = token && (a.mask == nullptr || a.mask[t]);
+  const E_* row = logits + (active ? t : 0) * E;
+  float v[V];
+  const float check = load_logits<VEC, LPT>(row, E, ll, active, v);
+  if (__any_sync(0xffffffffu, !(check == 0.f) || !active)) {
+    bool bad = false;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = lt + j * TPT;
-      if (e < E) coef[j] = (float)(f * __ldg(a.counts + e));
+    for (int i = 0; i < V; ++i) {
+      bad |= bad_logit(v[i]);
+      v[i] = active ? finite_logit(v[i]) : -CUDART_INF_F;
+    }
+    if (bad) set_status(a.status, MLR_STATUS_VALUE);
+  }
+  close_past<VEC, LPT>(E, ll, v);
+
+  // softmax over all experts: its divisor
+  float inv_all = 1.f, most = 0.f;
+  if (!a.sigmoid) {
+    most = v[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
+    most = part_max<LPT>(most);
+    if (!a.renormalize) {
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? __expf(v[i] - most) : 0.f;
+      all = part_sum<LPT>(all);
+      inv_all = 1.f / all;  // not used where all is 0
     }
   }
-  const bool by_weights = a.d_weights != nullptr;
-  for (int64_t t = (int64_t)blockIdx.x * TEAMS + team; t < a.T; t += (int64_t)gridDim.x * TEAMS) {
-    const E_* row = logits + t * E;
-    const bool masked = a.mask != nullptr && !a.mask[t];  // the same for the whole team
-    float dot = 0.f;  // sum of g w, which softmax over all experts takes from every one of them
-    float d[VPL] = {};
-    float p[VPL], s[VPL];
-    if (!masked && (a.counts != nullptr || (by_weights && !a.sigmoid && !a.renormalize)))
-      shares<TPT, VPL>(row, E, a.sigmoid, lt, red, p, s);
-    else
+  if (biased) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) p[j] = s[j] = 0.f;
-    if (by_weights && !masked) {
+    for (int j = 0; j < NU; ++j) {
+      const int e = (ll + LPT * j) * VEC;
 #pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (lt + j * TPT < E) row_s[lt + j * TPT] = 0.f;
-      if (TPT > 32) __syncthreads();
-      else __syncwarp();
-      if (lt < 32) {
-        int id = lt < K ? __ldg(a.ids + t * K + lt) : -1;
-        if (id < -1 || id >= E) {
-          set_status(status, MLR_STATUS_INDEX);
-          id = -1;
-        }
-        const float l = id >= 0 ? finite_logit(row + id) : -CUDART_INF_F;
-        const bool in = l > -CUDART_INF_F;
-        const float g = in ? a.scale * __ldg(a.d_weights + t * K + lt) : 0.f;
-        float dl;
-        if (a.sigmoid) {
-          const float si = in ? sigmoid_f(l) : 0.f;
-          if (a.renormalize) {
-            const float total = warp_sum(si);
-            const float mean = warp_sum(g * si);
-            dl = total > 0.f ? (g - mean / total) / total * si * (1.f - si) : 0.f;
-          } else {
-            dl = g * si * (1.f - si);
-          }
-        } else if (a.renormalize) {
-          const float most = warp_max(l);
-          const float si = in ? expf(l - most) : 0.f;
-          const float total = warp_sum(si);
-          const float mean = warp_sum(g * si);
-          dl = total > 0.f ? si / total * (g - mean / total) : 0.f;
-        } else {
-          dl = g;  // times p below
-        }
-        // an id that a token holds twice: the first place adds the others' in order
-        const uint32_t same = __match_any_sync(0xffffffffu, id);
-        float all = dl;
-        if (__any_sync(0xffffffffu, id >= 0 && (same & (same - 1)) != 0))
-          for (int k = 1; k < K; ++k) {
-            const float o = __shfl_sync(0xffffffffu, dl, k);
-            if (k > lt && ((same >> k) & 1)) all += o;
-          }
-        if (id >= 0 && lt == __ffs(same) - 1) row_s[id] = all;
+      for (int i = 0; i < VEC; ++i) {
+        const float b = a.bias != nullptr && e < E ? __ldg(a.bias + e + i) : 0.f;
+        const float c = quick_sigmoid(v[j * VEC + i]) + b;
+        v[j * VEC + i] = v[j * VEC + i] > -CUDART_INF_F && c < CUDART_INF_F ? c : -CUDART_INF_F;
       }
-      if (TPT > 32) __syncthreads();
-      else __syncwarp();
-#pragma unroll
-      for (int j = 0; j < VPL; ++j)
-        if (lt + j * TPT < E) d[j] = row_s[lt + j * TPT];
     }
-    // q: what multiplies the share; d: added as it is
+  }
+  bool slow = false;  // the same for a token's lanes
+  if (a.groups > 1) {
+    const int units = E / VEC, per = units / a.groups;  // units of a group
+    float2* best2 = reinterpret_cast<float2*>(mine) + sub * units;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      float q = coef[j];
-      if (!a.sigmoid && !a.renormalize) q += d[j];
-      dot = fmaf(p[j], q, dot);
-    }
-    dot = team_sum<TPT>(dot, red);
+    for (int j = 0; j < NU; ++j) {
+      float b0 = v[j * VEC], b1 = -CUDART_INF_F;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j) {
-      const int e = lt + j * TPT;
-      if (e >= E) continue;
-      float v;
-      if (a.sigmoid) v = p[j] * (1.f - s[j]) * (coef[j] - dot) + d[j];
-      else if (a.renormalize) v = p[j] * (coef[j] - dot) + d[j];
-      else v = p[j] * (coef[j] + d[j] - dot);
-      row_narrow(v, d_logits[t * E + e]);
+      for (int i = 1; i < VEC; ++i) {
+        b1 = fmaxf(b1, fminf(b0, v[j * VEC + i]));
+        b0 = fmaxf(b0, v[j * VEC + i]);
+      }
+      if (ll + LPT * j < units) best2[ll + LPT * j] = make_float2(b0, b1);
     }
-    if (TPT == 32) __syncwarp();
+    __syncwarp();
+    float score = -CUDART_INF_F, size = 0.f;  // lane g of the token: group g
+    if (ll < a.groups) {
+      float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F;
+      for (int i = 0; i < per; ++i) {
+        const float2 u = best2[ll * per + i];
+        b1 = fmaxf(fmaxf(b1, u.y), fminf(b0, u.x));
+        b0 = fmaxf(b0, u.x);
+      }
+      score = a.sigmoid && b1 > -CUDART_INF_F ? b0 + b1 : b0;
+      size = b1 > -CUDART_INF_F ? fabsf(b0) + fabsf(b1) : b0 > -CUDART_INF_F ? fabsf(b0) : 0.f;
+    }
+    __syncwarp();
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float o = __shfl_sync(0xffffffffu, score, g, LPT);
+      before += o > score || (o == score && g < ll);
+    }
+    const bool in = ll < a.groups && before < a.best;
+    if (a.sigmoid) {  // two sums of two scores: twice as much as two scores may differ, and the sums' roundings
+      const float least = -part_max<LPT>(in && score > -CUDART_INF_F ? -score : -CUDART_INF_F);
+      const float out = part_max<LPT>(!in ? score : -CUDART_INF_F);
+      const float apart = 2.f * near_score(part_max<LPT>(size));
+      slow = out > -CUDART_INF_F && least - out <= apart;
+    }
+    const uint32_t chosen = (__ballot_sync(0xffffffffu, in) & team) >> (sub * LPT);
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+      if (ll + LPT * j < units && ((chosen >> ((ll + LPT * j) / per)) & 1) == 0)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[j * VEC + i] = -CUDART_INF_F;
+  }
+
+  // the lower bound
+  float list[L];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    list[b] = v[b * (V / NB)];
+#pragma unroll
+    for (int i = 1; i < V / NB; ++i) list[b] = fmaxf(list[b], v[b * (V / NB) + i]);
+  }
+  sort_desc<NB>(list);
+  merge_lists<NB, L, LPT, 1>(list);
+  float bound = list[0];
+#pragma unroll
+  for (int i = 1; i < L; ++i)
+    if (i == K - 1) bound = list[i];
+  if (biased) bound -= near_score(bound);
+  bound = fmaxf(bound, -FLT_MAX);
+
+  // the candidates
+  uint32_t hit = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) hit |= v[i] >= bound ? 1u << i : 0u;
+  int at = __popc(hit);
+  const int own = at;
+#pragma unroll
+  for (int o = 1; o < LPT; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, at, o, LPT);
+    if (ll >= o) at += u;
+  }
+  const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
+  at -= own;
+  slow |= n > 2 * L;
+  while (hit != 0 && at < 2 * L) {
+    const int i = __ffs(hit) - 1;
+    hit &= hit - 1;
+    cand.id[at++] = (ll + LPT * (i / VEC)) * VEC + i % VEC;
+  }
+  __syncwarp();
+  int id[CPL];
+  float key[CPL], logit[CPL];
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    const int i = ll + c * LPT;
+    id[c] = -1;
+    key[c] = logit[c] = -CUDART_INF_F;
+    if (i < n && i < 2 * L) {
+      id[c] = cand.id[i];
+      key[c] = logit[c] = finite_logit(row + id[c]);
+      if (biased) key[c] = quick_sigmoid(logit[c]) + (a.bias != nullptr ? __ldg(a.bias + id[c]) : 0.f);
+    }
+    if (i < 2 * L) cand.key[i] = key[c];
+  }
+  __syncwarp();
+  // ranks: those surely above, and whether any other is as near as not to tell
+  int rank[CPL];
+  bool near = false;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    const float d = biased ? near_score(key[c]) : 0.f;
+    const float hi = key[c] + d, lo = key[c] - d;
+    float above = 0.f, about = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2 * L; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(&cand.key[i]);
+      above += (q.x > hi ? 1.f : 0.f) + (q.y > hi ? 1.f : 0.f) + (q.z > hi ? 1.f : 0.f) + (q.w > hi ? 1.f : 0.f);
+      about += (q.x >= lo ? 1.f : 0.f) + (q.y >= lo ? 1.f : 0.f) + (q.z >= lo ? 1.f : 0.f) + (q.w >= lo ? 1.f : 0.f);
+    }
+    rank[c] = id[c] >= 0 ? (int)above : K;
+    near |= rank[c] < K && about - above != 1.f;
+  }
+  const uint32_t unsure = __ballot_sync(0xffffffffu, near);
+  if (unsure != 0) {
+    if (biased) {
+#pragma unroll
+      for (int c = 0; c < CPL; ++c)
+        if ((unsure & team) && id[c] >= 0)
+          cand.exact[ll + c * LPT] = exact_score(logit[c], a.bias, id[c]);
+      __syncwarp();
+    }
+    if (unsure & team) {
+      const int m = min(n, 2 * L);
+#pragma unroll
+      for (int c = 0; c < CPL; ++c) {
+        if (id[c] < 0) continue;
+        const double k64 = biased ? cand.exact[ll + c * LPT] : 0.0;
+        rank[c] = 0;
+        for (int i = 0; i < m; ++i) {
+          const bool above = biased ? cand.exact[i] > k64 : cand.key[i] > key[c];
+          const bool same = biased ? cand.exact[i] == k64 : cand.key[i] == key[c];
+          rank[c] += above || (same && cand.id[i] < id[c]);
+        }
+      }
+    }
+  }
+
+  // weights
+  float s[CPL], total = 0.f;
+#pragma unroll
+  for (int c = 0; c < CPL; ++c) {
+    s[c] = 0.f;
+    if (id[c] >= 0 && rank[c] < K) {
+      s[c] = a.sigmoid ? sigmoid_f(logit[c]) : expf(logit[c] - most) * inv_all;
+      total += s[c];
+    }
+  }
+  if (a.renormalize) {
+    total = part_sum<LPT>(total);
+    total = total > 0.f ? 1.f / total : 0.f;
+  } else {
+    total = 1.f;
+  }
+  if (token && !slow) {
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+      if (id[c] >= 0 && rank[c] < K) {
+        a.ids[t * K + rank[c]] = id[c];
+        a.weights[t * K + rank[c]] = s[c] * total * a.scale;
+      }
+    for (int k = n + ll; k < K; k += LPT) {
+      a.ids[t * K + k] = -1;
+      a.weights[t * K + k] = 0.f;
+    }
+  }
+  uint32_t late = __ballot_sync(0xffffffffu, slow && token);
+  while (late != 0) {
+    const int o = (__ffs(late) - 1) / LPT;
+    late &= LPT == 32 ? 0u : ~(((1u << (LPT & 31)) - 1) << (o * LPT));
+    choose_exactly(a, logits + (t0 + o) * E, t0 + o, slow_key, slow_key + E, lane);
+    __syncwarp();
   }
 }
 
-int launched(cudaError_t err) {
-  if (err != cudaSuccess) {
-    (void)cudaGetLastError();  // not left for the next call to find
-    return MLR_ERR_CUDA;
-  }
-  note_launch();
-  return MLR_OK;
+template <typename E_, int VEC, int LPT, int V, int L>
+int launch_fast(const E_* logits, const RouteArgs& a, cudaStream_t stream) {
+  constexpr int TPW = 32 / LPT, WARPS = kFastThreads / 32;
+  auto kernel = route_fast_kernel<E_, VEC, LPT, V, L>;
+  const int64_t scratch = fast_scratch(a.E, a.groups, VEC, TPW);
+  const size_t smem = WARPS * (size_t)(scratch + TPW * sizeof(Candidates<LPT, L>));
+  return launched(launch_pdl(kernel, dim3((unsigned)ceil_div(a.T, WARPS * TPW)), dim3(kFastThreads), smem, stream, logits, a,
+                             (int)scratch));
 }
-int check_logits(const void* logits, int32_t T, int32_t E, int32_t K, int32_t dtype, int32_t scoring) {
-  if (T < 0 || E < 1 || K < 1 || (dtype != MLR_DTYPE_BF16 && dtype != MLR_DTYPE_F32) ||
-      (scoring != kSoftmax && scoring != kSigmoid))
-    return MLR_ERR_INVALID;
-  if (E > kMaxRouteExperts || K > kMaxRouteTopk || (int64_t)T * K >= INT32_MAX) return MLR_ERR_UNSUPPORTED;
-  if (T > 0 && (logits == nullptr || !aligned_to(logits, dtype == MLR_DTYPE_BF16 ? 2 : 4))) return MLR_ERR_INVALID;
-  return MLR_OK;
-}
-
-int64_t balance_blocks(int32_t T, int32_t E) {
-  const int64_t want = ceil_div(T, E <= 512 ? kBalanceThreads / 32 : 1), most = 2 * (int64_t)current_sms();
-  return want < 1 ? 1 : want < most ? want : most;
-}
-
-// f<TPT, VPL>() for E experts.
-template <typename F>
-int by_experts(int E, F f) {
-  using std::integral_constant;
-  constexpr integral_constant<int, 32> w{};
-  constexpr integral_constant<int, 256> b{};
-  if (E <= 32) return f(w, integral_constant<int, 1>{});
-  if (E <= 64) return f(w, integral_constant<int, 2>{});
-  if (E <= 128) return f(w, integral_constant<int, 4>{});
-  if (E <= 256) return f(w, integral_constant<int, 8>{});
-  if (E <= 512) return f(w, integral_constant<int, 16>{});
-  if (E <= 1024) return f(b, integral_constant<int, 4>{});
-  if (E <= 2048) return f(b, integral_constant<int, 8>{});
-  return f(b, integral_constant<int, 16>{});
+template <typename E_, int VEC, int L>
+int launch_fast_for(const E_* logits, const RouteArgs& a, cudaStream_t stream) {
+  if (a.E <= 64) return launch_fast<E_, VEC, 8, 8, L>(logits, a, stream);
+  if (a.E <= 128) return launch_fast<E_, VEC, 8, 16, L>(logits, a, stream);
+  if (a.E <= 256) return launch_fast<E_, VEC, 8, 32, L>(logits, a, stream);
+  if (a.E <= 512) return launch_fast<E_, VEC, 16, 32, L>(logits, a, stream);
+  return launch_fast<E_, VEC, 32, 32, L>(logits, a, stream);
 }
 
 template <typename E_>
 int run_route(const void* logits, const RouteArgs& a, cudaStream_t stream) {
+  const E_* l = static_cast<const E_*>(logits);
+  const int lpt = a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32;
+  if (a.E <= kPartExperts && a.K <= kFastTopk && a.groups <= lpt) {
+    constexpr int VEC = 16 / sizeof(E_);
+    const bool whole = a.E % VEC == 0 && a.E / a.groups % VEC == 0 && aligned_to(logits, 16);
+    if (whole) return a.K <= 8 ? launch_fast_for<E_, VEC, 8>(l, a, stream) : launch_fast_for<E_, VEC, 16>(l, a, stream);
+    return a.K <= 8 ? launch_fast_for<E_, 1, 8>(l, a, stream) : launch_fast_for<E_, 1, 16>(l, a, stream);
+  }
   const size_t per = (size_t)(a.E + a.groups) * sizeof(double);
   const int warps = per <= 8 * 1024 ? kRouteThreads / 32 : 1;
   const int64_t blocks = ceil_div(a.T, warps), most = (int64_t)current_sms() * 16;
   return launched(launch_pdl(route_kernel<E_>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32), per * warps,
-                             stream, static_cast<const E_*>(logits), a));
-}
-
-template <typename E_>
-int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int K, bool sigmoid, float* part,
-                int32_t* count, int32_t* status, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)balance_blocks(T, E);
-  return by_experts(E, [&](auto tpt, auto vpl) {
-    auto kernel = balance_kernel<tpt.value, vpl.value, E_>;
-    const size_t smem = (size_t)(E + 1) * 4 + (size_t)(kBalanceThreads / tpt.value) * E * 4;
-    return launched(launch_pdl(kernel, dim3(blocks), dim3(kBalanceThreads), smem, stream, static_cast<const E_*>(logits), ids,
-                               mask, T, E, K, sigmoid, part, count, status));
-  });
-}
-
-template <typename E_>
-int run_backward(const void* logits, const GradArgs& a, void* d_logits, int32_t* status, cudaStream_t stream) {
-  return by_experts(a.E, [&](auto tpt, auto vpl) {
-    auto kernel = route_backward_kernel<tpt.value, vpl.value, E_>;
-    const int teams = kBalanceThreads / tpt.value;
-    const int64_t want = ceil_div(a.T, teams), most = 8 * (int64_t)current_sms();
-    return launched(launch_pdl(kernel, dim3((unsigned)(want < most ? want : most)), dim3(kBalanceThreads), (size_t)teams * a.E * 4,
-                               stream, static_cast<const E_*>(logits), a, static_cast<E_*>(d_logits), status));
-  });
+                             stream, l, a));
 }
 
 }  // namespace
@@ -526,48 +543,4 @@ extern "C" int moe_route(const void* logits, const float* bias, const uint8_t* t
               scale, topk_ids, topk_weights, d_status};
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   return dtype == MLR_DTYPE_BF16 ? run_route<uint16_t>(logits, a, stream) : run_route<float>(logits, a, stream);
-}
-
-extern "C" size_t moe_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts) {
-  using namespace mlr;
-  if (num_tokens < 0 || num_experts < 1 || num_experts > kMaxRouteExperts) return 0;
-  return (size_t)balance_blocks(num_tokens, num_experts) * (2 * num_experts + 1) * 4;
-}
-
-extern "C" int moe_balance_loss(const void* logits, const int32_t* topk_ids, const uint8_t* token_mask, int32_t num_tokens,
-                                int32_t num_experts, int32_t topk, int32_t dtype, int32_t scoring, float* loss, int32_t* counts,
-                                void* workspace, size_t ws_bytes, int32_t* d_status, void* stream_) {
-  using namespace mlr;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
-  if (code != MLR_OK) return code;
-  if (loss == nullptr || counts == nullptr || (num_tokens > 0 && topk_ids == nullptr)) return MLR_ERR_INVALID;
-  if (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)) return MLR_ERR_CAPACITY;
-  if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
-  const int blocks = (int)balance_blocks(num_tokens, num_experts);
-  float* part = static_cast<float*>(workspace);
-  int32_t* count = reinterpret_cast<int32_t*>(part + (int64_t)blocks * num_experts);
-  auto run = dtype == MLR_DTYPE_BF16 ? run_balance<uint16_t> : run_balance<float>;
-  const int c = run(logits, topk_ids, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid, part, count, d_status, stream);
-  if (c != MLR_OK) return c;
-  return launched(launch_pdl(balance_total_kernel, dim3(1), dim3(kTotalThreads), 0, stream, (const float*)part,
-                             (const int32_t*)count, blocks, (int)num_experts, (int)topk, loss, counts));
-}
-
-extern "C" int moe_route_backward(const void* logits, const int32_t* topk_ids, const float* d_weights, const int32_t* counts,
-                                  const float* d_loss, const uint8_t* token_mask, int32_t num_tokens, int32_t num_experts,
-                                  int32_t topk, int32_t dtype, int32_t scoring, int32_t renormalize, float scale, void* d_logits,
-                                  int32_t* d_status, void* stream_) {
-  using namespace mlr;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
-  if (code != MLR_OK) return code;
-  if (num_tokens == 0) return MLR_OK;  // empty tensors may have no address
-  if ((counts == nullptr) != (d_loss == nullptr) || (d_weights == nullptr && counts == nullptr)) return MLR_ERR_INVALID;
-  if (d_logits == nullptr || !aligned_to(d_logits, dtype == MLR_DTYPE_BF16 ? 2 : 4) || (d_weights != nullptr && topk_ids == nullptr))
-    return MLR_ERR_INVALID;
-  const GradArgs a{topk_ids, d_weights, counts, d_loss, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
-                   renormalize != 0, scale};
-  return dtype == MLR_DTYPE_BF16 ? run_backward<uint16_t>(logits, a, d_logits, d_status, stream)
-                                 : run_backward<float>(logits, a, d_logits, d_status, stream);
 }
