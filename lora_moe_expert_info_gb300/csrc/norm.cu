@@ -23,7 +23,7 @@
 namespace mlr {
 namespace {
 
-constexpr int kMaxNormHidden = 32768;
+constexpr int kMaxNormHidden = 16384;
 constexpr int kGroupCols = 128;  // columns of an 8-bit scale
 
 // How the threads of a row hold it: LPT threads (a multiple of 32), NV units
@@ -92,8 +92,8 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int lpt, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-template <typename E_, int VEC, int NV, bool QUANT>
-__global__ void __launch_bounds__(1024)
+template <typename E_, int VEC, int NV, bool QUANT, int MOST>
+__global__ void __launch_bounds__(MOST, (NV <= (VEC == 1 ? 8 : 4) ? 1024 : 512) / MOST)
 norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w32, int T, int H, int lpt, float eps,
             E_* y, E_* r_out, uint8_t* codes, uint8_t* exps) {
   using U = typename Unit<E_, VEC>::T;
@@ -104,8 +104,9 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
   const int64_t at = row * H;
   pdl_wait();
   pdl_trigger();
+  constexpr bool kEarly = NV * VEC <= 32;  // the weight's columns are loaded before the sum is known
   U r[NV];
-  float wv[NV][VEC];
+  float wv[kEarly ? NV : 1][VEC];
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -138,16 +139,18 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
     widen_unit(r[j], a);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) sum = fmaf(a[i], a[i], sum);
-    if (c < H) load_weight<VEC>(w, w32, c, wv[j]);
+    if (kEarly && c < H) load_weight<VEC>(w, w32, c, wv[kEarly ? j : 0]);
   }
   const float m = 1.f / sqrtf(row_sum2(sum, 0.f, lpt, red).x / (float)H + eps);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
     float a[VEC];
+    float(&wj)[VEC] = wv[kEarly ? j : 0];
+    if (!kEarly && c < H) load_weight<VEC>(w, w32, c, wj);
     widen_unit(r[j], a);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) a[i] = c < H ? a[i] * m * wv[j][i] : 0.f;
+    for (int i = 0; i < VEC; ++i) a[i] = c < H ? a[i] * wj[i] * m : 0.f;  // bf16: r w is exact
     narrow_unit(a, r[j]);
     if (in && c < H && y != nullptr) *reinterpret_cast<U*>(y + at + c) = r[j];
   }
@@ -192,45 +195,168 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
 
 // The gradients.  A block takes rows blockIdx.x, + gridDim.x, ... (several at a
 // time where rows are short) and its threads keep the same columns, so that dw's
-// terms add up in registers; the sums of each place of a row in a block go to
-// `part` [places][H] and are added in order by sum_parts_kernel.
-template <typename E_, int VEC, int NV>
-__global__ void __launch_bounds__(1024)
-norm_backward_kernel(const E_* dy, const E_* __restrict__ r, const void* __restrict__ w, bool w32, const E_* d_r, int T,
-                     int H, int lpt, float eps, E_* dx, float* __restrict__ part) {
+// terms add up in registers; the blocks' sums go to `part` [blocks][H] and are added
+// in order by sum_parts_kernel.
+//
+// One thread's units of a row: its gradient, and its terms of dw.
+template <typename E_, int VEC, typename U>
+__device__ __forceinline__ void row_terms(const U& ru, const U& gu, const float (&w)[VEC], float& ss, float& hr) {
+  float a[VEC], g[VEC];
+  widen_unit(ru, a);
+  widen_unit(gu, g);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    ss = fmaf(a[i], a[i], ss);
+    hr = fmaf(g[i] * w[i], a[i], hr);
+  }
+}
+template <typename E_, int VEC, typename U>
+__device__ __forceinline__ U row_gradient(const U& ru, const U& gu, const U& eu, bool add, const float (&w)[VEC], float m,
+                                          float k, float (&acc)[VEC]) {
+  float a[VEC], g[VEC], d[VEC];
+  widen_unit(ru, a);
+  widen_unit(gu, g);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    acc[i] = fmaf(g[i], a[i] * m, acc[i]);
+    d[i] = m * (g[i] * w[i] - a[i] * k);
+  }
+  if (add) {
+    float e[VEC];
+    widen_unit(eu, e);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) d[i] += e[i];
+  }
+  U o;
+  narrow_unit(d, o);
+  return o;
+}
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Rows on the 16-byte grid: every thread copies its own units of the next rows to
+// shared memory (DEPTH rows in flight with the one in work, about 190 KB per SM), so
+// that neither a barrier nor the sums wait for HBM.
+template <typename E_, int NV, int DEPTH, int MOST, int PER_SM>
+__global__ void __launch_bounds__(MOST, PER_SM)
+norm_backward_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool w32, const E_* d_r, int T, int H, int lpt,
+                     float eps, E_* dx, float* __restrict__ part) {
+  constexpr int VEC = 16 / sizeof(E_);
+  extern __shared__ uint4 ring[];  // [DEPTH][3][NV][threads]
+  __shared__ float2 red[2][32];
+  const int threads = blockDim.x, rpb = threads / lpt;
+  const int sub = threadIdx.x / lpt, lt = threadIdx.x - sub * lpt;
+  auto slot = [&](int stage, int which, int j) { return ring + ((stage * 3 + which) * NV + j) * threads + threadIdx.x; };
+  const int64_t step = (int64_t)gridDim.x * rpb;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < T) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = unit_col<VEC>(lt, j, lpt);
+        if (c >= H) continue;
+        copy_async16(slot(stage, 0, j), r + row * H + c);
+        copy_async16(slot(stage, 1, j), dy + row * H + c);
+        if (d_r != nullptr) copy_async16(slot(stage, 2, j), d_r + row * H + c);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (unit_col<VEC>(lt, j, lpt) >= H)
+      for (int i = 0; i < DEPTH * 3; ++i) *slot(i / 3, i % 3, j) = make_uint4(0, 0, 0, 0);  // never fetched
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row0 = (int64_t)blockIdx.x * rpb + sub;
+#pragma unroll
+  for (int i = 0; i < DEPTH - 1; ++i) fetch(row0 + i * step, i);
+  float wv[NV][VEC] = {}, acc[NV][VEC] = {};
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = unit_col<VEC>(lt, j, lpt);
+    if (c < H) load_weight<VEC>(w, w32, c, wv[j]);
+  }
+  int stage = 0, turn = 0;
+  for (int64_t base = (int64_t)blockIdx.x * rpb; base < T; base += step, turn ^= 1) {
+    const int64_t row = base + sub;
+    fetch(row + (DEPTH - 1) * step, stage == 0 ? DEPTH - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    float ss = 0.f, hr = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) row_terms<E_, VEC>(*slot(stage, 0, j), *slot(stage, 1, j), wv[j], ss, hr);
+    const float2 s = row_sum2(ss, hr, lpt, red[turn]);
+    const float m = 1.f / sqrtf(s.x / (float)H + eps);
+    const float k = m * m * (s.y / (float)H);
+    if (row < T) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = unit_col<VEC>(lt, j, lpt);
+        if (c >= H) continue;
+        *reinterpret_cast<uint4*>(dx + row * H + c) = row_gradient<E_, VEC>(
+            *slot(stage, 0, j), *slot(stage, 1, j), *slot(stage, 2, j), d_r != nullptr, wv[j], m, k, acc[j]);
+      }
+    }
+    stage = stage == DEPTH - 1 ? 0 : stage + 1;
+  }
+  float* p = part + (int64_t)blockIdx.x * H;
+  if (rpb == 1) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = unit_col<VEC>(lt, j, lpt);
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4)
+        if (c < H) *reinterpret_cast<float4*>(p + c + i) = make_float4(acc[j][i], acc[j][i + 1], acc[j][i + 2], acc[j][i + 3]);
+    }
+    return;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  float* sums = reinterpret_cast<float*>(ring);  // [rpb][H]: no more than the ring of a row
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = unit_col<VEC>(lt, j, lpt);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c < H) sums[sub * H + c + i] = acc[j][i];
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < H; c += threads) {
+    float v = sums[c];
+    for (int i = 1; i < rpb; ++i) v += sums[i * H + c];
+    p[c] = v;
+  }
+}
+
+// Other rows, and those too long for the ring.
+template <typename E_, int VEC, int NV, int MOST>
+__global__ void __launch_bounds__(MOST)
+norm_backward_plain_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool w32, const E_* d_r, int T, int H,
+                           int lpt, float eps, E_* dx, float* __restrict__ part) {
   using U = typename Unit<E_, VEC>::T;
   __shared__ float2 red[2][32];
-  const int rpb = blockDim.x / lpt;
-  const int sub = threadIdx.x / lpt, lt = threadIdx.x - sub * lpt;
+  const int lt = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   float acc[NV][VEC] = {};
   int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * rpb; row0 < T; row0 += (int64_t)gridDim.x * rpb, turn ^= 1) {
-    const int64_t row = row0 + sub;
-    const bool in = row < T;
+  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
     const int64_t at = row * H;
     U ru[NV], gu[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
-      const bool have = in && c < H;
-      ru[j] = have ? *reinterpret_cast<const U*>(r + at + c) : U{};
-      gu[j] = have ? *reinterpret_cast<const U*>(dy + at + c) : U{};
+      ru[j] = c < H ? *reinterpret_cast<const U*>(r + at + c) : U{};
+      gu[j] = c < H ? *reinterpret_cast<const U*>(dy + at + c) : U{};
     }
     float ss = 0.f, hr = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
-      float a[VEC], g[VEC], wv[VEC] = {};
+      float wv[VEC] = {};
       if (c < H) load_weight<VEC>(w, w32, c, wv);
-      widen_unit(ru[j], a);
-      widen_unit(gu[j], g);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        ss = fmaf(a[i], a[i], ss);
-        hr = fmaf(g[i] * wv[i], a[i], hr);
-      }
+      row_terms<E_, VEC>(ru[j], gu[j], wv, ss, hr);
     }
     const float2 s = row_sum2(ss, hr, lpt, red[turn]);
     const float m = 1.f / sqrtf(s.x / (float)H + eps);
@@ -238,28 +364,14 @@ norm_backward_kernel(const E_* dy, const E_* __restrict__ r, const void* __restr
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
-      if (!(in && c < H)) continue;
-      float a[VEC], g[VEC], wv[VEC], d[VEC];
+      if (c >= H) continue;
+      float wv[VEC];
       load_weight<VEC>(w, w32, c, wv);
-      widen_unit(ru[j], a);
-      widen_unit(gu[j], g);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        acc[j][i] = fmaf(g[i], a[i] * m, acc[j][i]);
-        d[i] = m * (g[i] * wv[i] - a[i] * k);
-      }
-      if (d_r != nullptr) {
-        float e[VEC];
-        widen_unit(*reinterpret_cast<const U*>(d_r + at + c), e);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) d[i] += e[i];
-      }
-      U o;
-      narrow_unit(d, o);
-      *reinterpret_cast<U*>(dx + at + c) = o;
+      const U e = d_r != nullptr ? *reinterpret_cast<const U*>(d_r + at + c) : U{};
+      *reinterpret_cast<U*>(dx + at + c) = row_gradient<E_, VEC>(ru[j], gu[j], e, d_r != nullptr, wv, m, k, acc[j]);
     }
   }
-  float* p = part + ((int64_t)blockIdx.x * rpb + sub) * H;
+  float* p = part + (int64_t)blockIdx.x * H;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
@@ -270,25 +382,23 @@ norm_backward_kernel(const E_* dy, const E_* __restrict__ r, const void* __restr
 }
 
 // dw[c] = sum over i of part[i][c], in a fixed order: a block takes 32 columns,
-// warp k the rows k, k + 8, ...
-constexpr int kSumWarps = 8;
-__global__ void __launch_bounds__(kSumWarps * 32)
+// warp k the rows k, k + 32, ...
+__global__ void __launch_bounds__(1024)
 sum_parts_kernel(const float* __restrict__ part, int n, int H, float* __restrict__ dw) {
-  __shared__ float s[kSumWarps][32];
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   pdl_wait();
   pdl_trigger();
   float v = 0.f;
   if (c < H)
-    for (int i = warp; i < n; i += kSumWarps) v += part[(int64_t)i * H + c];
+#pragma unroll 8
+    for (int i = warp; i < n; i += 32) v += part[(int64_t)i * H + c];
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < H) {
-#pragma unroll
-    for (int k = 1; k < kSumWarps; ++k) v += s[k][lane];
-    dw[c] = v;
-  }
+  v = warp_sum(s[lane][warp]);
+  const int o = blockIdx.x * 32 + warp;
+  if (lane == 0 && o < H) dw[o] = v;
 }
 
 // Codes and exponents back to numbers.  VEC codes a thread (16 on the 16-byte
@@ -358,48 +468,72 @@ cudaError_t launch_norm(int T, int H, cudaStream_t stream, const E_* x, const E_
                       eps, out...);
   };
   if constexpr (VEC > 1) {
-    if (units <= 128) return run(norm_kernel<E_, VEC, 1, QUANT>, 1);
-    if (units <= 512) return run(norm_kernel<E_, VEC, 2, QUANT>, 2);
-    if (units <= 4096) return run(norm_kernel<E_, VEC, 4, QUANT>, 4);
-    return run(norm_kernel<E_, VEC, 8, QUANT>, 8);
+    if (units <= 128) return run(norm_kernel<E_, VEC, 1, QUANT, 128>, 1);
+    if (units <= 512) return run(norm_kernel<E_, VEC, 2, QUANT, 256>, 2);
+    if (units <= 2048) return run(norm_kernel<E_, VEC, 4, QUANT, 512>, 4);
+    return run(norm_kernel<E_, VEC, 8, QUANT, 512>, 8);
   } else {
-    if (units <= 1024) return run(norm_kernel<E_, 1, 4, QUANT>, 4);
-    if (units <= 8192) return run(norm_kernel<E_, 1, 8, QUANT>, 8);
-    return run(norm_kernel<E_, 1, 32, QUANT>, 32);
+    if (units <= 2048) return run(norm_kernel<E_, 1, 4, QUANT, 512>, 4);
+    if (units <= 4096) return run(norm_kernel<E_, 1, 8, QUANT, 512>, 8);
+    if (units <= 8192) return run(norm_kernel<E_, 1, 16, QUANT, 512>, 16);
+    return run(norm_kernel<E_, 1, 32, QUANT, 512>, 32);
   }
 }
 
-// How the gradient kernel is launched: units a thread, threads a row, rows a
-// block, blocks.
+// How the gradient kernel is launched.  On the 16-byte grid a thread has one unit of
+// rows up to 256 units, then two, the ring holding four or two rows; longer rows (and
+// all that lie off the grid) go without it.
 struct BackPlan {
-  int nv, lpt, rpb;
+  bool ring;
+  int nv, lpt, rpb;  // units a thread, threads a row, rows a block
   int64_t blocks;
 };
 BackPlan back_plan(int32_t T, int32_t H, int vec) {
   BackPlan b{};
   const int units = vec > 1 ? H / vec : (int)round_up(H, kGroupCols);
-  b.nv = vec > 1 ? (units <= 512 ? 1 : units <= 2048 ? 2 : units <= 4096 ? 4 : 8) : (units <= 2048 ? 4 : units <= 8192 ? 8 : 32);
+  b.ring = vec > 1 && units <= 2048;
+  if (b.ring) b.nv = units <= 256 ? 1 : 2;
+  else if (vec > 1) b.nv = 8;
+  else b.nv = units <= 2048 ? 4 : units <= 4096 ? 8 : units <= 8192 ? 16 : 32;
   b.lpt = row_lanes(units, b.nv);
-  b.rpb = rows_per_block(b.lpt);
-  const int64_t per_sm = b.lpt * b.rpb <= 256 ? 4 : b.lpt * b.rpb <= 512 ? 2 : 1;
-  const int64_t most = per_sm * current_sms(), want = ceil_div(T, b.rpb);
+  b.rpb = b.ring ? rows_per_block(b.lpt) : 1;
+  const int threads = b.lpt * b.rpb;
+  // threads that an SM's registers hold: 64 each, above eight units 128
+  const int per_sm = (b.ring || b.nv <= 8 ? 1024 : 512) / threads;
+  const int64_t most = (int64_t)(per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm) * current_sms(), want = ceil_div(T, b.rpb);
   b.blocks = want < most ? want : most;
   return b;
 }
 
-template <typename E_, int VEC>
-cudaError_t launch_backward(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const void* w, bool w32,
+template <typename E_>
+cudaError_t launch_backward_ring(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const void* w, bool w32,
                             const E_* d_r, int T, int H, float eps, E_* dx, float* part) {
+  // the shared memory that the largest block of the kernel takes, whatever this
+  // call's: a call in another thread does not lower it
+  auto run = [&](auto kernel, int most) {
+    const size_t per = 4 * 3 * sizeof(uint4);  // NV DEPTH = 4
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(per * most));
+    return err != cudaSuccess ? err
+                              : launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt * b.rpb), per * b.lpt * b.rpb, stream,
+                                           dy, r, w, w32, d_r, T, H, b.lpt, eps, dx, part);
+  };
+  if (b.nv == 1) return run(norm_backward_kernel<E_, 1, 4, 256, 4>, 256);
+  if (b.lpt <= 512) return run(norm_backward_kernel<E_, 2, 2, 512, 2>, 512);
+  return run(norm_backward_kernel<E_, 2, 2, 1024, 1>, 1024);
+}
+template <typename E_, int VEC>
+cudaError_t launch_backward_plain(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const void* w, bool w32,
+                                  const E_* d_r, int T, int H, float eps, E_* dx, float* part) {
   auto run = [&](auto kernel) {
-    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt * b.rpb), 0, stream, dy, r, w, w32, d_r, T, H, b.lpt,
-                      eps, dx, part);
+    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt), 0, stream, dy, r, w, w32, d_r, T, H, b.lpt, eps, dx, part);
   };
   if constexpr (VEC > 1) {
-    return b.nv == 1 ? run(norm_backward_kernel<E_, VEC, 1>) : b.nv == 2 ? run(norm_backward_kernel<E_, VEC, 2>)
-           : b.nv == 4 ? run(norm_backward_kernel<E_, VEC, 4>) : run(norm_backward_kernel<E_, VEC, 8>);
+    return run(norm_backward_plain_kernel<E_, VEC, 8, 512>);  // float32 rows of more than 8192 columns
   } else {
-    return b.nv == 4 ? run(norm_backward_kernel<E_, 1, 4>) : b.nv == 8 ? run(norm_backward_kernel<E_, 1, 8>)
-                                                                      : run(norm_backward_kernel<E_, 1, 32>);
+    return b.nv == 4    ? run(norm_backward_plain_kernel<E_, 1, 4, 512>)
+           : b.nv == 8  ? run(norm_backward_plain_kernel<E_, 1, 8, 512>)
+           : b.nv == 16 ? run(norm_backward_plain_kernel<E_, 1, 16, 512>)
+                        : run(norm_backward_plain_kernel<E_, 1, 32, 512>);
   }
 }
 
@@ -462,10 +596,25 @@ extern "C" size_t moe_rms_norm_backward_workspace_bytes(int32_t num_tokens, int3
   using namespace mlr;
   if (num_tokens < 0 || hidden < 1 || hidden > kMaxNormHidden || (dtype != MLR_DTYPE_BF16 && dtype != MLR_DTYPE_F32)) return 0;
   // the kernel for rows off the grid may be the one that runs, whatever the size
-  const BackPlan a = back_plan(num_tokens, hidden, 1), b = back_plan(num_tokens, hidden, dtype == MLR_DTYPE_BF16 ? 8 : 4);
-  const int64_t parts = a.blocks * a.rpb > b.blocks * b.rpb ? a.blocks * a.rpb : b.blocks * b.rpb;
+  const int64_t a = back_plan(num_tokens, hidden, 1).blocks, b = back_plan(num_tokens, hidden, dtype == MLR_DTYPE_BF16 ? 8 : 4).blocks;
+  const int64_t parts = a > b ? a : b;
   return (size_t)(parts > 0 ? parts : 1) * hidden * 4;
 }
+
+namespace mlr {
+namespace {
+template <typename E_>
+cudaError_t run_backward(bool whole, const BackPlan& b, cudaStream_t stream, const void* dy, const void* r, const void* w,
+                         bool w32, const void* d_r, int T, int H, float eps, void* dx, float* part) {
+  const E_ *g = static_cast<const E_*>(dy), *a = static_cast<const E_*>(r), *e = static_cast<const E_*>(d_r);
+  E_* o = static_cast<E_*>(dx);
+  if (b.ring) return launch_backward_ring<E_>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
+  if constexpr (sizeof(E_) == 4)
+    if (whole) return launch_backward_plain<E_, 4>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
+  return launch_backward_plain<E_, 1>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
+}
+}  // namespace
+}  // namespace mlr
 
 extern "C" int moe_rms_norm_backward(const void* dy, const void* r, const void* weight, const void* d_r, int32_t num_tokens,
                                      int32_t hidden, int32_t dtype, int32_t weight_dtype, float eps, void* dx,
@@ -484,26 +633,15 @@ extern "C" int moe_rms_norm_backward(const void* dy, const void* r, const void* 
   }
   if (dy == nullptr || r == nullptr || dx == nullptr) return MLR_ERR_INVALID;
   const BackPlan b = back_plan(num_tokens, hidden, whole ? 16 / es : 1);
-  if (workspace == nullptr || ws_bytes < (size_t)(b.blocks * b.rpb) * hidden * 4) return MLR_ERR_CAPACITY;
+  if (workspace == nullptr || ws_bytes < (size_t)b.blocks * hidden * 4) return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
   float* part = static_cast<float*>(workspace);
   const bool w32 = weight_dtype == MLR_DTYPE_F32;
-  const int T = num_tokens, H = hidden;
-  cudaError_t err;
-  if (dtype == MLR_DTYPE_BF16) {
-    const uint16_t *g = static_cast<const uint16_t*>(dy), *a = static_cast<const uint16_t*>(r), *e = static_cast<const uint16_t*>(d_r);
-    uint16_t* o = static_cast<uint16_t*>(dx);
-    err = whole ? launch_backward<uint16_t, 8>(b, stream, g, a, weight, w32, e, T, H, eps, o, part)
-                : launch_backward<uint16_t, 1>(b, stream, g, a, weight, w32, e, T, H, eps, o, part);
-  } else {
-    const float *g = static_cast<const float*>(dy), *a = static_cast<const float*>(r), *e = static_cast<const float*>(d_r);
-    float* o = static_cast<float*>(dx);
-    err = whole ? launch_backward<float, 4>(b, stream, g, a, weight, w32, e, T, H, eps, o, part)
-                : launch_backward<float, 1>(b, stream, g, a, weight, w32, e, T, H, eps, o, part);
-  }
-  if (const int c = launched(err); c != MLR_OK) return c;
-  return launched(launch_pdl(sum_parts_kernel, dim3((unsigned)ceil_div(H, 32)), dim3(kSumWarps * 32), 0, stream,
-                             (const float*)part, (int)(b.blocks * b.rpb), H, d_weight));
+  auto run = dtype == MLR_DTYPE_BF16 ? run_backward<uint16_t> : run_backward<float>;
+  const int c = launched(run(whole, b, stream, dy, r, weight, w32, d_r, num_tokens, hidden, eps, dx, part));
+  if (c != MLR_OK) return c;
+  return launched(launch_pdl(sum_parts_kernel, dim3((unsigned)ceil_div(hidden, 32)), dim3(1024), 0, stream,
+                             (const float*)part, (int)b.blocks, (int)hidden, d_weight));
 }
 
 extern "C" int moe_fp8_dequantize(const uint8_t* codes, const uint8_t* exps, int32_t rows, int32_t cols, int32_t dtype,

@@ -31,17 +31,45 @@ struct RouteArgs {
   int32_t* status;
 };
 
-// sigmoid(logit) + bias in 64 bits.
-__device__ __noinline__ double exact_score(float l, const float* bias, int e) {
-  return 1.0 / (1.0 + exp(-(double)l)) + (bias != nullptr ? (double)__ldg(bias + e) : 0.0);
+// Doubles as integers of the same order (there is no -0 among them), which are
+// compared in a few cycles: GB300 takes 16 to issue a comparison of doubles.
+constexpr long long kLowest = (long long)0x800fffffffffffff;  // -inf
+__device__ __forceinline__ long long ordered(double v) {
+  const long long b = __double_as_longlong(v);
+  return b ^ ((b >> 63) & 0x7fffffffffffffffll);
+}
+__device__ __forceinline__ double from_ordered(long long k) {
+  return __longlong_as_double(k ^ ((k >> 63) & 0x7fffffffffffffffll));
+}
+// sigmoid(logit) + bias in 64 bits, to a few units of the last place.  With t = e^-|l|
+// it is 1 / (1 + t) or t / (1 + t); t = 2^n e^r with n = -|l| / ln 2 rounded, e^r a
+// Taylor polynomial (|r| < 0.35: the 14th power's term is below 2^-57) summed
+// pairwise, as the latency of one operation after another is what this costs; the
+// quotient from a 32-bit one by two Newton steps.
+__device__ __forceinline__ double exact_score(float l, const float* bias, int e) {
+  const double x = -fabs((double)l);
+  const double n = rint(fmax(x, -750.0) * 1.4426950408889634);
+  const double r = fma(n, -0x1.473de6af278edp-34, fma(n, -0x1.62e42fef00000p-1, x));  // ln 2 in two parts: n times the first is exact
+  const double r2 = r * r, r4 = r2 * r2;
+  const double p01 = 1.0 + r, p23 = fma(r, 1.0 / 6, 0.5), p45 = fma(r, 1.0 / 120, 1.0 / 24), p67 = fma(r, 1.0 / 5040, 1.0 / 720),
+               p89 = fma(r, 1.0 / 362880, 1.0 / 40320), pab = fma(r, 1.0 / 39916800, 1.0 / 3628800),
+               pcd = fma(r, 1.0 / 6227020800.0, 1.0 / 479001600);
+  const double q0 = fma(r2, p23, p01), q4 = fma(r2, p67, p45), q8 = fma(r2, pab, p89);
+  const double p = fma(r4, fma(r4, fma(r4, pcd, q8), q4), q0);
+  const double t = x < -708.0 ? 0.0 : p * __longlong_as_double((long long)(1023 + (int)n) << 52);
+  const double d = 1.0 + t;
+  double y = (double)(1.f / (float)d);
+  y = fma(y, fma(-d, y, 1.0), y);
+  y = fma(y, fma(-d, y, 1.0), y);
+  return (l < 0.f ? t * y : y) + (bias != nullptr ? (double)__ldg(bias + e) : 0.0);
 }
 
 // The larger of two (score, index) pairs over the warp: the larger score, the
 // lower index of equal ones.
-__device__ __forceinline__ void warp_best(double& v, int& i) {
+__device__ __forceinline__ void warp_best(long long& v, int& i) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    const double u = __shfl_xor_sync(0xffffffffu, v, o);
+    const long long u = __shfl_xor_sync(0xffffffffu, v, o);
     const int k = __shfl_xor_sync(0xffffffffu, i, o);
     if (u > v || (u == v && k < i)) {
       v = u;
@@ -82,45 +110,44 @@ __device__ __forceinline__ void write_choice(const RouteArgs& a, const E_* row, 
 // One token by one warp, every score in 64 bits: keys [E] and group scores [groups]
 // in shared memory.
 template <typename E_>
-__device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, double* key, double* group, int lane) {
+__device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, long long* key, long long* group,
+                                            int lane) {
   const bool logit_key = !a.sigmoid || (a.bias == nullptr && a.groups == 1);
+#pragma unroll 4
   for (int e = lane; e < a.E; e += 32) {
     const float l = finite_logit(row + e);
-    double k = (double)l;
+    double k = (double)(l + 0.f);  // +0 for -0
     if (!logit_key && l > -CUDART_INF_F) {
       k = exact_score(l, a.bias, e);
       if (!(k < CUDART_INF)) k = -CUDART_INF;  // a bias that is NaN or +inf
     }
-    key[e] = k;
+    key[e] = ordered(k);
   }
   __syncwarp();
   if (a.groups > 1) {
     const int size = a.E / a.groups;
     for (int g = lane; g < a.groups; g += 32) {
-      double b0 = -CUDART_INF, b1 = -CUDART_INF;
+      long long b0 = kLowest, b1 = kLowest;
       for (int i = 0; i < size; ++i) {
-        const double k = key[g * size + i];
-        if (k > b0) {
-          b1 = b0;
-          b0 = k;
-        } else if (k > b1) {
-          b1 = k;
-        }
+        const long long k = key[g * size + i];
+        b1 = max(b1, min(b0, k));
+        b0 = max(b0, k);
       }
-      group[g] = a.sigmoid && b1 > -CUDART_INF ? b0 + b1 : b0;
+      group[g] = a.sigmoid && b1 > kLowest ? ordered(from_ordered(b0) + from_ordered(b1) + 0.0) : b0;
     }
     __syncwarp();
     for (int g = lane; g < a.groups; g += 32) {
+      const long long mine = group[g];
       int before = 0;
-      for (int o = 0; o < a.groups; ++o) before += group[o] > group[g] || (group[o] == group[g] && o < g);
+      for (int o = 0; o < a.groups; ++o) before += group[o] > mine || (group[o] == mine && o < g);
       if (before >= a.best)
-        for (int i = 0; i < size; ++i) key[g * size + i] = -CUDART_INF;
+        for (int i = 0; i < size; ++i) key[g * size + i] = kLowest;
     }
     __syncwarp();
   }
   int mine = -1;
   for (int k = 0; k < a.K; ++k) {
-    double v = -CUDART_INF;
+    long long v = kLowest;
     int i = INT32_MAX;
     for (int e = lane; e < a.E; e += 32)
       if (key[e] > v) {
@@ -128,9 +155,9 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, i
         i = e;
       }
     warp_best(v, i);
-    if (!(v > -CUDART_INF)) break;
+    if (v == kLowest) break;
     if (lane == k) mine = i;
-    if (lane == (i & 31)) key[i] = -CUDART_INF;
+    if (lane == (i & 31)) key[i] = kLowest;
     __syncwarp();
   }
   __syncwarp();
@@ -141,9 +168,9 @@ constexpr int kRouteThreads = 128;
 template <typename E_>
 __global__ void __launch_bounds__(kRouteThreads)
 route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a) {
-  extern __shared__ double smem[];
+  extern __shared__ long long smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  double* key = smem + (size_t)warp * (a.E + a.groups);
+  long long* key = smem + (size_t)warp * (a.E + a.groups);
   pdl_wait();
   pdl_trigger();
   for (int64_t t = (int64_t)blockIdx.x * warps + warp; t < a.T; t += (int64_t)gridDim.x * warps) {
@@ -237,7 +264,7 @@ constexpr int kFastTopk = 16;
 // the groups' two best of each unit; the candidates' keys (32 and 64 bits) and ids.
 template <int LPT, int L>
 struct alignas(16) Candidates {
-  double exact[2 * L];
+  long long exact[2 * L];
   float key[2 * L];
   int id[2 * L];
 };
@@ -258,7 +285,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPT, ll = lane % LPT;
   const uint32_t team = (LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1) << (sub * LPT));
   char* mine = fast_smem + (size_t)warp * (scratch_bytes + TPW * sizeof(Candidates<LPT, L>));
-  double* slow_key = reinterpret_cast<double*>(mine);
+  long long* slow_key = reinterpret_cast<long long*>(mine);
   Candidates<LPT, L>& cand = reinterpret_cast<Candidates<LPT, L>*>(mine + scratch_bytes)[sub];
   const int E = a.E, K = a.K;
   const bool biased = a.sigmoid && (a.bias != nullptr || a.groups > 1);
@@ -360,9 +387,9 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   float list[L];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    list[b] = v[b * (V / NB)];
+    list[b] = v[b];  // of every NB-th logit, so that a block has its share of every group
 #pragma unroll
-    for (int i = 1; i < V / NB; ++i) list[b] = fmaxf(list[b], v[b * (V / NB) + i]);
+    for (int i = b + NB; i < V; i += NB) list[b] = fmaxf(list[b], v[i]);
   }
   sort_desc<NB>(list);
   merge_lists<NB, L, LPT, 1>(list);
@@ -431,7 +458,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
 #pragma unroll
       for (int c = 0; c < CPL; ++c)
         if ((unsure & team) && id[c] >= 0)
-          cand.exact[ll + c * LPT] = exact_score(logit[c], a.bias, id[c]);
+          cand.exact[ll + c * LPT] = ordered(exact_score(logit[c], a.bias, id[c]));
       __syncwarp();
     }
     if (unsure & team) {
@@ -439,7 +466,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
 #pragma unroll
       for (int c = 0; c < CPL; ++c) {
         if (id[c] < 0) continue;
-        const double k64 = biased ? cand.exact[ll + c * LPT] : 0.0;
+        const long long k64 = biased ? cand.exact[ll + c * LPT] : 0;
         rank[c] = 0;
         for (int i = 0; i < m; ++i) {
           const bool above = biased ? cand.exact[i] > k64 : cand.key[i] > key[c];
@@ -515,7 +542,7 @@ int run_route(const void* logits, const RouteArgs& a, cudaStream_t stream) {
     if (whole) return a.K <= 8 ? launch_fast_for<E_, VEC, 8>(l, a, stream) : launch_fast_for<E_, VEC, 16>(l, a, stream);
     return a.K <= 8 ? launch_fast_for<E_, 1, 8>(l, a, stream) : launch_fast_for<E_, 1, 16>(l, a, stream);
   }
-  const size_t per = (size_t)(a.E + a.groups) * sizeof(double);
+  const size_t per = (size_t)(a.E + a.groups) * sizeof(long long);
   const int warps = per <= 8 * 1024 ? kRouteThreads / 32 : 1;
   const int64_t blocks = ceil_div(a.T, warps), most = (int64_t)current_sms() * 16;
   return launched(launch_pdl(route_kernel<E_>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(warps * 32), per * warps,

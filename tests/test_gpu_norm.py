@@ -38,7 +38,7 @@ def make(T, H, dtype, w_dtype=None, seed=0, shift=0):
 # rows of one column, below a vector, of 16-byte vectors and off them, ending inside a
 # group of 128 and at its end, one and several to a block, up to the largest
 SHAPES = [(1, 1), (3, 7), (5, 8), (33, 128), (7, 129), (9, 200), (4, 256), (130, 1000), (3, 1111), (2, 2048), (17, 2056), (5, 4099),
-          (2, 7168), (3, 8200), (2, 16384), (1, 20001), (2, 32768)]
+          (2, 7168), (3, 8200), (3, 8203), (2, 12288), (1, 16381), (2, 16384)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
