@@ -65,13 +65,17 @@ __device__ __forceinline__ void team_sync() {
   else __syncwarp();
 }
 
-// v: logits to s, zeros past E, in tokens that are not active and for logits that are
-// not finite.  Returns 1 / sum of s, 0 where that is 0.  Every thread of the warp
-// (the block) calls it.
-template <int VEC, int LPT, int V, typename E_>
-__device__ __forceinline__ float scores(const E_* row, int E, bool sigmoid, int ll, bool active, float* red, float (&v)[V]) {
-  const float check = load_logits<VEC, LPT>(row, E, ll, active, v);
-  if (__any_sync(0xffffffffu, !(check == 0.f)))
+// Turns that are fetched ahead where logits lie on the 16-byte grid.
+constexpr int kAhead = 2;
+template <int VEC, int LPT> constexpr bool kRing = VEC > 1 && !kBlockTokens<LPT>;
+template <int VEC, int LPT, int V> constexpr int kRingBytes = kRing<VEC, LPT> ? kAhead * V / VEC * kBalanceThreads * 16 : 0;
+
+// v: a token's logits to s, zeros past E and for logits that are not finite.  Returns 1 /
+// sum of s, 0 where that is 0 and for a token that is not active.  Every thread of the
+// warp (the block) calls it.
+template <int VEC, int LPT, int V>
+__device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active, float* red, float (&v)[V]) {
+  if (__any_sync(0xffffffffu, !(check_finite(v) == 0.f)))
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = finite_logit(v[i]);
   close_past<VEC, LPT>(E, ll, v);
@@ -95,31 +99,48 @@ __device__ __forceinline__ float scores(const E_* row, int E, bool sigmoid, int 
 // Sums of shares and pairs per expert over the block's tokens: part [blocks][E]
 // and count [blocks][E + 1] (the last one: tokens).
 template <int VEC, int LPT, int V, typename E_>
-__global__ void __launch_bounds__(kBalanceThreads)
+__global__ void __launch_bounds__(kBalanceThreads, V <= 16 && !kBlockTokens<LPT> ? 4 : 2)
 balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
                int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, int32_t* status) {
-  extern __shared__ int hist[];  // [E + 1] pairs, then float [warps (1 for a block's token)][E] shares
+  extern __shared__ uint4 ring[];  // the ring; then [E + 1] pairs; then float [warps (1 for a block's token)][E] shares
   __shared__ float red[kBalanceThreads / 32];
   constexpr int TEAMS = kTeams<LPT>, ROWS = kBlockTokens<LPT> ? 1 : kBalanceThreads / 32;
+  int* hist = reinterpret_cast<int*>(reinterpret_cast<char*>(ring) + kRingBytes<VEC, LPT, V>);
   float* sums = reinterpret_cast<float*>(hist + E + 1);
   const int team = threadIdx.x / LPT, ll = threadIdx.x % LPT;
   for (int e = threadIdx.x; e <= E; e += kBalanceThreads) hist[e] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  const int64_t step = (int64_t)gridDim.x * TEAMS;
+  auto fetch = [&](int64_t t, int stage) {
+    if constexpr (kRing<VEC, LPT>)
+      fetch_logits<VEC, LPT, V, kBalanceThreads>(ring, logits + t * E, E, ll, t < T, stage);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch((int64_t)blockIdx.x * TEAMS + team + i * step, i);
   float acc[V] = {};
-  int tokens = 0;
-  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += (int64_t)gridDim.x * TEAMS) {
+  int tokens = 0, stage = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += step) {
     const int64_t t = t0 + team;
     const bool active = t < T && (mask == nullptr || mask[t]);
+    // the place of this lane (the first ones of more than LPT), used at the turn's end
+    const int first = active && ll < K ? __ldg(ids + t * K + ll) : -1;
     float v[V];
-    const float inv = scores<VEC, LPT>(logits + (active ? t : 0) * E, E, sigmoid, ll, active, red, v);
+    if constexpr (kRing<VEC, LPT>) {
+      take_logits<VEC, LPT, V, kBalanceThreads, kAhead>(ring, E, ll, active, stage, v);
+      fetch(t + kAhead * step, stage);
+      stage = stage == kAhead - 1 ? 0 : stage + 1;
+    } else {
+      load_logits<VEC, LPT>(logits + (active ? t : 0) * E, E, ll, active, v);
+    }
+    const float inv = scores<VEC, LPT>(E, sigmoid, ll, active, red, v);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
     if (active) {
       ++tokens;
       for (int k = ll; k < K; k += LPT) {
-        const int id = __ldg(ids + t * K + k);
+        const int id = k == ll ? first : __ldg(ids + t * K + k);
         if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
         else if (id != -1) set_status(status, MLR_STATUS_INDEX);
       }
@@ -222,10 +243,10 @@ struct GradArgs {
 // take a place each (place ll + LPT c; in a block's token: its first warp) and laid
 // in a row of shared memory, zero elsewhere, from where the experts' lanes take it.
 template <int VEC, int LPT, int V, typename E_>
-__global__ void __launch_bounds__(kBalanceThreads)
+__global__ void __launch_bounds__(kBalanceThreads, V <= 16 && !kBlockTokens<LPT> ? 4 : 2)
 route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ GradArgs a, E_* __restrict__ d_logits,
                       int32_t* status) {
-  extern __shared__ float rows[];  // [teams][E], zero but for the chosen experts while a token is in work
+  extern __shared__ uint4 ring[];  // the ring (with shares); then float [teams][E], zero but for the chosen experts
   __shared__ float red[kBalanceThreads / 32];
   constexpr int TEAMS = kTeams<LPT>;
   constexpr int PL = kBlockTokens<LPT> ? 32 : LPT;  // lanes that take places
@@ -234,7 +255,7 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
   const int E = a.E, K = a.K;
   const bool by_weights = a.d_weights != nullptr, all_chosen = by_weights && !a.sigmoid && !a.renormalize;
   const bool shares = a.counts != nullptr || all_chosen;
-  float* row_s = rows + team * E;
+  float* row_s = reinterpret_cast<float*>(reinterpret_cast<char*>(ring) + (shares ? kRingBytes<VEC, LPT, V> : 0)) + team * E;
   if (by_weights) {
     for (int e = ll; e < E; e += LPT) row_s[e] = 0.f;
     team_sync<LPT>();
@@ -243,21 +264,40 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
   pdl_trigger();
   float coef[V] = {};
   if (a.counts != nullptr) {
-    const double n = max(1, __ldg(a.counts + E));
-    const double f = (double)__ldg(a.d_loss) * E / (K * n * n);
+    // in fp32: 64-bit operations for every expert of every thread took 14% of the time
+    const float n = (float)max(1, __ldg(a.counts + E));
+    const float f = __ldg(a.d_loss) * ((float)E / (float)K) / n / n;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
-      if (e < E) coef[i] = (float)(f * __ldg(a.counts + e));
+      if (e < E) coef[i] = f * (float)__ldg(a.counts + e);
     }
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < a.T; t0 += (int64_t)gridDim.x * TEAMS) {
+  const int64_t step = (int64_t)gridDim.x * TEAMS;
+  auto fetch = [&](int64_t t, int stage) {
+    if constexpr (kRing<VEC, LPT>)
+      fetch_logits<VEC, LPT, V, kBalanceThreads>(ring, logits + t * E, E, ll, t < a.T, stage);
+  };
+  if (shares)
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch((int64_t)blockIdx.x * TEAMS + team + i * step, i);
+  int stage = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < a.T; t0 += step) {
     const int64_t t = t0 + team;
     const bool active = t < a.T && (a.mask == nullptr || a.mask[t]);
     const E_* row = logits + (active ? t : 0) * E;
     float v[V] = {};
     float inv = 0.f;
-    if (shares) inv = scores<VEC, LPT>(row, E, a.sigmoid, ll, active, red, v);
+    if (shares) {
+      if constexpr (kRing<VEC, LPT>) {
+        take_logits<VEC, LPT, V, kBalanceThreads, kAhead>(ring, E, ll, active, stage, v);
+        fetch(t + kAhead * step, stage);
+        stage = stage == kAhead - 1 ? 0 : stage + 1;
+      } else {
+        load_logits<VEC, LPT>(row, E, ll, active, v);
+      }
+      inv = scores<VEC, LPT>(E, a.sigmoid, ll, active, red, v);
+    }
     int id[CP];
     if (by_weights) {
       if (!kBlockTokens<LPT> || threadIdx.x < 32) {
@@ -379,8 +419,10 @@ int by_experts(int E, F f) {
 }
 int lanes_of(int E) { return E <= 256 ? 8 : E <= 512 ? 16 : E <= kPartExperts ? 32 : kBalanceThreads; }
 
+// Blocks of an SM, by the registers of the two kernels.
+int blocks_per_sm(int E) { return E <= 128 ? 4 : 2; }
 int64_t balance_blocks(int32_t T, int32_t E) {
-  const int64_t want = ceil_div(T, kBalanceThreads / lanes_of(E)), most = 2 * (int64_t)current_sms();
+  const int64_t want = ceil_div(T, kBalanceThreads / lanes_of(E)), most = (int64_t)blocks_per_sm(E) * current_sms();
   return want < 1 ? 1 : want < most ? want : most;
 }
 
@@ -389,20 +431,23 @@ int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int
                 int32_t* count, int32_t* status, cudaStream_t stream) {
   const unsigned blocks = (unsigned)balance_blocks(T, E);
   return by_experts(E, [&](auto lpt, auto v) {
-    const size_t smem = (size_t)(E + 1) * 4 + (size_t)(kBlockTokens<lpt.value> ? 1 : kBalanceThreads / 32) * E * 4;
-    return launched(launch_pdl(balance_kernel<VEC, lpt.value, v.value, E_>, dim3(blocks), dim3(kBalanceThreads), smem, stream,
-                               static_cast<const E_*>(logits), ids, mask, T, E, K, sigmoid, part, count, status));
+    constexpr int ring = kRingBytes<VEC, lpt.value, v.value>;
+    constexpr int rows = kBlockTokens<lpt.value> ? 1 : kBalanceThreads / 32, cover = lpt.value * v.value;
+    auto bytes = [&](int experts) { return (size_t)ring + (experts + 1) * 4 + (size_t)rows * experts * 4; };
+    return launch_with_smem(balance_kernel<VEC, lpt.value, v.value, E_>, dim3(blocks), dim3(kBalanceThreads), bytes(E), (int)bytes(cover), stream,
+                       static_cast<const E_*>(logits), ids, mask, T, E, K, sigmoid, part, count, status);
   });
 }
 
 template <int VEC, typename E_>
 int run_backward(const void* logits, const GradArgs& a, void* d_logits, int32_t* status, cudaStream_t stream) {
   return by_experts(a.E, [&](auto lpt, auto v) {
-    constexpr int teams = kTeams<lpt.value>;
-    const int64_t want = ceil_div(a.T, teams), most = 2 * (int64_t)current_sms();
-    return launched(launch_pdl(route_backward_kernel<VEC, lpt.value, v.value, E_>, dim3((unsigned)(want < most ? want : most)),
-                               dim3(kBalanceThreads), (size_t)teams * a.E * 4, stream, static_cast<const E_*>(logits), a,
-                               static_cast<E_*>(d_logits), status));
+    constexpr int teams = kTeams<lpt.value>, ring = kRingBytes<VEC, lpt.value, v.value>, cover = lpt.value * v.value;
+    const int64_t want = ceil_div(a.T, teams), most = (int64_t)blocks_per_sm(a.E) * current_sms();
+    const bool shares = a.counts != nullptr || (!a.sigmoid && !a.renormalize);
+    const size_t smem = (shares ? ring : 0) + (a.d_weights != nullptr ? (size_t)teams * a.E * 4 : 0);
+    return launch_with_smem(route_backward_kernel<VEC, lpt.value, v.value, E_>, dim3((unsigned)(want < most ? want : most)), dim3(kBalanceThreads), smem,
+                       ring + teams * cover * 4, stream, static_cast<const E_*>(logits), a, static_cast<E_*>(d_logits), status);
   });
 }
 

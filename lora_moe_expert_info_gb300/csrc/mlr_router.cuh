@@ -37,10 +37,17 @@ __device__ __forceinline__ void load_unit(const E_* p, float (&v)[VEC]) {
   if constexpr (VEC == 1) v[0] = row_widen(__ldg(p));
   else row_widen(__ldg(reinterpret_cast<const uint4*>(p)), v);
 }
-// Loads them: zeros past E, and all where `active` is not set.  Returns NaN if one is
-// not finite, else 0.
+// NaN if one of them is not finite, else 0.
+template <int V>
+__device__ __forceinline__ float check_finite(const float (&v)[V]) {
+  float check = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) check = fmaf(v[i], 0.f, check);
+  return check;
+}
+// Loads them: zeros past E, and all where `active` is not set.
 template <int VEC, int LPT, int V, typename E_>
-__device__ __forceinline__ float load_logits(const E_* row, int E, int ll, bool active, float (&v)[V]) {
+__device__ __forceinline__ void load_logits(const E_* row, int E, int ll, bool active, float (&v)[V]) {
 #pragma unroll
   for (int j = 0; j < V / VEC; ++j) {
     const int e = (ll + LPT * j) * VEC;
@@ -51,10 +58,39 @@ __device__ __forceinline__ float load_logits(const E_* row, int E, int ll, bool 
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
   }
-  float check = 0.f;
+}
+// Logits on the 16-byte grid can be fetched some turns ahead: every thread of a block of
+// THREADS copies the units that it takes to places of its own in shared memory (16 bytes
+// each, one for every stage, unit and thread), which asks for no barrier; once they are
+// in registers their places are free for the next turn's.
+template <int THREADS>
+__device__ __forceinline__ uint4* ring_slot(uint4* ring, int units, int stage, int j) {
+  return ring + (stage * units + j) * THREADS + threadIdx.x;
+}
+template <int VEC, int LPT, int V, int THREADS, typename E_>
+__device__ __forceinline__ void fetch_logits(uint4* ring, const E_* row, int E, int ll, bool have, int stage) {
+  if (have)
 #pragma unroll
-  for (int i = 0; i < V; ++i) check = fmaf(v[i], 0.f, check);
-  return check;
+    for (int j = 0; j < V / VEC; ++j) {
+      const int e = (ll + LPT * j) * VEC;
+      if (e < E)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring_slot<THREADS>(ring, V / VEC, stage, j))),
+                     "l"(row + e)
+                     : "memory");
+    }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Takes the logits of the turn that was fetched AHEAD turns ago.
+template <int VEC, int LPT, int V, int THREADS, int AHEAD>
+__device__ __forceinline__ void take_logits(uint4* ring, int E, int ll, bool active, int stage, float (&v)[V]) {
+  asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+#pragma unroll
+  for (int j = 0; j < V / VEC; ++j) {
+    float u[VEC] = {};
+    if (active && (ll + LPT * j) * VEC < E) row_widen(*ring_slot<THREADS>(ring, V / VEC, stage, j), u);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
+  }
 }
 // -inf past E.
 template <int VEC, int LPT, int V>
@@ -87,6 +123,17 @@ inline int launched(cudaError_t err) {
   }
   note_launch();
   return MLR_OK;
+}
+
+// Launches with `smem` bytes of dynamic shared memory.  Above what needs no opt-in the
+// kernel is given `most`, which all of its calls stay below, not what this one needs: a
+// smaller call in another thread must not lower the limit before this one's launch.
+template <typename Kernel, typename... Args>
+int launch_with_smem(Kernel kernel, dim3 grid, dim3 block, size_t smem, int most, cudaStream_t stream, Args... args) {
+  cudaError_t err = cudaSuccess;
+  if (smem > 46 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (err == cudaSuccess) err = launch_pdl(kernel, grid, block, smem, stream, args...);
+  return launched(err);
 }
 
 inline int check_logits(const void* logits, int32_t T, int32_t E, int32_t K, int32_t dtype, int32_t scoring) {

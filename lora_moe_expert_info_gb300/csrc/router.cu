@@ -20,6 +20,7 @@ constexpr int kMaxGroups = 256;
 
 // Whether a logit is one that the caller hears of: NaN or +inf.
 __device__ __forceinline__ bool bad_logit(float v) { return !(v < CUDART_INF_F); }
+
 struct RouteArgs {
   const float* bias;
   const uint8_t* mask;
@@ -31,6 +32,10 @@ struct RouteArgs {
   int32_t* status;
 };
 
+// How near two sigmoid + bias may be in fp32 and still be in either order: each is
+// off by at most 2.25 2^-23 (ex2 2^-22 and its argument |l| 2^-23, both times s (1 -
+// s); 1 + e 2^-24; rcp 2^-23) and the sum's 2^-24 |c|; twice that, rounded up.
+__device__ __forceinline__ float near_score(float c) { return fmaf(fabsf(c), 0x1p-22f, 0x1p-20f); }
 // Doubles as integers of the same order (there is no -0 among them), which are
 // compared in a few cycles: GB300 takes 16 to issue a comparison of doubles.
 constexpr long long kLowest = (long long)0x800fffffffffffff;  // -inf
@@ -46,7 +51,7 @@ __device__ __forceinline__ double from_ordered(long long k) {
 // Taylor polynomial (|r| < 0.35: the 14th power's term is below 2^-57) summed
 // pairwise, as the latency of one operation after another is what this costs; the
 // quotient from a 32-bit one by two Newton steps.
-__device__ __forceinline__ double exact_score(float l, const float* bias, int e) {
+__device__ __noinline__ double exact_score(float l, const float* bias, int e) {
   const double x = -fabs((double)l);
   const double n = rint(fmax(x, -750.0) * 1.4426950408889634);
   const double r = fma(n, -0x1.473de6af278edp-34, fma(n, -0x1.62e42fef00000p-1, x));  // ln 2 in two parts: n times the first is exact
@@ -62,6 +67,42 @@ __device__ __forceinline__ double exact_score(float l, const float* bias, int e)
   y = fma(y, fma(-d, y, 1.0), y);
   y = fma(y, fma(-d, y, 1.0), y);
   return (l < 0.f ? t * y : y) + (bias != nullptr ? (double)__ldg(bias + e) : 0.0);
+}
+
+// A group's score, the sum of its two best scores, in 64 bits; `third` is set where a
+// third one is so near the second that 32 bits do not tell which of them it is.
+template <typename E_>
+__device__ __noinline__ long long exact_group(const RouteArgs& a, const E_* row, int g, bool& third) {
+  const int size = a.E / a.groups;
+  float b0 = -CUDART_INF_F, b1 = -CUDART_INF_F, b2 = -CUDART_INF_F;
+  int i0 = -1, i1 = -1;
+#pragma unroll 1
+  for (int e = g * size; e < (g + 1) * size; ++e) {
+    const float l = finite_logit(row + e);
+    const float c = quick_sigmoid(l) + (a.bias != nullptr ? __ldg(a.bias + e) : 0.f);
+    if (!(l > -CUDART_INF_F && c < CUDART_INF_F)) continue;
+    if (c > b1) {
+      b2 = b1;
+      b1 = c;
+      i1 = e;
+      if (c > b0) {
+        b1 = b0;
+        i1 = i0;
+        b0 = c;
+        i0 = e;
+      }
+    } else {
+      b2 = fmaxf(b2, c);
+    }
+  }
+  third = b1 > -CUDART_INF_F && b1 - b2 <= near_score(b1);
+  double sum = 0.0;
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int e = k == 0 ? i0 : i1;
+    if (e >= 0) sum += exact_score(finite_logit(row + e), a.bias, e);
+  }
+  return i0 < 0 ? kLowest : ordered(sum + 0.0);
 }
 
 // The larger of two (score, index) pairs over the warp: the larger score, the
@@ -113,7 +154,8 @@ template <typename E_>
 __device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, int64_t t, long long* key, long long* group,
                                             int lane) {
   const bool logit_key = !a.sigmoid || (a.bias == nullptr && a.groups == 1);
-#pragma unroll 4
+  // loops as they stand: this code is rarely run, and fetching it costs more than running it
+#pragma unroll 1
   for (int e = lane; e < a.E; e += 32) {
     const float l = finite_logit(row + e);
     double k = (double)(l + 0.f);  // +0 for -0
@@ -128,6 +170,7 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, i
     const int size = a.E / a.groups;
     for (int g = lane; g < a.groups; g += 32) {
       long long b0 = kLowest, b1 = kLowest;
+#pragma unroll 1
       for (int i = 0; i < size; ++i) {
         const long long k = key[g * size + i];
         b1 = max(b1, min(b0, k));
@@ -139,16 +182,20 @@ __device__ __noinline__ void choose_exactly(const RouteArgs& a, const E_* row, i
     for (int g = lane; g < a.groups; g += 32) {
       const long long mine = group[g];
       int before = 0;
+#pragma unroll 1
       for (int o = 0; o < a.groups; ++o) before += group[o] > mine || (group[o] == mine && o < g);
       if (before >= a.best)
+#pragma unroll 1
         for (int i = 0; i < size; ++i) key[g * size + i] = kLowest;
     }
     __syncwarp();
   }
   int mine = -1;
+#pragma unroll 1
   for (int k = 0; k < a.K; ++k) {
     long long v = kLowest;
     int i = INT32_MAX;
+#pragma unroll 1
     for (int e = lane; e < a.E; e += 32)
       if (key[e] > v) {
         v = key[e];
@@ -205,10 +252,6 @@ route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a)
 // A warp's time goes to the ALU pipe (maxima, comparisons), which takes an
 // instruction every two cycles.
 
-// How near two sigmoid + bias may be in fp32 and still be in either order: each is
-// off by at most 2.25 2^-23 (ex2 2^-22 and its argument |l| 2^-23, both times s (1 -
-// s); 1 + e 2^-24; rcp 2^-23) and the sum's 2^-24 |c|; twice that, rounded up.
-__device__ __forceinline__ float near_score(float c) { return fmaf(fabsf(c), 0x1p-22f, 0x1p-20f); }
 __device__ __forceinline__ void order_desc(float& a, float& b) {
   const float hi = fmaxf(a, b), lo = fminf(a, b);
   a = hi;
@@ -260,33 +303,45 @@ __device__ __forceinline__ void merge_lists(float (&x)[L]) {
 constexpr int kFastThreads = 128;
 constexpr int kFastTopk = 16;
 
-// Shared memory of a warp: keys in 64 bits for choose_exactly, the same bytes for
-// the groups' two best of each unit; the candidates' keys (32 and 64 bits) and ids.
-template <int LPT, int L>
+// Shared memory of a warp: the candidates' keys and ids, and room that is used for one
+// thing at a time: the 64-bit keys of choose_exactly, the groups' two best of each unit,
+// the 64-bit keys and the ranks of near candidates.
+template <int L> constexpr int kCap = 4 * L;  // candidates of a token
+template <int L>
 struct alignas(16) Candidates {
-  long long exact[2 * L];
-  float key[2 * L];
-  int id[2 * L];
+  float key[kCap<L>];
+  int id[kCap<L>];
 };
-__host__ __device__ constexpr int64_t fast_scratch(int E, int groups, int vec, int tokens) {
-  const int64_t slow = (int64_t)(E + groups) * 8, best = groups > 1 ? (int64_t)tokens * (E / vec) * 8 : 0;
-  return round_up(slow > best ? slow : best, 16);
+template <int L>
+struct alignas(16) Near {
+  long long key[kCap<L>];
+  int rank[kCap<L>];
+};
+template <int L>
+int64_t fast_scratch(int E, int groups, int vec, int tokens) {
+  const int64_t slow = (int64_t)(E + groups) * 8, best = groups > 1 ? (int64_t)tokens * (E / vec) * 8 : 0,
+                near = (int64_t)tokens * sizeof(Near<L>);
+  const int64_t most = slow > best ? slow : best;
+  return round_up(most > near ? most : near, 16);
 }
 
+__device__ __forceinline__ int round_up4(int n) { return (n + 3) & ~3; }
+
 template <typename E_, int VEC, int LPT, int V, int L>
-__global__ void __launch_bounds__(kFastThreads)
+__global__ void __launch_bounds__(kFastThreads, VEC == 1 ? 5 : 8)
 route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a, int scratch_bytes) {
   constexpr int NU = V / VEC;               // units of a lane
   constexpr int TPW = 32 / LPT;             // tokens of a warp
   constexpr int NB = 4 * L / LPT;           // block maxima of a lane
-  constexpr int CPL = (2 * L + LPT - 1) / LPT;  // candidates of a lane
+  constexpr int CAP = kCap<L>, CPL = CAP / LPT < 1 ? 1 : CAP / LPT;  // candidates of a token, of a lane
   static_assert(NB >= 1 && NB <= V && NB <= L && LPT * NB >= L, "lists grow to L");
-  extern __shared__ char fast_smem[];
+  extern __shared__ uint4 warp_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPT, ll = lane % LPT;
   const uint32_t team = (LPT == 32 ? 0xffffffffu : ((1u << LPT) - 1) << (sub * LPT));
-  char* mine = fast_smem + (size_t)warp * (scratch_bytes + TPW * sizeof(Candidates<LPT, L>));
+  char* mine = reinterpret_cast<char*>(warp_smem) + (size_t)warp * (scratch_bytes + TPW * sizeof(Candidates<L>));
   long long* slow_key = reinterpret_cast<long long*>(mine);
-  Candidates<LPT, L>& cand = reinterpret_cast<Candidates<LPT, L>*>(mine + scratch_bytes)[sub];
+  Near<L>& exact = reinterpret_cast<Near<L>*>(mine)[sub];
+  Candidates<L>& cand = reinterpret_cast<Candidates<L>*>(mine + scratch_bytes)[sub];
   const int E = a.E, K = a.K;
   const bool biased = a.sigmoid && (a.bias != nullptr || a.groups > 1);
   pdl_wait();
@@ -297,8 +352,8 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   const bool token = t < a.T, active = token && (a.mask == nullptr || a.mask[t]);
   const E_* row = logits + (active ? t : 0) * E;
   float v[V];
-  const float check = load_logits<VEC, LPT>(row, E, ll, active, v);
-  if (__any_sync(0xffffffffu, !(check == 0.f) || !active)) {
+  load_logits<VEC, LPT>(row, E, ll, active, v);
+  if (__any_sync(0xffffffffu, !(check_finite(v) == 0.f) || !active)) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -310,28 +365,35 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   close_past<VEC, LPT>(E, ll, v);
 
   // softmax over all experts: its divisor
-  float inv_all = 1.f, most = 0.f;
-  if (!a.sigmoid) {
-    most = v[0];
+  float all = 0.f;
+  if (!a.sigmoid && !a.renormalize) {
+    float most = v[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
     most = part_max<LPT>(most);
-    if (!a.renormalize) {
-      float all = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? __expf(v[i] - most) : 0.f;
-      all = part_sum<LPT>(all);
-      inv_all = 1.f / all;  // not used where all is 0
-    }
+    for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? __expf(v[i] - most) : 0.f;
+    all = part_sum<LPT>(all);
   }
   if (biased) {
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
       const int e = (ll + LPT * j) * VEC;
+      float b[VEC] = {};
+      if (a.bias != nullptr && e < E) {
+        if constexpr (VEC == 1) {
+          b[0] = __ldg(a.bias + e);
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 4) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(a.bias + e + i));
+            b[i] = q.x; b[i + 1] = q.y; b[i + 2] = q.z; b[i + 3] = q.w;
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float b = a.bias != nullptr && e < E ? __ldg(a.bias + e + i) : 0.f;
-        const float c = quick_sigmoid(v[j * VEC + i]) + b;
+        const float c = quick_sigmoid(v[j * VEC + i]) + b[i];
         v[j * VEC + i] = v[j * VEC + i] > -CUDART_INF_F && c < CUDART_INF_F ? c : -CUDART_INF_F;
       }
     }
@@ -368,12 +430,24 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
       const float o = __shfl_sync(0xffffffffu, score, g, LPT);
       before += o > score || (o == score && g < ll);
     }
-    const bool in = ll < a.groups && before < a.best;
+    bool in = ll < a.groups && before < a.best;
     if (a.sigmoid) {  // two sums of two scores: twice as much as two scores may differ, and the sums' roundings
       const float least = -part_max<LPT>(in && score > -CUDART_INF_F ? -score : -CUDART_INF_F);
       const float out = part_max<LPT>(!in ? score : -CUDART_INF_F);
       const float apart = 2.f * near_score(part_max<LPT>(size));
-      slow = out > -CUDART_INF_F && least - out <= apart;
+      const bool close = out > -CUDART_INF_F && least - out <= apart;
+      if (__any_sync(0xffffffffu, close)) {
+        bool third = false;
+        const long long sum = close && ll < a.groups ? exact_group(a, row, ll, third) : kLowest;
+        before = 0;
+#pragma unroll 1
+        for (int g = 0; g < a.groups; ++g) {
+          const long long o = __shfl_sync(0xffffffffu, sum, g, LPT);
+          before += o > sum || (o == sum && g < ll);
+        }
+        if (close) in = ll < a.groups && before < a.best;
+        slow = (__ballot_sync(0xffffffffu, third) & team) != 0;
+      }
     }
     const uint32_t chosen = (__ballot_sync(0xffffffffu, in) & team) >> (sub * LPT);
 #pragma unroll
@@ -393,17 +467,20 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   }
   sort_desc<NB>(list);
   merge_lists<NB, L, LPT, 1>(list);
+  const float most = list[0];
   float bound = list[0];
 #pragma unroll
   for (int i = 1; i < L; ++i)
     if (i == K - 1) bound = list[i];
   if (biased) bound -= near_score(bound);
   bound = fmaxf(bound, -FLT_MAX);
+  if (bound == 0.f) bound = -0.f;  // from which both zeros differ by +0
 
-  // the candidates
-  uint32_t hit = 0;
+  // the candidates: bit 31 - i of `hit` is logit i's, from the sign of a difference
+  uint32_t hit = 0xffffffffu;
 #pragma unroll
-  for (int i = 0; i < V; ++i) hit |= v[i] >= bound ? 1u << i : 0u;
+  for (int i = 0; i < V; ++i) hit = __funnelshift_l(__float_as_uint(v[i] - bound), hit, 1);
+  hit = ~hit << (32 - V);
   int at = __popc(hit);
   const int own = at;
 #pragma unroll
@@ -413,68 +490,94 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   }
   const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
   at -= own;
-  slow |= n > 2 * L;
-  while (hit != 0 && at < 2 * L) {
-    const int i = __ffs(hit) - 1;
-    hit &= hit - 1;
+  slow |= n > CAP;
+  while (hit != 0 && at < CAP) {
+    const int i = __clz(hit);
+    hit &= ~(0x80000000u >> i);
     cand.id[at++] = (ll + LPT * (i / VEC)) * VEC + i % VEC;
   }
+  int longest = n;  // of the warp's tokens
+#pragma unroll
+  for (int o = LPT; o < 32; o <<= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  longest = min(longest, CAP);
   __syncwarp();
-  int id[CPL];
+  int id[CPL], rank[CPL];
   float key[CPL], logit[CPL];
 #pragma unroll
   for (int c = 0; c < CPL; ++c) {
-    const int i = ll + c * LPT;
     id[c] = -1;
+    rank[c] = K;
     key[c] = logit[c] = -CUDART_INF_F;
-    if (i < n && i < 2 * L) {
+    const int i = ll + c * LPT;
+    if (c * LPT >= round_up4(longest)) continue;
+    if (i < n) {
       id[c] = cand.id[i];
       key[c] = logit[c] = finite_logit(row + id[c]);
       if (biased) key[c] = quick_sigmoid(logit[c]) + (a.bias != nullptr ? __ldg(a.bias + id[c]) : 0.f);
     }
-    if (i < 2 * L) cand.key[i] = key[c];
+    if (i < CAP) cand.key[i] = key[c];
   }
   __syncwarp();
   // ranks: those surely above, and whether any other is as near as not to tell
-  int rank[CPL];
   bool near = false;
 #pragma unroll
   for (int c = 0; c < CPL; ++c) {
-    const float d = biased ? near_score(key[c]) : 0.f;
-    const float hi = key[c] + d, lo = key[c] - d;
+    if (c * LPT >= longest) continue;
     float above = 0.f, about = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2 * L; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(&cand.key[i]);
-      above += (q.x > hi ? 1.f : 0.f) + (q.y > hi ? 1.f : 0.f) + (q.z > hi ? 1.f : 0.f) + (q.w > hi ? 1.f : 0.f);
-      about += (q.x >= lo ? 1.f : 0.f) + (q.y >= lo ? 1.f : 0.f) + (q.z >= lo ? 1.f : 0.f) + (q.w >= lo ? 1.f : 0.f);
+    if (biased) {
+      const float d = near_score(key[c]), hi = key[c] + d, lo = key[c] - d;
+      for (int i = 0; i < longest; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&cand.key[i]);
+        above += (q.x > hi ? 1.f : 0.f) + (q.y > hi ? 1.f : 0.f) + (q.z > hi ? 1.f : 0.f) + (q.w > hi ? 1.f : 0.f);
+        about += (q.x >= lo ? 1.f : 0.f) + (q.y >= lo ? 1.f : 0.f) + (q.z >= lo ? 1.f : 0.f) + (q.w >= lo ? 1.f : 0.f);
+      }
+    } else {
+      for (int i = 0; i < longest; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&cand.key[i]);
+        above += (q.x > key[c] ? 1.f : 0.f) + (q.y > key[c] ? 1.f : 0.f) + (q.z > key[c] ? 1.f : 0.f) + (q.w > key[c] ? 1.f : 0.f);
+      }
     }
-    rank[c] = id[c] >= 0 ? (int)above : K;
-    near |= rank[c] < K && about - above != 1.f;
+    if (id[c] >= 0) rank[c] = (int)above;
+    near |= biased && rank[c] < K && about - above != 1.f;
+  }
+  if (!biased) {
+    // equal logits have one rank, the lowest, so that there are more of them in the
+    // first K or their sum is less
+    const int m = min(n, K);
+    int ranks = 0;  // sum, and 2^16 for each
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) ranks += rank[c] < K ? 65536 + rank[c] : 0;
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) ranks += __shfl_xor_sync(0xffffffffu, ranks, o);
+    near = ranks != 65536 * m + m * (m - 1) / 2;
   }
   const uint32_t unsure = __ballot_sync(0xffffffffu, near);
   if (unsure != 0) {
+    const bool again = (unsure & team) != 0;
+    const int m = again ? min(n, CAP) : 0;
     if (biased) {
-#pragma unroll
-      for (int c = 0; c < CPL; ++c)
-        if ((unsure & team) && id[c] >= 0)
-          cand.exact[ll + c * LPT] = ordered(exact_score(logit[c], a.bias, id[c]));
+#pragma unroll 1
+      for (int i = ll; i < m; i += LPT)
+        exact.key[i] = ordered(exact_score(finite_logit(row + cand.id[i]), a.bias, cand.id[i]));
       __syncwarp();
     }
-    if (unsure & team) {
-      const int m = min(n, 2 * L);
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        if (id[c] < 0) continue;
-        const long long k64 = biased ? cand.exact[ll + c * LPT] : 0;
-        rank[c] = 0;
-        for (int i = 0; i < m; ++i) {
-          const bool above = biased ? cand.exact[i] > k64 : cand.key[i] > key[c];
-          const bool same = biased ? cand.exact[i] == k64 : cand.key[i] == key[c];
-          rank[c] += above || (same && cand.id[i] < id[c]);
-        }
+#pragma unroll 1
+    for (int i = ll; i < m; i += LPT) {
+      const long long k64 = biased ? exact.key[i] : 0;
+      const float k32 = cand.key[i];
+      const int e = cand.id[i];
+      int r = 0;
+#pragma unroll 1
+      for (int o = 0; o < m; ++o) {
+        const bool above = biased ? exact.key[o] > k64 : cand.key[o] > k32;
+        const bool same = biased ? exact.key[o] == k64 : cand.key[o] == k32;
+        r += above || (same && cand.id[o] < e);
       }
+      exact.rank[i] = r;
     }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c)
+      if (again && id[c] >= 0) rank[c] = exact.rank[ll + c * LPT];  // written by this lane
   }
 
   // weights
@@ -483,22 +586,19 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   for (int c = 0; c < CPL; ++c) {
     s[c] = 0.f;
     if (id[c] >= 0 && rank[c] < K) {
-      s[c] = a.sigmoid ? sigmoid_f(logit[c]) : expf(logit[c] - most) * inv_all;
+      s[c] = a.sigmoid ? sigmoid_f(logit[c]) : __expf(logit[c] - most);
       total += s[c];
     }
   }
-  if (a.renormalize) {
-    total = part_sum<LPT>(total);
-    total = total > 0.f ? 1.f / total : 0.f;
-  } else {
-    total = 1.f;
-  }
+  if (a.renormalize) total = part_sum<LPT>(total);
+  else total = a.sigmoid ? 1.f : all;
+  const float factor = total > 0.f ? a.scale / total : 0.f;
   if (token && !slow) {
 #pragma unroll
     for (int c = 0; c < CPL; ++c)
       if (id[c] >= 0 && rank[c] < K) {
         a.ids[t * K + rank[c]] = id[c];
-        a.weights[t * K + rank[c]] = s[c] * total * a.scale;
+        a.weights[t * K + rank[c]] = s[c] * factor;
       }
     for (int k = n + ll; k < K; k += LPT) {
       a.ids[t * K + k] = -1;
@@ -518,8 +618,8 @@ template <typename E_, int VEC, int LPT, int V, int L>
 int launch_fast(const E_* logits, const RouteArgs& a, cudaStream_t stream) {
   constexpr int TPW = 32 / LPT, WARPS = kFastThreads / 32;
   auto kernel = route_fast_kernel<E_, VEC, LPT, V, L>;
-  const int64_t scratch = fast_scratch(a.E, a.groups, VEC, TPW);
-  const size_t smem = WARPS * (size_t)(scratch + TPW * sizeof(Candidates<LPT, L>));
+  const int64_t scratch = fast_scratch<L>(a.E, a.groups, VEC, TPW);
+  const size_t smem = WARPS * (size_t)(scratch + TPW * sizeof(Candidates<L>));  // below 40 KB
   return launched(launch_pdl(kernel, dim3((unsigned)ceil_div(a.T, WARPS * TPW)), dim3(kFastThreads), smem, stream, logits, a,
                              (int)scratch));
 }
@@ -538,7 +638,7 @@ int run_route(const void* logits, const RouteArgs& a, cudaStream_t stream) {
   const int lpt = a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32;
   if (a.E <= kPartExperts && a.K <= kFastTopk && a.groups <= lpt) {
     constexpr int VEC = 16 / sizeof(E_);
-    const bool whole = a.E % VEC == 0 && a.E / a.groups % VEC == 0 && aligned_to(logits, 16);
+    const bool whole = a.E % VEC == 0 && a.E / a.groups % VEC == 0 && aligned_to(logits, 16) && aligned_to(a.bias, 16);
     if (whole) return a.K <= 8 ? launch_fast_for<E_, VEC, 8>(l, a, stream) : launch_fast_for<E_, VEC, 16>(l, a, stream);
     return a.K <= 8 ? launch_fast_for<E_, 1, 8>(l, a, stream) : launch_fast_for<E_, 1, 16>(l, a, stream);
   }
