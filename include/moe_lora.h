@@ -624,7 +624,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  * moe_rms_norm_backward: with m = 1 / sqrt(mean(r^2) + eps) and h = dy weight
  *   dx = m (h - r m^2 mean(h r)) + d_r, the gradient of both x and residual (d_r: what
  *   reaches r otherwise, null for none), and d_weight[c] = sum over rows of dy r m,
- *   float32.  dx may be dy or d_r.  workspace of moe_rms_norm_backward_workspace_bytes.
+ *   float32.  dx may be dy or d_r.  workspace of moe_rms_norm_backward_workspace_bytes,
+ *   256-byte aligned.
  * Sums are held in fp32 in a fixed order: results are bit-identical between runs.
  * Limit: hidden <= 16384.
  *
@@ -645,6 +646,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   are not masked, c_e their pairs of expert e and p = softmax(logits), or
  *   sigmoid(logits) over their sum.  counts int32 [num_experts + 1]: c, then N.  Ids
  *   other than -1 outside [0, num_experts) set MLR_STATUS_INDEX; neither counts.
+ *   workspace of moe_balance_loss_workspace_bytes, 256-byte aligned; null is taken where
+ *   that is 1 (up to 2^19 logits of at most 256 experts, taken in one launch).
  * moe_route_backward: d_logits of type `dtype` from d_weights [num_tokens, topk]
  *   (nullable) and, given counts and d_loss[1] (both or neither), from the balance loss;
  *   zeros in masked tokens.  The same id twice in a token: both gradients are added.

@@ -96,12 +96,24 @@ __device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active
   return active && sum > 0.f ? 1.f / sum : 0.f;
 }
 
-// Sums of shares and pairs per expert over the block's tokens: part [blocks][E]
-// and count [blocks][E + 1] (the last one: tokens).
-template <int VEC, int LPT, int V, typename E_>
+// The loss of v = sum over experts of shares times pairs.
+__device__ __forceinline__ float loss_of(double v, int tokens, int E, int K) {
+  const double n = tokens > 0 ? tokens : 1;
+  return (float)(v * E / (K * n * n));
+}
+
+constexpr int kLossCluster = 8;
+// Up to this many logits one cluster of eight blocks takes the whole batch, which saves
+// the workspace and the second launch.
+constexpr int64_t kOneClusterLogits = 1 << 19;
+
+// Sums of shares and pairs per expert over the block's tokens.  ONE: the grid is one
+// cluster, which adds them over distributed shared memory and writes counts and loss;
+// else part [blocks][E] and count [blocks][E + 1] (the last one: tokens).
+template <int VEC, int LPT, int V, bool ONE, typename E_>
 __global__ void __launch_bounds__(kBalanceThreads, V <= 16 && !kBlockTokens<LPT> ? 4 : 2)
 balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
-               int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, int32_t* status) {
+               int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, float* __restrict__ loss, int32_t* status) {
   extern __shared__ uint4 ring[];  // the ring; then [E + 1] pairs; then float [warps (1 for a block's token)][E] shares
   __shared__ float red[kBalanceThreads / 32];
   constexpr int TEAMS = kTeams<LPT>, ROWS = kBlockTokens<LPT> ? 1 : kBalanceThreads / 32;
@@ -160,12 +172,44 @@ balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, c
     }
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
-    count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+    if (!ONE) count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
     if (e == E) continue;
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) v += sums[i * E + e];
-    part[(int64_t)blockIdx.x * E + e] = v;
+    if (ONE) sums[e] = v;  // read above by this thread alone
+    else part[(int64_t)blockIdx.x * E + e] = v;
+  }
+  if constexpr (ONE) {
+    namespace cg = cooperative_groups;
+    __shared__ double total;
+    const cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    double mine = 0.0;
+    for (int e = blockIdx.x * 32 + threadIdx.x; threadIdx.x < 32 && e <= E; e += kLossCluster * 32) {
+      int c = 0;
+      float v = 0.f;
+#pragma unroll
+      for (int b = 0; b < kLossCluster; ++b) {
+        c += cluster.map_shared_rank(hist, b)[e];
+        if (e < E) v += cluster.map_shared_rank(sums, b)[e];
+      }
+      count[e] = c;
+      if (e < E) mine += (double)v * c;
+    }
+    if (threadIdx.x < 32) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      if (threadIdx.x == 0) total = mine;
+    }
+    cluster.sync();
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      int n = 0;
+      for (int b = 0; b < kLossCluster; ++b) n += cluster.map_shared_rank(hist, b)[E];
+      for (int b = 1; b < kLossCluster; ++b) mine += *cluster.map_shared_rank(&total, b);
+      *loss = loss_of(mine, n, E, K);
+    }
+    cluster.sync();  // the blocks' shared memory is read until here
   }
 }
 
@@ -222,8 +266,7 @@ balance_total_kernel(const float* __restrict__ part, const int32_t* __restrict__
     double v = 0.0;
     for (int i = 0; i < kTotalCluster; ++i) v += *cluster.map_shared_rank(&total, i);
     const int n = *cluster.map_shared_rank(&tokens, E / 32 % kTotalCluster);
-    const double d = n > 0 ? n : 1;
-    *loss = (float)(v * E / (K * d * d));
+    *loss = loss_of(v, n, E, K);
   }
   cluster.sync();  // the blocks' shared memory is read until here
 }
@@ -426,16 +469,47 @@ int64_t balance_blocks(int32_t T, int32_t E) {
   return want < 1 ? 1 : want < most ? want : most;
 }
 
+bool one_cluster(int32_t T, int32_t E) { return E <= 256 && (int64_t)T * E <= kOneClusterLogits; }
+
 template <int VEC, typename E_>
 int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int T, int E, int K, bool sigmoid, float* part,
-                int32_t* count, int32_t* status, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)balance_blocks(T, E);
+                int32_t* count, float* loss, int32_t* counts, int32_t* status, cudaStream_t stream) {
+  const E_* l = static_cast<const E_*>(logits);
   return by_experts(E, [&](auto lpt, auto v) {
     constexpr int ring = kRingBytes<VEC, lpt.value, v.value>;
     constexpr int rows = kBlockTokens<lpt.value> ? 1 : kBalanceThreads / 32, cover = lpt.value * v.value;
     auto bytes = [&](int experts) { return (size_t)ring + (experts + 1) * 4 + (size_t)rows * experts * 4; };
-    return launch_with_smem(balance_kernel<VEC, lpt.value, v.value, E_>, dim3(blocks), dim3(kBalanceThreads), bytes(E), (int)bytes(cover), stream,
-                       static_cast<const E_*>(logits), ids, mask, T, E, K, sigmoid, part, count, status);
+    if constexpr (lpt.value == 8) {
+      if (one_cluster(T, E)) {
+        auto kernel = balance_kernel<VEC, lpt.value, v.value, true, E_>;
+        const size_t smem = bytes(E);
+        cudaError_t err = cudaSuccess;
+        if (smem > 46 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(cover));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kLossCluster);
+        cfg.blockDim = dim3(kBalanceThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kLossCluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        if (err == cudaSuccess)
+          err = cudaLaunchKernelEx(&cfg, kernel, l, ids, mask, T, E, K, sigmoid, (float*)nullptr, counts, loss, status);
+        return launched(err);
+      }
+    }
+    const int blocks = (int)balance_blocks(T, E);
+    const int c = launch_with_smem(balance_kernel<VEC, lpt.value, v.value, false, E_>, dim3(blocks), dim3(kBalanceThreads),
+                                   bytes(E), (int)bytes(cover), stream, l, ids, mask, T, E, K, sigmoid, part, count,
+                                   (float*)nullptr, status);
+    if (c != MLR_OK) return c;
+    return launched(launch_pdl(balance_total_kernel, dim3(kTotalCluster), dim3(kTotalThreads), 0, stream, (const float*)part,
+                               (const int32_t*)count, blocks, E, K, loss, counts));
   });
 }
 
@@ -467,6 +541,7 @@ int by_type(int dtype, int E, const void* logits, const void* d_logits, F f) {
 extern "C" size_t moe_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts) {
   using namespace mlr;
   if (num_tokens < 0 || num_experts < 1 || num_experts > kMaxRouteExperts) return 0;
+  if (one_cluster(num_tokens, num_experts)) return 1;  // nothing is kept
   return (size_t)balance_blocks(num_tokens, num_experts) * (2 * num_experts + 1) * 4;
 }
 
@@ -478,18 +553,16 @@ extern "C" int moe_balance_loss(const void* logits, const int32_t* topk_ids, con
   const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
   if (code != MLR_OK) return code;
   if (loss == nullptr || counts == nullptr || (num_tokens > 0 && topk_ids == nullptr)) return MLR_ERR_INVALID;
-  if (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)) return MLR_ERR_CAPACITY;
+  if (!(one_cluster(num_tokens, num_experts) && workspace == nullptr) &&
+      (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)))
+    return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
-  const int blocks = (int)balance_blocks(num_tokens, num_experts);
   float* part = static_cast<float*>(workspace);
-  int32_t* count = reinterpret_cast<int32_t*>(part + (int64_t)blocks * num_experts);
-  const int c = by_type(dtype, num_experts, logits, nullptr, [&](auto vec, auto e) {
+  int32_t* count = reinterpret_cast<int32_t*>(part + (part ? balance_blocks(num_tokens, num_experts) * num_experts : 0));
+  return by_type(dtype, num_experts, logits, nullptr, [&](auto vec, auto e) {
     return run_balance<vec.value, decltype(e)>(logits, topk_ids, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
-                                               part, count, d_status, stream);
+                                               part, count, loss, counts, d_status, stream);
   });
-  if (c != MLR_OK) return c;
-  return launched(launch_pdl(balance_total_kernel, dim3(kTotalCluster), dim3(kTotalThreads), 0, stream, (const float*)part,
-                             (const int32_t*)count, blocks, (int)num_experts, (int)topk, loss, counts));
 }
 
 extern "C" int moe_route_backward(const void* logits, const int32_t* topk_ids, const float* d_weights, const int32_t* counts,

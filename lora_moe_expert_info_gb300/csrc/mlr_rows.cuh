@@ -37,6 +37,64 @@ __device__ __forceinline__ void row_narrow(const float (&v)[8], uint4& q) {
   q = make_uint4(row_narrow2(v[0], v[1]), row_narrow2(v[2], v[3]), row_narrow2(v[4], v[5]), row_narrow2(v[6], v[7]));
 }
 
+// Elementwise fp32 operations on the values of a vector, two to an instruction; each is
+// rounded as the single operation is.
+template <int N>
+__device__ __forceinline__ void row_add(float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) a[0] += b[0];
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 s = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      a[i] = s.x;
+      a[i + 1] = s.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void row_mul(float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) a[0] *= b[0];
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 s = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+      a[i] = s.x;
+      a[i + 1] = s.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ void row_scale(float (&a)[N], float b) {
+  if constexpr (N == 1) a[0] *= b;
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 s = __fmul2_rn(make_float2(a[i], a[i + 1]), make_float2(b, b));
+      a[i] = s.x;
+      a[i + 1] = s.y;
+    }
+}
+// c[i] + a[i] b[i], and the sum over i of a[i] b[i] (two chains).
+template <int N>
+__device__ __forceinline__ void row_fma(const float (&a)[N], const float (&b)[N], float (&c)[N]) {
+  if constexpr (N == 1) c[0] = fmaf(a[0], b[0], c[0]);
+  else
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 s = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+      c[i] = s.x;
+      c[i + 1] = s.y;
+    }
+}
+template <int N>
+__device__ __forceinline__ float row_dot(const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) return a[0] * b[0];
+  else {
+    float2 s = __fmul2_rn(make_float2(a[0], a[1]), make_float2(b[0], b[1]));
+#pragma unroll
+    for (int i = 2; i < N; i += 2) s = __ffma2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), s);
+    return s.x + s.y;
+  }
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);

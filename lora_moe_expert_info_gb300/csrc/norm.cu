@@ -49,26 +49,34 @@ __device__ __forceinline__ void narrow_unit(const float (&v)[4], uint4& q) { row
 __device__ __forceinline__ void narrow_unit(const float (&v)[1], uint16_t& q) { row_narrow(v[0], q); }
 __device__ __forceinline__ void narrow_unit(const float (&v)[1], float& q) { q = v[0]; }
 
-// The weight's columns c to c + VEC - 1.  bf16 or float32, whatever the rows' type.
-template <int VEC>
-__device__ __forceinline__ void load_weight(const void* w, bool w32, int c, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = w32 ? __ldg(static_cast<const float*>(w) + c) : row_widen(__ldg(static_cast<const uint16_t*>(w) + c));
-  } else if (w32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + c);
+// VEC columns of the weight (bf16 or float32, whatever the rows' type) as they lie in
+// memory, so that they take few registers while a row's sum is found.
+template <typename W_, int VEC>
+struct WeightUnit {
+  uint32_t w[VEC * sizeof(W_) / 4];
+  __device__ __forceinline__ void load(const W_* p) {
+    if constexpr (VEC * sizeof(W_) == 8) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = q.x; w[1] = q.y;
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC / 4; ++i) {
-      const float4 q = __ldg(p + i);
-      v[4 * i] = q.x; v[4 * i + 1] = q.y; v[4 * i + 2] = q.z; v[4 * i + 3] = q.w;
+      for (int i = 0; i < (int)(VEC * sizeof(W_) / 16); ++i) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = q.x; w[4 * i + 1] = q.y; w[4 * i + 2] = q.z; w[4 * i + 3] = q.w;
+      }
     }
-  } else if constexpr (VEC == 8) {
-    row_widen(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + c)), v);
-  } else {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + c));
-    v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
-    v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
   }
-}
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(W_) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+  }
+};
+template <typename W_>
+struct WeightUnit<W_, 1> {
+  W_ w;
+  __device__ __forceinline__ void load(const W_* p) { w = __ldg(p); }
+  __device__ __forceinline__ float at(int) const { return row_widen(w); }
+};
 
 // The exponent s of a group from the fp32 bits of its largest magnitude: the
 // smallest integer with amax 2^-s <= 448 = 1.75 2^8, not below -127; 0 for zeros.
@@ -92,12 +100,40 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int lpt, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-template <typename E_, int VEC, int NV, bool QUANT, int MOST>
-__global__ void __launch_bounds__(MOST, (NV <= (VEC == 1 ? 8 : 4) ? 1024 : 512) / MOST)
-norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w32, int T, int H, int lpt, float eps,
-            E_* y, E_* r_out, uint8_t* codes, uint8_t* exps) {
+// 1 / sqrt(mean + eps) of a row, from its threads' sums of squares.  The rounding errors
+// of threads and warps average out over a row; what is left of fp32's errors from there
+// on would move values over rounding borders of bf16 or of the 8 bits, so the last sums,
+// the quotient and the root carry their remainders and the result is rounded once.
+// `red`: a float per warp of the block; every thread of the block calls it.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  const float s = a.x + b.x, t = s - a.x;
+  return make_float2(s, (a.x - (s - t)) + (b.x - t) + a.y + b.y);
+}
+__device__ __forceinline__ float row_inverse_rms(float sum, int H, float eps, int lpt, float* red) {
+  float2 s = make_float2(warp_sum(sum), 0.f);
+  if (lpt > 32) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wpr = lpt >> 5;
+    if (lane == 0) red[warp] = s.x;
+    __syncthreads();
+    s.x = lane < wpr ? red[warp / wpr * wpr + lane] : 0.f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)  // of at most 16 warps
+      s = add2(s, make_float2(__shfl_xor_sync(0xffffffffu, s.x, o), __shfl_xor_sync(0xffffffffu, s.y, o)));
+    s = make_float2(__shfl_sync(0xffffffffu, s.x, 0), __shfl_sync(0xffffffffu, s.y, 0));
+  }
+  const float h = (float)H, q = s.x / h;
+  const float2 v = add2(make_float2(q, (fmaf(-q, h, s.x) + s.y) / h), make_float2(eps, 0.f));
+  const float m = 1.f / sqrtf(v.x), p = m * m;
+  // one step of Newton's, from the exact square of m; none for infinities, NaN and 1 / 0
+  const float left = fmaf(-v.y, p, fmaf(-v.x, fmaf(m, m, -p), fmaf(-v.x, p, 1.f)));
+  return fabsf(left) < 1e-3f ? fmaf(0.5f * m, left, m) : m;
+}
+
+template <typename E_, typename W_, int VEC, int NV, bool QUANT, int MOST>
+__global__ void __launch_bounds__(MOST, (NV <= (VEC == 1 ? 8 : 4) ? 1024 : VEC == 8 && QUANT ? 640 : 512) / MOST)
+norm_kernel(const E_* x, const E_* residual, const W_* __restrict__ w, int T, int H, int lpt, float eps, E_* y, E_* r_out, uint8_t* codes, uint8_t* exps) {
   using U = typename Unit<E_, VEC>::T;
-  __shared__ float2 red[32];
+  __shared__ float red[16];
   const int sub = threadIdx.x / lpt, lt = threadIdx.x - sub * lpt;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x / lpt) + sub;
   const bool in = row < T;
@@ -106,7 +142,7 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
   pdl_trigger();
   constexpr bool kEarly = NV * VEC <= 32;  // the weight's columns are loaded before the sum is known
   U r[NV];
-  float wv[kEarly ? NV : 1][VEC];
+  WeightUnit<W_, VEC> wu[kEarly ? NV : 1];
   float sum = 0.f;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -125,8 +161,7 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
       float a[VEC], b[VEC];
       widen_unit(r[j], a);
       widen_unit(q[j], b);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) a[i] += b[i];
+      row_add(a, b);
       narrow_unit(a, r[j]);
       const int c = unit_col<VEC>(lt, j, lpt);
       if (in && c < H) *reinterpret_cast<U*>(r_out + at + c) = r[j];
@@ -137,21 +172,25 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
     const int c = unit_col<VEC>(lt, j, lpt);
     float a[VEC];
     widen_unit(r[j], a);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) sum = fmaf(a[i], a[i], sum);
-    if (kEarly && c < H) load_weight<VEC>(w, w32, c, wv[kEarly ? j : 0]);
+    sum += row_dot(a, a);
+    if (kEarly && c < H) wu[kEarly ? j : 0].load(w + c);
   }
-  const float m = 1.f / sqrtf(row_sum2(sum, 0.f, lpt, red).x / (float)H + eps);
+  const float m = row_inverse_rms(sum, H, eps, lpt, red);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
     float a[VEC];
-    float(&wj)[VEC] = wv[kEarly ? j : 0];
-    if (!kEarly && c < H) load_weight<VEC>(w, w32, c, wj);
-    widen_unit(r[j], a);
+    WeightUnit<W_, VEC>& wj = wu[kEarly ? j : 0];
+    if (!kEarly && c < H) wj.load(w + c);
+    if (c < H) {
+      float wf[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) a[i] = c < H ? a[i] * wj[i] * m : 0.f;  // bf16: r w is exact
-    narrow_unit(a, r[j]);
+      for (int i = 0; i < VEC; ++i) wf[i] = wj.at(i);
+      widen_unit(r[j], a);
+      row_mul(a, wf);  // exact for bf16 rows and weight
+      row_scale(a, m);
+      narrow_unit(a, r[j]);
+    }
     if (in && c < H && y != nullptr) *reinterpret_cast<U*>(y + at + c) = r[j];
   }
   if constexpr (QUANT) {
@@ -163,22 +202,29 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
       float a[UPG][VEC];
       uint32_t most = 0;
 #pragma unroll
-      for (int u = 0; u < UPG; ++u) {
-        widen_unit(r[j + u], a[u]);
+      for (int u = 0; u < UPG; ++u) widen_unit(r[j + u], a[u]);
+      if constexpr (VEC == 8) {  // magnitudes of bf16 are ordered as their bits: two at a time
+        most = __vmaxu2(__vmaxu2(r[j].x & 0x7fff7fffu, r[j].y & 0x7fff7fffu), __vmaxu2(r[j].z & 0x7fff7fffu, r[j].w & 0x7fff7fffu));
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) most = max(most, __float_as_uint(a[u][i]) & 0x7fffffffu);
+        for (int o = LANES / 2; o > 0; o >>= 1) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, o));
+        most = max(most & 0xffff0000u, most << 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < UPG; ++u)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) most = max(most, __float_as_uint(a[u][i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
       }
-#pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
       const int s = group_exp(most);
-      const float up = exp2_neg(s);
       const int c = unit_col<VEC>(lt, j, lpt);
+#pragma unroll
+      for (int u = 0; u < UPG; ++u) row_scale(a[u], exp2_neg(s));
       if constexpr (VEC > 1) {
         uint32_t q[VEC / 4];
 #pragma unroll
         for (int i = 0; i < VEC / 4; ++i)
-          q[i] = f32x2_to_e4m3x2(a[0][4 * i] * up, a[0][4 * i + 1] * up) |
-                 (f32x2_to_e4m3x2(a[0][4 * i + 2] * up, a[0][4 * i + 3] * up) << 16);
+          q[i] = f32x2_to_e4m3x2(a[0][4 * i], a[0][4 * i + 1]) | (f32x2_to_e4m3x2(a[0][4 * i + 2], a[0][4 * i + 3]) << 16);
         if (in && c < H) {
           if constexpr (VEC == 8) *reinterpret_cast<uint2*>(codes + at + c) = make_uint2(q[0], q[1]);
           else *reinterpret_cast<uint32_t*>(codes + at + c) = q[0];
@@ -186,7 +232,7 @@ norm_kernel(const E_* x, const E_* residual, const void* __restrict__ w, bool w3
       } else {
 #pragma unroll
         for (int u = 0; u < UPG; ++u)
-          if (in && c + 32 * u < H) codes[at + c + 32 * u] = (uint8_t)f32x2_to_e4m3x2(a[u][0] * up, 0.f);
+          if (in && c + 32 * u < H) codes[at + c + 32 * u] = (uint8_t)f32x2_to_e4m3x2(a[u][0], 0.f);
       }
       if (in && c < H && (lt & (LANES - 1)) == 0) exps[row * groups + c / kGroupCols] = (uint8_t)(s + 127);
     }
@@ -204,11 +250,9 @@ __device__ __forceinline__ void row_terms(const U& ru, const U& gu, const float 
   float a[VEC], g[VEC];
   widen_unit(ru, a);
   widen_unit(gu, g);
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    ss = fmaf(a[i], a[i], ss);
-    hr = fmaf(g[i] * w[i], a[i], hr);
-  }
+  ss += row_dot(a, a);
+  row_mul(g, w);
+  hr += row_dot(g, a);
 }
 template <typename E_, int VEC, typename U>
 __device__ __forceinline__ U row_gradient(const U& ru, const U& gu, const U& eu, bool add, const float (&w)[VEC], float m,
@@ -217,15 +261,18 @@ __device__ __forceinline__ U row_gradient(const U& ru, const U& gu, const U& eu,
   widen_unit(ru, a);
   widen_unit(gu, g);
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    acc[i] = fmaf(g[i], a[i] * m, acc[i]);
-    d[i] = m * (g[i] * w[i] - a[i] * k);
-  }
+  for (int i = 0; i < VEC; ++i) d[i] = a[i];
+  row_scale(d, m);
+  row_fma(g, d, acc);
+  // m g w - m^3 mean(h r) r, with k = -m^2 mean(h r)
+  row_scale(d, k);
+  row_mul(g, w);
+  row_scale(g, m);
+  row_add(d, g);
   if (add) {
     float e[VEC];
     widen_unit(eu, e);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) d[i] += e[i];
+    row_add(d, e);
   }
   U o;
   narrow_unit(d, o);
@@ -239,10 +286,10 @@ __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
 // Rows on the 16-byte grid: every thread copies its own units of the next rows to
 // shared memory (DEPTH rows in flight with the one in work, about 190 KB per SM), so
 // that neither a barrier nor the sums wait for HBM.
-template <typename E_, int NV, int DEPTH, int MOST, int PER_SM>
+template <typename E_, typename W_, int NV, int DEPTH, int MOST, int PER_SM>
 __global__ void __launch_bounds__(MOST, PER_SM)
-norm_backward_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool w32, const E_* d_r, int T, int H, int lpt,
-                     float eps, E_* dx, float* __restrict__ part) {
+norm_backward_kernel(const E_* dy, const E_* r, const W_* __restrict__ w, const E_* d_r, int T, int H, int lpt, float eps,
+                     E_* dx, float* __restrict__ part) {
   constexpr int VEC = 16 / sizeof(E_);
   extern __shared__ uint4 ring[];  // [DEPTH][3][NV][threads]
   __shared__ float2 red[2][32];
@@ -276,7 +323,12 @@ norm_backward_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
-    if (c < H) load_weight<VEC>(w, w32, c, wv[j]);
+    WeightUnit<W_, VEC> u;
+    if (c < H) {
+      u.load(w + c);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) wv[j][i] = u.at(i);
+    }
   }
   int stage = 0, turn = 0;
   for (int64_t base = (int64_t)blockIdx.x * rpb; base < T; base += step, turn ^= 1) {
@@ -288,7 +340,7 @@ norm_backward_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool
     for (int j = 0; j < NV; ++j) row_terms<E_, VEC>(*slot(stage, 0, j), *slot(stage, 1, j), wv[j], ss, hr);
     const float2 s = row_sum2(ss, hr, lpt, red[turn]);
     const float m = 1.f / sqrtf(s.x / (float)H + eps);
-    const float k = m * m * (s.y / (float)H);
+    const float k = -m * m * (s.y / (float)H);
     if (row < T) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -330,10 +382,17 @@ norm_backward_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool
 }
 
 // Other rows, and those too long for the ring.
-template <typename E_, int VEC, int NV, int MOST>
+template <typename W_, int VEC>
+__device__ __forceinline__ void load_weight(const W_* w, int c, float (&v)[VEC]) {
+  WeightUnit<W_, VEC> u;
+  u.load(w + c);
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) v[i] = u.at(i);
+}
+template <typename E_, typename W_, int VEC, int NV, int MOST>
 __global__ void __launch_bounds__(MOST)
-norm_backward_plain_kernel(const E_* dy, const E_* r, const void* __restrict__ w, bool w32, const E_* d_r, int T, int H,
-                           int lpt, float eps, E_* dx, float* __restrict__ part) {
+norm_backward_plain_kernel(const E_* dy, const E_* r, const W_* __restrict__ w, const E_* d_r, int T, int H, int lpt,
+                           float eps, E_* dx, float* __restrict__ part) {
   using U = typename Unit<E_, VEC>::T;
   __shared__ float2 red[2][32];
   const int lt = threadIdx.x;
@@ -355,18 +414,18 @@ norm_backward_plain_kernel(const E_* dy, const E_* r, const void* __restrict__ w
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
       float wv[VEC] = {};
-      if (c < H) load_weight<VEC>(w, w32, c, wv);
+      if (c < H) load_weight<W_, VEC>(w, c, wv);
       row_terms<E_, VEC>(ru[j], gu[j], wv, ss, hr);
     }
     const float2 s = row_sum2(ss, hr, lpt, red[turn]);
     const float m = 1.f / sqrtf(s.x / (float)H + eps);
-    const float k = m * m * (s.y / (float)H);
+    const float k = -m * m * (s.y / (float)H);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
       if (c >= H) continue;
       float wv[VEC];
-      load_weight<VEC>(w, w32, c, wv);
+      load_weight<W_, VEC>(w, c, wv);
       const U e = d_r != nullptr ? *reinterpret_cast<const U*>(d_r + at + c) : U{};
       *reinterpret_cast<U*>(dx + at + c) = row_gradient<E_, VEC>(ru[j], gu[j], e, d_r != nullptr, wv, m, k, acc[j]);
     }
@@ -458,25 +517,37 @@ int row_lanes(int units, int nv) { return (int)ceil_div(units, 32 * nv) * 32; }
 // Short rows share a block of 128 threads.
 int rows_per_block(int lpt) { return lpt <= 64 ? 128 / lpt : 1; }
 
-template <typename E_, int VEC, bool QUANT, typename... Args>
-cudaError_t launch_norm(int T, int H, cudaStream_t stream, const E_* x, const E_* res, const void* w, bool w32, float eps,
-                        Args... out) {
+template <typename E_, typename W_, int VEC, bool QUANT, typename... Args>
+cudaError_t launch_norm(int T, int H, cudaStream_t stream, const E_* x, const E_* res, const W_* w, float eps, Args... out) {
   const int units = VEC > 1 ? H / VEC : (int)round_up(H, kGroupCols);
   auto run = [&](auto kernel, int nv) {
     const int lpt = row_lanes(units, nv), rpb = rows_per_block(lpt);
-    return launch_pdl(kernel, dim3((unsigned)ceil_div(T, rpb)), dim3(lpt * rpb), 0, stream, x, res, w, w32, T, H, lpt,
-                      eps, out...);
+    return launch_pdl(kernel, dim3((unsigned)ceil_div(T, rpb)), dim3(lpt * rpb), 0, stream, x, res, w, T, H, lpt, eps,
+                      out...);
   };
   if constexpr (VEC > 1) {
-    if (units <= 128) return run(norm_kernel<E_, VEC, 1, QUANT, 128>, 1);
-    if (units <= 512) return run(norm_kernel<E_, VEC, 2, QUANT, 256>, 2);
-    if (units <= 2048) return run(norm_kernel<E_, VEC, 4, QUANT, 512>, 4);
-    return run(norm_kernel<E_, VEC, 8, QUANT, 512>, 8);
+    // With many rows few threads take each, which wait for one another less; with few
+    // rows many do, as there is nothing else to run meanwhile (us, 1, 256 and 16384 rows
+    // of bf16: 7168 columns in two units a thread 2.1, 3.1, 159, in eight 3.2, 3.8, 135;
+    // 1024 columns in one 1.5, 1.7, 24.0, in two 1.7, 1.8, 21.1; 512 columns in two at
+    // all sizes).
+    const bool many = T > 1024;
+    if (units > 64 && units <= 128 && !many) return run(norm_kernel<E_, W_, VEC, 1, QUANT, 128>, 1);
+    if (units <= 512) return run(norm_kernel<E_, W_, VEC, 2, QUANT, 256>, 2);
+    if constexpr (VEC == 8) {
+      if (units <= 1024)
+        return many ? run(norm_kernel<E_, W_, 8, 8, QUANT, 128>, 8) : run(norm_kernel<E_, W_, 8, 2, QUANT, 512>, 2);
+      return many ? run(norm_kernel<E_, W_, 8, 8, QUANT, 256>, 8) : run(norm_kernel<E_, W_, 8, 4, QUANT, 512>, 4);
+    } else {
+      // float32 in eight units a thread: 7168 columns 265 -> 305 us (16384 rows)
+      if (units <= 2048) return run(norm_kernel<E_, W_, 4, 4, QUANT, 512>, 4);
+      return run(norm_kernel<E_, W_, 4, 8, QUANT, 512>, 8);
+    }
   } else {
-    if (units <= 2048) return run(norm_kernel<E_, 1, 4, QUANT, 512>, 4);
-    if (units <= 4096) return run(norm_kernel<E_, 1, 8, QUANT, 512>, 8);
-    if (units <= 8192) return run(norm_kernel<E_, 1, 16, QUANT, 512>, 16);
-    return run(norm_kernel<E_, 1, 32, QUANT, 512>, 32);
+    if (units <= 2048) return run(norm_kernel<E_, W_, 1, 4, QUANT, 512>, 4);
+    if (units <= 4096) return run(norm_kernel<E_, W_, 1, 8, QUANT, 512>, 8);
+    if (units <= 8192) return run(norm_kernel<E_, W_, 1, 16, QUANT, 512>, 16);
+    return run(norm_kernel<E_, W_, 1, 32, QUANT, 512>, 32);
   }
 }
 
@@ -498,42 +569,43 @@ BackPlan back_plan(int32_t T, int32_t H, int vec) {
   b.lpt = row_lanes(units, b.nv);
   b.rpb = b.ring ? rows_per_block(b.lpt) : 1;
   const int threads = b.lpt * b.rpb;
-  // threads that an SM's registers hold: 64 each, above eight units 128
-  const int per_sm = (b.ring || b.nv <= 8 ? 1024 : 512) / threads;
+  // threads that an SM's registers hold: 64 each, 40 for four single elements, 128 for more than eight
+  const int per_sm = (b.ring ? 1024 : b.nv <= 4 ? 1536 : b.nv <= 8 ? 1024 : 512) / threads;
   const int64_t most = (int64_t)(per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm) * current_sms(), want = ceil_div(T, b.rpb);
   b.blocks = want < most ? want : most;
   return b;
 }
 
-template <typename E_>
-cudaError_t launch_backward_ring(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const void* w, bool w32,
-                            const E_* d_r, int T, int H, float eps, E_* dx, float* part) {
+template <typename E_, typename W_>
+cudaError_t launch_backward_ring(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const W_* w, const E_* d_r,
+                                 int T, int H, float eps, E_* dx, float* part) {
   // the shared memory that the largest block of the kernel takes, whatever this
   // call's: a call in another thread does not lower it
   auto run = [&](auto kernel, int most) {
-    const size_t per = 4 * 3 * sizeof(uint4);  // NV DEPTH = 4
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(per * most));
+    const size_t per = 4 * 3 * sizeof(uint4), smem = per * b.lpt * b.rpb;  // NV DEPTH = 4
+    cudaError_t err = cudaSuccess;
+    if (smem > 46 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(per * most));
     return err != cudaSuccess ? err
-                              : launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt * b.rpb), per * b.lpt * b.rpb, stream,
-                                           dy, r, w, w32, d_r, T, H, b.lpt, eps, dx, part);
+                              : launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt * b.rpb), smem, stream, dy, r, w, d_r, T,
+                                           H, b.lpt, eps, dx, part);
   };
-  if (b.nv == 1) return run(norm_backward_kernel<E_, 1, 4, 256, 4>, 256);
-  if (b.lpt <= 512) return run(norm_backward_kernel<E_, 2, 2, 512, 2>, 512);
-  return run(norm_backward_kernel<E_, 2, 2, 1024, 1>, 1024);
+  if (b.nv == 1) return run(norm_backward_kernel<E_, W_, 1, 4, 256, 4>, 256);
+  if (b.lpt <= 512) return run(norm_backward_kernel<E_, W_, 2, 2, 512, 2>, 512);
+  return run(norm_backward_kernel<E_, W_, 2, 2, 1024, 1>, 1024);
 }
-template <typename E_, int VEC>
-cudaError_t launch_backward_plain(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const void* w, bool w32,
-                                  const E_* d_r, int T, int H, float eps, E_* dx, float* part) {
+template <typename E_, typename W_, int VEC>
+cudaError_t launch_backward_plain(const BackPlan& b, cudaStream_t stream, const E_* dy, const E_* r, const W_* w, const E_* d_r,
+                                  int T, int H, float eps, E_* dx, float* part) {
   auto run = [&](auto kernel) {
-    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt), 0, stream, dy, r, w, w32, d_r, T, H, b.lpt, eps, dx, part);
+    return launch_pdl(kernel, dim3((unsigned)b.blocks), dim3(b.lpt), 0, stream, dy, r, w, d_r, T, H, b.lpt, eps, dx, part);
   };
   if constexpr (VEC > 1) {
-    return run(norm_backward_plain_kernel<E_, VEC, 8, 512>);  // float32 rows of more than 8192 columns
+    return run(norm_backward_plain_kernel<E_, W_, VEC, 8, 512>);  // float32 rows of more than 8192 columns
   } else {
-    return b.nv == 4    ? run(norm_backward_plain_kernel<E_, 1, 4, 512>)
-           : b.nv == 8  ? run(norm_backward_plain_kernel<E_, 1, 8, 512>)
-           : b.nv == 16 ? run(norm_backward_plain_kernel<E_, 1, 16, 512>)
-                        : run(norm_backward_plain_kernel<E_, 1, 32, 512>);
+    return b.nv == 4    ? run(norm_backward_plain_kernel<E_, W_, 1, 4, 512>)
+           : b.nv == 8  ? run(norm_backward_plain_kernel<E_, W_, 1, 8, 512>)
+           : b.nv == 16 ? run(norm_backward_plain_kernel<E_, W_, 1, 16, 512>)
+                        : run(norm_backward_plain_kernel<E_, W_, 1, 32, 512>);
   }
 }
 
@@ -555,14 +627,35 @@ int check_norm(int32_t T, int32_t H, int32_t dtype, int32_t w_dtype, const void*
   return MLR_OK;
 }
 
-template <typename E_, bool QUANT>
-int run_norm(bool whole, const void* x, const void* residual, const void* w, bool w32, int T, int H, float eps, void* y,
-             void* r_out, uint8_t* codes, uint8_t* exps, cudaStream_t stream) {
+template <typename E_, typename W_, bool QUANT>
+int run_norm(bool whole, const void* x, const void* residual, const void* weight, int T, int H, float eps, void* y, void* r_out,
+             uint8_t* codes, uint8_t* exps, cudaStream_t stream) {
   const E_ *xp = static_cast<const E_*>(x), *rp = static_cast<const E_*>(residual);
+  const W_* w = static_cast<const W_*>(weight);
   E_ *yp = static_cast<E_*>(y), *op = static_cast<E_*>(r_out);
   constexpr int VEC = 16 / sizeof(E_);
-  return launched(whole ? launch_norm<E_, VEC, QUANT>(T, H, stream, xp, rp, w, w32, eps, yp, op, codes, exps)
-                        : launch_norm<E_, 1, QUANT>(T, H, stream, xp, rp, w, w32, eps, yp, op, codes, exps));
+  return launched(whole ? launch_norm<E_, W_, VEC, QUANT>(T, H, stream, xp, rp, w, eps, yp, op, codes, exps)
+                        : launch_norm<E_, W_, 1, QUANT>(T, H, stream, xp, rp, w, eps, yp, op, codes, exps));
+}
+
+template <typename E_, typename W_>
+int run_backward(bool whole, const BackPlan& b, cudaStream_t stream, const void* dy, const void* r, const void* weight,
+                 const void* d_r, int T, int H, float eps, void* dx, float* part) {
+  const E_ *g = static_cast<const E_*>(dy), *a = static_cast<const E_*>(r), *e = static_cast<const E_*>(d_r);
+  const W_* w = static_cast<const W_*>(weight);
+  E_* o = static_cast<E_*>(dx);
+  if (b.ring) return launched(launch_backward_ring<E_, W_>(b, stream, g, a, w, e, T, H, eps, o, part));
+  if constexpr (sizeof(E_) == 4)
+    if (whole) return launched(launch_backward_plain<E_, W_, 4>(b, stream, g, a, w, e, T, H, eps, o, part));
+  return launched(launch_backward_plain<E_, W_, 1>(b, stream, g, a, w, e, T, H, eps, o, part));
+}
+
+// f<E_, W_>() for the types of rows and weight.
+template <typename F>
+int by_types(int32_t dtype, int32_t weight_dtype, F f) {
+  const bool w32 = weight_dtype == MLR_DTYPE_F32;
+  if (dtype == MLR_DTYPE_BF16) return w32 ? f(uint16_t{}, float{}) : f(uint16_t{}, uint16_t{});
+  return w32 ? f(float{}, float{}) : f(float{}, uint16_t{});
 }
 
 }  // namespace
@@ -584,12 +677,10 @@ extern "C" int moe_rms_norm(const void* x, const void* residual, const void* wei
   // a vector's codes are stored together
   if (codes != nullptr && !aligned_to(codes, 16)) whole = false;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const bool w32 = weight_dtype == MLR_DTYPE_F32;
-  auto run = [&](auto f) {
-    return f(whole, x, residual, weight, w32, num_tokens, hidden, eps, y, residual_out, codes, exps, stream);
-  };
-  if (dtype == MLR_DTYPE_BF16) return codes != nullptr ? run(run_norm<uint16_t, true>) : run(run_norm<uint16_t, false>);
-  return codes != nullptr ? run(run_norm<float, true>) : run(run_norm<float, false>);
+  return by_types(dtype, weight_dtype, [&](auto e, auto w) {
+    auto run = codes != nullptr ? run_norm<decltype(e), decltype(w), true> : run_norm<decltype(e), decltype(w), false>;
+    return run(whole, x, residual, weight, num_tokens, hidden, eps, y, residual_out, codes, exps, stream);
+  });
 }
 
 extern "C" size_t moe_rms_norm_backward_workspace_bytes(int32_t num_tokens, int32_t hidden, int32_t dtype) {
@@ -600,21 +691,6 @@ extern "C" size_t moe_rms_norm_backward_workspace_bytes(int32_t num_tokens, int3
   const int64_t parts = a > b ? a : b;
   return (size_t)(parts > 0 ? parts : 1) * hidden * 4;
 }
-
-namespace mlr {
-namespace {
-template <typename E_>
-cudaError_t run_backward(bool whole, const BackPlan& b, cudaStream_t stream, const void* dy, const void* r, const void* w,
-                         bool w32, const void* d_r, int T, int H, float eps, void* dx, float* part) {
-  const E_ *g = static_cast<const E_*>(dy), *a = static_cast<const E_*>(r), *e = static_cast<const E_*>(d_r);
-  E_* o = static_cast<E_*>(dx);
-  if (b.ring) return launch_backward_ring<E_>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
-  if constexpr (sizeof(E_) == 4)
-    if (whole) return launch_backward_plain<E_, 4>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
-  return launch_backward_plain<E_, 1>(b, stream, g, a, w, w32, e, T, H, eps, o, part);
-}
-}  // namespace
-}  // namespace mlr
 
 extern "C" int moe_rms_norm_backward(const void* dy, const void* r, const void* weight, const void* d_r, int32_t num_tokens,
                                      int32_t hidden, int32_t dtype, int32_t weight_dtype, float eps, void* dx,
@@ -636,9 +712,9 @@ extern "C" int moe_rms_norm_backward(const void* dy, const void* r, const void* 
   if (workspace == nullptr || ws_bytes < (size_t)b.blocks * hidden * 4) return MLR_ERR_CAPACITY;
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
   float* part = static_cast<float*>(workspace);
-  const bool w32 = weight_dtype == MLR_DTYPE_F32;
-  auto run = dtype == MLR_DTYPE_BF16 ? run_backward<uint16_t> : run_backward<float>;
-  const int c = launched(run(whole, b, stream, dy, r, weight, w32, d_r, num_tokens, hidden, eps, dx, part));
+  const int c = by_types(dtype, weight_dtype, [&](auto e, auto w) {
+    return run_backward<decltype(e), decltype(w)>(whole, b, stream, dy, r, weight, d_r, num_tokens, hidden, eps, dx, part);
+  });
   if (c != MLR_OK) return c;
   return launched(launch_pdl(sum_parts_kernel, dim3((unsigned)ceil_div(hidden, 32)), dim3(1024), 0, stream,
                              (const float*)part, (int)b.blocks, (int)hidden, d_weight));

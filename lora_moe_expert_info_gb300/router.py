@@ -134,15 +134,17 @@ def moe_balance_loss(logits, topk_ids, scoring: str = "softmax", token_mask: Opt
     on = _launch_stream(logits, "moe_balance_loss")
     loss = _out(loss, "loss", (), torch.float32, dev)
     counts = _out(counts, "counts", (E + 1,), torch.int32, dev)
-    if workspace is None:
-        wsb = lib.moe_balance_loss_workspace_bytes(T, E)
-        workspace = torch.empty(max(wsb, 1), dtype=torch.uint8, device=dev)
-    else:
+    if workspace is not None:
         _req(workspace, "workspace", getattr(workspace, "dtype", None), dev)  # of any type
+    else:
+        wsb = lib.moe_balance_loss_workspace_bytes(T, E)
+        if wsb > 1:
+            workspace = torch.empty(wsb, dtype=torch.uint8, device=dev)
     status = torch.zeros(1, dtype=torch.int32, device=dev) if check else None
     _check_host(lib.moe_balance_loss(logits.data_ptr(), topk_ids.data_ptr(), _address(token_mask), T, E, K, dtype,
-                                     code, loss.data_ptr(), counts.data_ptr(), workspace.data_ptr(),
-                                     workspace.nbytes, _address(status), on), "moe_balance_loss")
+                                     code, loss.data_ptr(), counts.data_ptr(), _address(workspace),
+                                     0 if workspace is None else workspace.nbytes, _address(status), on),
+                "moe_balance_loss")
     if check:
         _check_device(status, "moe_balance_loss")
     return loss, counts

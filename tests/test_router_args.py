@@ -82,7 +82,9 @@ def test_balance_and_gradient_refusals(lib):
         return lib.moe_balance_loss(logits, ids, None, T, E, K, dtype, scoring, loss, counts, w, n, None, None)
     for bad in (dict(logits=None), dict(ids=None), dict(loss=None), dict(counts=None), dict(K=0), dict(w=ctypes.c_void_p(0x1010))):
         assert f(**bad) == INVALID, bad
-    assert f(w=None) == CAPACITY and f(n=ctypes.c_size_t(16)) == CAPACITY and f(E=5000) == UNSUPPORTED
+    big = dict(T=4096, E=256)  # past the single launch, which takes no workspace
+    assert ws(2048, 256) == 1 and ws(2049, 256) > 4 * 513 and ws(4, 257) >= 4 * 515
+    assert f(w=None, **big) == CAPACITY and f(n=ctypes.c_size_t(16), **big) == CAPACITY and f(E=5000) == UNSUPPORTED
 
     def g(logits=FAKE, ids=FAKE, dw=FAKE, counts=FAKE, dl=FAKE, T=4, E=16, K=2, dtype=1, scoring=0, out=FAKE):
         return lib.moe_route_backward(logits, ids, dw, counts, dl, None, T, E, K, dtype, scoring, 1, 1.0, out, None, None)
