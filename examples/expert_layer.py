@@ -1,11 +1,12 @@
 """An expert layer trained through the sorted rows, then served from 4-bit experts.
 
-Training: tokens are sorted by expert (MoePermute), every expert's rows go
+Training: each token's experts are chosen (MoeRoute), tokens sorted by expert
+(MoePermute), every expert's rows go
 through its frozen weights plus trainable low-rank adapters with plain matrix
 products, and the rows are weighted and summed back (MoeUnpermute); gradients
 reach the adapters, the router and the tokens.  Serving: the adapters are merged,
-the experts quantised once (fp4_quantize), and fp4_moe_forward answers a prompt
-and single tokens from them.
+the experts quantised once (fp4_quantize), and moe_route and fp4_moe_forward answer
+a prompt and single tokens from them.
 
     python examples/expert_layer.py [--steps 20] [--fmt nvfp4]
 """
@@ -19,12 +20,13 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from lora_moe_expert_info_gb300 import fp4  # noqa: E402
 from lora_moe_expert_info_gb300.permute import MoePermute, MoeUnpermute  # noqa: E402
+from lora_moe_expert_info_gb300.router import MoeRoute, moe_route  # noqa: E402
 
 
 def route(x, router, topk):
-    """Expert ids int32 [T, K] and renormalised weights float32 [T, K]."""
-    top = (x.float() @ router).softmax(-1).topk(topk, dim=-1)
-    return top.indices.int(), top.values / top.values.sum(-1, keepdim=True)
+    """Expert ids int32 [T, K] and renormalised weights float32 [T, K], with gradients."""
+    weights, ids, _, _ = MoeRoute.apply(x.float() @ router, topk)
+    return ids, weights
 
 
 class ExpertLayer(torch.nn.Module):
@@ -80,7 +82,7 @@ class QuantisedExperts:
 
     @torch.no_grad()
     def __call__(self, x):
-        ids, weights = route(x, self.layer.router, self.layer.topk)
+        ids, weights = moe_route(x.float() @ self.layer.router, self.layer.topk)
         return fp4.fp4_moe_forward(x, ids, weights, *self.matrices, self.fmt, *self.scales, self.x_scale, self.h_scale)
 
 

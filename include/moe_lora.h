@@ -315,6 +315,25 @@ int fused_moe_lora_forward_fp8_w8a8(const mlr_bf16* x, const int32_t* topk_ids, 
                                     int32_t num_loras, int32_t max_rank, mlr_bf16* y, void* workspace,
                                     size_t ws_bytes, int32_t* d_status, void* stream);
 
+/*
+ * fused_moe_lora_forward_fp8_w8a8_xq -- the same layer where x stands in 8 bits
+ * already, as moe_rms_norm leaves it: x_codes uint8 [T, H] (16-byte aligned) and
+ * x_exps uint8 [T, ceil(H/128)] (bytes below 255) are what gate_up's base GEMM
+ * multiplies; x itself feeds the LoRA shrink.  With the codes of x's own
+ * quantisation y is bit-identical to that of fused_moe_lora_forward_fp8_w8a8.
+ */
+int fused_moe_lora_forward_fp8_w8a8_xq(const mlr_bf16* x, const uint8_t* x_codes, const uint8_t* x_exps,
+                                       const int32_t* topk_ids, const float* topk_weights,
+                                       const int32_t* token_lora_mapping, const int32_t* lora_ranks,
+                                       const float* scalings, const uint8_t* w_gate_up_q,
+                                       const uint8_t* w_gate_up_exp, const uint8_t* w_down_q,
+                                       const uint8_t* w_down_exp, const mlr_bf16* lora_a_gu,
+                                       const mlr_bf16* lora_b_gu, const mlr_bf16* lora_a_down,
+                                       const mlr_bf16* lora_b_down, int32_t num_tokens, int32_t topk,
+                                       int32_t num_experts, int32_t hidden, int32_t intermediate,
+                                       int32_t num_loras, int32_t max_rank, mlr_bf16* y, void* workspace,
+                                       size_t ws_bytes, int32_t* d_status, void* stream);
+
 /* Scratch bytes lora_linear_forward needs for these sizes (0 on bad sizes). */
 size_t lora_linear_workspace_bytes(int32_t num_tokens, int32_t in_features, int32_t out_features,
                                    int32_t num_loras, int32_t max_rank, int32_t num_slices);

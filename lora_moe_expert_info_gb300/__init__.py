@@ -116,6 +116,8 @@ def library() -> ctypes.CDLL:
                 lib.fused_moe_lora_workspace_bytes_fp8_w8a8.argtypes = [i32] * 7
                 lib.fused_moe_lora_forward_fp8_w8a8.restype = ctypes.c_int
                 lib.fused_moe_lora_forward_fp8_w8a8.argtypes = [vp] * 14 + [i32] * 7 + [vp, vp, sz, vp, vp]
+                lib.fused_moe_lora_forward_fp8_w8a8_xq.restype = ctypes.c_int
+                lib.fused_moe_lora_forward_fp8_w8a8_xq.argtypes = [vp] * 16 + [i32] * 7 + [vp, vp, sz, vp, vp]
             if hasattr(lib, "lora_linear_forward"):
                 lib.lora_linear_workspace_bytes.restype = sz
                 lib.lora_linear_workspace_bytes.argtypes = [i32] * 6
@@ -462,10 +464,11 @@ def fused_moe_lora_forward_fp8(x, topk_ids, topk_weights, token_lora_mapping, lo
 
 def _quant_forward(fn_name, x, topk_ids, topk_weights, token_lora_mapping, lora_ranks, scalings, quant,
                    lora_a_gu, lora_b_gu, lora_a_down, lora_b_down, y, workspace, stream, check, status,
-                   I_of, code_shapes, side_shapes, ws_fn="fused_moe_lora_workspace_bytes"):
+                   I_of, code_shapes, side_shapes, ws_fn="fused_moe_lora_workspace_bytes", x_quant=()):
     """Shared marshalling of the quantised-expert forwards: `quant` is the list of
     (tensor, name, dtype) of the code / scale / zero arrays in C argument order;
-    code_shapes(E, I, H) and side_shapes(E, I, H) give their expected shapes."""
+    code_shapes(E, I, H) and side_shapes(E, I, H) give their expected shapes.
+    x_quant: x's own codes and exponents, which follow x."""
     lib = library()
     if not hasattr(lib, fn_name):
         raise RuntimeError(f"library built without {fn_name}")
@@ -506,7 +509,7 @@ def _quant_forward(fn_name, x, topk_ids, topk_weights, token_lora_mapping, lora_
     if check and status is None:
         status = torch.zeros(1, dtype=torch.int32, device=dev)
     code = getattr(lib, fn_name)(
-        _ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(token_lora_mapping), _ptr(lora_ranks),
+        _ptr(x), *[_ptr(t) for t in x_quant], _ptr(topk_ids), _ptr(topk_weights), _ptr(token_lora_mapping), _ptr(lora_ranks),
         _ptr(scalings), *[_ptr(t) for t, _, _ in quant], _ptr(lora_a_gu), _ptr(lora_b_gu), _ptr(lora_a_down),
         _ptr(lora_b_down), T, K, E, H, I, L, R, _ptr(y), _ptr(workspace), workspace.numel(), _ptr(status),
         _stream(stream))
@@ -569,20 +572,33 @@ def fused_moe_lora_forward_fp8_w8a8(x, topk_ids, topk_weights, token_lora_mappin
                                     lora_a_gu, lora_b_gu, lora_a_down, lora_b_down,
                                     y: Optional[torch.Tensor] = None,
                                     workspace: Optional[torch.Tensor] = None, stream=None,
-                                    check: bool = True, status: Optional[torch.Tensor] = None) -> torch.Tensor:
+                                    check: bool = True, status: Optional[torch.Tensor] = None,
+                                    x_codes: Optional[torch.Tensor] = None,
+                                    x_exps: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The layer on the FP8 tensor cores: w_gate_up_q [E,2I,H] and w_down_q
     [E,H,I] E4M3 codes (uint8), w_gate_up_exp [E,ceil(2I/128),ceil(H/128)] and
     w_down_exp [E,ceil(H/128),ceil(I/128)] uint8 biased block exponents (scale
     2^(e-127)); the activations of the base GEMMs are quantised per token and
-    128-channel group on the way (see the C header)."""
+    128-channel group on the way (see the C header).  x_codes [T,H] and x_exps
+    [T,ceil(H/128)] (both or neither): x in 8 bits already, as norm.rms_norm_fp8
+    leaves it."""
     cb = lambda n: (n + 127) // 128  # noqa: E731
     quant = [(w_gate_up_q, "w_gate_up_q", torch.uint8), (w_gate_up_exp, "w_gate_up_exp", torch.uint8),
              (w_down_q, "w_down_q", torch.uint8), (w_down_exp, "w_down_exp", torch.uint8)]
-    return _quant_forward("fused_moe_lora_forward_fp8_w8a8", x, topk_ids, topk_weights, token_lora_mapping,
-                          lora_ranks, scalings, quant, lora_a_gu, lora_b_gu, lora_a_down, lora_b_down, y,
+    if (x_codes is None) != (x_exps is None):
+        raise ValueError("fused_moe_lora_forward_fp8_w8a8: x_codes and x_exps go together")
+    fn, x_quant = "fused_moe_lora_forward_fp8_w8a8", ()
+    if x_codes is not None:
+        fn, x_quant = fn + "_xq", (x_codes, x_exps)
+        for t, n in ((x_codes, "x_codes"), (x_exps, "x_exps")):
+            _req(t, n, torch.uint8, x.device)
+        if x_codes.shape != x.shape or tuple(x_exps.shape) != (x.shape[0], cb(x.shape[1])):
+            raise ValueError("fused_moe_lora_forward_fp8_w8a8: inconsistent shapes")
+    return _quant_forward(fn, x, topk_ids, topk_weights,
+                          token_lora_mapping, lora_ranks, scalings, quant, lora_a_gu, lora_b_gu, lora_a_down, lora_b_down, y,
                           workspace, stream, check, status, lambda w: w.shape[1] // 2,
                           lambda E, I, H: [(E, 2 * I, H), (E, cb(2 * I), cb(H)), (E, H, I), (E, cb(H), cb(I))],
-                          lambda E, I, H: [], ws_fn="fused_moe_lora_workspace_bytes_fp8_w8a8")
+                          lambda E, I, H: [], ws_fn="fused_moe_lora_workspace_bytes_fp8_w8a8", x_quant=x_quant)
 
 
 @_on_stream

@@ -1717,7 +1717,9 @@ gather_x_tok_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 // [H/128][cap] biased exponents (rows [n, cap): zero codes, exponent 127).
 // Token-major (TOK: a token's groups are quantised once and written to the
 // rows of its K pairs) or row-major, like gather_x_tok_kernel and
-// gather_x_kernel.  Half a warp takes one group, eight values per lane.
+// gather_x_kernel.  Half a warp takes one group, eight values per lane.  xq, xe
+// (nullable): x as the caller has it in 8 bits already, codes [T][H] and exponent
+// bytes [T][ceil(H/128)], taken instead of quantising x.
 template <bool TOK>
 __global__ void __launch_bounds__(kGatherThreads)
 gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ topk_ids,
@@ -1725,7 +1727,8 @@ gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ t
                    const int32_t* __restrict__ pos,
                    const uint32_t* __restrict__ n_valid, int T, int K, int E, int L, int H, int64_t cap,
                    uint16_t* __restrict__ xs, uint8_t* __restrict__ x8, uint8_t* __restrict__ sx,
-                   float* __restrict__ yacc, int64_t yacc_n4) {
+                   float* __restrict__ yacc, int64_t yacc_n4, const uint8_t* __restrict__ xq,
+                   const uint8_t* __restrict__ xe) {
   pdl_wait();  // the predecessor on the stream has completed
   pdl_trigger();
   const int64_t n = *n_valid;
@@ -1755,21 +1758,33 @@ gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ t
       for (int j = 0; j < kPairs; ++j) {
         if (g0 + 2 * j >= ng) break;  // the same for both halves
         const int g = g0 + 2 * j + half, c = g * 16 + hl;
-        const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m = max(m, max(wv[k] & 0x7fffu, (wv[k] >> 16) & 0x7fffu));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));  // within the half
-        const int s = mx_group_exp_bf16(m);
-        const float sc = exp2_neg(s);
         uint32_t q[2];
+        uint32_t eb = 127;  // the exponent byte
+        if (xq != nullptr) {
+          uint2 w = make_uint2(0, 0);
+          if (tok >= 0 && g < ng) {
+            if (c * 8 < H) w = __ldg(reinterpret_cast<const uint2*>(xq + tok * H + c * 8));
+            eb = __ldg(xe + tok * ng + g);
+          }
+          q[0] = w.x;
+          q[1] = w.y;
+        } else {
+          const uint32_t wv[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+          uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < 4; k += 2) {
-          const uint32_t lo = f32x2_to_e4m3x2(__uint_as_float(wv[k] << 16) * sc, __uint_as_float(wv[k] & 0xffff0000u) * sc);
-          const uint32_t hi =
-              f32x2_to_e4m3x2(__uint_as_float(wv[k + 1] << 16) * sc, __uint_as_float(wv[k + 1] & 0xffff0000u) * sc);
-          q[k / 2] = lo | (hi << 16);
+          for (int k = 0; k < 4; ++k) m = max(m, max(wv[k] & 0x7fffu, (wv[k] >> 16) & 0x7fffu));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));  // within the half
+          const int s = mx_group_exp_bf16(m);
+          const float sc = exp2_neg(s);
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            const uint32_t lo = f32x2_to_e4m3x2(__uint_as_float(wv[k] << 16) * sc, __uint_as_float(wv[k] & 0xffff0000u) * sc);
+            const uint32_t hi =
+                f32x2_to_e4m3x2(__uint_as_float(wv[k + 1] << 16) * sc, __uint_as_float(wv[k + 1] & 0xffff0000u) * sc);
+            q[k / 2] = lo | (hi << 16);
+          }
+          eb = (uint32_t)(s + 127);
         }
         for (uint32_t dm = dests; dm; dm &= dm - 1) {
           const int64_t u = TOK ? (int64_t)__shfl_sync(0xffffffffu, myu, __ffs(dm) - 1) : task;
@@ -1777,7 +1792,7 @@ gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ t
             *reinterpret_cast<uint4*>(xs + ((int64_t)(c >> 3) * cap + u) * 64 + (c & 7) * 8) = v[j];
           if (g < ng) {
             *reinterpret_cast<uint2*>(x8 + ((int64_t)g * cap + u) * 128 + hl * 8) = make_uint2(q[0], q[1]);
-            if (hl == 0) sx[(int64_t)g * cap + u] = (uint8_t)(s + 127);
+            if (hl == 0) sx[(int64_t)g * cap + u] = (uint8_t)eb;
           }
         }
       }
@@ -2395,8 +2410,8 @@ bool make_map3_u8(CUtensorMap* m, const void* base, uint64_t d0, uint64_t d1, ui
 // [E][2I][ceil(H/128)] and s_d, z_d [E][H][ceil(I/128)]; kQMx: E4M3 codes
 // with power-of-two block scales given as biased exponents in z_gu
 // [E][ceil(2I/128)][ceil(H/128)] and z_d [E][ceil(H/128)][ceil(I/128)], the
-// activations quantised on the way (s_gu, s_d unused); kQNone: bf16, the
-// scales unused.
+// activations quantised on the way (s_gu, s_d unused; x_codes and x_exps, both
+// or neither: x as it stands in 8 bits already); kQNone: bf16, the scales unused.
 int moe_forward(const mlr_bf16* x, const int32_t* topk_ids, const float* topk_weights,
                 const int32_t* token_lora_mapping, const int32_t* lora_ranks, const float* scalings,
                 const void* w_gate_up, const void* w_down, const float* s_gu, const float* s_d,
@@ -2404,7 +2419,7 @@ int moe_forward(const mlr_bf16* x, const int32_t* topk_ids, const float* topk_we
                 const mlr_bf16* lora_a_gu, const mlr_bf16* lora_b_gu, const mlr_bf16* lora_a_down,
                 const mlr_bf16* lora_b_down, int32_t T, int32_t K, int32_t E, int32_t H, int32_t I, int32_t L,
                 int32_t R, mlr_bf16* y, void* workspace, size_t ws_bytes, int32_t* d_status,
-                cudaStream_t stream) {
+                cudaStream_t stream, const uint8_t* x_codes = nullptr, const uint8_t* x_exps = nullptr) {
   const bool mx = qf == kQMx;
   const FwdLayout f = fwd_layout(T, K, E, H, I, L, R, mx);
   if (!f.ok) {
@@ -2424,6 +2439,7 @@ int moe_forward(const mlr_bf16* x, const int32_t* topk_ids, const float* topk_we
                 (reinterpret_cast<uintptr_t>(s_d) & 3) != 0))
     return MLR_ERR_INVALID;
   if ((qf == kQU4 || mx) && (z_gu == nullptr || z_d == nullptr)) return MLR_ERR_INVALID;
+  if ((reinterpret_cast<uintptr_t>(x_codes) & 15) != 0) return MLR_ERR_INVALID;
   if (L > 0) {
     const void* lo[] = {lora_ranks, scalings, lora_a_gu, lora_b_gu, lora_a_down, lora_b_down};
     for (const void* q : lo)
@@ -2619,7 +2635,7 @@ int moe_forward(const mlr_bf16* x, const int32_t* topk_ids, const float* topk_we
         mx ? launch_pdl(tok_major ? gather_x_mx_kernel<true> : gather_x_mx_kernel<false>, dim3(grid),
                         dim3(kGatherThreads), 0, stream, x, topk_ids, token_lora_mapping, (const int32_t*)usorted,
                         (const int32_t*)pos, ustart + f.al.NB, T, K, E, L, H, f.cap, xs, x8, sx, yacc,
-                        det ? 0 : (int64_t)T * H / 4)
+                        det ? 0 : (int64_t)T * H / 4, x_codes, x_exps)
            : tok_major
                ? launch_pdl(gather_x_tok_kernel, dim3(grid), dim3(kGatherThreads), 0, stream, x, topk_ids,
                             token_lora_mapping, (const int32_t*)usorted, (const int32_t*)pos, ustart + f.al.NB, T, K,
@@ -2800,6 +2816,23 @@ extern "C" int fused_moe_lora_forward_fp8_w8a8(const mlr_bf16* x, const int32_t*
                           w_down_q, nullptr, nullptr, w_gate_up_exp, w_down_exp, mlr::kQMx, lora_a_gu, lora_b_gu,
                           lora_a_down, lora_b_down, T, K, E, H, I, L, R, y, workspace, ws_bytes, d_status,
                           static_cast<cudaStream_t>(stream_));
+}
+
+extern "C" int fused_moe_lora_forward_fp8_w8a8_xq(const mlr_bf16* x, const uint8_t* x_codes, const uint8_t* x_exps,
+                                                  const int32_t* topk_ids, const float* topk_weights,
+                                                  const int32_t* token_lora_mapping, const int32_t* lora_ranks,
+                                                  const float* scalings, const uint8_t* w_gate_up_q,
+                                                  const uint8_t* w_gate_up_exp, const uint8_t* w_down_q,
+                                                  const uint8_t* w_down_exp, const mlr_bf16* lora_a_gu,
+                                                  const mlr_bf16* lora_b_gu, const mlr_bf16* lora_a_down,
+                                                  const mlr_bf16* lora_b_down, int32_t T, int32_t K, int32_t E,
+                                                  int32_t H, int32_t I, int32_t L, int32_t R, mlr_bf16* y,
+                                                  void* workspace, size_t ws_bytes, int32_t* d_status, void* stream_) {
+  if (T > 0 && (x_codes == nullptr || x_exps == nullptr)) return MLR_ERR_INVALID;
+  return mlr::moe_forward(x, topk_ids, topk_weights, token_lora_mapping, lora_ranks, scalings, w_gate_up_q,
+                          w_down_q, nullptr, nullptr, w_gate_up_exp, w_down_exp, mlr::kQMx, lora_a_gu, lora_b_gu,
+                          lora_a_down, lora_b_down, T, K, E, H, I, L, R, y, workspace, ws_bytes, d_status,
+                          static_cast<cudaStream_t>(stream_), x_codes, x_exps);
 }
 
 // ------------------------------------------------------------------------

@@ -120,6 +120,29 @@ def test_binding_checks():
             bad()
 
 
+def test_layer_in_8_bits_refusals(lib):
+    """The W8A8 layer with x in 8 bits: both of codes and exponents, of x's shape."""
+    T, K, E, H, I, L, R = 8, 2, 3, 128, 64, 2, 16
+    f = lib.fused_moe_lora_forward_fp8_w8a8_xq
+    big = ctypes.c_size_t(1 << 30)
+    tail = [T, K, E, H, I, L, R, FAKE, FAKE, big, None, None]
+    assert f(FAKE, None, FAKE, *[FAKE] * 13, *tail) == INVALID
+    assert f(FAKE, FAKE, None, *[FAKE] * 13, *tail) == INVALID
+    assert f(FAKE, ctypes.c_void_p(0x1008), FAKE, *[FAKE] * 13, *tail) == INVALID
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    x = torch.zeros(T, H, dtype=BF)
+    args = (x, torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K), torch.zeros(T, dtype=torch.int32),
+            torch.zeros(L, dtype=torch.int32), torch.zeros(L), u8(E, 2 * I, H), u8(E, 1, 1), u8(E, H, I), u8(E, 1, 1),
+            torch.zeros(L, E, 2, R, H, dtype=BF), torch.zeros(L, E, 2, I, R, dtype=BF), torch.zeros(L, E, R, I, dtype=BF),
+            torch.zeros(L, E, H, R, dtype=BF))
+    for kw in (dict(x_codes=u8(T, H)), dict(x_exps=u8(T, 1)), dict(x_codes=u8(T, H - 1), x_exps=u8(T, 1)),
+               dict(x_codes=u8(T, H), x_exps=u8(T, 2))):
+        with pytest.raises(ValueError):
+            mlr.fused_moe_lora_forward_fp8_w8a8(*args, **kw)
+    with pytest.raises(TypeError):
+        mlr.fused_moe_lora_forward_fp8_w8a8(*args, x_codes=x, x_exps=u8(T, 1))
+
+
 def calls():
     x, w = torch.zeros(4, 64, dtype=BF), torch.zeros(64)
     l, ids, g = torch.zeros(4, 16), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
