@@ -68,7 +68,8 @@ __device__ __forceinline__ void team_sync() {
 // Turns that are fetched ahead where logits lie on the 16-byte grid.
 constexpr int kAhead = 2;
 template <int VEC, int LPT> constexpr bool kRing = VEC > 1 && !kBlockTokens<LPT>;
-template <int VEC, int LPT, int V> constexpr int kRingBytes = kRing<VEC, LPT> ? kAhead * V / VEC * kBalanceThreads * 16 : 0;
+template <int VEC, int LPT, int V, int THREADS = kBalanceThreads>
+constexpr int kRingBytes = kRing<VEC, LPT> ? kAhead * V / VEC * THREADS * 16 : 0;
 
 // v: a token's logits to s, zeros past E and for logits that are not finite.  Returns 1 /
 // sum of s, 0 where that is 0 and for a token that is not active.  Every thread of the
@@ -84,10 +85,7 @@ __device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += v[i] = quick_sigmoid(v[i]);
   } else {
-    float most = v[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
-    most = team_max<LPT>(most, red);
+    float most = team_max<LPT>(max_of<0, 1>(v), red);
     most = most > -CUDART_INF_F ? most : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += v[i] = __expf(v[i] - most);
@@ -106,41 +104,50 @@ constexpr int kLossCluster = 8;
 // Up to this many logits one cluster of eight blocks takes the whole batch, which saves
 // the workspace and the second launch.
 constexpr int64_t kOneClusterLogits = 1 << 19;
+template <int V> constexpr int kOneThreads = V == 32 ? 512 : 1024;  // of its blocks, by their registers
 
 // Sums of shares and pairs per expert over the block's tokens.  ONE: the grid is one
 // cluster, which adds them over distributed shared memory and writes counts and loss;
 // else part [blocks][E] and count [blocks][E + 1] (the last one: tokens).
 template <int VEC, int LPT, int V, bool ONE, typename E_>
-__global__ void __launch_bounds__(kBalanceThreads, V <= 16 && !kBlockTokens<LPT> ? 4 : 2)
+__global__ void __launch_bounds__(ONE ? kOneThreads<V> : kBalanceThreads, ONE ? 1 : V <= 16 && !kBlockTokens<LPT> ? 4 : 2)
 balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T, int E,
                int K, bool sigmoid, float* __restrict__ part, int32_t* __restrict__ count, float* __restrict__ loss, int32_t* status) {
   extern __shared__ uint4 ring[];  // the ring; then [E + 1] pairs; then float [warps (1 for a block's token)][E] shares
   __shared__ float red[kBalanceThreads / 32];
-  constexpr int TEAMS = kTeams<LPT>, ROWS = kBlockTokens<LPT> ? 1 : kBalanceThreads / 32;
-  int* hist = reinterpret_cast<int*>(reinterpret_cast<char*>(ring) + kRingBytes<VEC, LPT, V>);
+  constexpr int THREADS = ONE ? kOneThreads<V> : kBalanceThreads;
+  constexpr int TEAMS = THREADS / LPT, ROWS = kBlockTokens<LPT> ? 1 : THREADS / 32;
+  int* hist = reinterpret_cast<int*>(reinterpret_cast<char*>(ring) + kRingBytes<VEC, LPT, V, THREADS>);
   float* sums = reinterpret_cast<float*>(hist + E + 1);
   const int team = threadIdx.x / LPT, ll = threadIdx.x % LPT;
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e <= E; e += THREADS) hist[e] = 0;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int64_t step = (int64_t)gridDim.x * TEAMS;
   auto fetch = [&](int64_t t, int stage) {
     if constexpr (kRing<VEC, LPT>)
-      fetch_logits<VEC, LPT, V, kBalanceThreads>(ring, logits + t * E, E, ll, t < T, stage);
+      fetch_logits<VEC, LPT, V, THREADS>(ring, logits + t * E, E, ll, t < T, stage);
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch((int64_t)blockIdx.x * TEAMS + team + i * step, i);
   float acc[V] = {};
   int tokens = 0, stage = 0;
+  // whether the next turn's token counts, and its place of this lane (the first of more
+  // than LPT), asked for a turn before they are used
+  auto counts_in = [&](int64_t t) { return t < T && (mask == nullptr || mask[t]); };
+  auto place = [&](int64_t t) { return t < T && ll < K ? __ldg(ids + t * K + ll) : -1; };
+  bool next_active = counts_in((int64_t)blockIdx.x * TEAMS + team);
+  int next_first = place((int64_t)blockIdx.x * TEAMS + team);
   for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += step) {
     const int64_t t = t0 + team;
-    const bool active = t < T && (mask == nullptr || mask[t]);
-    // the place of this lane (the first ones of more than LPT), used at the turn's end
-    const int first = active && ll < K ? __ldg(ids + t * K + ll) : -1;
+    const bool active = next_active;
+    const int first = next_first;
+    next_active = counts_in(t + step);
+    next_first = place(t + step);
     float v[V];
     if constexpr (kRing<VEC, LPT>) {
-      take_logits<VEC, LPT, V, kBalanceThreads, kAhead>(ring, E, ll, active, stage, v);
+      take_logits<VEC, LPT, V, THREADS, kAhead>(ring, E, ll, active, stage, v);
       fetch(t + kAhead * step, stage);
       stage = stage == kAhead - 1 ? 0 : stage + 1;
     } else {
@@ -148,7 +155,11 @@ balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, c
     }
     const float inv = scores<VEC, LPT>(E, sigmoid, ll, active, red, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
+    for (int i = 0; i < V; i += 2) {
+      const float2 q = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv), make_float2(acc[i], acc[i + 1]));
+      acc[i] = q.x;
+      acc[i + 1] = q.y;
+    }
     if (active) {
       ++tokens;
       for (int k = ll; k < K; k += LPT) {
@@ -171,7 +182,7 @@ balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, c
       if (e < E) sums[(kBlockTokens<LPT> ? 0 : threadIdx.x >> 5) * E + e] = acc[i];
     }
   __syncthreads();
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
+  for (int e = threadIdx.x; e <= E; e += THREADS) {
     if (!ONE) count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
     if (e == E) continue;
     float v = 0.f;
@@ -482,12 +493,17 @@ int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int
     if constexpr (lpt.value == 8) {
       if (one_cluster(T, E)) {
         auto kernel = balance_kernel<VEC, lpt.value, v.value, true, E_>;
-        const size_t smem = bytes(E);
+        constexpr int threads = kOneThreads<v.value>;
+        auto of_one = [&](int experts) {
+          return (size_t)kRingBytes<VEC, lpt.value, v.value, threads> + (experts + 1) * 4 + (size_t)threads / 32 * experts * 4;
+        };
+        const size_t smem = of_one(E);
         cudaError_t err = cudaSuccess;
-        if (smem > 46 * 1024) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes(cover));
+        if (smem > 46 * 1024)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)of_one(cover));
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kLossCluster);
-        cfg.blockDim = dim3(kBalanceThreads);
+        cfg.blockDim = dim3(threads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];

@@ -40,14 +40,38 @@ __device__ __forceinline__ void load_unit(const E_* p, float (&v)[VEC]) {
 // NaN if one of them is not finite, else 0.
 template <int V>
 __device__ __forceinline__ float check_finite(const float (&v)[V]) {
-  float check = 0.f;
+  float2 check = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < V; ++i) check = fmaf(v[i], 0.f, check);
-  return check;
+  for (int i = 0; i < V; i += 2) check = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(0.f, 0.f), check);
+  return check.x + check.y;
+}
+// The larger of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// The largest of v[FIRST], v[FIRST + STEP], ...
+template <int FIRST, int STEP, int V>
+__device__ __forceinline__ float max_of(const float (&v)[V]) {
+  float m = v[FIRST];
+#pragma unroll
+  for (int i = FIRST + STEP; i < V; i += 2 * STEP) m = i + STEP < V ? max3(m, v[i], v[i + STEP < V ? i + STEP : i]) : fmaxf(m, v[i]);
+  return m;
 }
 // Loads them: zeros past E, and all where `active` is not set.
 template <int VEC, int LPT, int V, typename E_>
 __device__ __forceinline__ void load_logits(const E_* row, int E, int ll, bool active, float (&v)[V]) {
+  if (E == LPT * V && __all_sync(0xffffffffu, active)) {  // nothing to put in the place of any
+#pragma unroll
+    for (int j = 0; j < V / VEC; ++j) {
+      float u[VEC];
+      load_unit<E_, VEC>(row + (ll + LPT * j) * VEC, u);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < V / VEC; ++j) {
     const int e = (ll + LPT * j) * VEC;

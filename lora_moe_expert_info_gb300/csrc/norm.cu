@@ -398,16 +398,34 @@ norm_backward_plain_kernel(const E_* dy, const E_* r, const W_* __restrict__ w, 
   const int lt = threadIdx.x;
   pdl_wait();
   pdl_trigger();
+  constexpr bool kNext = NV * VEC <= 8;  // the next row is loaded while this one is in work
   float acc[NV][VEC] = {};
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
-    const int64_t at = row * H;
-    U ru[NV], gu[NV];
+  U rn[kNext ? NV : 1], gn[kNext ? NV : 1], en[kNext ? NV : 1];
+  auto load = [&](int64_t row, U(&ru)[NV], U(&gu)[NV], U(&eu)[NV]) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = unit_col<VEC>(lt, j, lpt);
-      ru[j] = c < H ? *reinterpret_cast<const U*>(r + at + c) : U{};
-      gu[j] = c < H ? *reinterpret_cast<const U*>(dy + at + c) : U{};
+      const bool have = row < T && c < H;
+      ru[j] = have ? *reinterpret_cast<const U*>(r + row * H + c) : U{};
+      gu[j] = have ? *reinterpret_cast<const U*>(dy + row * H + c) : U{};
+      eu[j] = have && d_r != nullptr ? *reinterpret_cast<const U*>(d_r + row * H + c) : U{};
+    }
+  };
+  if constexpr (kNext) load(blockIdx.x, rn, gn, en);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < T; row += gridDim.x, turn ^= 1) {
+    const int64_t at = row * H;
+    U ru[NV], gu[NV], eu[NV];
+    if constexpr (kNext) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        ru[j] = rn[j];
+        gu[j] = gn[j];
+        eu[j] = en[j];
+      }
+      load(row + gridDim.x, rn, gn, en);
+    } else {
+      load(row, ru, gu, eu);
     }
     float ss = 0.f, hr = 0.f;
 #pragma unroll
@@ -426,8 +444,7 @@ norm_backward_plain_kernel(const E_* dy, const E_* r, const W_* __restrict__ w, 
       if (c >= H) continue;
       float wv[VEC];
       load_weight<W_, VEC>(w, c, wv);
-      const U e = d_r != nullptr ? *reinterpret_cast<const U*>(d_r + at + c) : U{};
-      *reinterpret_cast<U*>(dx + at + c) = row_gradient<E_, VEC>(ru[j], gu[j], e, d_r != nullptr, wv, m, k, acc[j]);
+      *reinterpret_cast<U*>(dx + at + c) = row_gradient<E_, VEC>(ru[j], gu[j], eu[j], d_r != nullptr, wv, m, k, acc[j]);
     }
   }
   float* p = part + (int64_t)blockIdx.x * H;
@@ -565,12 +582,12 @@ BackPlan back_plan(int32_t T, int32_t H, int vec) {
   b.ring = vec > 1 && units <= 2048;
   if (b.ring) b.nv = units <= 256 ? 1 : 2;
   else if (vec > 1) b.nv = 8;
-  else b.nv = units <= 2048 ? 4 : units <= 4096 ? 8 : units <= 8192 ? 16 : 32;
+  else b.nv = units <= 2048 ? 4 : units <= 8192 ? 8 : 16;
   b.lpt = row_lanes(units, b.nv);
   b.rpb = b.ring ? rows_per_block(b.lpt) : 1;
   const int threads = b.lpt * b.rpb;
-  // threads that an SM's registers hold: 64 each, 40 for four single elements, 128 for more than eight
-  const int per_sm = (b.ring ? 1024 : b.nv <= 4 ? 1536 : b.nv <= 8 ? 1024 : 512) / threads;
+  // threads that an SM's registers hold
+  const int per_sm = (!b.ring && (vec > 1 || (b.nv == 8 && b.lpt <= 512)) ? 576 : 1024) / threads;
   const int64_t most = (int64_t)(per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm) * current_sms(), want = ceil_div(T, b.rpb);
   b.blocks = want < most ? want : most;
   return b;
@@ -602,10 +619,12 @@ cudaError_t launch_backward_plain(const BackPlan& b, cudaStream_t stream, const 
   if constexpr (VEC > 1) {
     return run(norm_backward_plain_kernel<E_, W_, VEC, 8, 512>);  // float32 rows of more than 8192 columns
   } else {
-    return b.nv == 4    ? run(norm_backward_plain_kernel<E_, W_, 1, 4, 512>)
-           : b.nv == 8  ? run(norm_backward_plain_kernel<E_, W_, 1, 8, 512>)
-           : b.nv == 16 ? run(norm_backward_plain_kernel<E_, W_, 1, 16, 512>)
-                        : run(norm_backward_plain_kernel<E_, W_, 1, 32, 512>);
+    // (us, 8192 rows of 5001 bf16 in eight elements a thread 234, in sixteen of half as
+    // many threads 431; 4096 of 11317 in sixteen 257, in thirty-two 450)
+    return b.nv == 4       ? run(norm_backward_plain_kernel<E_, W_, 1, 4, 512>)
+           : b.nv == 16    ? run(norm_backward_plain_kernel<E_, W_, 1, 16, 1024>)
+           : b.lpt <= 512 ? run(norm_backward_plain_kernel<E_, W_, 1, 8, 512>)
+                          : run(norm_backward_plain_kernel<E_, W_, 1, 8, 1024>);
   }
 }
 

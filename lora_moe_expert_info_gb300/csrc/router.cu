@@ -241,7 +241,7 @@ route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a)
 
 // ------------------------------------------------------- the choice, fast --
 // LPT lanes take a token, V logits each (in units of VEC: unit number lane + LPT j),
-// so a warp has 32 / LPT tokens at once.  The K-th largest of 4 L block maxima (L >= K
+// so a warp has 32 / LPT tokens at once.  The L-th largest of 4 L block maxima (L >= K
 // the length of the sorted lists) is a lower bound of the K-th largest score; the
 // few scores above it -- 1.15 L of them where scores are in no order -- are the
 // candidates, which are ranked against one another.  Where two candidates are nearer
@@ -279,23 +279,23 @@ __device__ __forceinline__ void sort_desc(float (&x)[M]) {
         for (int i = 0; i < k; ++i)
           if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order_desc(x[i + j], x[i + j + k]);
 }
-// The L largest of the lists x[0..N) of LPT lanes, in descending order in each.
+// The lists x[0..N) of LPT lanes merged to their L largest, in descending order, up to
+// the last step: x and y are then the lists of a token's two halves.
 template <int N, int L, int LPT, int O>
-__device__ __forceinline__ void merge_lists(float (&x)[L]) {
-  if constexpr (O < LPT) {
-    float y[N];
+__device__ __forceinline__ void merge_lists(float (&x)[L], float (&y)[L]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = __shfl_xor_sync(0xffffffffu, x[i], O);
+  for (int i = 0; i < N; ++i) y[i] = __shfl_xor_sync(0xffffffffu, x[i], O);
+  if constexpr (2 * O < LPT) {
     if constexpr (N < L) {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[2 * N - 1 - i] = y[i];
       bitonic_desc<2 * N>(x);
-      merge_lists<2 * N, L, LPT, 2 * O>(x);
+      merge_lists<2 * N, L, LPT, 2 * O>(x, y);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = fmaxf(x[i], y[N - 1 - i]);
       bitonic_desc<N>(x);
-      merge_lists<N, L, LPT, 2 * O>(x);
+      merge_lists<N, L, LPT, 2 * O>(x, y);
     }
   }
 }
@@ -367,10 +367,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   // softmax over all experts: its divisor
   float all = 0.f;
   if (!a.sigmoid && !a.renormalize) {
-    float most = v[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
-    most = part_max<LPT>(most);
+    const float most = part_max<LPT>(max_of<0, 1>(v));
 #pragma unroll
     for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? __expf(v[i] - most) : 0.f;
     all = part_sum<LPT>(all);
@@ -457,29 +454,33 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
         for (int i = 0; i < VEC; ++i) v[j * VEC + i] = -CUDART_INF_F;
   }
 
-  // the lower bound
-  float list[L];
+  // the lower bound: the L-th largest block maximum
+  float list[L], other[L];
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
     list[b] = v[b];  // of every NB-th logit, so that a block has its share of every group
 #pragma unroll
-    for (int i = b + NB; i < V; i += NB) list[b] = fmaxf(list[b], v[i]);
+    for (int i = b + NB; i < V; i += 2 * NB)
+      list[b] = i + NB < V ? max3(list[b], v[i], v[i + NB < V ? i + NB : i]) : fmaxf(list[b], v[i]);
   }
   sort_desc<NB>(list);
-  merge_lists<NB, L, LPT, 1>(list);
-  const float most = list[0];
-  float bound = list[0];
+  merge_lists<NB, L, LPT, 1>(list, other);
+  const float most = fmaxf(list[0], other[0]);
+  float bound = fmaxf(list[0], other[L - 1]);
 #pragma unroll
-  for (int i = 1; i < L; ++i)
-    if (i == K - 1) bound = list[i];
+  for (int i = 1; i < L; ++i) bound = fminf(bound, fmaxf(list[i], other[L - 1 - i]));
   if (biased) bound -= near_score(bound);
   bound = fmaxf(bound, -FLT_MAX);
-  if (bound == 0.f) bound = -0.f;  // from which both zeros differ by +0
+  if (bound == 0.f) bound = -0.f;  // so that either zero less this is +0
 
   // the candidates: bit 31 - i of `hit` is logit i's, from the sign of a difference
   uint32_t hit = 0xffffffffu;
 #pragma unroll
-  for (int i = 0; i < V; ++i) hit = __funnelshift_l(__float_as_uint(v[i] - bound), hit, 1);
+  for (int i = 0; i < V; i += 2) {
+    const float2 d = __fadd2_rn(make_float2(v[i], v[i + 1]), make_float2(-bound, -bound));
+    hit = __funnelshift_l(__float_as_uint(d.x), hit, 1);
+    hit = __funnelshift_l(__float_as_uint(d.y), hit, 1);
+  }
   hit = ~hit << (32 - V);
   int at = __popc(hit);
   const int own = at;
