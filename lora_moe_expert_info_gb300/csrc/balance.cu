@@ -65,11 +65,10 @@ __device__ __forceinline__ void team_sync() {
   else __syncwarp();
 }
 
-// Turns that are fetched ahead where logits lie on the 16-byte grid.
-constexpr int kAhead = 2;
+// Logits on the 16-byte grid are fetched a turn ahead (two or three turns: 2 to 4% slower).
 template <int VEC, int LPT> constexpr bool kRing = VEC > 1 && !kBlockTokens<LPT>;
 template <int VEC, int LPT, int V, int THREADS = kBalanceThreads>
-constexpr int kRingBytes = kRing<VEC, LPT> ? kAhead * V / VEC * THREADS * 16 : 0;
+constexpr int kRingBytes = kRing<VEC, LPT> ? V / VEC * THREADS * 16 : 0;
 
 // v: a token's logits to s, zeros past E and for logits that are not finite.  Returns 1 /
 // sum of s, 0 where that is 0 and for a token that is not active.  Every thread of the
@@ -125,31 +124,29 @@ balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, c
   pdl_wait();
   pdl_trigger();
   const int64_t step = (int64_t)gridDim.x * TEAMS;
-  auto fetch = [&](int64_t t, int stage) {
+  auto fetch = [&](int64_t t) {
     if constexpr (kRing<VEC, LPT>)
-      fetch_logits<VEC, LPT, V, THREADS>(ring, logits + t * E, E, ll, t < T, stage);
+      fetch_logits<VEC, LPT, V, THREADS>(ring, logits + t * E, E, ll, t < T);
   };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch((int64_t)blockIdx.x * TEAMS + team + i * step, i);
+  fetch((int64_t)blockIdx.x * TEAMS + team);
   float acc[V] = {};
-  int tokens = 0, stage = 0;
+  int tokens = 0;
   // whether the next turn's token counts, and its place of this lane (the first of more
   // than LPT), asked for a turn before they are used
-  auto counts_in = [&](int64_t t) { return t < T && (mask == nullptr || mask[t]); };
+  auto counts_in = [&](int64_t t) { return t >= T ? 0 : mask == nullptr ? 1 : (int)__ldg(mask + t); };
   auto place = [&](int64_t t) { return t < T && ll < K ? __ldg(ids + t * K + ll) : -1; };
-  bool next_active = counts_in((int64_t)blockIdx.x * TEAMS + team);
+  int next_active = counts_in((int64_t)blockIdx.x * TEAMS + team);  // compared when it is used
   int next_first = place((int64_t)blockIdx.x * TEAMS + team);
   for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += step) {
     const int64_t t = t0 + team;
-    const bool active = next_active;
+    const bool active = next_active != 0;
     const int first = next_first;
     next_active = counts_in(t + step);
     next_first = place(t + step);
     float v[V];
     if constexpr (kRing<VEC, LPT>) {
-      take_logits<VEC, LPT, V, THREADS, kAhead>(ring, E, ll, active, stage, v);
-      fetch(t + kAhead * step, stage);
-      stage = stage == kAhead - 1 ? 0 : stage + 1;
+      take_logits<VEC, LPT, V, THREADS>(ring, E, ll, active, v);
+      fetch(t + step);
     } else {
       load_logits<VEC, LPT>(logits + (active ? t : 0) * E, E, ll, active, v);
     }
@@ -328,14 +325,11 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
     }
   }
   const int64_t step = (int64_t)gridDim.x * TEAMS;
-  auto fetch = [&](int64_t t, int stage) {
+  auto fetch = [&](int64_t t) {
     if constexpr (kRing<VEC, LPT>)
-      fetch_logits<VEC, LPT, V, kBalanceThreads>(ring, logits + t * E, E, ll, t < a.T, stage);
+      fetch_logits<VEC, LPT, V, kBalanceThreads>(ring, logits + t * E, E, ll, t < a.T);
   };
-  if (shares)
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch((int64_t)blockIdx.x * TEAMS + team + i * step, i);
-  int stage = 0;
+  if (shares) fetch((int64_t)blockIdx.x * TEAMS + team);
   for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < a.T; t0 += step) {
     const int64_t t = t0 + team;
     const bool active = t < a.T && (a.mask == nullptr || a.mask[t]);
@@ -344,9 +338,8 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
     float inv = 0.f;
     if (shares) {
       if constexpr (kRing<VEC, LPT>) {
-        take_logits<VEC, LPT, V, kBalanceThreads, kAhead>(ring, E, ll, active, stage, v);
-        fetch(t + kAhead * step, stage);
-        stage = stage == kAhead - 1 ? 0 : stage + 1;
+        take_logits<VEC, LPT, V, kBalanceThreads>(ring, E, ll, active, v);
+        if (a.mask != nullptr) fetch(t + step);
       } else {
         load_logits<VEC, LPT>(row, E, ll, active, v);
       }
@@ -449,6 +442,9 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
         }
       }
     }
+    // A mask's loads space the turns out, and the next logits are best asked for at once;
+    // without one after this turn's stores (262144 x 256: 84 and 88 us, 96 and 88).
+    if (shares && a.mask == nullptr) fetch(t + step);
     if (by_weights) {
       team_sync<LPT>();
       if (!kBlockTokens<LPT> || threadIdx.x < 32)

@@ -83,35 +83,29 @@ __device__ __forceinline__ void load_logits(const E_* row, int E, int ll, bool a
     for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
   }
 }
-// Logits on the 16-byte grid can be fetched some turns ahead: every thread of a block of
+// Logits on the 16-byte grid can be fetched a turn ahead: every thread of a block of
 // THREADS copies the units that it takes to places of its own in shared memory (16 bytes
-// each, one for every stage, unit and thread), which asks for no barrier; once they are
-// in registers their places are free for the next turn's.
-template <int THREADS>
-__device__ __forceinline__ uint4* ring_slot(uint4* ring, int units, int stage, int j) {
-  return ring + (stage * units + j) * THREADS + threadIdx.x;
-}
+// each, one for every unit and thread), which asks for no barrier; once they are in
+// registers their places are free for the next turn's.
 template <int VEC, int LPT, int V, int THREADS, typename E_>
-__device__ __forceinline__ void fetch_logits(uint4* ring, const E_* row, int E, int ll, bool have, int stage) {
+__device__ __forceinline__ void fetch_logits(uint4* ring, const E_* row, int E, int ll, bool have) {
   if (have)
 #pragma unroll
     for (int j = 0; j < V / VEC; ++j) {
       const int e = (ll + LPT * j) * VEC;
       if (e < E)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring_slot<THREADS>(ring, V / VEC, stage, j))),
-                     "l"(row + e)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(ring + j * THREADS + threadIdx.x)), "l"(row + e)
                      : "memory");
     }
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
-// Takes the logits of the turn that was fetched AHEAD turns ago.
-template <int VEC, int LPT, int V, int THREADS, int AHEAD>
-__device__ __forceinline__ void take_logits(uint4* ring, int E, int ll, bool active, int stage, float (&v)[V]) {
-  asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+template <int VEC, int LPT, int V, int THREADS>
+__device__ __forceinline__ void take_logits(const uint4* ring, int E, int ll, bool active, float (&v)[V]) {
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
   for (int j = 0; j < V / VEC; ++j) {
     float u[VEC] = {};
-    if (active && (ll + LPT * j) * VEC < E) row_widen(*ring_slot<THREADS>(ring, V / VEC, stage, j), u);
+    if (active && (ll + LPT * j) * VEC < E) row_widen(ring[j * THREADS + threadIdx.x], u);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[j * VEC + i] = u[i];
   }
