@@ -100,16 +100,17 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int lpt, float2* re
   return make_float2(warp_sum(v.x), warp_sum(v.y));
 }
 
-// 1 / sqrt(mean + eps) of a row, from its threads' sums of squares.  The rounding errors
-// of threads and warps average out over a row; what is left of fp32's errors from there
-// on would move values over rounding borders of bf16 or of the 8 bits, so the last sums,
-// the quotient and the root carry their remainders and the result is rounded once.
+// 1 / sqrt(mean + eps) of a row as the sum of two floats, from its threads' sums of
+// squares.  The rounding errors of threads and warps average out over a row; what is
+// left of fp32's errors from there on would move values over rounding borders of bf16 or
+// of the 8 bits, so the last sums, the quotient and the root carry their remainders, and
+// y is rounded once (8192 x 7168 bf16: 140 values off a border, 480 without).
 // `red`: a float per warp of the block; every thread of the block calls it.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const float s = a.x + b.x, t = s - a.x;
   return make_float2(s, (a.x - (s - t)) + (b.x - t) + a.y + b.y);
 }
-__device__ __forceinline__ float row_inverse_rms(float sum, int H, float eps, int lpt, float* red) {
+__device__ __forceinline__ float2 row_inverse_rms(float sum, int H, float eps, int lpt, float* red) {
   float2 s = make_float2(warp_sum(sum), 0.f);
   if (lpt > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wpr = lpt >> 5;
@@ -126,7 +127,30 @@ __device__ __forceinline__ float row_inverse_rms(float sum, int H, float eps, in
   const float m = 1.f / sqrtf(v.x), p = m * m;
   // one step of Newton's, from the exact square of m; none for infinities, NaN and 1 / 0
   const float left = fmaf(-v.y, p, fmaf(-v.x, fmaf(m, m, -p), fmaf(-v.x, p, 1.f)));
-  return fabsf(left) < 1e-3f ? fmaf(0.5f * m, left, m) : m;
+  return make_float2(m, fabsf(left) < 1e-3f ? 0.5f * m * left : 0.f);
+}
+// a w (m.x + m.y), rounded once; EXACT: a w needs no more than fp32's bits.  Rows whose
+// m is far from 1 go the plain way, as a w alone might overflow.
+template <bool EXACT, int N>
+__device__ __forceinline__ void row_output(float (&a)[N], const float (&w)[N], float2 m) {
+  if (!(m.x > 0x1p-40f && m.x < 0x1p40f)) {
+    row_scale(a, m.x);
+    row_mul(a, w);
+  } else if constexpr (N == 1) {
+    const float p = a[0] * w[0], left = EXACT ? 0.f : fmaf(a[0], w[0], -p);
+    a[0] = fmaf(p, m.x, fmaf(p, m.y, left * m.x));
+  } else {
+    const float2 hi = make_float2(m.x, m.x), lo = make_float2(m.y, m.y);
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 x = make_float2(a[i], a[i + 1]), v = make_float2(w[i], w[i + 1]), p = __fmul2_rn(x, v);
+      float2 t = __fmul2_rn(p, lo);
+      if constexpr (!EXACT) t = __ffma2_rn(__ffma2_rn(x, v, make_float2(-p.x, -p.y)), hi, t);
+      t = __ffma2_rn(p, hi, t);
+      a[i] = t.x;
+      a[i + 1] = t.y;
+    }
+  }
 }
 
 template <typename E_, typename W_, int VEC, int NV, bool QUANT, int MOST>
@@ -175,7 +199,7 @@ norm_kernel(const E_* x, const E_* residual, const W_* __restrict__ w, int T, in
     sum += row_dot(a, a);
     if (kEarly && c < H) wu[kEarly ? j : 0].load(w + c);
   }
-  const float m = row_inverse_rms(sum, H, eps, lpt, red);
+  const float2 m = row_inverse_rms(sum, H, eps, lpt, red);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
@@ -187,8 +211,7 @@ norm_kernel(const E_* x, const E_* residual, const W_* __restrict__ w, int T, in
 #pragma unroll
       for (int i = 0; i < VEC; ++i) wf[i] = wj.at(i);
       widen_unit(r[j], a);
-      row_mul(a, wf);  // exact for bf16 rows and weight
-      row_scale(a, m);
+      row_output<sizeof(E_) == 2 && sizeof(W_) == 2>(a, wf, m);
       narrow_unit(a, r[j]);
     }
     if (in && c < H && y != nullptr) *reinterpret_cast<U*>(y + at + c) = r[j];
