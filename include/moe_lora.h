@@ -645,7 +645,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   reaches r otherwise, null for none), and d_weight[c] = sum over rows of dy r m,
  *   float32.  dx may be dy or d_r.  workspace of moe_rms_norm_backward_workspace_bytes,
  *   256-byte aligned.
- * Sums are held in fp32 in a fixed order: results are bit-identical between runs.
+ * Sums are held in fp32 in a fixed order: results are bit-identical between runs.  A
+ *   row's sum of squares must stay within fp32's range (beyond it y comes out 0).
  * Limit: hidden <= 16384.
  *
  * moe_route: each token's topk experts from logits [num_tokens, num_experts].
