@@ -245,9 +245,9 @@ route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a)
 // the length of the sorted lists) is a lower bound of the K-th largest score; the
 // few scores above it -- 1.15 L of them where scores are in no order -- are the
 // candidates, which are ranked against one another.  Where two candidates are nearer
-// than their 32 bits tell, the candidates alone are computed in 64; where there are
-// more than 2 L of them, or two groups are that near, the token goes through
-// choose_exactly.
+// than their 32 bits tell, the candidates alone are computed in 64; of equal logits at
+// the bound only the first K stay; where there are more than 4 L of them even so, or
+// a third expert might be one of a group's two, the token goes through choose_exactly.
 //
 // A warp's time goes to the ALU pipe (maxima, comparisons), which takes an
 // instruction every two cycles.
@@ -298,6 +298,38 @@ __device__ __forceinline__ void merge_lists(float (&x)[L], float (&y)[L]) {
       merge_lists<N, L, LPT, 2 * O>(x, y);
     }
   }
+}
+
+// Of the logits in `hit` (bit 31 - i: the lane's i-th) those above the bound and the K of
+// lowest index that are equal to it: no other of these can be chosen.
+template <int VEC, int LPT, int V, typename E_>
+__device__ __noinline__ uint32_t first_equals(const E_* row, float bound, uint32_t hit, int K, int ll) {
+  uint32_t keep = 0;
+  for (uint32_t left = hit; left != 0;) {
+    const int i = __clz(left);
+    left &= ~(0x80000000u >> i);
+    if (finite_logit(row + (ll + LPT * (i / VEC)) * VEC + i % VEC) > bound) keep |= 0x80000000u >> i;
+  }
+  __syncwarp();
+  const uint32_t equal = hit & ~keep;
+#pragma unroll 1
+  for (int j = 0, before = 0; j < V / VEC; ++j) {  // in the order of the experts: by unit, then by lane
+    uint32_t own = equal & ((0xffffffffu << (32 - VEC)) >> (j * VEC));
+    int upto = __popc(own);
+#pragma unroll
+    for (int o = 1; o < LPT; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o, LPT);
+      if (ll >= o) upto += u;
+    }
+    for (int room = K - before - (upto - __popc(own)); own != 0 && room > 0; --room) {
+      const uint32_t first = 0x80000000u >> __clz(own);
+      keep |= first;
+      own &= ~first;
+    }
+    __syncwarp();
+    before += __shfl_sync(0xffffffffu, upto, LPT - 1, LPT);
+  }
+  return keep;
 }
 
 constexpr int kFastThreads = 128;
@@ -432,7 +464,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
       const float least = -part_max<LPT>(in && score > -CUDART_INF_F ? -score : -CUDART_INF_F);
       const float out = part_max<LPT>(!in ? score : -CUDART_INF_F);
       const float apart = 2.f * near_score(part_max<LPT>(size));
-      const bool close = out > -CUDART_INF_F && least - out <= apart;
+      const bool close = out > -CUDART_INF_F && !(least - out > apart);  // sums may pass fp32's range
       if (__any_sync(0xffffffffu, close)) {
         bool third = false;
         const long long sum = close && ll < a.groups ? exact_group(a, row, ll, third) : kLowest;
@@ -482,15 +514,24 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
     hit = __funnelshift_l(__float_as_uint(d.y), hit, 1);
   }
   hit = ~hit << (32 - V);
-  int at = __popc(hit);
-  const int own = at;
+  int at, n;  // where the lane's candidates go, and how many the token has
+  auto count = [&] {
+    const int own = __popc(hit);
+    at = own;
 #pragma unroll
-  for (int o = 1; o < LPT; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, at, o, LPT);
-    if (ll >= o) at += u;
+    for (int o = 1; o < LPT; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, at, o, LPT);
+      if (ll >= o) at += u;
+    }
+    n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
+    at -= own;
+  };
+  count();
+  if (!biased && __any_sync(0xffffffffu, n > CAP)) {  // rows of equal logits (of zeros, say, that pad a batch)
+    const uint32_t fewer = first_equals<VEC, LPT, V>(row, bound, hit, K, ll);
+    if (n > CAP) hit = fewer;
+    count();
   }
-  const int n = __shfl_sync(0xffffffffu, at, LPT - 1, LPT);
-  at -= own;
   slow |= n > CAP;
   while (hit != 0 && at < CAP) {
     const int i = __clz(hit);

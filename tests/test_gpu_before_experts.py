@@ -1,4 +1,6 @@
 """The operators before the experts used together with the layers that follow them."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -130,3 +132,43 @@ def test_a_block_trained(cuda_device):
     for a, t in zip(got, (xd, rd, gd, td, md)):
         # products of float32 matrices in between: a few hundred roundings of 2^-24 in a row
         assert float((a - t.grad).norm() / t.grad.norm()) < 1e-4
+
+
+def test_two_host_threads(cuda_device):
+    """The operators called by two threads at once, each on a stream of its own."""
+    T, H, E, K = 700, 520, 96, 6
+    one = torch.ones(1, device="cuda")
+
+    def inputs(seed):
+        g = torch.Generator().manual_seed(seed)
+        x, res = (torch.randn(T, H, generator=g).to(BF).cuda() for _ in range(2))
+        return x, res, torch.ones(H, dtype=BF, device="cuda"), torch.randn(T, E, generator=g).cuda()
+
+    def block(x, res, gain, l):
+        codes, exps, y, r = norm.rms_norm_fp8(x, gain, 1e-6, res)
+        ids, w = rt.moe_route(l, K, "sigmoid", None, 8, 4)
+        loss, counts = rt.moe_balance_loss(l, ids, "sigmoid")
+        dl = rt.moe_route_backward(l, ids, w, counts, one, "sigmoid")
+        return codes, exps, y, r, ids, w, loss, counts, dl, *norm.rms_norm_backward(y, r, gain, 1e-6, res)
+
+    sets = [inputs(s) for s in range(2)]
+    want = [block(*s) for s in sets]
+    torch.cuda.synchronize()
+    wrong, failed = [], []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    out = block(*sets[i])
+                    torch.cuda.current_stream().synchronize()
+                    wrong.extend(n for n, (a, b) in enumerate(zip(out, want[i])) if not torch.equal(a, b))
+        except Exception as e:  # noqa: BLE001  an exception of a thread is not the test's
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and not wrong

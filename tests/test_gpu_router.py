@@ -103,6 +103,40 @@ def test_ties_go_to_the_lowest_index(cuda_device, scoring, E, K, G, best, dtype)
         check_route(l, K, scoring, (bias * 40).round() / 40, G, best)
 
 
+@pytest.mark.parametrize("E,K", [(64, 8), (128, 1), (130, 16), (256, 8), (256, 10), (392, 8), (512, 16), (1000, 6), (1024, 12)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_rows_of_equal_logits(cuda_device, E, K, dtype, shift):
+    """Rows of one value, with none to many logits above it, and others below."""
+    T = 90
+    rng = np.random.default_rng(E + K)
+    rows = np.zeros((T, E))
+    for t in range(T):
+        rows[t] = rng.choice([0.0, -0.0, 1.5, -3.25])
+        at = rng.permutation(E)
+        more = (0, 1, K - 1, K, K + 3, 30, 31, 32, 40, E // 2)[t % 10]
+        rows[t, at[:more]] = 4 + rng.integers(0, 1 + t % 3, more)
+        rows[t, at[more:more + (t % 4) * E // 8]] = -8.0
+    l = torch.empty(T * E + shift, dtype=dtype, device="cuda")[shift:].view(T, E)
+    l.copy_(torch.from_numpy(rows))
+    check_route(l, K)
+    check_route(l, K, "sigmoid", renormalize=False)
+    if E % 8 == 0:
+        check_route(l, min(K, E // 4), "softmax", None, 8, 2, renormalize=False)
+
+
+def test_biases_whose_sums_pass_the_range(cuda_device):
+    """Scores near float32's largest, whose pairs' sums are beyond it, still have an order."""
+    E, G = 32, 4
+    bias = torch.zeros(E, device="cuda")
+    for i, b in {1: 2.0e38, 5: 3.0e38, 8: 3.1e38, 9: 2.5e38, 20: 3.3e38, 22: 3.0e38, 27: 1.0e38, -1: 2.0e37}.items():
+        bias[i] = b
+    l = logits_of(64, E, seed=5)
+    for best in (1, 2, 3):
+        check_route(l, 4, "sigmoid", bias, G, best)
+        check_route(l, 4, "sigmoid", -bias, G, best)
+
+
 @pytest.mark.parametrize("E,G,best", [(64, 1, 1), (256, 1, 1), (64, 4, 2), (256, 8, 4)])
 def test_scores_that_32_bits_do_not_tell_apart(cuda_device, E, G, best):
     """Pairs of experts whose sigmoid + bias differ by about 1e-8, in either order."""
