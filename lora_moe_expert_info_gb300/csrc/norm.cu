@@ -14,11 +14,12 @@
 // A row stays in the registers of its threads (the gradients': in their places of
 // shared memory) between the pass that reads it and the one that writes it, so every
 // tensor is moved once, and HBM bounds all of it.  8192 rows of 7168 bf16: residual and
-// norm 72 us (96% of the copy rate), with the 8 bits 90 (87%: 54% of the issue slots at
-// 20 warps an SM), gradients 76 (91%), 8 bits back 29 (89%).  1 to 256 rows: 2 to 4 us.
+// norm 72 us (96% of the copy rate), with the 8 bits 89 (87%: 54% of the issue slots at
+// 20 warps an SM), gradients 76 (91%), 8 bits back 27 (97%).  1 to 256 rows: 2 to 4 us.
 #include <cuda_fp16.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 #include "mlr_profile.cuh"
 #include "mlr_rows.cuh"
@@ -519,45 +520,100 @@ sum_parts_kernel(const float* __restrict__ part, int n, int H, float* __restrict
   if (lane == 0 && o < H) dw[o] = v;
 }
 
-// Codes and exponents back to numbers.  VEC codes a thread (16 on the 16-byte
-// grid, which one group holds; else 1).
+// Codes and exponents back to numbers, in units of VEC codes, as many as fill 16 bytes
+// of the output, so that a warp's store has whole lines.
+constexpr int kBackThreads = 256;
+
+// 2^(e - 127); a byte of 255 stands for NaN
+__device__ __forceinline__ float scale_of(uint32_t e) {
+  return __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : e << 23);
+}
+__device__ __forceinline__ float2 widen_codes(uint32_t two) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+template <int VEC> using Codes = std::conditional_t<VEC == 8, uint2, std::conditional_t<VEC == 4, uint32_t, uint8_t>>;
+// The numbers of a unit, code k times scale(k).
+template <int VEC, typename E_, typename F>
+__device__ __forceinline__ void write_back(Codes<VEC> q, F scale, E_* out) {
+  if constexpr (VEC == 1) {
+    row_narrow(widen_codes(q).x * scale(0), *out);
+  } else {
+    uint32_t w[2];
+    if constexpr (VEC == 8) w[0] = q.x, w[1] = q.y;
+    else w[0] = q;
+    float v[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC / 2; ++k) {
+      const float2 f = widen_codes(w[k / 2] >> (16 * (k & 1)));
+      v[2 * k] = f.x * scale(2 * k);
+      v[2 * k + 1] = f.y * scale(2 * k + 1);
+    }
+    uint4 o;
+    row_narrow(v, o);
+    *reinterpret_cast<uint4*>(out) = o;
+  }
+}
+
+// Rows of whole units, two to a thread (8192 x 7168 to bf16: 26.8 us; one 32.1; four 27.1
+// and slower for few rows; 16 codes to a thread, whose stores have half sectors, 29.7).
+constexpr int kBackUnits = 2;
 template <typename E_, int VEC>
-__global__ void __launch_bounds__(256)
-fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t n, int H, int groups,
+__global__ void __launch_bounds__(kBackThreads)
+fp8_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t units, int per_row, int groups,
                       E_* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
+  const int64_t first = (int64_t)blockIdx.x * (kBackThreads * kBackUnits) + threadIdx.x;
+  Codes<VEC> q[kBackUnits];
+  uint32_t e[kBackUnits];
+#pragma unroll
+  for (int j = 0; j < kBackUnits; ++j) {
+    const int64_t u = first + j * kBackThreads;
+    if (u >= units) break;
+    const int64_t row = units <= UINT32_MAX ? (uint32_t)u / (uint32_t)per_row : u / per_row;
+    q[j] = __ldg(reinterpret_cast<const Codes<VEC>*>(codes) + u);
+    e[j] = __ldg(exps + row * groups + (int)(u - row * per_row) * VEC / kGroupCols);
+  }
+#pragma unroll
+  for (int j = 0; j < kBackUnits; ++j) {
+    const int64_t u = first + j * kBackThreads;
+    if (u >= units) break;
+    const float scale = scale_of(e[j]);
+    write_back<VEC>(q[j], [&](int) { return scale; }, out + u * VEC);
+  }
+}
+
+// Rows of other lengths: a unit may begin in one group and end in the next one, which is
+// the next exponent, of the next row too.  Where that one ends as well (the last group of a
+// row has fewer than VEC columns), and for the last codes, they are taken one by one.
+template <typename E_, int VEC>
+__global__ void __launch_bounds__(kBackThreads)
+fp8_dequantize_ragged_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ exps, int64_t n, int H, int groups,
+                             E_* __restrict__ out) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t i = ((int64_t)blockIdx.x * kBackThreads + threadIdx.x) * VEC;
   if (i >= n) return;
-  const int64_t row = i / H;
-  const uint32_t e = __ldg(exps + row * groups + (int)(i - row * H) / kGroupCols);
-  // 2^(e - 127); a byte of 255 stands for NaN
-  const float scale = __uint_as_float(e == 0 ? 0x00400000u : e == 255 ? 0x7fc00000u : e << 23);
-  if constexpr (VEC == 1) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)__ldg(codes + i)));
-    row_narrow(__half2float(__ushort_as_half((uint16_t)h)) * scale, out[i]);
-  } else {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(codes + i));
-    const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-    constexpr int N = 16 / sizeof(E_);  // numbers of an output vector
-    float v[16];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(qw[k / 2] >> (16 * (k & 1)))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[2 * k] = f.x * scale;
-      v[2 * k + 1] = f.y * scale;
-    }
-#pragma unroll
-    for (int k = 0; k < 16 / N; ++k) {
-      float p[N];
-#pragma unroll
-      for (int u = 0; u < N; ++u) p[u] = v[k * N + u];
-      uint4 o;
-      row_narrow(p, o);
-      reinterpret_cast<uint4*>(out + i)[k] = o;
+  const int64_t row = n <= UINT32_MAX ? (uint32_t)i / (uint32_t)H : i / H;
+  const int c = (int)(i - row * H);
+  int64_t at = row * groups + c / kGroupCols;
+  const int first = min(kGroupCols - c % kGroupCols, H - c);  // columns left of the unit's group
+  const int second = first == H - c ? min(kGroupCols, H) : min(kGroupCols, H - c - first);
+  if (i + VEC <= n && first + second >= VEC) {
+    const Codes<VEC> q = __ldg(reinterpret_cast<const Codes<VEC>*>(codes + i));
+    const float s0 = scale_of(__ldg(exps + at)), s1 = scale_of(__ldg(exps + at + (first < VEC ? 1 : 0)));
+    write_back<VEC>(q, [&](int k) { return k < first ? s0 : s1; }, out + i);
+    return;
+  }
+  int left = first, col = c;
+  for (int64_t k = i; k < min(i + VEC, n); ++k) {
+    row_narrow(widen_codes(__ldg(codes + k)).x * scale_of(__ldg(exps + at)), out[k]);
+    if (++col == H) col = 0;
+    if (--left == 0) {
+      ++at;
+      left = min(kGroupCols, H - col);
     }
   }
 }
@@ -790,17 +846,20 @@ extern "C" int moe_fp8_dequantize(const uint8_t* codes, const uint8_t* exps, int
   if (n == 0) return MLR_OK;
   if (codes == nullptr || exps == nullptr || out == nullptr || !aligned_to(out, dtype == MLR_DTYPE_BF16 ? 2 : 4))
     return MLR_ERR_INVALID;
-  const bool whole = cols % 16 == 0 && aligned_to(codes, 16) && aligned_to(out, 16);
-  const int64_t blocks = ceil_div(n, 256 * (whole ? 16 : 1));
-  if (blocks > INT32_MAX) return MLR_ERR_UNSUPPORTED;
   const int groups = (int)ceil_div(cols, kGroupCols);
-  auto run = [&](auto kernel, auto* o) {
-    return launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(256), 0, stream, codes, exps, n, (int)cols, groups, o));
+  auto run = [&](auto kernel, int64_t blocks, int64_t count, int per_row, auto* o) {
+    if (blocks > INT32_MAX) return (int)MLR_ERR_UNSUPPORTED;
+    return launched(launch_pdl(kernel, dim3((unsigned)blocks), dim3(kBackThreads), 0, stream, codes, exps, count, per_row, groups, o));
   };
-  if (dtype == MLR_DTYPE_BF16) {
-    uint16_t* o = static_cast<uint16_t*>(out);
-    return whole ? run(fp8_dequantize_kernel<uint16_t, 16>, o) : run(fp8_dequantize_kernel<uint16_t, 1>, o);
-  }
-  float* o = static_cast<float*>(out);
-  return whole ? run(fp8_dequantize_kernel<float, 16>, o) : run(fp8_dequantize_kernel<float, 1>, o);
+  auto pick = [&](auto vec, auto* o) {
+    using E_ = std::remove_pointer_t<decltype(o)>;
+    constexpr int V = vec.value;
+    if (!aligned_to(codes, V) || !aligned_to(out, 16))
+      return run(fp8_dequantize_kernel<E_, 1>, ceil_div(n, kBackThreads * kBackUnits), n, (int)cols, o);
+    if (cols % V == 0)
+      return run(fp8_dequantize_kernel<E_, V>, ceil_div(n / V, kBackThreads * kBackUnits), n / V, (int)(cols / V), o);
+    return run(fp8_dequantize_ragged_kernel<E_, V>, ceil_div(n, kBackThreads * V), n, (int)cols, o);
+  };
+  if (dtype == MLR_DTYPE_BF16) return pick(std::integral_constant<int, 8>{}, static_cast<uint16_t*>(out));
+  return pick(std::integral_constant<int, 4>{}, static_cast<float*>(out));
 }

@@ -7,6 +7,8 @@ roundings around it, so y is within (u + (H / 2 + 8) 2^-24) |y|.  Gradients are 
 terms have the magnitude `mag`, each within (H + 16) 2^-24 of itself (m^3's error
 is 3 H / 2 2^-24, the dot product's H 2^-24: 3 H in all), then rounded once.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -133,6 +135,43 @@ def test_large_scale_codes(cuda_device):
         rc, re = ox.eight_bits(f64(y))
         assert np.array_equal(codes.cpu().numpy(), rc) and np.array_equal(exps.cpu().numpy(), re)
         assert np.array_equal(f64(norm.fp8_dequantize(codes, exps, F32)), ox.from_eight_bits(rc, re))
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (37, 1), (3, 5), (700, 7), (1, 8), (5, 12), (9, 127), (40, 128), (33, 129), (21, 130), (6, 133), (17, 1111),
+                                 (3, 2044), (4, 7168), (2, 16384)])
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("shift", [0, 1, 4])
+def test_every_code_back(cuda_device, T, H, out, shift):
+    """All codes and exponents, rows that end inside a unit, bases off the grid."""
+    g = torch.Generator().manual_seed(T + H)
+    codes = torch.randint(0, 256, (T * H + shift,), generator=g, dtype=torch.uint8).cuda()[shift:].view(T, H)
+    exps = torch.randint(0, 256, (T, (H + 127) // 128), generator=g, dtype=torch.uint8).cuda()
+    want = torch.from_numpy(ox.from_eight_bits(codes.cpu().numpy(), exps.cpu().numpy()))
+    want[(codes.cpu() & 127) == 127] = math.nan
+    want[exps.cpu().repeat_interleave(128, 1)[:, :H] == 255] = math.nan
+    # four bits are exact but below the range's normal numbers: half a step there
+    room = 2.0 ** -134 * (want.abs() < 2.0 ** -126) if out == BF else torch.zeros(T, H)
+    want = want.to(out)  # beyond the range: infinity
+    for at in (0, shift):
+        o = torch.full((T * H + at + 3,), 7.0, dtype=out, device="cuda")
+        back = norm.fp8_dequantize(codes, exps, out, o[at:at + T * H].view(T, H)).cpu()
+        same = (back == want) | (back.isnan() & want.isnan())
+        assert (same | ((back.double() - want.double()).abs() <= room)).all()
+        assert (o[:at] == 7).all() and (o[at + T * H:] == 7).all()
+
+
+@pytest.mark.parametrize("H", [7176, 7177])
+def test_codes_beyond_32_bits(cuda_device, H):
+    T = 600011
+    codes = torch.full((T, H), 0x38, dtype=torch.uint8, device=cuda_device)  # ones
+    exps = torch.full((T, (H + 127) // 128), 128, dtype=torch.uint8, device=cuda_device)
+    g = torch.Generator().manual_seed(0)
+    codes[-9:] = torch.randint(0, 127, (9, H), generator=g, dtype=torch.uint8).cuda()
+    exps[-9:] = torch.randint(100, 140, (9, exps.shape[1]), generator=g, dtype=torch.uint8).cuda()
+    assert codes.numel() > 2 ** 32
+    out = norm.fp8_dequantize(codes, exps)
+    assert torch.equal(out[-9:], norm.fp8_dequantize(codes[-9:].clone(), exps[-9:].clone()))
+    assert (out[:-9] == 2).all()
 
 
 @pytest.mark.parametrize("H", [256, 1001])
