@@ -12,6 +12,10 @@
 //   w (g - sum g w / scale) [(1 - s) for sigmoid]       renormalised
 //   scale g s (1 - s)                                   sigmoid
 //   p (scale g - sum scale g p), of all experts         softmax
+//
+// Both are bound by HBM: logits are read once a pass, a turn ahead of their use, and a
+// token's stay in the registers of its lanes.  262144 x 256 float32, padded, sigmoid: loss
+// 49 us (83% of the copy rate), gradient 86 (92%).  4096 x 128: 11 and 3 us.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -101,7 +105,8 @@ __device__ __forceinline__ float loss_of(double v, int tokens, int E, int K) {
 
 constexpr int kLossCluster = 8;
 // Up to this many logits one cluster of eight blocks takes the whole batch, which saves
-// the workspace and the second launch.
+// the workspace and the second launch: 4096 x 128 takes a caller 17 us instead of 20, though
+// the device 11 instead of 5.6.
 constexpr int64_t kOneClusterLogits = 1 << 19;
 template <int V> constexpr int kOneThreads = V == 32 ? 512 : 1024;  // of its blocks, by their registers
 
@@ -532,8 +537,9 @@ int run_backward(const void* logits, const GradArgs& a, void* d_logits, int32_t*
     const int64_t want = ceil_div(a.T, teams), most = (int64_t)blocks_per_sm(a.E) * current_sms();
     const bool shares = a.counts != nullptr || (!a.sigmoid && !a.renormalize);
     const size_t smem = (shares ? ring : 0) + (a.d_weights != nullptr ? (size_t)teams * a.E * 4 : 0);
-    return launch_with_smem(route_backward_kernel<VEC, lpt.value, v.value, E_>, dim3((unsigned)(want < most ? want : most)), dim3(kBalanceThreads), smem,
-                       ring + teams * cover * 4, stream, static_cast<const E_*>(logits), a, static_cast<E_*>(d_logits), status);
+    return launch_with_smem(route_backward_kernel<VEC, lpt.value, v.value, E_>, dim3((unsigned)(want < most ? want : most)),
+                            dim3(kBalanceThreads), smem, ring + teams * cover * 4, stream, static_cast<const E_*>(logits), a,
+                            static_cast<E_*>(d_logits), status);
   });
 }
 

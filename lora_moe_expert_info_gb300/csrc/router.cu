@@ -9,6 +9,11 @@
 //
 // The choice is decided by the real numbers that the scores stand for: where
 // 32 bits do not tell two of them apart, they are computed in 64.
+//
+// A token's logits are read once and stay in registers.  A million tokens, 8 of 256
+// experts: 240 us, 70% of the copy rate; what bounds it is the ALU pipe (55% busy) and
+// the latency of the merges and ranks, at 45% of the warps.  One token 2.8 us; 256
+// tokens of 256 experts in groups with biases 7.5, 10 where some scores are near.
 #include <float.h>
 
 #include "mlr_router.cuh"
@@ -250,7 +255,9 @@ route_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteArgs a)
 // a third expert might be one of a group's two, the token goes through choose_exactly.
 //
 // A warp's time goes to the ALU pipe (maxima, comparisons), which takes an
-// instruction every two cycles.
+// instruction every two cycles.  A block has one turn: blocks that stay and fetch the
+// next tokens' logits ahead take 339 us for a million tokens instead of 255 (fewer of
+// them for the memory, and candidates that L1 has lost).
 
 __device__ __forceinline__ void order_desc(float& a, float& b) {
   const float hi = fmaxf(a, b), lo = fminf(a, b);
