@@ -75,7 +75,8 @@ __device__ __noinline__ double exact_score(float l, const float* bias, int e) {
 }
 
 // A group's score, the sum of its two best scores, in 64 bits; `third` is set where a
-// third one is so near the second that 32 bits do not tell which of them it is.
+// third one is so near the second that 32 bits do not tell which of them it is, unless
+// all that are so near have one logit and one bias.
 template <typename E_>
 __device__ __noinline__ long long exact_group(const RouteArgs& a, const E_* row, int g, bool& third) {
   const int size = a.E / a.groups;
@@ -100,7 +101,15 @@ __device__ __noinline__ long long exact_group(const RouteArgs& a, const E_* row,
       b2 = fmaxf(b2, c);
     }
   }
-  third = b1 > -CUDART_INF_F && b1 - b2 <= near_score(b1);
+  third = false;
+  if (b1 > -CUDART_INF_F && b1 - b2 <= near_score(b1)) {
+    const float l1 = finite_logit(row + i1), c1 = a.bias != nullptr ? __ldg(a.bias + i1) : 0.f;
+#pragma unroll 1
+    for (int e = g * size; e < (g + 1) * size; ++e) {
+      const float l = finite_logit(row + e), c = a.bias != nullptr ? __ldg(a.bias + e) : 0.f;
+      third |= l > -CUDART_INF_F && fabsf(quick_sigmoid(l) + c - b1) <= near_score(b1) && (l != l1 || c != c1);
+    }
+  }
   double sum = 0.0;
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
@@ -307,15 +316,31 @@ __device__ __forceinline__ void merge_lists(float (&x)[L], float (&y)[L]) {
   }
 }
 
-// Of the logits in `hit` (bit 31 - i: the lane's i-th) those above the bound and the K of
-// lowest index that are equal to it: no other of these can be chosen.
+// Of the logits in `hit` (bit 31 - i: the lane's i-th) all but those equal to the one at
+// the bound, and of these the K of lowest index: no other of them can be chosen.  With
+// choice scores, equal are those of one logit and one bias.
 template <int VEC, int LPT, int V, typename E_>
-__device__ __noinline__ uint32_t first_equals(const E_* row, float bound, uint32_t hit, int K, int ll) {
+__device__ __noinline__ uint32_t first_equals(const E_* row, const float* bias, bool biased, float bound, uint32_t hit, int K, int ll) {
+  auto expert = [&](int i) { return (ll + LPT * (i / VEC)) * VEC + i % VEC; };
+  auto bias_of = [&](int e) { return biased && bias != nullptr ? __ldg(bias + e) : 0.f; };
+  float logit = bound, its_bias = 0.f;
+  if (biased) {
+    int at = INT32_MAX;
+    for (uint32_t left = hit; left != 0; left &= left - 1) {
+      const int e = expert(31 - (__ffs(left) - 1));
+      if (quick_sigmoid(finite_logit(row + e)) + bias_of(e) == bound) at = min(at, e);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) at = min(at, __shfl_xor_sync(0xffffffffu, at, o));
+    if (at == INT32_MAX) at = 0;  // none of the hits: then none is equal, or equals of any one go
+    logit = finite_logit(row + at);
+    its_bias = bias_of(at);
+  }
   uint32_t keep = 0;
-  for (uint32_t left = hit; left != 0;) {
-    const int i = __clz(left);
-    left &= ~(0x80000000u >> i);
-    if (finite_logit(row + (ll + LPT * (i / VEC)) * VEC + i % VEC) > bound) keep |= 0x80000000u >> i;
+  for (uint32_t left = hit; left != 0; left &= left - 1) {
+    const int i = 31 - (__ffs(left) - 1), e = expert(i);
+    if (!(finite_logit(row + e) == logit && bias_of(e) == its_bias)) keep |= 0x80000000u >> i;
   }
   __syncwarp();
   const uint32_t equal = hit & ~keep;
@@ -508,6 +533,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   float bound = fmaxf(list[0], other[L - 1]);
 #pragma unroll
   for (int i = 1; i < L; ++i) bound = fminf(bound, fmaxf(list[i], other[L - 1 - i]));
+  const float kth = bound;
   if (biased) bound -= near_score(bound);
   bound = fmaxf(bound, -FLT_MAX);
   if (bound == 0.f) bound = -0.f;  // so that either zero less this is +0
@@ -534,8 +560,8 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
     at -= own;
   };
   count();
-  if (!biased && __any_sync(0xffffffffu, n > CAP)) {  // rows of equal logits (of zeros, say, that pad a batch)
-    const uint32_t fewer = first_equals<VEC, LPT, V>(row, bound, hit, K, ll);
+  if (__any_sync(0xffffffffu, n > CAP)) {  // rows of equal logits (of zeros, say, that pad a batch)
+    const uint32_t fewer = first_equals<VEC, LPT, V>(row, a.bias, biased, kth, hit, K, ll);
     if (n > CAP) hit = fewer;
     count();
   }

@@ -125,6 +125,26 @@ def test_rows_of_equal_logits(cuda_device, E, K, dtype, shift):
         check_route(l, min(K, E // 4), "softmax", None, 8, 2, renormalize=False)
 
 
+@pytest.mark.parametrize("E,G,best,K", [(64, 1, 1, 8), (256, 1, 1, 8), (256, 8, 4, 8), (256, 8, 2, 16), (520, 1, 1, 10), (96, 8, 3, 6), (1000, 4, 1, 6)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_of_equal_scores(cuda_device, E, G, best, K, dtype):
+    """The same for sigmoid scoring: biases of one value, of a few, and of values that
+    32 bits hardly tell apart, over rows of a few logits."""
+    T = 80
+    rng = np.random.default_rng(E + G)
+    l = np.zeros((T, E))
+    for t in range(T):
+        l[t] = rng.choice([0.0, 1.5, -2.0])
+        at = rng.permutation(E)
+        more = (0, 1, K, 31, 40, E // 2)[t % 6]
+        l[t, at[:more]] = 0.25 * rng.integers(-8, 9, more)
+    l = torch.from_numpy(l).to(dtype).cuda()
+    steps = torch.from_numpy(rng.integers(0, 3, E)).cuda()
+    for bias in (None, torch.zeros(E, device="cuda"), 0.5 * steps.float(), 0.3 + steps.float() * 2.0 ** -24,
+                 torch.where(steps == 0, 0.7, 0.3).float()):
+        check_route(l, K, "sigmoid", bias, G, best)
+
+
 def test_biases_whose_sums_pass_the_range(cuda_device):
     """Scores near float32's largest, whose pairs' sums are beyond it, still have an order."""
     E, G = 32, 4
