@@ -672,6 +672,9 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   (nullable) and, given counts and d_loss[1] (both or neither), from the balance loss;
  *   zeros in masked tokens.  The same id twice in a token: both gradients are added.
  *   topk, scoring, renormalize and scale as in the forward calls.
+ * Sigmoids are held in fp32: a logit below -87 may count as one of 0 (in weights, loss
+ *   and gradients; the choice is not affected), which leaves a token that has no other
+ *   with weights of 0 where `renormalize`, and out of the loss's shares.
  * Limits: num_experts <= 4096, topk <= 32, num_groups <= 256, num_tokens * topk < 2^31 - 1.
  */
 #define MLR_SCORE_SOFTMAX 0

@@ -7,8 +7,8 @@
 // or the sum of its two best (sigmoid).  Ties go to the lowest index.  With s =
 // softmax(logits) or sigmoid(logits): w_k = scale s_k [/ sum of the chosen s].
 //
-// The choice is decided by the real numbers that the scores stand for: where
-// 32 bits do not tell two of them apart, they are computed in 64.
+// The choice is decided by the numbers that the scores stand for: where 32 bits do not
+// tell two of them apart, they are computed in 64, to a few units of the last place.
 //
 // A token's logits are read once and stay in registers.  A million tokens, 8 of 256
 // experts: 240 us, 70% of the copy rate; what bounds it is the ALU pipe (55% busy) and
