@@ -676,6 +676,7 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   and gradients; the choice is not affected), which leaves a token that has no other
  *   with weights of 0 where `renormalize`, and out of the loss's shares.
  * Limits: num_experts <= 4096, topk <= 32, num_groups <= 256, num_tokens * topk < 2^31 - 1.
+ *   Arrays that do not lie on their elements' grid are refused (MLR_ERR_INVALID).
  */
 #define MLR_SCORE_SOFTMAX 0
 #define MLR_SCORE_SIGMOID 1

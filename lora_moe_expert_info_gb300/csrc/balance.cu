@@ -571,6 +571,7 @@ extern "C" int moe_balance_loss(const void* logits, const int32_t* topk_ids, con
   const int code = check_logits(logits, num_tokens, num_experts, topk, dtype, scoring);
   if (code != MLR_OK) return code;
   if (loss == nullptr || counts == nullptr || (num_tokens > 0 && topk_ids == nullptr)) return MLR_ERR_INVALID;
+  if (!on_word_grid({topk_ids, loss, counts, d_status})) return MLR_ERR_INVALID;
   if (!(one_cluster(num_tokens, num_experts) && workspace == nullptr) &&
       (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)))
     return MLR_ERR_CAPACITY;
@@ -593,7 +594,8 @@ extern "C" int moe_route_backward(const void* logits, const int32_t* topk_ids, c
   if (code != MLR_OK) return code;
   if (num_tokens == 0) return MLR_OK;  // empty tensors may have no address
   if ((counts == nullptr) != (d_loss == nullptr) || (d_weights == nullptr && counts == nullptr)) return MLR_ERR_INVALID;
-  if (d_logits == nullptr || !aligned_to(d_logits, dtype == MLR_DTYPE_BF16 ? 2 : 4) || (d_weights != nullptr && topk_ids == nullptr))
+  if (d_logits == nullptr || !aligned_to(d_logits, dtype == MLR_DTYPE_BF16 ? 2 : 4) || (d_weights != nullptr && topk_ids == nullptr) ||
+      !on_word_grid({topk_ids, d_weights, counts, d_loss, d_status}))
     return MLR_ERR_INVALID;
   const GradArgs a{topk_ids, d_weights, counts, d_loss, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
                    renormalize != 0, scale};

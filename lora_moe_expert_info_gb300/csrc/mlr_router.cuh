@@ -3,6 +3,8 @@
 #pragma once
 #include <math_constants.h>
 
+#include <initializer_list>
+
 #include "mlr_profile.cuh"
 #include "mlr_rows.cuh"
 
@@ -161,6 +163,12 @@ inline int check_logits(const void* logits, int32_t T, int32_t E, int32_t K, int
   if (E > kMaxRouteExperts || K > kMaxRouteTopk || (int64_t)T * K >= INT32_MAX) return MLR_ERR_UNSUPPORTED;
   if (T > 0 && (logits == nullptr || !aligned_to(logits, dtype == MLR_DTYPE_BF16 ? 2 : 4))) return MLR_ERR_INVALID;
   return MLR_OK;
+}
+// Whether arrays of 32-bit elements lie on their grid (those not given do).
+inline bool on_word_grid(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!aligned_to(p, 4)) return false;
+  return true;
 }
 
 }  // namespace mlr

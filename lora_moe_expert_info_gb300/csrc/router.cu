@@ -736,7 +736,7 @@ extern "C" int moe_route(const void* logits, const float* bias, const uint8_t* t
   if (code != MLR_OK) return code;
   if (num_groups < 1 || topk_groups < 1 || topk_groups > num_groups || num_experts % num_groups != 0 ||
       (int64_t)topk > (int64_t)topk_groups * (num_experts / num_groups) || (bias != nullptr && scoring != kSigmoid) ||
-      !aligned_to(bias, 4))
+      !on_word_grid({bias, topk_ids, topk_weights, d_status}))
     return MLR_ERR_INVALID;
   if (num_groups > kMaxGroups) return MLR_ERR_UNSUPPORTED;
   if (num_tokens == 0) return MLR_OK;
