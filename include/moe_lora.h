@@ -637,7 +637,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   max|y| <= 448 * 2^s (0 for zeros), codes [num_tokens, hidden] the nearest E4M3
  *   values of y * 2^-s for y as rounded to `dtype` (infinities saturate, NaN stays),
  *   exps [num_tokens, ceil(hidden / 128)] the bytes s + 127.  y null: codes alone.
- *   y may be x, residual_out may be residual.
+ *   y may be x (without a residual r is then gone), residual_out may be residual; one
+ *   place for both outputs is refused.
  * moe_fp8_dequantize: code * 2^(exp - 127) of codes [rows, cols], rounded to `dtype`
  *   (bf16 holds every such number that is not below its range); an exp byte of 255: NaN.
  * moe_rms_norm_backward: with m = 1 / sqrt(mean(r^2) + eps) and h = dy weight

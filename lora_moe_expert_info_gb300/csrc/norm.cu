@@ -789,7 +789,7 @@ extern "C" int moe_rms_norm(const void* x, const void* residual, const void* wei
   if (!(eps >= 0.f)) return MLR_ERR_INVALID;
   if (num_tokens == 0) return MLR_OK;  // empty tensors may have no address
   if (x == nullptr || (residual == nullptr) != (residual_out == nullptr) || (codes == nullptr) != (exps == nullptr) ||
-      (y == nullptr && codes == nullptr))
+      (y == nullptr && codes == nullptr) || (y != nullptr && y == residual_out))
     return MLR_ERR_INVALID;
   // a vector's codes are stored together
   if (codes != nullptr && !aligned_to(codes, 16)) whole = false;

@@ -86,7 +86,8 @@ def _norm(x, weight, eps, residual, y, residual_out, codes, exps, eight, with_y,
 def rms_norm(x, weight, eps: float = 1e-6, residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
              residual_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(y, r) of x [T, H]: r = x + residual (x itself without one), y its norm
-    times weight [H].  y may be x and residual_out may be residual."""
+    times weight [H].  y may be x (which without a residual is r too, and then gone)
+    and residual_out may be residual."""
     return _norm(x, weight, eps, residual, y, residual_out, None, None, False, True, "rms_norm")[2:]
 
 

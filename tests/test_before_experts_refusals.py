@@ -40,3 +40,9 @@ def test_gradient_of_addresses_off_the_grid(lib, name):
     a = dict(ids=FAKE, d_weights=FAKE, counts=FAKE, d_loss=FAKE, status=None) | {name: HALF}
     assert lib.moe_route_backward(FAKE, a["ids"], a["d_weights"], a["counts"], a["d_loss"], None, 4, 16, 2, 1, 0, 1, 1.0,
                                   FAKE, a["status"], None) == mlr.MLR_ERR_INVALID
+
+
+@pytest.mark.parametrize("codes", [None, ctypes.c_void_p(0x9000)])
+def test_norm_with_one_place_for_both_outputs(lib, codes):
+    """y and the new residual stream in one buffer: the second would be lost."""
+    assert lib.moe_rms_norm(FAKE, FAKE, FAKE, 4, 64, 0, 0, 1e-6, FAKE, FAKE, codes, codes, None) == mlr.MLR_ERR_INVALID
