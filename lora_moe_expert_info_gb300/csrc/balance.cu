@@ -376,20 +376,21 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
 #pragma unroll
           for (int c = 0; c < CP; ++c) {
             s[c] = id[c] < 0 ? 0.f : a.sigmoid ? sigmoid_f(s[c]) : expf(s[c] - most);
+            dl[c] = a.sigmoid ? 1.f - s[c] : 1.f;
             total += s[c];
-            mean = fmaf(g[c], s[c], mean);
           }
-          if (a.renormalize) {
+          if (a.renormalize) {  // s to the shares of the weights
             total = part_sum<PL>(total);
+            const float lift = lift_of(total), inverse = total > 0.f ? 1.f / (total * lift) : 0.f;
+#pragma unroll
+            for (int c = 0; c < CP; ++c) {
+              s[c] = s[c] * lift * inverse;
+              mean = fmaf(g[c], s[c], mean);
+            }
             mean = part_sum<PL>(mean);
-            total = total > 0.f ? 1.f / total : 0.f;
-            mean *= total;
-          } else {
-            total = 1.f;
-            mean = 0.f;
           }
 #pragma unroll
-          for (int c = 0; c < CP; ++c) dl[c] = s[c] * total * (g[c] - mean) * (a.sigmoid ? 1.f - s[c] : 1.f);
+          for (int c = 0; c < CP; ++c) dl[c] *= s[c] * (g[c] - mean);
         }
         // an expert that a token holds twice gets both, in order
         bool twice = K > PL;

@@ -22,7 +22,14 @@ template <typename E_>
 __device__ __forceinline__ float finite_logit(const E_* p) {
   return finite_logit(row_widen(*p));
 }
-__device__ __forceinline__ float sigmoid_f(float v) { return 1.f / (1.f + expf(-v)); }
+// By e^-|v|, which does not overflow: fp32's bits down to -87, 0 below -103.
+__device__ __forceinline__ float sigmoid_f(float v) {
+  const float e = expf(-fabsf(v));
+  return (v < 0.f ? e : 1.f) / (1.f + e);
+}
+// Sums of sigmoids down to the smallest float are divisors: what is multiplied by this
+// first, divisor and dividends, has a reciprocal.
+__device__ __forceinline__ float lift_of(float total) { return total < 0x1p-100f ? 0x1p100f : 1.f; }
 // The same with the hardware's exponential and reciprocal: relative error below
 // (|v| + 5) 2^-23, at most 2.25 2^-23 as a difference.
 __device__ __forceinline__ float quick_sigmoid(float v) {

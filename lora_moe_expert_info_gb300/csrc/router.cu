@@ -667,13 +667,13 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   }
   if (a.renormalize) total = part_sum<LPT>(total);
   else total = a.sigmoid ? 1.f : all;
-  const float factor = total > 0.f ? a.scale / total : 0.f;
+  const float lift = lift_of(total), inverse = total > 0.f ? 1.f / (total * lift) : 0.f;
   if (token && !slow) {
 #pragma unroll
     for (int c = 0; c < CPL; ++c)
       if (id[c] >= 0 && rank[c] < K) {
         a.ids[t * K + rank[c]] = id[c];
-        a.weights[t * K + rank[c]] = s[c] * factor;
+        a.weights[t * K + rank[c]] = s[c] * lift * inverse * a.scale;  // the quotient, at most 1, before the scale
       }
     for (int k = n + ll; k < K; k += LPT) {
       a.ids[t * K + k] = -1;
