@@ -495,8 +495,9 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
     if (a.sigmoid) {  // two sums of two scores: twice as much as two scores may differ, and the sums' roundings
       const float least = -part_max<LPT>(in && score > -CUDART_INF_F ? -score : -CUDART_INF_F);
       const float out = part_max<LPT>(!in ? score : -CUDART_INF_F);
-      const float apart = 2.f * near_score(part_max<LPT>(size));
-      const bool close = out > -CUDART_INF_F && !(least - out > apart);  // sums may pass fp32's range
+      // a sum that passes fp32's range may look like an empty group's or like another such sum
+      const float widest = part_max<LPT>(size), apart = 2.f * near_score(widest);
+      const bool close = !(widest < CUDART_INF_F) || (out > -CUDART_INF_F && !(least - out > apart));
       if (__any_sync(0xffffffffu, close)) {
         bool third = false;
         const long long sum = close && ll < a.groups ? exact_group(a, row, ll, third) : kLowest;

@@ -53,3 +53,33 @@ def test_weights_of_the_smallest_sigmoids(cuda_device, E, K, scale):
     rd = ox.weights_backward(g.astype(float), l.astype(float), ref, "sigmoid", True, scale)
     mag = 2 * scale * np.abs(g).sum(1, keepdims=True)  # a weight's share is at most 1
     assert np.all(np.abs(f64(d) - rd) <= (eps + 4 * 2.0 ** -24) * mag)
+
+
+@pytest.mark.parametrize("E,G,K", [(32, 4, 4), (256, 8, 8), (130, 10, 6), (512, 16, 16), (48, 3, 20)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_groups_whose_sums_pass_the_range_downwards(cuda_device, E, G, K, dtype):
+    """Biases that push all experts of some groups so far away that two scores add up to
+    less than float32's lowest: those groups still have an order, above the empty ones."""
+    T, size = 40, E // G
+    rng = np.random.default_rng(E)
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(E)).to(dtype).cuda()
+    l[1::4, :size] = -math.inf                     # an empty group before all others
+    l[2::4, 2 * size:2 * size + size] = -math.inf  # one among them
+    l[3::4, 1:size] = -math.inf                    # a group of one expert
+    lowest = float(np.finfo(np.float32).min)
+    for case in range(5):
+        b = -(1.8e38 + 1.5e38 * rng.random(E))     # all groups beyond the range
+        if case == 1:
+            b[:size], b[size:2 * size] = -3.0e38, -2.0e38
+        elif case == 2:
+            b[:] = lowest                          # of equal scores the lowest index
+        elif case == 3:
+            b[-size:] = 0.1 * rng.random(size)     # one group within it
+        elif case == 4:
+            b[size:2 * size] = 1.9e38              # one beyond it upwards
+        bias = torch.from_numpy(b.astype(np.float32)).cuda()
+        for best in range(-(-K // size), G):
+            ids, w = rt.moe_route(l, K, "sigmoid", bias, G, best)
+            ref = ox.choose(f64(l), K, "sigmoid", f64(bias), G, best)
+            assert np.array_equal(ids.cpu().numpy(), ref), (case, best)
+            assert torch.isfinite(w).all()
