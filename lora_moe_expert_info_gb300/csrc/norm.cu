@@ -17,6 +17,8 @@
 // norm 72 us (96% of the copy rate), with the 8 bits 89 (87%: 54% of the issue slots at
 // 20 warps an SM), gradients 76 (91%), 8 bits back 27 (97%).  1 to 256 rows: 2 to 4 us.
 #include <cuda_fp16.h>
+#include <float.h>
+#include <math_constants.h>
 
 #include <initializer_list>
 #include <type_traits>
@@ -113,17 +115,20 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return s;
 }
 
-// 1 / sqrt(mean + eps) of a row as the sum of two floats, from its threads' sums of
-// squares.  The rounding errors of threads and warps average out over a row; what is
-// left of fp32's errors from there on would move values over rounding borders of bf16 or
-// of the 8 bits, so the last sums, the quotient and the root carry their remainders, and
-// y is rounded once (8192 x 7168 bf16: 140 values off a border, 480 without).
+// 1 / sqrt(mean + eps) of a row as up (hi + lo), from its threads' sums of squares.  The
+// rounding errors of threads and warps average out over a row; what is left of fp32's
+// errors from there on would move values over rounding borders of bf16 or of the 8 bits, so
+// the last sums, the quotient and the root carry their remainders, and y is rounded once
+// (8192 x 7168 bf16: 140 values off a border, 480 without).  up is a power of two that
+// leaves hi + lo in [1, 2]: a row times it is near 1, so that its products with the weight
+// pass the range only where y does.  lo > 0: a product of infinity stays one.
 // `red`: a float per warp of the block; every thread of the block calls it.
+struct InverseRms { float up, hi, lo; };
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   const float s = a.x + b.x, t = s - a.x;
   return make_float2(s, (a.x - (s - t)) + (b.x - t) + a.y + b.y);
 }
-__device__ __forceinline__ float2 row_inverse_rms(float sum, int H, float eps, int lpt, float* red) {
+__device__ __forceinline__ InverseRms row_inverse_rms(float sum, int H, float eps, int lpt, float* red) {
   float2 s = make_float2(warp_sum(sum), 0.f);
   if (lpt > 32) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wpr = lpt >> 5;
@@ -138,25 +143,35 @@ __device__ __forceinline__ float2 row_inverse_rms(float sum, int H, float eps, i
   const float h = (float)H, q = s.x / h;
   const float2 v = add2(make_float2(q, (fmaf(-q, h, s.x) + s.y) / h), make_float2(eps, 0.f));
   const float m = 1.f / sqrtf(v.x), p = m * m;
-  // one step of Newton's, from the exact square of m; none for infinities, NaN and 1 / 0
-  const float left = fmaf(-v.y, p, fmaf(-v.x, fmaf(m, m, -p), fmaf(-v.x, p, 1.f)));
-  return make_float2(m, fabsf(left) < 1e-3f ? 0.5f * m * left : 0.f);
+  if (!(m > 0.f && m < CUDART_INF_F)) return {m, 1.f, 0x1p-60f};  // of infinities, NaN and zeros
+  // one step of Newton's, from the exact square of m (none where that is out of range)
+  float left = fmaf(-v.y, p, fmaf(-v.x, fmaf(m, m, -p), fmaf(-v.x, p, 1.f)));
+  if (!(fabsf(left) < 0x1p-20f)) left = 0.f;  // m is within two units of the last place
+  const float up = __uint_as_float(__float_as_uint(m) & 0x7f800000u), hi = m / up;
+  return {up, hi - 0x1p-20f, fmaf(0.5f * hi, left, 0x1p-20f)};
 }
-// a w (m.x + m.y), rounded once; EXACT: a w needs no more than fp32's bits.  Rows whose
-// m is far from 1 go the plain way, as a w alone might overflow.
+// The product p, kept off infinity so that its remainder is a number.
+__device__ __forceinline__ float within_range(float p) {
+  float o;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(o) : "f"(p), "f"(FLT_MAX));
+  return o;
+}
+// a w up (hi + lo), rounded once; EXACT: a w needs no more than fp32's bits.
 template <bool EXACT, int N>
-__device__ __forceinline__ void row_output(float (&a)[N], const float (&w)[N], float2 m) {
-  if (!(m.x > 0x1p-40f && m.x < 0x1p40f)) {
-    row_scale(a, m.x);
-    row_mul(a, w);
-  } else if constexpr (N == 1) {
-    const float p = a[0] * w[0], left = EXACT ? 0.f : fmaf(a[0], w[0], -p);
-    a[0] = fmaf(p, m.x, fmaf(p, m.y, left * m.x));
+__device__ __forceinline__ void row_output(float (&a)[N], const float (&w)[N], InverseRms m) {
+  row_scale(a, m.up);
+  if constexpr (N == 1) {
+    float p = a[0] * w[0];
+    if constexpr (!EXACT) p = within_range(p);
+    const float left = EXACT ? 0.f : fmaf(a[0], w[0], -p);
+    a[0] = fmaf(p, m.hi, EXACT ? p * m.lo : fmaf(p, m.lo, left * m.hi));
   } else {
-    const float2 hi = make_float2(m.x, m.x), lo = make_float2(m.y, m.y);
+    const float2 hi = make_float2(m.hi, m.hi), lo = make_float2(m.lo, m.lo);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float2 x = make_float2(a[i], a[i + 1]), v = make_float2(w[i], w[i + 1]), p = __fmul2_rn(x, v);
+      const float2 x = make_float2(a[i], a[i + 1]), v = make_float2(w[i], w[i + 1]);
+      float2 p = __fmul2_rn(x, v);
+      if constexpr (!EXACT) p = make_float2(within_range(p.x), within_range(p.y));
       float2 t = __fmul2_rn(p, lo);
       if constexpr (!EXACT) t = __ffma2_rn(__ffma2_rn(x, v, make_float2(-p.x, -p.y)), hi, t);
       t = __ffma2_rn(p, hi, t);
@@ -218,7 +233,7 @@ norm_kernel(const E_* x, const E_* residual, const W_* __restrict__ w, int T, in
     sum += row_dot(a, a);
     if (kEarly && c < H) wu[kEarly ? j : 0].load(w + c);
   }
-  const float2 m = row_inverse_rms(sum, H, eps, lpt, red);
+  const InverseRms m = row_inverse_rms(sum, H, eps, lpt, red);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = unit_col<VEC>(lt, j, lpt);
