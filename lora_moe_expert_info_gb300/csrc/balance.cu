@@ -15,8 +15,9 @@
 //
 // Both are bound by HBM: logits are read once a pass, a turn ahead of their use, and a
 // token's stay in the registers of its lanes.  262144 x 256 float32, padded, sigmoid: loss
-// 49 us (83% of the copy rate), gradient 86 (92%).  4096 x 128: 11 and 3 us.
+// 49 us (83% of the copy rate), gradient 89 (89%).  4096 x 128: 11 and 3 us.
 #include <cooperative_groups.h>
+#include <float.h>
 
 #include <type_traits>
 
@@ -74,15 +75,23 @@ template <int VEC, int LPT> constexpr bool kRing = VEC > 1 && !kBlockTokens<LPT>
 template <int VEC, int LPT, int V, int THREADS = kBalanceThreads>
 constexpr int kRingBytes = kRing<VEC, LPT> ? V / VEC * THREADS * 16 : 0;
 
-// v: a token's logits to s, zeros past E and for logits that are not finite.  Returns 1 /
-// sum of s, 0 where that is 0 and for a token that is not active.  Every thread of the
-// warp (the block) calls it.
+// A token's logits in v, those that are not finite and those past E to -inf.  Every thread of
+// the warp calls it.
 template <int VEC, int LPT, int V>
-__device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active, float* red, float (&v)[V]) {
+__device__ __forceinline__ void close_logits(int E, int ll, float (&v)[V]) {
   if (__any_sync(0xffffffffu, !(check_finite(v) == 0.f)))
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = finite_logit(v[i]);
   close_past<VEC, LPT>(E, ll, v);
+}
+// 1 / sum, 0 where that is next to 0 (sigmoids have lost bits there, and the quotient might
+// overflow) and for a token that is not active.
+__device__ __forceinline__ float inverse_of(float sum, bool active) { return active && sum >= FLT_MIN ? 1.f / sum : 0.f; }
+// v: a token's logits to s, zeros past E and for logits that are not finite.  Returns the
+// inverse of their sum.  Every thread of the warp (the block) calls it.
+template <int VEC, int LPT, int V>
+__device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active, float* red, float (&v)[V]) {
+  close_logits<VEC, LPT>(E, ll, v);
   float sum = 0.f;
   if (sigmoid) {
 #pragma unroll
@@ -93,8 +102,23 @@ __device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += v[i] = __expf(v[i] - most);
   }
-  sum = team_sum<LPT>(sum, red);
-  return active && sum > 0.f ? 1.f / sum : 0.f;
+  return inverse_of(team_sum<LPT>(sum, red), active);
+}
+// v: a token's logits to s (1 - s) of sigmoids s; `mean` the sum of s coef over that of s.
+template <int VEC, int LPT, int V>
+__device__ __forceinline__ float slopes(int E, int ll, bool active, float* red, const float (&coef)[V], float (&v)[V],
+                                        float& mean) {
+  close_logits<VEC, LPT>(E, ll, v);
+  float sum = 0.f, dot = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float s = quick_sigmoid(v[i], v[i]);
+    sum += s;
+    dot = fmaf(s, coef[i], dot);
+  }
+  const float inv = inverse_of(team_sum<LPT>(sum, red), active);
+  mean = team_sum<LPT>(dot, red) * inv;
+  return inv;
 }
 
 // The loss of v = sum over experts of shares times pairs.
@@ -340,7 +364,7 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
     const bool active = t < a.T && (a.mask == nullptr || a.mask[t]);
     const E_* row = logits + (active ? t : 0) * E;
     float v[V] = {};
-    float inv = 0.f;
+    float inv = 0.f, dot = 0.f;
     if (shares) {
       if constexpr (kRing<VEC, LPT>) {
         take_logits<VEC, LPT, V, kBalanceThreads>(ring, E, ll, active, v);
@@ -348,7 +372,7 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
       } else {
         load_logits<VEC, LPT>(row, E, ll, active, v);
       }
-      inv = scores<VEC, LPT>(E, a.sigmoid, ll, active, red, v);
+      inv = a.sigmoid ? slopes<VEC, LPT>(E, ll, active, red, coef, v, dot) : scores<VEC, LPT>(E, false, ll, active, red, v);
     }
     int id[CP];
     if (by_weights) {
@@ -375,8 +399,8 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
           if (!a.sigmoid) most = part_max<PL>(most);
 #pragma unroll
           for (int c = 0; c < CP; ++c) {
+            dl[c] = a.sigmoid ? sigmoid_f(-s[c]) : 1.f;  // not 1 - s, which cancels
             s[c] = id[c] < 0 ? 0.f : a.sigmoid ? sigmoid_f(s[c]) : expf(s[c] - most);
-            dl[c] = a.sigmoid ? 1.f - s[c] : 1.f;
             total += s[c];
           }
           if (a.renormalize) {  // s to the shares of the weights
@@ -412,19 +436,20 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
       team_sync<LPT>();
     }
     // d: what the place's lane has left of an expert
-    float dot = 0.f;
+    if (shares && !a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < V / VEC; ++j) {
-      const int e = (ll + LPT * j) * VEC;
+      for (int j = 0; j < V / VEC; ++j) {
+        const int e = (ll + LPT * j) * VEC;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const int n = j * VEC + i;
-        float q = coef[n];
-        if (all_chosen && e < E) q += row_s[e + i];
-        dot = fmaf(v[n], q, dot);
+        for (int i = 0; i < VEC; ++i) {
+          const int n = j * VEC + i;
+          float q = coef[n];
+          if (all_chosen && e < E) q += row_s[e + i];
+          dot = fmaf(v[n], q, dot);
+        }
       }
+      dot = team_sum<LPT>(dot, red) * inv;
     }
-    if (shares) dot = team_sum<LPT>(dot, red) * inv;
 #pragma unroll
     for (int j = 0; j < V / VEC; ++j) {
       const int e = (ll + LPT * j) * VEC;
@@ -435,8 +460,7 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
         const int n = j * VEC + i;
         const float d = by_weights ? row_s[e + i] : 0.f;
         const float p = v[n] * inv;
-        if (all_chosen) o[i] = p * (coef[n] + d - dot);
-        else o[i] = fmaf(a.sigmoid ? p * (1.f - v[n]) : p, coef[n] - dot, d);
+        o[i] = all_chosen ? p * (coef[n] + d - dot) : fmaf(p, coef[n] - dot, d);
       }
       if (t < a.T) {
         if constexpr (VEC == 1) {

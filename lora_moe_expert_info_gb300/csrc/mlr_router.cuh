@@ -38,6 +38,14 @@ __device__ __forceinline__ float quick_sigmoid(float v) {
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
+// The same, and in `slope` s (1 - s) from the smaller of the two: 1 - s from s would cancel.
+__device__ __forceinline__ float quick_sigmoid(float v, float& slope) {
+  float e, r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fabsf(v) * -1.44269504f));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  slope = e * r * r;
+  return v < 0.f ? e * r : r;
+}
 
 // A token's logits in LPT lanes, V each: unit j of lane ll is number ll + LPT j, VEC
 // logits (16 bytes, or one where rows lie off that grid).

@@ -83,3 +83,51 @@ def test_groups_whose_sums_pass_the_range_downwards(cuda_device, E, G, K, dtype)
             ref = ox.choose(f64(l), K, "sigmoid", f64(bias), G, best)
             assert np.array_equal(ids.cpu().numpy(), ref), (case, best)
             assert torch.isfinite(w).all()
+
+
+def complement(l):
+    """1 - sigmoid, without the difference."""
+    return ox.sigmoid(-l)
+
+
+@pytest.mark.parametrize("E,K", KINDS)
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gradients_of_sigmoids_near_one(cuda_device, E, K, renormalize):
+    """Logits of 8 to 80: the gradients have the factor 1 - sigmoid, which is far below the
+    last place of the sigmoid, and are right relative to themselves."""
+    T = 200
+    rng = np.random.default_rng(E)
+    l = rng.uniform(8, np.linspace(9, 80, T)[:, None], (T, E)).astype(np.float32)
+    l[:, ::3] *= -1
+    lt = torch.from_numpy(l).cuda()
+    ids, _ = rt.moe_route(lt, K, "sigmoid")
+    idn, ln = ids.cpu().numpy(), l.astype(float)
+    g = rng.normal(size=(T, K)).astype(np.float32)
+    near, gd = np.take_along_axis(complement(ln), idn, 1), g.astype(float)
+    s = np.take_along_axis(ox.sigmoid(ln), idn, 1)
+    if renormalize:
+        share = s / s.sum(1, keepdims=True)
+        part = 2.5 * share * (gd - (gd * share).sum(1, keepdims=True)) * near
+        mag = 2.5 * share * (np.abs(gd) + (np.abs(gd) * share).sum(1, keepdims=True)) * near
+    else:
+        part = 2.5 * gd * s * near
+        mag = np.abs(part)
+    want, room = np.zeros((T, E)), np.zeros((T, E))
+    np.put_along_axis(want, idn, part, 1)
+    np.put_along_axis(room, idn, mag, 1)
+    # a share: exponential and quotient 6, divisor 6 + K, 2 more; the mean of K shares 14 + 2 K;
+    # the complement 6, products 4
+    eps = (3 * K + 40) * 2.0 ** -24
+    d = rt.moe_route_backward(lt, ids, torch.from_numpy(g).cuda(), scoring="sigmoid", renormalize=renormalize, scale=2.5)
+    assert np.all(np.abs(f64(d) - want) <= eps * room + 2.0 ** -140)
+    # the loss's: p (1 - s) (a - sum p a)
+    loss, counts = rt.moe_balance_loss(lt, ids, "sigmoid")
+    one = torch.tensor([0.7], device="cuda")
+    a = float(one) * f64(counts)[:E] * E / (K * T * T)
+    p = ox.sigmoid(ln) / ox.sigmoid(ln).sum(1, keepdims=True)
+    want = p * complement(ln) * (a - (p * a).sum(1, keepdims=True))
+    room = p * complement(ln) * (a + (p * a).sum(1, keepdims=True))
+    # the same with sums over E experts, and reciprocals a unit of the last place off
+    eps = (3 * E + 56) * 2.0 ** -24
+    d = rt.moe_route_backward(lt, ids, counts=counts, d_loss=one, scoring="sigmoid")
+    assert np.all(np.abs(f64(d) - want) <= eps * room + 2.0 ** -140)
