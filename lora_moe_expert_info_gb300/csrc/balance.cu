@@ -308,6 +308,20 @@ balance_total_kernel(const float* __restrict__ part, const int32_t* __restrict__
   cluster.sync();  // the blocks' shared memory is read until here
 }
 
+// a b with what its rounding leaves, as the sum of two floats.
+__device__ __forceinline__ float2 product2(float a, float b) {
+  const float p = a * b;
+  return make_float2(p, fmaf(a, b, -p));
+}
+// d E / (K n^2) so.
+__device__ __forceinline__ float2 coefficient2(float d, float E, float K, float n) {
+  const float2 nn = product2(n, n), a = product2(d, E);
+  float2 b = product2(nn.x, K);
+  b.y = fmaf(nn.y, K, b.y);
+  const float q = a.x / b.x;
+  return make_float2(q, __fdividef(fmaf(-q, b.x, a.x) + fmaf(-q, b.y, a.y), b.x));
+}
+
 struct GradArgs {
   const int32_t* ids;
   const float* d_weights;  // nullable: no gradient of the weights
@@ -344,13 +358,16 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
   pdl_trigger();
   float coef[V] = {};
   if (a.counts != nullptr) {
-    // in fp32: 64-bit operations for every expert of every thread took 14% of the time
-    const float n = (float)max(1, __ldg(a.counts + E));
-    const float f = __ldg(a.d_loss) * ((float)E / (float)K) / n / n;
+    // as the sum of two floats, so that a coefficient is rounded once (64-bit operations for
+    // every expert of every thread took 14% of the time); counts are, beyond 2^24
+    const float2 f = coefficient2(__ldg(a.d_loss), (float)E, (float)K, (float)max(1, __ldg(a.counts + E)));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
-      if (e < E) coef[i] = f * (float)__ldg(a.counts + e);
+      if (e < E) {
+        const float c = (float)__ldg(a.counts + e);
+        coef[i] = fmaf(f.x, c, f.y * c);
+      }
     }
   }
   const int64_t step = (int64_t)gridDim.x * TEAMS;

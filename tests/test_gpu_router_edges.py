@@ -131,3 +131,19 @@ def test_gradients_of_sigmoids_near_one(cuda_device, E, K, renormalize):
     eps = (3 * E + 56) * 2.0 ** -24
     d = rt.moe_route_backward(lt, ids, counts=counts, d_loss=one, scoring="sigmoid")
     assert np.all(np.abs(f64(d) - want) <= eps * room + 2.0 ** -140)
+
+
+@pytest.mark.parametrize("T,K", [(7, 3), (1531, 3), (12347, 7), (300001, 5), (1000003, 1)])
+def test_coefficients_of_the_loss_are_rounded_once(cuda_device, T, K):
+    """Two experts with equal logits and every pair with the first: its gradient is exactly a
+    quarter of d_loss c E / (K N^2), in one rounding (2^-24) of that number.  Its two factors
+    are held to 2^-44; the rest (2 a / 4, halves of 1) is exact."""
+    l = torch.full((T, 2), 0.75, device="cuda")
+    ids = torch.zeros(T, K, dtype=torch.int32, device="cuda")
+    _, counts = rt.moe_balance_loss(l, ids)
+    assert counts.tolist() == [T * K, 0, T]
+    for v in (0.01, 0.3, 1.0, 1.7, 1e-20, 3e20):
+        one = torch.tensor([v], device="cuda")
+        d = f64(rt.moe_route_backward(l, ids, counts=counts, d_loss=one))
+        want = float(one) * T * K * 2 / (K * float(T) * T) / 4
+        assert np.all(np.abs(d[:, 0] - want) <= 2.0 ** -24 * (1 + 2.0 ** -10) * want) and np.array_equal(d[:, 1], -d[:, 0])
