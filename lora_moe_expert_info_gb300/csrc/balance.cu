@@ -132,6 +132,7 @@ constexpr int kLossCluster = 8;
 // the workspace and the second launch: 4096 x 128 takes a caller 17 us instead of 20, though
 // the device 11 instead of 5.6.
 constexpr int64_t kOneClusterLogits = 1 << 19;
+constexpr uint32_t kTurns = 64;  // of a thread's sum of shares
 template <int V> constexpr int kOneThreads = V == 32 ? 512 : 1024;  // of its blocks, by their registers
 
 // Sums of shares and pairs per expert over the block's tokens.  ONE: the grid is one
@@ -152,61 +153,72 @@ balance_kernel(const E_* __restrict__ logits, const int32_t* __restrict__ ids, c
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int64_t step = (int64_t)gridDim.x * TEAMS;
-  auto fetch = [&](int64_t t) {
+  // tokens as unsigned numbers: the one a turn after the last is below 2^32
+  const uint32_t step = gridDim.x * TEAMS;
+  uint32_t t = blockIdx.x * TEAMS + team;
+  auto fetch = [&](uint32_t t) {
     if constexpr (kRing<VEC, LPT>)
-      fetch_logits<VEC, LPT, V, THREADS>(ring, logits + t * E, E, ll, t < T);
+      fetch_logits<VEC, LPT, V, THREADS>(ring, logits + (int64_t)t * E, E, ll, t < (uint32_t)T);
   };
-  fetch((int64_t)blockIdx.x * TEAMS + team);
-  float acc[V] = {};
+  fetch(t);
   int tokens = 0;
   // whether the next turn's token counts, and its place of this lane (the first of more
   // than LPT), asked for a turn before they are used
-  auto counts_in = [&](int64_t t) { return t >= T ? 0 : mask == nullptr ? 1 : (int)__ldg(mask + t); };
-  auto place = [&](int64_t t) { return t < T && ll < K ? __ldg(ids + t * K + ll) : -1; };
-  int next_active = counts_in((int64_t)blockIdx.x * TEAMS + team);  // compared when it is used
-  int next_first = place((int64_t)blockIdx.x * TEAMS + team);
-  for (int64_t t0 = (int64_t)blockIdx.x * TEAMS; t0 < T; t0 += step) {
-    const int64_t t = t0 + team;
-    const bool active = next_active != 0;
-    const int first = next_first;
-    next_active = counts_in(t + step);
-    next_first = place(t + step);
-    float v[V];
-    if constexpr (kRing<VEC, LPT>) {
-      take_logits<VEC, LPT, V, THREADS>(ring, E, ll, active, v);
-      fetch(t + step);
-    } else {
-      load_logits<VEC, LPT>(logits + (active ? t : 0) * E, E, ll, active, v);
-    }
-    const float inv = scores<VEC, LPT>(E, sigmoid, ll, active, red, v);
+  auto counts_in = [&](uint32_t t) { return t >= (uint32_t)T ? 0 : mask == nullptr ? 1 : (int)__ldg(mask + t); };
+  auto place = [&](uint32_t t) { return t < (uint32_t)T && ll < K ? __ldg(ids + (int64_t)t * K + ll) : -1; };
+  int next_active = counts_in(t);  // compared when it is used
+  int next_first = place(t);
+  // Sums go to the warp's row (the block's) kTurns at a time: in a longer one, rows of one
+  // kind would be rounded the same way at every addition.
+  uint32_t left = blockIdx.x * TEAMS < (uint32_t)T ? (T - blockIdx.x * TEAMS - 1) / step + 1 : 0;  // turns
+  bool added = false;
+  do {
+    float acc[V] = {};
+    uint32_t turns = min(left, kTurns);
+    left -= turns;
+    for (; turns > 0; --turns, t += step) {
+      const bool active = next_active != 0;
+      const int first = next_first;
+      next_active = counts_in(t + step);
+      next_first = place(t + step);
+      float v[V];
+      if constexpr (kRing<VEC, LPT>) {
+        take_logits<VEC, LPT, V, THREADS>(ring, E, ll, active, v);
+        fetch(t + step);
+      } else {
+        load_logits<VEC, LPT>(logits + (active ? (int64_t)t : 0) * E, E, ll, active, v);
+      }
+      const float inv = scores<VEC, LPT>(E, sigmoid, ll, active, red, v);
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 q = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv), make_float2(acc[i], acc[i + 1]));
-      acc[i] = q.x;
-      acc[i + 1] = q.y;
-    }
-    if (active) {
-      ++tokens;
-      for (int k = ll; k < K; k += LPT) {
-        const int id = k == ll ? first : __ldg(ids + t * K + k);
-        if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
-        else if (id != -1) set_status(status, MLR_STATUS_INDEX);
+      for (int i = 0; i < V; i += 2) {
+        const float2 q = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(inv, inv), make_float2(acc[i], acc[i + 1]));
+        acc[i] = q.x;
+        acc[i + 1] = q.y;
+      }
+      if (active) {
+        ++tokens;
+        for (int k = ll; k < K; k += LPT) {
+          const int id = k == ll ? first : __ldg(ids + (int64_t)t * K + k);
+          if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+          else if (id != -1) set_status(status, MLR_STATUS_INDEX);
+        }
       }
     }
-  }
+    if constexpr (!kBlockTokens<LPT>)
+#pragma unroll
+      for (int o = LPT; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (kBlockTokens<LPT> || (threadIdx.x & 31) < LPT)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
+        float* sum = sums + (kBlockTokens<LPT> ? 0 : threadIdx.x >> 5) * E + e;
+        if (e < E) *sum = added ? *sum + acc[i] : acc[i];
+      }
+    added = true;
+  } while (left > 0);
   if (ll == 0) atomicAdd(&hist[E], tokens);
-  if constexpr (!kBlockTokens<LPT>)
-#pragma unroll
-    for (int o = LPT; o < 32; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-  if (kBlockTokens<LPT> || (threadIdx.x & 31) < LPT)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = (ll + LPT * (i / VEC)) * VEC + i % VEC;
-      if (e < E) sums[(kBlockTokens<LPT> ? 0 : threadIdx.x >> 5) * E + e] = acc[i];
-    }
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += THREADS) {
     if (!ONE) count[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];

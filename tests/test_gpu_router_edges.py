@@ -147,3 +147,20 @@ def test_coefficients_of_the_loss_are_rounded_once(cuda_device, T, K):
         d = f64(rt.moe_route_backward(l, ids, counts=counts, d_loss=one))
         want = float(one) * T * K * 2 / (K * float(T) * T) / 4
         assert np.all(np.abs(d[:, 0] - want) <= 2.0 ** -24 * (1 + 2.0 ** -10) * want) and np.array_equal(d[:, 1], -d[:, 0])
+
+
+@pytest.mark.parametrize("E,log_T,dtype", [(2, 27, BF), (3, 26, F32), (8, 26, BF), (64, 22, F32)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_shares_of_very_many_tokens(cuda_device, E, log_T, dtype, scoring):
+    """Rows of one kind, as padding gives, where every addition is rounded the same way: with
+    all pairs of expert 0 the loss is E times its share.  A sum of a thread takes 64 shares
+    at a time, and there are then at most T / 2^16 + 64 of these, of warps and of blocks."""
+    T = 1 << log_T
+    row = torch.linspace(0.3, -0.9, E).to(dtype)
+    l = row.cuda().expand(T, E).contiguous()
+    ids = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    loss, counts = rt.moe_balance_loss(l, ids, scoring)
+    assert int(counts[0]) == T == int(counts[-1])
+    s = ox.scores(f64(row)[None], scoring)[0]
+    want = E * s[0] / s.sum()
+    assert abs(float(loss) - want) <= (64 + T / 2 ** 16 / 16 + 64 + E + 24) * 2.0 ** -24 * want
