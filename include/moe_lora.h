@@ -675,7 +675,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   topk, scoring, renormalize and scale as in the forward calls.
  * Sigmoids are held in fp32: a logit below -87 may count as one of 0 (in weights, loss
  *   and gradients; the choice is not affected), which leaves a token that has no other
- *   with weights of 0 where `renormalize`, and out of the loss's shares.
+ *   with weights of 0 where `renormalize`, and out of the loss's shares; a share of the
+ *   loss below 2^-126 may count as 0.
  * Limits: num_experts <= 4096, topk <= 32, num_groups <= 256, num_tokens * topk < 2^31 - 1.
  *   Arrays that do not lie on their elements' grid are refused (MLR_ERR_INVALID).
  */

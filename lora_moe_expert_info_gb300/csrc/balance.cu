@@ -95,12 +95,12 @@ __device__ __forceinline__ float scores(int E, bool sigmoid, int ll, bool active
   float sum = 0.f;
   if (sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += v[i] = quick_sigmoid(v[i]);
+    for (int i = 0; i < V; ++i) sum += v[i] = share_sigmoid(v[i]);
   } else {
     float most = team_max<LPT>(max_of<0, 1>(v), red);
     most = most > -CUDART_INF_F ? most : 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += v[i] = __expf(v[i] - most);
+    for (int i = 0; i < V; ++i) sum += v[i] = share_exp(v[i] - most);
   }
   return inverse_of(team_sum<LPT>(sum, red), active);
 }
@@ -112,7 +112,7 @@ __device__ __forceinline__ float slopes(int E, int ll, bool active, float* red, 
   float sum = 0.f, dot = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float s = quick_sigmoid(v[i], v[i]);
+    const float s = share_sigmoid(v[i], v[i]);
     sum += s;
     dot = fmaf(s, coef[i], dot);
   }

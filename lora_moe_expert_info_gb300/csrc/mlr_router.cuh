@@ -38,13 +38,27 @@ __device__ __forceinline__ float quick_sigmoid(float v) {
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
-// The same, and in `slope` s (1 - s) from the smaller of the two: 1 - s from s would cancel.
-__device__ __forceinline__ float quick_sigmoid(float v, float& slope) {
-  float e, r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(fabsf(v) * -1.44269504f));
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+// e^x for x <= 0 in a few instructions, whatever x within 5 2^-24 of itself: 2^h with h = x /
+// ln 2 rounded, times 1 plus x - h ln 2, which the rounding leaves.  0 below 2^-126.
+__device__ __forceinline__ float share_exp(float x) {
+  x = fmaxf(x, -100.f);  // -inf has no remainder
+  const float h = x * 1.44269504f, left = fmaf(h, 1.90465421e-9f, fmaf(h, -0x1.62e43p-1f, x));  // ln 2 in two parts
+  float p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(h));
+  return fmaf(p, left, p);
+}
+// The sigmoid within 9 2^-24 of itself down to -87; in `slope` s (1 - s) from the smaller of
+// the two, as 1 - s from s would cancel.
+__device__ __forceinline__ float share_sigmoid(float v, float& slope) {
+  const float e = share_exp(-fabsf(v));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   slope = e * r * r;
   return v < 0.f ? e * r : r;
+}
+__device__ __forceinline__ float share_sigmoid(float v) {
+  float slope;
+  return share_sigmoid(v, slope);
 }
 
 // A token's logits in LPT lanes, V each: unit j of lane ll is number ll + LPT j, VEC

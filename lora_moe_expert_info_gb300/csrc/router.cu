@@ -433,7 +433,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   if (!a.sigmoid && !a.renormalize) {
     const float most = part_max<LPT>(max_of<0, 1>(v));
 #pragma unroll
-    for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? __expf(v[i] - most) : 0.f;
+    for (int i = 0; i < V; ++i) all += v[i] > -CUDART_INF_F ? share_exp(v[i] - most) : 0.f;
     all = part_sum<LPT>(all);
   }
   if (biased) {
@@ -662,7 +662,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   for (int c = 0; c < CPL; ++c) {
     s[c] = 0.f;
     if (id[c] >= 0 && rank[c] < K) {
-      s[c] = a.sigmoid ? sigmoid_f(logit[c]) : __expf(logit[c] - most);
+      s[c] = a.sigmoid ? sigmoid_f(logit[c]) : expf(logit[c] - most);
       total += s[c];
     }
   }

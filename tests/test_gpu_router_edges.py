@@ -164,3 +164,44 @@ def test_shares_of_very_many_tokens(cuda_device, E, log_T, dtype, scoring):
     s = ox.scores(f64(row)[None], scoring)[0]
     want = E * s[0] / s.sum()
     assert abs(float(loss) - want) <= (64 + T / 2 ** 16 / 16 + 64 + E + 24) * 2.0 ** -24 * want
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("E,K", [(4, 3), (8, 8), (64, 16), (6, 2), (1100, 3), (40, 20)])
+def test_far_below_the_largest(cuda_device, E, K, dtype):
+    """Weights, shares and gradients of logits up to 86 below the row's largest, at whole
+    numbers so that the differences are exact: right relative to themselves, whose error is
+    the exponential's few units of the last place, not one that grows with the difference."""
+    T = 87
+    rng = np.random.default_rng(E + K)
+    l = np.full((T, E), -np.inf)
+    for t in range(T):
+        at = rng.permutation(E)[:K]
+        l[t, at] = 20 - rng.integers(0, t + 1, K)
+        l[t, at[0]], l[t, at[1]] = 20.0, 20.0 - t
+    lt = torch.from_numpy(l).to(dtype).cuda()
+    # in units of 2^-24: an exponential 5, a sigmoid from it 9 (1 + e 1, reciprocal 2, product 1);
+    # the divisor's K terms K + 9; quotient, scale and final sum 2: K + 20
+    eps = (2 * K + 20) * 2.0 ** -24
+    half = 2.0 ** -8 if dtype == BF else 2.0 ** -24
+    for renormalize in (True, False):
+        ids, w = rt.moe_route(lt, K, renormalize=renormalize, scale=2.5)
+        ref = ox.choose(l, K, "softmax")
+        assert np.array_equal(ids.cpu().numpy(), ref)
+        rw = ox.weights(l, ref, "softmax", renormalize, 2.5)
+        assert np.all(np.abs(f64(w) - rw) <= eps * rw)
+    # the loss of a token's smallest expert alone, by itself: 1 token, its share
+    for t in range(0, T, 9):
+        for scoring in ("softmax", "sigmoid"):
+            row = l[t:t + 1] - (20 if scoring == "sigmoid" else 0)
+            rowt = torch.from_numpy(row).to(dtype).cuda()
+            low = int(np.where(np.isfinite(row[0]), row[0], 1e9).argmin())
+            one = torch.full((1, 1), low, dtype=torch.int32, device="cuda")
+            loss, counts = rt.moe_balance_loss(rowt, one, scoring)
+            want, rc = ox.balance(row, np.array([[low]]), scoring)
+            assert abs(float(loss) - want) <= eps * want
+            dl = torch.ones(1, device="cuda")
+            d = f64(rt.moe_route_backward(rowt, one, counts=counts, d_loss=dl, scoring=scoring))
+            rd = ox.balance_backward(1.0, row, rc, 1, scoring)
+            # of p (a - p_low a) [(1 - s)]: the others' gradients are p times p_low
+            assert np.all(np.abs(d - rd) <= (half + 2 * eps) * np.abs(rd) + 2.0 ** -133 + 2 * (half + 2 * eps) * want * ox.scores(row, scoring))
