@@ -513,6 +513,17 @@ route_backward_kernel(const E_* __restrict__ logits, const __grid_constant__ Gra
       team_sync<LPT>();
     }
   }
+  // Coefficients beyond the range (a loss scale that ran over) made NaN of the masked tokens'
+  // zeros: each thread writes its own again.  A coefficient is at most d_loss E, E of them E times that.
+  if (a.counts != nullptr && a.mask != nullptr && !(fabsf(__ldg(a.d_loss)) < FLT_MAX / kMaxRouteExperts / kMaxRouteExperts)) {
+#pragma unroll 1
+    for (int64_t t = (int64_t)blockIdx.x * TEAMS + team; t < a.T; t += step) {
+      if (a.mask[t]) continue;
+#pragma unroll 1
+      for (int e = ll * VEC; e < E; e += LPT * VEC)
+        for (int i = 0; i < VEC; ++i) row_narrow(0.f, d_logits[t * E + e + i]);
+    }
+  }
 }
 
 // f<LPT, V>() for E experts.

@@ -205,3 +205,19 @@ def test_far_below_the_largest(cuda_device, E, K, dtype):
             rd = ox.balance_backward(1.0, row, rc, 1, scoring)
             # of p (a - p_low a) [(1 - s)]: the others' gradients are p times p_low
             assert np.all(np.abs(d - rd) <= (half + 2 * eps) * np.abs(rd) + 2.0 ** -133 + 2 * (half + 2 * eps) * want * ox.scores(row, scoring))
+
+
+@pytest.mark.parametrize("E", [16, 61, 256, 1100])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_masked_tokens_under_an_infinite_gradient(cuda_device, E, scoring):
+    """A loss scale that ran over leaves zeros in masked tokens."""
+    l = torch.randn(50, E, generator=torch.Generator().manual_seed(0)).cuda()
+    mask = torch.arange(50, device="cuda") % 3 != 1
+    ids, w = rt.moe_route(l, 4, scoring, token_mask=mask)
+    _, counts = rt.moe_balance_loss(l, ids, scoring, mask)
+    for v in (math.inf, math.nan, 3e38):
+        bad = torch.full((1,), v, device="cuda")
+        for g in (None, w, torch.full_like(w, v)):
+            for renormalize in (True, False):
+                d = rt.moe_route_backward(l, ids, g, counts, bad, scoring, renormalize, 1.0, mask)
+                assert not d[~mask].any() and (v == 3e38 or not torch.isfinite(d[mask]).all())
