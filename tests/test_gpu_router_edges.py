@@ -221,3 +221,31 @@ def test_masked_tokens_under_an_infinite_gradient(cuda_device, E, scoring):
             for renormalize in (True, False):
                 d = rt.moe_route_backward(l, ids, g, counts, bad, scoring, renormalize, 1.0, mask)
                 assert not d[~mask].any() and (v == 3e38 or not torch.isfinite(d[mask]).all())
+
+
+@pytest.mark.parametrize("E,dtype", [(1024, BF), (1020, BF), (1024, F32)])
+def test_offsets_beyond_32_bits(cuda_device, E, dtype):
+    """More than 2^31 logits through the kernels of up to 1024 experts: the last tokens come
+    out as they do alone."""
+    T, K = (1 << 31) // E + 5, 4
+    l = torch.zeros(T, E, dtype=dtype, device="cuda")
+    tail = torch.randn(7, E, generator=torch.Generator().manual_seed(1)).to(dtype).cuda()
+    l[-7:] = tail
+    assert l.numel() > 1 << 31
+    bias = torch.linspace(0, 0.1, E, device="cuda")
+    for scoring, b, G, best in (("softmax", None, 1, 1), ("sigmoid", bias, 4, 2)):
+        ids, w = rt.moe_route(l, K, scoring, b, G, best, token_mask=None)
+        i2, w2 = rt.moe_route(tail, K, scoring, b, G, best)
+        assert torch.equal(ids[-7:], i2) and torch.equal(w[-7:], w2)
+        assert (ids[:-7] == ids[0]).all() and (w[:-7] == w[0]).all()
+        loss, counts = rt.moe_balance_loss(l, ids, scoring)
+        of_tail = torch.bincount(i2.flatten().long(), minlength=E)
+        first = torch.zeros(E, dtype=torch.long, device="cuda")
+        first[ids[0].long()] = T - 7
+        assert int(counts[-1]) == T and torch.equal(counts[:-1].long(), first + of_tail)
+        assert abs(float(loss) - 1) < 1e-2  # all but seven tokens use every expert alike
+        one = torch.ones(1, device="cuda")
+        d = rt.moe_route_backward(l, ids, w, counts, one, scoring)
+        assert torch.equal(d[-7:], rt.moe_route_backward(tail, i2, w2, counts, one, scoring))
+        assert (d[:-7] == d[0]).all()
+        del d
