@@ -1717,10 +1717,11 @@ gather_x_tok_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
 // [H/128][cap] biased exponents (rows [n, cap): zero codes, exponent 127).
 // Token-major (TOK: a token's groups are quantised once and written to the
 // rows of its K pairs) or row-major, like gather_x_tok_kernel and
-// gather_x_kernel.  Half a warp takes one group, eight values per lane.  xq, xe
-// (nullable): x as the caller has it in 8 bits already, codes [T][H] and exponent
-// bytes [T][ceil(H/128)], taken instead of quantising x.
-template <bool TOK>
+// gather_x_kernel.  Half a warp takes one group, eight values per lane.  CODES: xq,
+// xe are x as the caller has it in 8 bits already, codes [T][H] and exponent bytes
+// [T][ceil(H/128)], taken instead of quantising x (a kernel of its own: a branch took
+// 2 us of 337 of the layer of 4096 tokens that has none).
+template <bool TOK, bool CODES>
 __global__ void __launch_bounds__(kGatherThreads)
 gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ topk_ids,
                    const int32_t* __restrict__ mapping, const int32_t* __restrict__ usorted,
@@ -1760,7 +1761,7 @@ gather_x_mx_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ t
         const int g = g0 + 2 * j + half, c = g * 16 + hl;
         uint32_t q[2];
         uint32_t eb = 127;  // the exponent byte
-        if (xq != nullptr) {
+        if constexpr (CODES) {
           uint2 w = make_uint2(0, 0);
           if (tok >= 0 && g < ng) {
             if (c * 8 < H) w = __ldg(reinterpret_cast<const uint2*>(xq + tok * H + c * 8));
@@ -2632,7 +2633,9 @@ int moe_forward(const mlr_bf16* x, const int32_t* topk_ids, const float* topk_we
     const int64_t blocks = ceil_div(tasks > 0 ? tasks : 1, kGatherThreads / 32);
     const int grid = (int)(blocks < 16 * sm_count() ? blocks : 16 * sm_count());
     const cudaError_t e =
-        mx ? launch_pdl(tok_major ? gather_x_mx_kernel<true> : gather_x_mx_kernel<false>, dim3(grid),
+        mx ? launch_pdl(x_codes != nullptr ? (tok_major ? gather_x_mx_kernel<true, true> : gather_x_mx_kernel<false, true>)
+                                           : (tok_major ? gather_x_mx_kernel<true, false> : gather_x_mx_kernel<false, false>),
+                        dim3(grid),
                         dim3(kGatherThreads), 0, stream, x, topk_ids, token_lora_mapping, (const int32_t*)usorted,
                         (const int32_t*)pos, ustart + f.al.NB, T, K, E, L, H, f.cap, xs, x8, sx, yacc,
                         det ? 0 : (int64_t)T * H / 4, x_codes, x_exps)
