@@ -128,10 +128,14 @@ __device__ __forceinline__ float loss_of(double v, int tokens, int E, int K) {
 }
 
 constexpr int kLossCluster = 8;
-// Up to this many logits one cluster of eight blocks takes the whole batch, which saves
-// the workspace and the second launch: 4096 x 128 takes a caller 17 us instead of 20, though
-// the device 11 instead of 5.6.
+// One cluster of eight blocks can take a batch of up to this many logits, without a workspace
+// and a second launch.  It does so up to kOneClusterTokens, which saves a caller 4 us and costs
+// the device 0.3 to 6, more with every turn of its few blocks (us of a caller and of the device,
+// the cluster and two launches: 1024 x 8 14.6 and 5.1, 19.1 and 4.5; 4096 x 128 15.6 and 11.5,
+// 19.6 and 5.8; 8192 x 8 14.6 and 12.1, 19.6 and 6.1; 16384 x 8 20.7 and 20.3, 19.3 and 8.6;
+// 65536 x 8 68 and 68, 19.9 and 11.9), and beyond where no workspace is given.
 constexpr int64_t kOneClusterLogits = 1 << 19;
+constexpr int kOneClusterTokens = 8192;
 constexpr uint32_t kTurns = 64;  // of a thread's sum of shares
 template <int V> constexpr int kOneThreads = V == 32 ? 512 : 1024;  // of its blocks, by their registers
 
@@ -557,7 +561,7 @@ int run_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int
     constexpr int rows = kBlockTokens<lpt.value> ? 1 : kBalanceThreads / 32, cover = lpt.value * v.value;
     auto bytes = [&](int experts) { return (size_t)ring + (experts + 1) * 4 + (size_t)rows * experts * 4; };
     if constexpr (lpt.value == 8) {
-      if (one_cluster(T, E)) {
+      if (part == nullptr) {
         auto kernel = balance_kernel<VEC, lpt.value, v.value, true, E_>;
         constexpr int threads = kOneThreads<v.value>;
         auto of_one = [&](int experts) {
@@ -624,7 +628,7 @@ int by_type(int dtype, int E, const void* logits, const void* d_logits, F f) {
 extern "C" size_t moe_balance_loss_workspace_bytes(int32_t num_tokens, int32_t num_experts) {
   using namespace mlr;
   if (num_tokens < 0 || num_experts < 1 || num_experts > kMaxRouteExperts) return 0;
-  if (one_cluster(num_tokens, num_experts)) return 1;  // nothing is kept
+  if (one_cluster(num_tokens, num_experts) && num_tokens <= kOneClusterTokens) return 1;  // nothing is kept
   return (size_t)balance_blocks(num_tokens, num_experts) * (2 * num_experts + 1) * 4;
 }
 
@@ -637,12 +641,13 @@ extern "C" int moe_balance_loss(const void* logits, const int32_t* topk_ids, con
   if (code != MLR_OK) return code;
   if (loss == nullptr || counts == nullptr || (num_tokens > 0 && topk_ids == nullptr)) return MLR_ERR_INVALID;
   if (!on_word_grid({topk_ids, loss, counts, d_status})) return MLR_ERR_INVALID;
-  if (!(one_cluster(num_tokens, num_experts) && workspace == nullptr) &&
-      (workspace == nullptr || ws_bytes < moe_balance_loss_workspace_bytes(num_tokens, num_experts)))
-    return MLR_ERR_CAPACITY;
+  const bool one = one_cluster(num_tokens, num_experts);
+  const bool fits = workspace != nullptr && ws_bytes >= moe_balance_loss_workspace_bytes(num_tokens, num_experts);
+  if (!one && !fits) return MLR_ERR_CAPACITY;
+  const bool two = fits && !(one && num_tokens <= kOneClusterTokens);
   if (!aligned_to(workspace, 256)) return MLR_ERR_INVALID;
-  float* part = static_cast<float*>(workspace);
-  int32_t* count = reinterpret_cast<int32_t*>(part + (part ? balance_blocks(num_tokens, num_experts) * num_experts : 0));
+  float* part = two ? static_cast<float*>(workspace) : nullptr;
+  int32_t* count = two ? reinterpret_cast<int32_t*>(part + balance_blocks(num_tokens, num_experts) * num_experts) : nullptr;
   return by_type(dtype, num_experts, logits, nullptr, [&](auto vec, auto e) {
     return run_balance<vec.value, decltype(e)>(logits, topk_ids, token_mask, num_tokens, num_experts, topk, scoring == kSigmoid,
                                                part, count, loss, counts, d_status, stream);

@@ -46,3 +46,10 @@ def test_gradient_of_addresses_off_the_grid(lib, name):
 def test_norm_with_one_place_for_both_outputs(lib, codes):
     """y and the new residual stream in one buffer: the second would be lost."""
     assert lib.moe_rms_norm(FAKE, FAKE, FAKE, 4, 64, 0, 0, 1e-6, FAKE, FAKE, codes, codes, None) == mlr.MLR_ERR_INVALID
+
+
+def test_workspace_of_the_loss_by_tokens(lib):
+    """One launch without a workspace pays only up to so many tokens, however few experts."""
+    ws = lib.moe_balance_loss_workspace_bytes
+    assert ws(8192, 8) == ws(8192, 64) == ws(4096, 128) == 1
+    assert ws(8193, 8) > 4 * 17 and ws(65536, 8) > 4 * 17 and ws(8193, 64) > 4 * 129 and ws(8192, 65) > 4 * 131

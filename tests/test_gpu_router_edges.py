@@ -249,3 +249,22 @@ def test_offsets_beyond_32_bits(cuda_device, E, dtype):
         assert torch.equal(d[-7:], rt.moe_route_backward(tail, i2, w2, counts, one, scoring))
         assert (d[:-7] == d[0]).all()
         del d
+
+
+@pytest.mark.parametrize("T,E", [(8192, 8), (8193, 8), (65536, 8), (16384, 32), (8193, 61), (4096, 128)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_loss_with_and_without_a_workspace(cuda_device, T, E, scoring):
+    """Up to 2^19 logits in one launch and in two, chosen by the workspace given."""
+    K = 3
+    l = torch.randn(T, E, generator=torch.Generator().manual_seed(E)).cuda()
+    ids, _ = rt.moe_route(l, K, scoring)
+    loss, counts = rt.moe_balance_loss(l, ids, scoring)
+    out = torch.zeros((), device="cuda"), torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    code = rt._lib().moe_balance_loss(l.data_ptr(), ids.data_ptr(), None, T, E, K, 1, rt.SCORING[scoring], out[0].data_ptr(),
+                                      out[1].data_ptr(), None, 0, None, torch.cuda.current_stream().cuda_stream)
+    assert code == 0
+    ref, rc = ox.balance(f64(l), ids.cpu().numpy(), scoring)
+    # sums of T / 64 + 64 shares at most, of warps and blocks; over experts; ten roundings of each share
+    room = (T / 64 + 64 + 64 + E + 10) * 2.0 ** -24 * ref
+    for a, c in ((loss, counts), out):
+        assert np.array_equal(c.cpu().numpy(), rc) and abs(float(a) - ref) <= room
