@@ -1,5 +1,6 @@
 // mlr_router.cuh -- what the router's choice and the balance loss have in common:
-// logits as fp32, and a token's logits in the lanes of a part of a warp.
+// logits as fp32, their exponentials and sigmoids, and a token's logits in the lanes of a
+// part of a warp.
 #pragma once
 #include <math_constants.h>
 
@@ -38,8 +39,9 @@ __device__ __forceinline__ float quick_sigmoid(float v) {
   asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
 }
-// e^x for x <= 0 in a few instructions, whatever x within 5 2^-24 of itself: 2^h with h = x /
-// ln 2 rounded, times 1 plus x - h ln 2, which the rounding leaves.  0 below 2^-126.
+// e^x for x <= 0 in a few instructions, whatever x within 5 2^-24 of itself (3.3 measured from
+// -87 to 0; 64 without the remainder): 2^h with h = x / ln 2 rounded, times 1 plus x - h ln 2,
+// which the rounding leaves.  0 below 2^-126.
 __device__ __forceinline__ float share_exp(float x) {
   x = fmaxf(x, -100.f);  // -inf has no remainder
   const float h = x * 1.44269504f, left = fmaf(h, 1.90465421e-9f, fmaf(h, -0x1.62e43p-1f, x));  // ln 2 in two parts
@@ -163,15 +165,6 @@ __device__ __forceinline__ float part_max(float v) {
 #pragma unroll
   for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
-}
-
-inline int launched(cudaError_t err) {
-  if (err != cudaSuccess) {
-    (void)cudaGetLastError();  // not left for the next call to find
-    return MLR_ERR_CUDA;
-  }
-  note_launch();
-  return MLR_OK;
 }
 
 // Launches with `smem` bytes of dynamic shared memory.  Above what needs no opt-in the

@@ -633,15 +633,6 @@ fp8_dequantize_ragged_kernel(const uint8_t* __restrict__ codes, const uint8_t* _
   }
 }
 
-int launched(cudaError_t err) {
-  if (err != cudaSuccess) {
-    (void)cudaGetLastError();  // not left for the next call to find
-    return MLR_ERR_CUDA;
-  }
-  note_launch();
-  return MLR_OK;
-}
-
 // Threads of a row of `units` units, nv of them a thread.
 int row_lanes(int units, int nv) { return (int)ceil_div(units, 32 * nv) * 32; }
 // Short rows share a block of 128 threads.

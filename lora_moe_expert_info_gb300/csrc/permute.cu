@@ -759,15 +759,6 @@ cudaError_t allow_smem(Kernel kernel, size_t need, int most) {
   if (need <= 40 * 1024) return cudaSuccess;  // with the static part within the 48 KB that need no opt-in
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
-int launched(cudaError_t err, int kernels) {
-  if (err != cudaSuccess) {
-    (void)cudaGetLastError();  // not left for the next call to find
-    return MLR_ERR_CUDA;
-  }
-  note_launch(kernels);
-  return MLR_OK;
-}
-
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <int VB>

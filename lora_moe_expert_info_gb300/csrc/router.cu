@@ -133,8 +133,7 @@ __device__ __forceinline__ void warp_best(long long& v, int& i) {
   }
 }
 
-// The weights of the chosen experts, lane k place k (id -1: none); `most` is the
-// largest finite logit of the token (softmax).
+// The weights of the chosen experts, lane k place k (id -1: none, and after the others).
 template <typename E_>
 __device__ __forceinline__ void write_choice(const RouteArgs& a, const E_* row, int64_t t, int id, int lane) {
   float s = 0.f;

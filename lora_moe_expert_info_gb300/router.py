@@ -10,8 +10,9 @@ of -1 masks a pair.  Logits are bf16 or float32, [T, E]; one that is not finite
 counts as -inf and its expert is never chosen (NaN and +inf are reported by
 check=True).  Choice scores are compared in 64 bits where 32 do not tell them apart,
 ties go to the lowest index, and sums run in a fixed order: results are bit-identical
-between runs.  Sigmoids are float32: logits below -87 may weigh nothing.  Every step runs in the library's kernels; nothing here synchronises unless
-check=True.  All tensors are contiguous and on the current CUDA device.
+between runs.  Sigmoids are float32: logits below -87 may weigh nothing.  Every step
+runs in the library's kernels; nothing here synchronises unless check=True.  All
+tensors are contiguous and on the current CUDA device.
 """
 from __future__ import annotations
 
