@@ -683,6 +683,7 @@ route_fast_kernel(const E_* __restrict__ logits, const __grid_constant__ RouteAr
   uint32_t late = __ballot_sync(0xffffffffu, slow && token);
   while (late != 0) {
     const int o = (__ffs(late) - 1) / LPT;
+    __syncwarp();  // what the near candidates' keys and ranks are read from is the keys' place here
     late &= LPT == 32 ? 0u : ~(((1u << (LPT & 31)) - 1) << (o * LPT));
     choose_exactly(a, logits + (t0 + o) * E, t0 + o, slow_key, slow_key + E, lane);
     __syncwarp();
