@@ -17,8 +17,6 @@
 // norm 72 us (96% of the copy rate), with the 8 bits 89 (87%: 54% of the issue slots at
 // 20 warps an SM), gradients 76 (91%), 8 bits back 27 (97%).  1 to 256 rows: 2 to 4 us.
 #include <cuda_fp16.h>
-#include <float.h>
-#include <math_constants.h>
 
 #include <initializer_list>
 #include <type_traits>
@@ -119,9 +117,9 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
 // rounding errors of threads and warps average out over a row; what is left of fp32's
 // errors from there on would move values over rounding borders of bf16 or of the 8 bits, so
 // the last sums, the quotient and the root carry their remainders, and y is rounded once
-// (8192 x 7168 bf16: 140 values off a border, 480 without).  up is a power of two that
-// leaves hi + lo in [1, 2]: a row times it is near 1, so that its products with the weight
-// pass the range only where y does.  lo > 0: a product of infinity stays one.
+// (8192 x 7168 bf16: 140 values off a border, 480 without).  up is a power of two and hi + lo
+// in [1, 2]; lo > 2^-20, so that what it gives has the sign of what hi does and products of
+// infinity stay infinite.  No branch: one costs 3 to 13% of the time of a row.
 // `red`: a float per warp of the block; every thread of the block calls it.
 struct InverseRms { float up, hi, lo; };
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -143,40 +141,37 @@ __device__ __forceinline__ InverseRms row_inverse_rms(float sum, int H, float ep
   const float h = (float)H, q = s.x / h;
   const float2 v = add2(make_float2(q, (fmaf(-q, h, s.x) + s.y) / h), make_float2(eps, 0.f));
   const float m = 1.f / sqrtf(v.x), p = m * m;
-  if (!(m > 0.f && m < CUDART_INF_F)) return {m, 1.f, 0x1p-60f};  // of infinities, NaN and zeros
   // one step of Newton's, from the exact square of m (none where that is out of range)
   float left = fmaf(-v.y, p, fmaf(-v.x, fmaf(m, m, -p), fmaf(-v.x, p, 1.f)));
   if (!(fabsf(left) < 0x1p-20f)) left = 0.f;  // m is within two units of the last place
-  const float up = __uint_as_float(__float_as_uint(m) & 0x7f800000u), hi = m / up;
-  return {up, hi - 0x1p-20f, fmaf(0.5f * hi, left, 0x1p-20f)};
+  const uint32_t b = __float_as_uint(m);
+  const float hi = __uint_as_float((b & 0x7fffffu) | 0x3f800000u);  // up is 0 or infinite where m is
+  return {m == m ? __uint_as_float(b & 0x7f800000u) : m, hi - 0x1p-19f, fmaf(0.5f * hi, left, 0x1p-19f)};
 }
-// The product p, kept off infinity so that its remainder is a number.
-__device__ __forceinline__ float within_range(float p) {
-  float o;
-  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(o) : "f"(p), "f"(FLT_MAX));
-  return o;
-}
-// a w up (hi + lo), rounded once; EXACT: a w needs no more than fp32's bits.
+// a w up (hi + lo), rounded once; what is multiplied first is a row near 1, so that it passes
+// fp32's range only where y does.  EXACT (rows and weight in bf16): a w needs no more than
+// fp32's bits.
 template <bool EXACT, int N>
 __device__ __forceinline__ void row_output(float (&a)[N], const float (&w)[N], InverseRms m) {
-  row_scale(a, m.up);
+  if constexpr (EXACT) row_scale(a, m.up);
+  const float h = EXACT ? m.hi : m.up * m.hi, l = EXACT ? m.lo : m.up * m.lo;
   if constexpr (N == 1) {
-    float p = a[0] * w[0];
-    if constexpr (!EXACT) p = within_range(p);
-    const float left = EXACT ? 0.f : fmaf(a[0], w[0], -p);
-    a[0] = fmaf(p, m.hi, EXACT ? p * m.lo : fmaf(p, m.lo, left * m.hi));
+    const float p = a[0] * (EXACT ? w[0] : h);
+    a[0] = EXACT ? fmaf(p, h, p * l) : fmaf(p, w[0], fmaf(a[0], l, fmaf(a[0], h, -p)) * w[0]);
   } else {
-    const float2 hi = make_float2(m.hi, m.hi), lo = make_float2(m.lo, m.lo);
+    const float2 hi = make_float2(h, h), lo = make_float2(l, l);
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-      const float2 x = make_float2(a[i], a[i + 1]), v = make_float2(w[i], w[i + 1]);
-      float2 p = __fmul2_rn(x, v);
-      if constexpr (!EXACT) p = make_float2(within_range(p.x), within_range(p.y));
-      float2 t = __fmul2_rn(p, lo);
-      if constexpr (!EXACT) t = __ffma2_rn(__ffma2_rn(x, v, make_float2(-p.x, -p.y)), hi, t);
-      t = __ffma2_rn(p, hi, t);
-      a[i] = t.x;
-      a[i + 1] = t.y;
+      const float2 x = make_float2(a[i], a[i + 1]), v = make_float2(w[i], w[i + 1]), p = __fmul2_rn(x, EXACT ? v : hi);
+      float2 y;
+      if constexpr (EXACT) {
+        y = __ffma2_rn(p, hi, __fmul2_rn(p, lo));
+      } else {
+        const float2 left = __ffma2_rn(x, lo, __ffma2_rn(x, hi, make_float2(-p.x, -p.y)));
+        y = __ffma2_rn(p, v, __fmul2_rn(left, v));
+      }
+      a[i] = y.x;
+      a[i + 1] = y.y;
     }
   }
 }
