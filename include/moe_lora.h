@@ -320,7 +320,8 @@ int fused_moe_lora_forward_fp8_w8a8(const mlr_bf16* x, const int32_t* topk_ids, 
  * already, as moe_rms_norm leaves it: x_codes uint8 [T, H] (16-byte aligned) and
  * x_exps uint8 [T, ceil(H/128)] (bytes below 255) are what gate_up's base GEMM
  * multiplies; x itself feeds the LoRA shrink.  With the codes of x's own
- * quantisation y is bit-identical to that of fused_moe_lora_forward_fp8_w8a8.
+ * quantisation y is bit-identical to that of fused_moe_lora_forward_fp8_w8a8,
+ * which is the faster of the two: x is read and sorted in bf16 here as well.
  */
 int fused_moe_lora_forward_fp8_w8a8_xq(const mlr_bf16* x, const uint8_t* x_codes, const uint8_t* x_exps,
                                        const int32_t* topk_ids, const float* topk_weights,
@@ -647,7 +648,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   float32.  dx may be dy or d_r.  workspace of moe_rms_norm_backward_workspace_bytes,
  *   256-byte aligned.
  * Sums are held in fp32 in a fixed order: results are bit-identical between runs.  A
- *   row's sum of squares must stay within fp32's range (beyond it y comes out 0).
+ *   row's sum of squares must stay within fp32's range (beyond it y comes out 0; below it,
+ *   without eps, infinite or NaN).
  * Limit: hidden <= 16384.
  *
  * moe_route: each token's topk experts from logits [num_tokens, num_experts].
@@ -674,11 +676,13 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   (nullable) and, given counts and d_loss[1] (both or neither), from the balance loss;
  *   zeros in masked tokens.  The same id twice in a token: both gradients are added.
  *   topk, scoring, renormalize and scale as in the forward calls.
- * Sigmoids are held in fp32: a logit below -87 may count as one of 0 (in weights, loss
- *   and gradients; the choice is not affected), which leaves a token that has no other
- *   with weights of 0 where `renormalize`, and out of the loss's shares; a share of the
- *   loss below 2^-126 may count as 0.
+ * Sigmoids are held in fp32: that of a logit below -87 has fewer bits or counts as 0 (in
+ *   weights, loss and gradients; the choice is not affected), which may leave a token that
+ *   has no other with weights of 0 where `renormalize`, and out of the loss's shares; a
+ *   share of the loss below 2^-126 may count as 0.
  * Limits: num_experts <= 4096, topk <= 32, num_groups <= 256, num_tokens * topk < 2^31 - 1.
+ *   The choice is fast up to 1024 experts, 16 places and 8 groups (16 from 257 experts, 32 from
+ *   513), and 10 to 40 times slower beyond.
  *   Arrays that do not lie on their elements' grid are refused (MLR_ERR_INVALID).
  */
 #define MLR_SCORE_SOFTMAX 0

@@ -581,7 +581,7 @@ def fused_moe_lora_forward_fp8_w8a8(x, topk_ids, topk_weights, token_lora_mappin
     2^(e-127)); the activations of the base GEMMs are quantised per token and
     128-channel group on the way (see the C header).  x_codes [T,H] and x_exps
     [T,ceil(H/128)] (both or neither): x in 8 bits already, as norm.rms_norm_fp8
-    leaves it."""
+    leaves it.  y is the same, but not sooner: x is read and sorted in bf16 too."""
     cb = lambda n: (n + 127) // 128  # noqa: E731
     quant = [(w_gate_up_q, "w_gate_up_q", torch.uint8), (w_gate_up_exp, "w_gate_up_exp", torch.uint8),
              (w_down_q, "w_down_q", torch.uint8), (w_down_exp, "w_down_exp", torch.uint8)]

@@ -14,8 +14,10 @@
 // A row stays in the registers of its threads (the gradients': in their places of
 // shared memory) between the pass that reads it and the one that writes it, so every
 // tensor is moved once, and HBM bounds all of it.  8192 rows of 7168 bf16: residual and
-// norm 72 us (96% of the copy rate), with the 8 bits 89 (87%: 54% of the issue slots at
-// 20 warps an SM), gradients 76 (91%), 8 bits back 27 (97%).  1 to 256 rows: 2 to 4 us.
+// norm 71 us (97% of the copy rate), with the 8 bits 87 (89%: 47% of the issue slots at 20
+// warps an SM, whose 96 registers spill 88 bytes a thread), gradients 76 (91%), 8 bits
+// back 27 (97%).  float32: 144 (96%), gradients 136.  1 to 256 rows: 2 to 4 us.  Rows off the
+// 16-byte grid go element by element, 24 to 84% of the rate, their gradients 14 to 63%.
 #include <cuda_fp16.h>
 
 #include <initializer_list>

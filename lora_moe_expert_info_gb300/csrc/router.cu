@@ -11,9 +11,13 @@
 // tell two of them apart, they are computed in 64, to a few units of the last place.
 //
 // A token's logits are read once and stay in registers.  A million tokens, 8 of 256
-// experts: 240 us, 70% of the copy rate; what bounds it is the ALU pipe (55% busy) and
+// experts: 241 us, 70% of the copy rate; what bounds it is the ALU pipe (56% busy) and
 // the latency of the merges and ranks, at 45% of the warps.  One token 2.8 us; 256
 // tokens of 256 experts in groups with biases 7.5, 10 where some scores are near.
+// Few experts cost as much as 64 (a million tokens, 2 of 8: 171 us).  More than 1024
+// experts, 16 places, or groups than a token has lanes (8 up to 256 experts, 16 up to 512,
+// else 32) go through the exact choice alone: 262144 tokens, 20 of 256 experts 1155 us (16 of
+// them 120); 65536 tokens, 8 of 2048 experts 2775 (8 of 1024 64); in 16 groups 1140 (in 8 54).
 #include <float.h>
 
 #include "mlr_router.cuh"
