@@ -670,8 +670,8 @@ int moe_fp4_expert_product(const uint8_t* a_codes, const uint8_t* a_scales, cons
  *   sigmoid(logits) over their sum.  counts int32 [num_experts + 1]: c, then N.  Ids
  *   other than -1 outside [0, num_experts) set MLR_STATUS_INDEX; neither counts.
  *   workspace of moe_balance_loss_workspace_bytes, 256-byte aligned.  Up to 2^19 logits of
- *   at most 256 experts null is taken too (one launch, which is as fast where the size is 1,
- *   up to 8192 tokens, and slower above).
+ *   at most 256 experts null is taken too: one launch, as it is where the size is 1, and
+ *   slower than two for more than 8192 tokens.
  * moe_route_backward: d_logits of type `dtype` from d_weights [num_tokens, topk]
  *   (nullable) and, given counts and d_loss[1] (both or neither), from the balance loss;
  *   zeros in masked tokens.  The same id twice in a token: both gradients are added.

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from lora_moe_expert_info_gb300 import router as rt
+from lora_moe_expert_info_gb300 import norm, router as rt
 from oracle import router as ox
 
 pytestmark = pytest.mark.gpu
@@ -268,3 +268,32 @@ def test_loss_with_and_without_a_workspace(cuda_device, T, E, scoring):
     room = (T / 64 + 64 + 64 + E + 10) * 2.0 ** -24 * ref
     for a, c in ((loss, counts), out):
         assert np.array_equal(c.cpu().numpy(), rc) and abs(float(a) - ref) <= room
+
+
+def test_a_training_step_from_one_graph(cuda_device):
+    """Norm, router product, choice with its loss, and their gradients captured together and
+    replayed on another batch with more padding, against the same step run eagerly."""
+    T, H, E, K = 96, 256, 32, 4
+    g = torch.Generator().manual_seed(0)
+    x, res, up = (torch.randn(T, H, generator=g).cuda() for _ in range(3))
+    gain, gate = torch.randn(H, generator=g).cuda().requires_grad_(), (torch.randn(H, E, generator=g) / 16).cuda().requires_grad_()
+    mask = torch.arange(T, device="cuda") < 90
+
+    def step():
+        y, r = norm.RmsNorm.apply(x, gain, 1e-6, res)
+        w, _, loss, _ = rt.MoeRoute.apply(y @ gate, K, "sigmoid", None, 8, 4, True, 2.5, mask)
+        return torch.autograd.grad(w.square().sum() + loss + (y * up).sum() + r.sum(), (gain, gate))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    x.copy_(torch.randn(T, H, generator=g))
+    mask[50:] = False
+    graph.replay()
+    for a, b in zip(out, step()):
+        assert torch.equal(a, b)
